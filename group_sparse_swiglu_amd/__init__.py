@@ -11,7 +11,10 @@ update_load_balance_bias; and, from the Megatron-Core developer guide page
 "core.inference.moe.sigmoid_topk", sigmoid_topk_routing; and, from the
 parameter-golf pull request 1105 page, the LeakyReLU(0.5)^2 MLP with a stored
 activation gradient (leaky_mlp_fwd / leaky_mlp_bwd); and, from the FlashFFN
-README, the multi-head sub-network FFN core (mhffn_fwd / mhffn_bwd).
+README, the multi-head sub-network FFN core (mhffn_fwd / mhffn_bwd).  Beside
+them: the feed-forward products in 8-bit floating point with block scales
+(fp8_quantize, fp8_quantize_weight, fp8_matmul, fp8_linear) and the whole
+expert layer for a few tokens (moe_decode).
 """
 from __future__ import annotations
 
@@ -30,10 +33,13 @@ __all__ = [
     "FfnContext", "EXPORTED_SYMBOLS", "sigmoid_topk_supported", "sigmoid_topk_routing",
     "leaky_mlp_workspace_size", "leaky_mlp_fwd", "leaky_mlp_bwd", "leaky_mlp_saved_views",
     "mhffn_supported", "mhffn_fwd", "mhffn_bwd",
+    "fp8_quantize", "fp8_quantize_weight", "fp8_matmul", "fp8_matmul_workspace_size", "fp8_linear",
+    "moe_decode", "moe_decode_supported", "moe_decode_workspace_size",
 ]
 
 ESG_F32 = 0
 ESG_BF16 = 1
+ESG_E4M3 = 2
 STATUS_GROUP_OUT_OF_RANGE = 1
 STATUS_GROUP_DUPLICATE = 2
 
@@ -86,6 +92,16 @@ _SIGNATURES = {
     "esg_sigmoid_topk_supported": (_c_int, [_c_int, _c_int]),
     "esg_sigmoid_topk_routing": (_c_int, [_c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_f, _c_int, _c_vp, _c_vp,
                                           _c_vp]),
+    "esg_fp8_quant_rows": (_c_int, [_c_vp, _c_int, _c_int, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "esg_fp8_quant_tiles": (_c_int, [_c_vp, _c_int, _c_int, _c_int, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "esg_fp8_matmul_workspace_size": (_c_int, [_c_int, _c_int, _c_int, ctypes.POINTER(_c_size)]),
+    "esg_fp8_matmul": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_vp, _c_vp,
+                                _c_size, _c_vp]),
+    "esg_moe_decode_supported": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "esg_moe_decode_workspace_size": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_c_size)]),
+    "esg_moe_decode": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
+                                _c_int, _c_int, _c_int, _c_int, _c_f, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_size,
+                                _c_vp]),
     "esg_mfma_rate_probe": (_c_int, [_c_int, _c_int, _c_vp, _c_vp]),
     "esg_timing_enable": (_c_int, [_c_int]),
     "esg_timing_reset": (_c_int, []),
@@ -478,6 +494,216 @@ def sigmoid_topk_routing(logits, expert_bias, topk: int, scaling_factor: Optiona
         _dev(probs, "probs", torch.float32), _dev(indices, "indices", torch.int64), _stream(logits.device)),
         "sigmoid_topk_routing")
     return probs, indices
+
+
+def _ceil128(n: int) -> int:
+    return (n + 127) // 128
+
+
+def fp8_quantize(x, transposed: bool = False):
+    """Rows to e4m3 with a float32 scale per 1 x 128 block.
+
+    x: float32 or bfloat16 [M, K], K a multiple of 16 -> (q float8_e4m3fn
+    [M, K], scale [M, ceil(K/128)]).  ``transposed`` adds, from the same read,
+    the blocks of 128 rows of a column, for a contraction over the rows:
+    (q, scale, qt [K, M16], scale_t [K, ceil(M/128)]) with M16 = M rounded up to
+    a multiple of 16 (zeros past M)."""
+    if x.dim() != 2:
+        raise EsgError("x must be [rows, cols]")
+    M, K = x.shape
+    code = _dtype_code(x)
+    dev = x.device
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    q = torch.empty(M, K, dtype=e4m3, device=dev)
+    scale = torch.empty(M, _ceil128(K), dtype=f32, device=dev)
+    qt = scale_t = None
+    if transposed:
+        qt = torch.empty(K, (M + 15) // 16 * 16, dtype=e4m3, device=dev)
+        scale_t = torch.empty(K, _ceil128(M), dtype=f32, device=dev)
+    _check(lib().esg_fp8_quant_rows(_dev(x, "x"), code, M, K, q.data_ptr(), scale.data_ptr(),
+                                    None if qt is None else qt.data_ptr(),
+                                    None if qt is None else scale_t.data_ptr(), _stream(dev)), "fp8_quantize")
+    return (q, scale, qt, scale_t) if transposed else (q, scale)
+
+
+def fp8_quantize_weight(w, transposed: bool = False):
+    """Weights to e4m3 with a float32 scale per 128 x 128 block.
+
+    w: float32 or bfloat16 [N, K] or [batch, N, K], K a multiple of 16 -> (q like
+    w in float8_e4m3fn, scale [..., ceil(N/128), ceil(K/128)]).  ``transposed``
+    adds the transposes of the same values: (q, scale, qt [..., K, N16],
+    scale_t [..., ceil(K/128), ceil(N/128)]), N16 = N rounded up to a multiple
+    of 16 (zeros past N)."""
+    if w.dim() not in (2, 3):
+        raise EsgError("w must be [rows, cols] or [batch, rows, cols]")
+    lead, (N, K) = w.shape[:-2], w.shape[-2:]
+    code = _dtype_code(w)
+    dev = w.device
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    q = torch.empty(w.shape, dtype=e4m3, device=dev)
+    scale = torch.empty(*lead, _ceil128(N), _ceil128(K), dtype=f32, device=dev)
+    qt = scale_t = None
+    if transposed:
+        qt = torch.empty(*lead, K, (N + 15) // 16 * 16, dtype=e4m3, device=dev)
+        scale_t = torch.empty(*lead, _ceil128(K), _ceil128(N), dtype=f32, device=dev)
+    _check(lib().esg_fp8_quant_tiles(_dev(w, "w"), code, lead[0] if lead else 1, N, K, q.data_ptr(),
+                                     scale.data_ptr(), None if qt is None else qt.data_ptr(),
+                                     None if qt is None else scale_t.data_ptr(), _stream(dev)),
+           "fp8_quantize_weight")
+    return (q, scale, qt, scale_t) if transposed else (q, scale)
+
+
+def fp8_matmul_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of scratch esg_fp8_matmul needs for this shape (0 for most)."""
+    need = _c_size()
+    _check(lib().esg_fp8_matmul_workspace_size(M, N, K, ctypes.byref(need)), "fp8_matmul_workspace_size")
+    return need.value
+
+
+def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, workspace: Optional[dict] = None):
+    """y = A B^T of e4m3 operands with block scales -> [M, N] (bfloat16 or float32).
+
+    a, a_scale: [M, K] and [M, ceil(K/128)] as fp8_quantize gives them; b: [N, K]
+    with b_scale [ceil(N/128), ceil(K/128)] (fp8_quantize_weight) or
+    [N, ceil(K/128)] (fp8_quantize).  ``workspace``: optional dict reused across
+    calls to hold the scratch buffer."""
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise EsgError("a must be [M, K] and b [N, K]")
+    (M, K), N = a.shape, b.shape[0]
+    kb = (K + 127) // 128
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    if a_scale.shape != (M, kb):
+        raise EsgError("a_scale must be [M, ceil(K/128)]")
+    rows = b_scale.shape == (N, kb)
+    if not rows and b_scale.shape != ((N + 127) // 128, kb):
+        raise EsgError("b_scale must be [ceil(N/128), ceil(K/128)] or [N, ceil(K/128)]")
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=a.device)
+    elif out.shape != (M, N):
+        raise EsgError("out must be [M, N]")
+    code = _dtype_code(out)
+    need = fp8_matmul_workspace_size(M, N, K)
+    ws = _ws(need, a.device, workspace, "fp8_matmul") if need else None
+    _check(lib().esg_fp8_matmul(_dev(a, "a", e4m3), _dev(a_scale, "a_scale", f32), _dev(b, "b", e4m3),
+                                _dev(b_scale, "b_scale", f32), int(rows), code, M, N, K, _dev(out, "out"),
+                                None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                _stream(a.device)), "fp8_matmul")
+    return out
+
+
+class _Fp8Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(fctx, x, w):
+        need_x, need_w = fctx.needs_input_grad
+        x2 = x.reshape(-1, x.shape[-1]).contiguous()
+        xq = fp8_quantize(x2, transposed=need_w)
+        wq = fp8_quantize_weight(w.contiguous(), transposed=need_x)
+        y = fp8_matmul(xq[0], xq[1], wq[0], wq[1], out_dtype=x.dtype)
+        fctx.save_for_backward(*(xq[2:] if need_w else (None, None)), *(wq[2:] if need_x else (None, None)))
+        fctx.esg = (x.shape, x.dtype, w.shape, w.dtype)
+        return y.view(*x.shape[:-1], w.shape[0])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(fctx, dy):
+        xqt, xst, wqt, wst = fctx.saved_tensors
+        xshape, xdtype, wshape, wdtype = fctx.esg
+        dq = fp8_quantize(dy.reshape(-1, wshape[0]).contiguous(), transposed=xqt is not None)
+        dx = dw = None
+        if wqt is not None:
+            dx = fp8_matmul(dq[0], dq[1], wqt, wst, out_dtype=xdtype).view(xshape)
+        if xqt is not None:
+            if xqt.shape[1] == 0:
+                dw = torch.zeros(wshape, dtype=wdtype, device=dy.device)
+            else:
+                dw = fp8_matmul(dq[2], dq[3], xqt, xst, out_dtype=wdtype)
+        return dx, dw
+
+
+def fp8_linear(x, w):
+    """Differentiable y = x W^T with every product in e4m3 with block scales.
+
+    x: [..., K], w: [N, K] (float32 or bfloat16, K and N multiples of 16); y has
+    the dtype of x, the gradients those of x and w.  Forward and input gradient
+    take W in 128 x 128 blocks and x, dy in 1 x 128 ones; the weight gradient
+    takes dy and x in blocks of 128 tokens.  What the backward keeps of x and W
+    is their e4m3 transposes."""
+    if w.dim() != 2 or x.shape[-1] != w.shape[1]:
+        raise EsgError("x must be [..., K] and w [N, K]")
+    if w.shape[0] % 16 or w.shape[1] % 16:
+        raise EsgError("both dimensions of w must be multiples of 16")
+    return _Fp8Linear.apply(x, w)
+
+
+def moe_decode_supported(tokens: int, experts: int, topk: int, d_model: int, d_ff: int,
+                         dtype=torch.bfloat16) -> bool:
+    """Whether moe_decode takes this shape (at most 64 tokens) and weight dtype."""
+    code = {torch.bfloat16: ESG_BF16, torch.float8_e4m3fn: ESG_E4M3}.get(dtype, -1)
+    return bool(lib().esg_moe_decode_supported(tokens, experts, topk, d_model, d_ff, code))
+
+
+def moe_decode_workspace_size(tokens: int, experts: int, topk: int, d_model: int, d_ff: int) -> int:
+    need = _c_size()
+    _check(lib().esg_moe_decode_workspace_size(tokens, experts, topk, d_model, d_ff, ctypes.byref(need)),
+           "moe_decode_workspace_size")
+    return need.value
+
+
+def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scaling_factor: Optional[float] = None,
+               scales=None, out=None, workspace: Optional[dict] = None):
+    """A whole expert layer for at most 64 tokens -> (y, probs, indices).
+
+    x: bfloat16 [T, d]; w_router: bfloat16 [E, d]; expert_bias: float32 [E] (a
+    strided view is accepted); w_gate, w_up: [E, ff, d] and w_down: [E, d, ff],
+    bfloat16, or float8_e4m3fn with ``scales`` = (gate, up, down) from
+    fp8_quantize_weight.  Routing as sigmoid_topk_routing on x w_router^T; y:
+    bfloat16 [T, d], probs: float32 [T, topk], indices: int64 [T, topk].
+    ``out`` may supply the three; ``workspace``: optional dict reused across
+    calls to hold the scratch buffer."""
+    if x.dim() != 2 or w_gate.dim() != 3:
+        raise EsgError("x must be [T, d] and the expert weights [E, rows, cols]")
+    T, d = x.shape
+    E, ff, _ = w_gate.shape
+    if w_gate.shape != (E, ff, d) or w_up.shape != (E, ff, d) or w_down.shape != (E, d, ff) or \
+            w_router.shape != (E, d):
+        raise EsgError("shapes: w_router [E,d], w_gate/w_up [E,ff,d], w_down [E,d,ff]")
+    bf, f32, dev = torch.bfloat16, torch.float32, x.device
+    wt = w_gate.dtype
+    if wt == bf:
+        code, sc = ESG_BF16, (None, None, None)
+    elif wt == torch.float8_e4m3fn:
+        if scales is None:
+            raise EsgError("float8 expert weights need their scales")
+        fb, db = (ff + 127) // 128, (d + 127) // 128
+        for s, shape in zip(scales, ((E, fb, db), (E, fb, db), (E, db, fb))):
+            if s.shape != shape:
+                raise EsgError("scales must be [E, ceil(rows/128), ceil(cols/128)] of each weight")
+        code, sc = ESG_E4M3, tuple(_dev(s, "scales", f32) for s in scales)
+    else:
+        raise EsgError(f"unsupported weight dtype {wt}; use bfloat16 or float8_e4m3fn")
+    if expert_bias.dim() != 1 or expert_bias.shape[0] != E or expert_bias.dtype != f32:
+        raise EsgError("expert_bias must be float32 [E]")
+    if not expert_bias.is_cuda or expert_bias.device != dev:
+        raise EsgError("expert_bias must be on the GPU of x")
+    stride = expert_bias.stride(0) if E > 1 else 1
+    if stride < 1:
+        raise EsgError("expert_bias must have a positive stride")
+    ws = _ws(moe_decode_workspace_size(T, E, topk, d, ff), dev, workspace, "moe_decode")
+    if out is None:
+        y = torch.empty(T, d, dtype=bf, device=dev)
+        probs = torch.empty(T, topk, dtype=f32, device=dev)
+        indices = torch.empty(T, topk, dtype=torch.int64, device=dev)
+    else:
+        y, probs, indices = out
+        if y.shape != (T, d) or probs.shape != (T, topk) or indices.shape != (T, topk):
+            raise EsgError("out must be [T, d], [T, topk] and [T, topk]")
+    _check(lib().esg_moe_decode(
+        _dev(x, "x", bf), _dev(w_router, "w_router", bf), expert_bias.data_ptr(), stride, _dev(w_gate, "w_gate", wt),
+        _dev(w_up, "w_up", wt), _dev(w_down, "w_down", wt), *sc, code, T, E, topk, d, ff,
+        1.0 if scaling_factor is None else float(scaling_factor), int(scaling_factor is not None), _dev(y, "y", bf),
+        _dev(probs, "probs", f32), _dev(indices, "indices", torch.int64), ws.data_ptr(), ws.numel(), _stream(dev)),
+        "moe_decode")
+    return y, probs, indices
 
 
 def mfma_rate_probe(blocks: int, iters: int, out: torch.Tensor) -> None:

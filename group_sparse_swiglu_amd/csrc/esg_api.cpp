@@ -482,6 +482,113 @@ int esg_sigmoid_topk_routing(const float* logits, const float* expert_bias, int 
                                         apply_scaling, probs, indices, (hipStream_t)stream));
 }
 
+namespace {
+// rows of cols elements quantised in blocks of 128: cols a multiple of 16, and
+// the launch's workgroups (one per 128 x 128 tile at most) within 2^31
+int quant_shape(int dtype, int batch, int rows, int cols) {
+  if (dtype != ESG_F32 && dtype != ESG_BF16) return ESG_ERR_UNSUPPORTED;
+  if (batch < 0 || rows < 0 || cols <= 0) return ESG_ERR_INVALID_ARG;
+  if (cols % 16 || rows > (1 << 30) || cols > (1 << 22)) return ESG_ERR_UNSUPPORTED;
+  const double tiles = (double)batch * ((rows + 127) / 128) * ((cols + 127) / 128);
+  return tiles < 2147483647.0 ? ESG_OK : ESG_ERR_UNSUPPORTED;
+}
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+}  // namespace
+
+int esg_fp8_quant_rows(const void* x, int dtype, int rows, int cols, void* q, float* scale, void* qt, float* scale_t,
+                       void* stream) {
+  const int e = quant_shape(dtype, 1, rows, cols);
+  if (e != ESG_OK) return e;
+  if (rows == 0) return ESG_OK;
+  if ((qt == nullptr) != (scale_t == nullptr)) return ESG_ERR_INVALID_ARG;
+  for (const void* p : {x, (const void*)q, (const void*)(qt ? qt : q)})
+    if (p == nullptr || !aligned16(p)) return ESG_ERR_INVALID_ARG;
+  if (scale == nullptr || !aligned4(scale) || !aligned4(scale_t)) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_quant_rows(dtype, x, rows, cols, q, scale, qt, scale_t, (hipStream_t)stream));
+}
+
+int esg_fp8_quant_tiles(const void* w, int dtype, int batch, int rows, int cols, void* q, float* scale, void* qt,
+                        float* scale_t, void* stream) {
+  const int e = quant_shape(dtype, batch, rows, cols);
+  if (e != ESG_OK) return e;
+  if (batch == 0 || rows == 0) return ESG_OK;
+  if ((qt == nullptr) != (scale_t == nullptr)) return ESG_ERR_INVALID_ARG;
+  for (const void* p : {w, (const void*)q, (const void*)(qt ? qt : q)})
+    if (p == nullptr || !aligned16(p)) return ESG_ERR_INVALID_ARG;
+  if (scale == nullptr || !aligned4(scale) || !aligned4(scale_t)) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_quant_tiles(dtype, w, batch, rows, cols, q, scale, qt, scale_t, (hipStream_t)stream));
+}
+
+namespace {
+int fp8_shape(int M, int N, int K) {
+  if (M < 0 || N < 0 || K <= 0) return ESG_ERR_INVALID_ARG;
+  if (K % 16 || K > (1 << 22) || M > (1 << 30) || N > (1 << 30)) return ESG_ERR_UNSUPPORTED;
+  // one workgroup per output tile of at least 16 x 128
+  if ((double)((M + 127) / 128) * ((N + 15) / 16) >= 2147483647.0) return ESG_ERR_UNSUPPORTED;
+  return ESG_OK;
+}
+}  // namespace
+
+int esg_fp8_matmul_workspace_size(int M, int N, int K, size_t* workspace_bytes) {
+  if (workspace_bytes == nullptr) return ESG_ERR_INVALID_ARG;
+  const int e = fp8_shape(M, N, K);
+  if (e != ESG_OK) return e;
+  *workspace_bytes = fp8_matmul_workspace_bytes(M, N, K);
+  return ESG_OK;
+}
+
+int esg_fp8_matmul(const void* a, const float* a_scale, const void* b, const float* b_scale, int b_scale_rows,
+                   int out_dtype, int M, int N, int K, void* y, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  const int e = fp8_shape(M, N, K);
+  if (e != ESG_OK) return e;
+  if (out_dtype != ESG_F32 && out_dtype != ESG_BF16) return ESG_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return ESG_OK;
+  for (const void* p : {a, b, (const void*)y})
+    if (p == nullptr || !aligned16(p)) return ESG_ERR_INVALID_ARG;
+  if (a_scale == nullptr || b_scale == nullptr || !aligned4(a_scale) || !aligned4(b_scale))
+    return ESG_ERR_INVALID_ARG;
+  const size_t need = fp8_matmul_workspace_bytes(M, N, K);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return ESG_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_fp8_matmul(a, a_scale, b, b_scale, b_scale_rows != 0, out_dtype, M, N, K, y, workspace,
+                                      (hipStream_t)stream));
+}
+
+int esg_moe_decode_supported(int tokens, int experts, int topk, int d_model, int d_ff, int w_dtype) {
+  return tokens >= 0 && tokens <= kMoeMaxTokens && experts >= 1 && experts <= kMoeMaxExperts && topk >= 1 &&
+         topk <= kRouteMaxK && topk <= experts && d_model >= 16 && d_model % 16 == 0 && d_model <= (1 << 20) &&
+         d_ff >= 16 && d_ff % 16 == 0 && d_ff <= (1 << 20) && (w_dtype == ESG_BF16 || w_dtype == ESG_E4M3);
+}
+
+int esg_moe_decode_workspace_size(int tokens, int experts, int topk, int d_model, int d_ff, size_t* workspace_bytes) {
+  if (workspace_bytes == nullptr || tokens < 0) return ESG_ERR_INVALID_ARG;
+  if (!esg_moe_decode_supported(tokens, experts, topk, d_model, d_ff, ESG_BF16)) return ESG_ERR_UNSUPPORTED;
+  *workspace_bytes = moe_decode_workspace_bytes(tokens, experts, topk, d_ff);
+  return ESG_OK;
+}
+
+int esg_moe_decode(const void* x, const void* w_router, const float* expert_bias, int bias_stride, const void* w_gate,
+                   const void* w_up, const void* w_down, const float* s_gate, const float* s_up, const float* s_down,
+                   int w_dtype, int tokens, int experts, int topk, int d_model, int d_ff, float scaling_factor,
+                   int apply_scaling, void* y, float* probs, int64_t* indices, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  if (tokens < 0 || bias_stride < 1) return ESG_ERR_INVALID_ARG;
+  if (!esg_moe_decode_supported(tokens, experts, topk, d_model, d_ff, w_dtype)) return ESG_ERR_UNSUPPORTED;
+  if (tokens == 0) return ESG_OK;
+  for (const void* p : {x, w_router, w_gate, w_up, w_down, (const void*)y})
+    if (p == nullptr || !aligned16(p)) return ESG_ERR_INVALID_ARG;
+  if (expert_bias == nullptr || probs == nullptr || indices == nullptr) return ESG_ERR_INVALID_ARG;
+  if (w_dtype == ESG_E4M3 && (s_gate == nullptr || s_up == nullptr || s_down == nullptr)) return ESG_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < moe_decode_workspace_bytes(tokens, experts, topk, d_ff))
+    return ESG_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return ESG_ERR_INVALID_ARG;
+  const MoeCall c{x,      w_router, expert_bias, bias_stride, w_gate, w_up,           w_down,        s_gate, s_up,  s_down,
+                  w_dtype, tokens,  experts,     topk,        d_model, d_ff,          scaling_factor, apply_scaling, y,
+                  probs,  indices};
+  return hip_status(launch_moe_decode(c, workspace, (hipStream_t)stream));
+}
+
 int esg_mfma_rate_probe(int blocks, int iters, float* out, void* stream) {
   if (blocks <= 0 || iters <= 0 || out == nullptr) return ESG_ERR_INVALID_ARG;
   return hip_status(launch_mfma_probe(blocks, iters, out, (hipStream_t)stream));

@@ -1,0 +1,471 @@
+// Matrix product of 8-bit floating point (e4m3) operands with a float32 scale
+// per block of 128 K elements:
+//   y[m, n] = sum over k of a[m, k] sa[m, k/128] * b[n, k] sb[n or n/128, k/128]
+// a: [M, K] (activations), b: [N, K] (weights); the blocks of b are 1 x 128
+// (SB_ROWS) or 128 x 128 (SB_TILES).  K is a multiple of 16.
+//
+// One 16 x 16 x 128 product covers exactly one block of K, so the inner sum of
+// a block comes out of the matrix core unscaled and is added to the float32
+// result with its scales by vector FMAs, four per product.  b is the products'
+// row side: a lane then holds four consecutive n of one m, so it needs one
+// a-scale and (128 x 128 blocks) a wave-uniform b-scale per product.
+//
+// Precision: the 8-bit matrix product aligns the terms of a sum to its largest
+// and drops what falls below (measured on normal data with channels of unequal
+// size: 2.1e-5 to 3.0e-5 of the result's norm, the same for every 8-bit form),
+// while bf16 products keep float32 accuracy (1.3e-8).  A bf16 result rounds at
+// 1.7e-3, so it takes the 8-bit products; a float32 result would lose bits it
+// can hold, so its operands are widened to bf16 (exactly) on the way into bf16
+// products, at half the matrix rate.
+//
+// Two kernels: tile_kernel for M > kSkinnyM (operand tiles staged through LDS),
+// skinny_kernel for few rows, where the product is a read of b.
+#include <algorithm>
+
+#include "esg_fp8.hpp"
+#include "esg_internal.hpp"
+#include "esg_pipe.hpp"
+
+namespace esg {
+namespace {
+
+enum { SB_TILES = 0, SB_ROWS = 1 };
+// OUT_PART: float32 partial sums of a split K axis (FINE: of a float32 result)
+enum { OUT_F32 = 0, OUT_BF16 = 1, OUT_PART = 2, OUT_PART_FINE = 3 };
+__host__ __device__ constexpr bool fine(int out) { return out == OUT_F32 || out == OUT_PART_FINE; }
+
+// One K block of a 16-row operand as a lane holds it: 16 bytes of chunk g and
+// 16 of chunk g + 4, as they are, or widened to bf16 (four products of 32 K).
+template <bool FINE>
+struct Frag;
+template <>
+struct Frag<false> {
+  uint4 v[2];
+  __device__ __forceinline__ Frag() {}
+  __device__ __forceinline__ Frag(const uint4& lo, const uint4& hi) : v{lo, hi} {}
+};
+template <>
+struct Frag<true> {
+  uint4 v[4];
+  __device__ __forceinline__ Frag() {}
+  __device__ __forceinline__ Frag(const uint4& lo, const uint4& hi)
+      : v{e4m3x8_to_bf16(lo.x, lo.y), e4m3x8_to_bf16(lo.z, lo.w), e4m3x8_to_bf16(hi.x, hi.y),
+          e4m3x8_to_bf16(hi.z, hi.w)} {}
+};
+__device__ __forceinline__ f32x4 mma_block(const Frag<false>& a, const Frag<false>& b) {
+  return mma_e4m3_k128(a.v[0], a.v[1], b.v[0], b.v[1]);
+}
+__device__ __forceinline__ f32x4 mma_block(const Frag<true>& a, const Frag<true>& b) {
+  f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) mma_bf16(d, a.v[s], b.v[s]);
+  return d;
+}
+
+
+struct Fp8Args {
+  const uint8_t* a;
+  const uint8_t* b;
+  const float* sa;
+  const float* sb;
+  void* y;
+  float* part;    // [splits][M][N] float32 partial sums of a split K axis
+  int M, N, K, KB;
+  int nm, nn;     // tiles along m and n
+  int splits, kb_split;  // K splits, blocks of K in one
+};
+
+// ---------------------------------------------------------------------------
+// Tiles.  BM x BN outputs per workgroup; K in steps of one block (128 bytes
+// per row) through two direct-to-LDS stages of K-row tiles.  The scales of
+// four K blocks at a time go through registers to LDS, [4][BM + BN] floats in
+// two alternating slots.
+// ---------------------------------------------------------------------------
+template <int BM, int BN>
+struct Tile {
+  static constexpr int NW = BM * BN / (128 * 64) < 4 ? 4 : BM * BN / (128 * 64);  // waves
+  static constexpr int NTH = NW * 64;
+  static constexpr int WM = 64;                         // m per wave
+  static constexpr int WN = BM * BN / (NW * WM);        // n per wave
+  static constexpr int NWM = BM / WM;                   // waves along m
+  static constexpr int FM = WM / 16, FN = WN / 16;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int SROWS = BM + BN;
+  static constexpr int SLOT = 4 * SROWS;                // floats of one scale slot
+  static constexpr int LDS = 2 * STAGE + 2 * SLOT * 4;
+  static_assert(SROWS == NTH, "one scale row per thread");
+  static_assert(WN <= 128, "the n range of a wave lies in one 128-row block");
+};
+
+template <int ROWS, int NW>
+struct RowDma {
+  static constexpr int NI = ROWS / 8 / NW;  // 1 KB instructions (8 rows of 128 bytes) per wave and stage
+  uint32_t base[NI];
+  int koff;
+  __device__ __forceinline__ void init(int w, int lane, int rows, int K) {
+    const int c = (lane & 7) ^ (lane >> 3);
+    koff = c * 16;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = (w * NI + i) * 8 + (lane >> 3);
+      base[i] = r < rows ? (uint32_t)r * (uint32_t)K + koff : kOOB;
+    }
+  }
+  // k0: first K element of the step; chunks at or past K read zeros
+  __device__ __forceinline__ void issue(const DmaSrc& src, ESG_LDS char* st, int w, int k0, int K) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      dma16(src, st + (w * NI + i) * 1024, base[i] != kOOB && k0 + koff < K ? base[i] + (uint32_t)k0 : kOOB);
+  }
+};
+
+// Block id -> tile: each XCD (id % 8) takes a contiguous run of an order that
+// walks eight m tiles, then the next n tile, so the 32 workgroups of an XCD
+// share operand panels in its L2.
+__device__ __forceinline__ void tile_of(int id, int total, int nm, int nn, int& tm, int& tn) {
+  const int per = total >> 3, extra = total & 7, x = id & 7;
+  const int o = x * per + (x < extra ? x : extra) + (id >> 3);
+  const int band = 8 * nn;
+  const int bi = o / band, in = o - bi * band;
+  const int rows = min(8, nm - bi * 8);
+  tm = bi * 8 + in % rows;
+  tn = in / rows;
+}
+
+template <int BM, int BN, int SB, int OUT>
+__global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Args g) {
+  using C = Tile<BM, BN>;
+  __shared__ __attribute__((aligned(1024))) char lds_[C::LDS];
+  ESG_LDS char* const lds = (ESG_LDS char*)lds_;
+  ESG_LDS float* const slots = (ESG_LDS float*)(lds + 2 * C::STAGE);
+  const int lane = threadIdx.x & 63, w = wave_id();
+  int tm, tn;
+  tile_of(blockIdx.x, g.nm * g.nn, g.nm, g.nn, tm, tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int mrows = min(BM, g.M - m0), nrows = min(BN, g.N - n0);
+  const int kb0 = blockIdx.y * g.kb_split, kb1 = min(g.KB, kb0 + g.kb_split);
+  const int nk = kb1 - kb0;
+
+  const DmaSrc ra = make_dma_src(g.a + (size_t)m0 * g.K, (uint32_t)mrows * (uint32_t)g.K);
+  const DmaSrc rb = make_dma_src(g.b + (size_t)n0 * g.K, (uint32_t)nrows * (uint32_t)g.K);
+  RowDma<BM, C::NW> da;
+  RowDma<BN, C::NW> db;
+  da.init(w, lane, mrows, g.K);
+  db.init(w, lane, nrows, g.K);
+
+  // this thread's row of scales (rows outside the matrix take the last one; their outputs are not stored)
+  const float* srow;
+  if ((int)threadIdx.x < BM) {
+    srow = g.sa + (size_t)min(m0 + (int)threadIdx.x, g.M - 1) * g.KB;
+  } else {
+    const int n = min(n0 + (int)threadIdx.x - BM, g.N - 1);
+    srow = g.sb + (size_t)(SB == SB_ROWS ? n : n / kQB) * g.KB;
+  }
+  float sreg[4];
+  auto load_scales = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sreg[e] = kb + e < kb1 ? srow[kb + e] : 0.f;
+  };
+  auto put_scales = [&](int slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) slots[slot * C::SLOT + e * C::SROWS + threadIdx.x] = sreg[e];
+  };
+  auto issue = [&](int t) __attribute__((always_inline)) {
+    const int k0 = (kb0 + t) * kQB;
+    ESG_LDS char* st = lds + (t & 1) * C::STAGE;
+    da.issue(ra, st, w, k0, g.K);
+    db.issue(rb, st + C::A_BYTES, w, k0, g.K);
+  };
+
+  const int wm = w % C::NWM, wn = w / C::NWM;
+  const int lr = lane & 15, lg = lane >> 4;
+  f32x4 acc[C::FN][C::FM];
+  zero_acc(acc);
+
+  load_scales(kb0);
+  issue(0);
+  put_scales(0);
+  for (int t = 0; t < nk; ++t) {
+    wait_vmcnt<0>();
+    wait_lgkm0();
+    barrier();
+    // the scales' wait comes before this step's loads: nothing is in flight here
+    if ((t & 3) == 2 && t + 2 < nk) put_scales(((t >> 2) + 1) & 1);
+    if (t + 1 < nk) issue(t + 1);
+    if ((t & 3) == 0 && t + 4 < nk) load_scales(kb0 + t + 4);
+    const ESG_LDS char* ta = lds + (t & 1) * C::STAGE;
+    const ESG_LDS char* tb = ta + C::A_BYTES;
+    const ESG_LDS float* sc = slots + ((t >> 2) & 1) * C::SLOT + (t & 3) * C::SROWS;
+    Frag<fine(OUT)> am[C::FM];
+    float fm[C::FM];
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) {
+      const int r = wm * C::WM + j * 16 + lr;
+      am[j] = Frag<fine(OUT)>(frag_krow(ta, r, lg), frag_krow(ta, r, lg + 4));
+      fm[j] = sc[r];
+      if constexpr (SB == SB_TILES) fm[j] *= sc[BM + wn * C::WN];
+    }
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) {
+      const int r = wn * C::WN + i * 16 + lr;
+      const Frag<fine(OUT)> bn(frag_krow(tb, r, lg), frag_krow(tb, r, lg + 4));
+      f32x4 sn = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (SB == SB_ROWS) sn = *(const ESG_LDS f32x4*)(sc + BM + wn * C::WN + i * 16 + lg * 4);
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j) {
+        const f32x4 d = mma_block(bn, am[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = SB == SB_ROWS ? fm[j] * sn[e] : fm[j];
+          acc[i][j][e] = fmaf(d[e], f, acc[i][j][e]);
+        }
+      }
+    }
+  }
+
+  // a lane holds n = 4 consecutive of one m
+  const bool vec = (g.N & 3) == 0;
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j) {
+    const int m = m0 + wm * C::WM + j * 16 + lr;
+    if (m >= g.M) continue;
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) {
+      const int n = n0 + wn * C::WN + i * 16 + lg * 4;
+      const size_t at = (size_t)m * g.N + n;
+      if constexpr (OUT == OUT_BF16) {
+        bf16_t* y = (bf16_t*)g.y + at;
+        if (vec && n < g.N) {
+          *(uint2*)y = make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < g.N) store_elem<bf16_t>(y + e, acc[i][j][e]);
+        }
+      } else {
+        float* y = (OUT != OUT_F32 ? g.part + (size_t)blockIdx.y * g.M * g.N : (float*)g.y) + at;
+        if (vec && n < g.N) {
+          *(float4*)y = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < g.N) y[e] = acc[i][j][e];
+        }
+      }
+    }
+  }
+}
+
+// y = sum of the K splits' partials, in split order
+template <typename T>
+__global__ __launch_bounds__(256) void fp8_reduce_kernel(const float* __restrict__ part, int splits, size_t n,
+                                                         T* __restrict__ y) {
+  for (size_t i = (blockIdx.x * (size_t)256 + threadIdx.x) * 4; i < n; i += (size_t)gridDim.x * 1024) {
+    if (i + 4 <= n && (n & 3) == 0) {
+      float4 s = *(const float4*)(part + i);
+      for (int z = 1; z < splits; ++z) {
+        const float4 v = *(const float4*)(part + (size_t)z * n + i);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+      const float o[4] = {s.x, s.y, s.z, s.w};
+      Quad<T>::store(y + i, o);
+    } else {
+      for (size_t e = i; e < i + 4 && e < n; ++e) {
+        float s = part[e];
+        for (int z = 1; z < splits; ++z) s += part[(size_t)z * n + e];
+        store_elem<T>(y + e, s);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: a workgroup takes 16 rows of b and all of a (MT tiles of 16 rows);
+// its waves take the K blocks in turn, b straight from memory into the
+// products' operand registers, and add their sums in LDS in wave order.
+// ---------------------------------------------------------------------------
+constexpr int kSkinnyM = 64;
+constexpr int kSkinnyWaves = 8;
+
+template <int MT, int SB, int OUT>
+__global__ __launch_bounds__(kSkinnyWaves * 64) void fp8_skinny_kernel(Fp8Args g) {
+  __shared__ f32x4 red[kSkinnyWaves][MT][64];
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int lr = lane & 15, lg = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const uint8_t* brow = g.b + (size_t)min(n0 + lr, g.N - 1) * g.K;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  f32x4 acc[MT];
+  zero_acc(acc);
+  constexpr int U = MT == 1 ? 4 : 2;  // K blocks in flight
+  for (int kb0 = w; kb0 < g.KB; kb0 += kSkinnyWaves * U) {
+    uint4 b[U][2], a[U][MT][2];
+    float fm[U][MT];
+    f32x4 fn[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = kb0 + u * kSkinnyWaves;
+      const int k = kb * kQB + lg * 16;
+      const bool on = kb < g.KB;
+      b[u][0] = on && k < g.K ? *(const uint4*)(brow + k) : zero;
+      b[u][1] = on && k + 64 < g.K ? *(const uint4*)(brow + k + 64) : zero;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const int m = j * 16 + lr;
+        const uint8_t* arow = g.a + (size_t)m * g.K;
+        const bool in = on && m < g.M;
+        a[u][j][0] = in && k < g.K ? *(const uint4*)(arow + k) : zero;
+        a[u][j][1] = in && k + 64 < g.K ? *(const uint4*)(arow + k + 64) : zero;
+        fm[u][j] = in ? g.sa[(size_t)m * g.KB + kb] : 0.f;
+      }
+      if constexpr (SB == SB_TILES) {
+        const float s = on ? g.sb[(size_t)(n0 / kQB) * g.KB + kb] : 0.f;
+        fn[u] = f32x4{s, s, s, s};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          fn[u][e] = on && n0 + lg * 4 + e < g.N ? g.sb[(size_t)(n0 + lg * 4 + e) * g.KB + kb] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kb0 + u * kSkinnyWaves >= g.KB) continue;
+      const Frag<fine(OUT)> bn(b[u][0], b[u][1]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const Frag<fine(OUT)> am(a[u][j][0], a[u][j][1]);
+        const f32x4 d = mma_block(bn, am);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(d[e], fm[u][j] * fn[u][e], acc[j][e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) red[w][j][lane] = acc[j];
+  __syncthreads();
+  // output o: n = o % 16 of row m = o / 16; it sits in lane (n / 4) * 16 + m % 16, element n % 4
+  const float* rf = (const float*)red;
+  for (int o = threadIdx.x; o < MT * 256; o += kSkinnyWaves * 64) {
+    const int n = o & 15, m = o >> 4;
+    const int at = ((m >> 4) * 64 + (n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+    float s = rf[at];
+#pragma unroll
+    for (int v = 1; v < kSkinnyWaves; ++v) s += rf[v * MT * 256 + at];
+    if (m < g.M && n0 + n < g.N) {
+      const size_t out = (size_t)m * g.N + n0 + n;
+      if constexpr (OUT == OUT_BF16)
+        store_elem<bf16_t>((bf16_t*)g.y + out, s);
+      else
+        ((float*)g.y)[out] = s;
+    }
+  }
+}
+
+template <int SB, int OUT>
+hipError_t launch_skinny(const Fp8Args& g, hipStream_t stream) {
+  const dim3 grid((g.N + 15) / 16), block(kSkinnyWaves * 64);
+  LaunchTimer timer("fp8_skinny", stream);
+  if (g.M <= 16)
+    hipLaunchKernelGGL((fp8_skinny_kernel<1, SB, OUT>), grid, block, 0, stream, g);
+  else if (g.M <= 32)
+    hipLaunchKernelGGL((fp8_skinny_kernel<2, SB, OUT>), grid, block, 0, stream, g);
+  else
+    hipLaunchKernelGGL((fp8_skinny_kernel<4, SB, OUT>), grid, block, 0, stream, g);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int SB, int OUT>
+hipError_t launch_tiles(const Fp8Args& g, hipStream_t stream) {
+  LaunchTimer timer("fp8_tile", stream);
+  hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, SB, OUT>), dim3(g.nm * g.nn, g.splits), dim3(Tile<BM, BN>::NTH), 0,
+                     stream, g);
+  return hipGetLastError();
+}
+
+// Tile size and K splits by shape alone (so a shape rounds alike everywhere).
+struct Plan {
+  bool skinny = false, big = false;
+  int nm = 0, nn = 0, splits = 1, kb_split = 0;
+};
+
+Plan plan(int M, int N, int K) {
+  Plan p;
+  const int KB = (K + kQB - 1) / kQB;
+  p.kb_split = KB;
+  if (M <= kSkinnyM) {
+    p.skinny = true;
+    return p;
+  }
+  const long long big = (long long)((M + 255) / 256) * ((N + 255) / 256);
+  p.big = big >= kNominalCUs;
+  const int t = p.big ? 256 : 128;
+  p.nm = (M + t - 1) / t;
+  p.nn = (N + t - 1) / t;
+  if (!p.big) {
+    const long long tiles = (long long)p.nm * p.nn;
+    // split K while the tiles leave slots idle (two workgroups per CU) and a split keeps eight blocks or more
+    int s = (int)std::max<long long>(1, 2 * kNominalCUs / std::max<long long>(1, tiles));
+    s = std::min(s, std::max(1, KB / 8));
+    s = std::min(s, 16);
+    p.kb_split = (KB + s - 1) / s;
+    p.splits = (KB + p.kb_split - 1) / p.kb_split;
+  }
+  return p;
+}
+
+}  // namespace
+
+size_t fp8_matmul_workspace_bytes(int M, int N, int K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  const Plan p = plan(M, N, K);
+  return p.splits > 1 ? (size_t)p.splits * M * N * 4 : 0;
+}
+
+template <int SB>
+static hipError_t run(Fp8Args& g, const Plan& p, int out_bf16, hipStream_t stream) {
+  if (p.skinny) return out_bf16 ? launch_skinny<SB, OUT_BF16>(g, stream) : launch_skinny<SB, OUT_F32>(g, stream);
+  if (p.big)
+    return out_bf16 ? launch_tiles<256, 256, SB, OUT_BF16>(g, stream) : launch_tiles<256, 256, SB, OUT_F32>(g, stream);
+  if (p.splits == 1)
+    return out_bf16 ? launch_tiles<128, 128, SB, OUT_BF16>(g, stream) : launch_tiles<128, 128, SB, OUT_F32>(g, stream);
+  const hipError_t e = out_bf16 ? launch_tiles<128, 128, SB, OUT_PART>(g, stream)
+                                : launch_tiles<128, 128, SB, OUT_PART_FINE>(g, stream);
+  if (e != hipSuccess) return e;
+  const size_t n = (size_t)g.M * g.N;
+  const unsigned blocks = (unsigned)std::min<size_t>((n + 1023) / 1024, 2048);
+  LaunchTimer timer("fp8_reduce", stream);
+  if (out_bf16)
+    hipLaunchKernelGGL(fp8_reduce_kernel<bf16_t>, dim3(blocks), dim3(256), 0, stream, g.part, g.splits, n,
+                       (bf16_t*)g.y);
+  else
+    hipLaunchKernelGGL(fp8_reduce_kernel<float>, dim3(blocks), dim3(256), 0, stream, g.part, g.splits, n,
+                       (float*)g.y);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_matmul(const void* a, const float* sa, const void* b, const float* sb, int sb_rows, int out_dtype,
+                             int M, int N, int K, void* y, void* workspace, hipStream_t stream) {
+  const Plan p = plan(M, N, K);
+  Fp8Args g{};
+  g.a = (const uint8_t*)a;
+  g.b = (const uint8_t*)b;
+  g.sa = sa;
+  g.sb = sb;
+  g.y = y;
+  g.part = (float*)workspace;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.KB = (K + kQB - 1) / kQB;
+  g.nm = p.nm;
+  g.nn = p.nn;
+  g.splits = p.splits;
+  g.kb_split = p.kb_split;
+  return sb_rows ? run<SB_ROWS>(g, p, out_dtype == 1, stream) : run<SB_TILES>(g, p, out_dtype == 1, stream);
+}
+
+}  // namespace esg

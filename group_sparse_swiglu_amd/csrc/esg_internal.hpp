@@ -180,6 +180,37 @@ hipError_t launch_sigmoid_topk(const float* logits, const float* bias, int bias_
                                float scaling, int apply_scaling, float* probs, int64_t* indices,
                                hipStream_t stream);
 
+// ---- 8-bit floating point with block scales (esg_quant.hip, esg_fp8_gemm.hip) ---
+// dtype: 0 float32, 1 bf16 source; qt / scale_t NULL: no transposed form
+hipError_t launch_quant_rows(int dtype, const void* x, int rows, int cols, void* q, float* scale, void* qt,
+                             float* scale_t, hipStream_t stream);
+hipError_t launch_quant_tiles(int dtype, const void* w, int batch, int rows, int cols, void* q, float* scale, void* qt,
+                              float* scale_t, hipStream_t stream);
+size_t fp8_matmul_workspace_bytes(int M, int N, int K);
+hipError_t launch_fp8_matmul(const void* a, const float* sa, const void* b, const float* sb, int sb_rows, int out_dtype,
+                             int M, int N, int K, void* y, void* workspace, hipStream_t stream);
+
+// ---- whole expert layer for a few tokens (esg_moe.hip) --------------------------
+constexpr int kMoeMaxTokens = 64;     // a 64-bit token set per expert
+constexpr int kMoeMaxExperts = 1024;
+struct MoeCall {
+  const void* x;
+  const void* w_router;
+  const float* expert_bias;
+  int bias_stride;
+  const void *w_gate, *w_up, *w_down;
+  const float *s_gate, *s_up, *s_down;
+  int w_dtype;  // 1 bf16, 2 e4m3
+  int tokens, experts, topk, d_model, d_ff;
+  float scaling;
+  int apply_scaling;
+  void* y;
+  float* probs;
+  int64_t* indices;
+};
+size_t moe_decode_workspace_bytes(int tokens, int experts, int topk, int d_ff);
+hipError_t launch_moe_decode(const MoeCall& c, void* workspace, hipStream_t stream);
+
 // Compute units of the current device (cached per device): for launch sizes
 // that do not change results.  Rules that decide how a sum is split (and so
 // its rounding) or how buffers are laid out use kNominalCUs instead, so a

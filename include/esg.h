@@ -50,6 +50,7 @@ extern "C" {
 /* dtypes */
 #define ESG_F32 0
 #define ESG_BF16 1
+#define ESG_E4M3 2  /* 8-bit floating point (1 sign, 4 exponent, 3 fraction bits, no infinity); only where a call says so */
 
 /* bits OR-ed into the optional device status word by the bucketing pass */
 #define ESG_STATUS_GROUP_OUT_OF_RANGE 1   /* an id < 0 or >= G was skipped */
@@ -383,6 +384,96 @@ int esg_sigmoid_topk_supported(int num_experts, int topk);
 int esg_sigmoid_topk_routing(const float* logits, const float* expert_bias, int bias_stride, int tokens,
                              int num_experts, int topk, float scaling_factor, int apply_scaling, float* probs,
                              int64_t* indices, void* stream);
+
+/*
+ * Quantisation to 8-bit floating point (e4m3) with a float32 scale per block of
+ * 128 elements.  With a the largest magnitude of a block, at least 2^-100:
+ *   scale = a / 448;  q = e4m3(x * (448 / a))
+ * (448 is the largest e4m3 value; the quotients and the product are each
+ * rounded once to float32, q to nearest even), so x is about q * scale.  A
+ * block that holds an infinity or NaN gets an infinite or NaN scale, and every
+ * product with it is NaN; other blocks are not affected.
+ *
+ * esg_fp8_quant_rows: x [rows, cols] (ESG_F32 or ESG_BF16) in 1 x 128 blocks:
+ *   q     e4m3 [rows, cols];   scale  float [rows, ceil(cols/128)].
+ *   With qt and scale_t (both or neither), the same read also gives the blocks
+ *   of 128 rows of a column, transposed, for a contraction over the rows:
+ *   qt    e4m3 [cols, rows16], rows16 = rows rounded up to a multiple of 16,
+ *         zeros past rows;      scale_t  float [cols, ceil(rows/128)].
+ * esg_fp8_quant_tiles: w [batch, rows, cols] in 128 x 128 blocks:
+ *   q     e4m3 [batch, rows, cols]; scale float [batch, ceil(rows/128), ceil(cols/128)];
+ *   qt    e4m3 [batch, cols, rows16] and scale_t [batch, ceil(cols/128), ceil(rows/128)]
+ *         (both or neither): the transposes of the same values.
+ * A last block of fewer than 128 rows or columns is a block like the others.
+ * rows == 0 or batch == 0 enqueues nothing.
+ * Errors: ESG_ERR_INVALID_ARG (null pointer, x, w, q or qt not 16-byte aligned,
+ * a scale not 4-byte aligned, one of qt and scale_t without the other, negative
+ * size, cols <= 0), ESG_ERR_UNSUPPORTED (dtype, cols not a multiple of 16, cols
+ * above 2^22, rows above 2^30, or 2^31 tiles of 128 x 128 or more).
+ */
+int esg_fp8_quant_rows(const void* x, int dtype, int rows, int cols, void* q, float* scale, void* qt, float* scale_t,
+                       void* stream);
+int esg_fp8_quant_tiles(const void* w, int dtype, int batch, int rows, int cols, void* q, float* scale, void* qt,
+                        float* scale_t, void* stream);
+
+/*
+ * Product of e4m3 operands with block scales:
+ *   y[m, n] = sum_k  a[m, k] a_scale[m, k/128] * b[n, k] B(n, k/128)
+ * a: e4m3 [M, K]; a_scale: float [M, ceil(K/128)]; b: e4m3 [N, K];
+ * b_scale_rows == 0: B(n, j) = b_scale[n/128, j], b_scale float
+ * [ceil(N/128), ceil(K/128)] (weights quantised in tiles); else B(n, j) =
+ * b_scale[n, j], b_scale float [N, ceil(K/128)].  y: [M, N], out_dtype ESG_F32
+ * or ESG_BF16, overwritten.  Products and sums are float32; the order of a sum
+ * depends on the shape only, and no atomics are used (bitwise reproducible).
+ * The three products of a linear layer y = x W^T, with x and dy quantised in
+ * rows (and transposed), W in tiles (and transposed):
+ *   y = (xq, wq); dx = (dyq, wqt); dW = (dyqt, xqt, b_scale_rows = 1).
+ * workspace: esg_fp8_matmul_workspace_size() bytes, 16-byte aligned (shapes
+ * with few output tiles split K and add the parts there; it may be 0, then
+ * workspace may be NULL).  M == 0 or N == 0 enqueues nothing.
+ * Errors: ESG_ERR_INVALID_ARG (null pointer, a, b or y not 16-byte aligned,
+ * negative size, K <= 0), ESG_ERR_UNSUPPORTED (out_dtype, K not a multiple of 16 or above
+ * 2^22, M or N above 2^30, or 2^31 output tiles), ESG_ERR_WORKSPACE.
+ */
+int esg_fp8_matmul_workspace_size(int M, int N, int K, size_t* workspace_bytes);
+int esg_fp8_matmul(const void* a, const float* a_scale, const void* b, const float* b_scale, int b_scale_rows,
+                   int out_dtype, int M, int N, int K, void* y, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/*
+ * A whole mixture-of-experts feed-forward layer for a few tokens (decode):
+ *   s[t,e] = sigmoid(x[t] . w_router[e])  (the fp32 sum's fp64 sigmoid, rounded once to fp32);
+ *   indices, probs: the top-k rule of esg_sigmoid_topk_routing on s and expert_bias;
+ *   y[t] = sum_j probs[t,j] (SiLU(x[t] Wg^T) * (x[t] Wu^T)) Wd^T,
+ *          Wg, Wu, Wd those of expert indices[t,j].
+ * Each chosen expert's weights are read once, however many tokens chose it, and
+ * no other expert's at all (an infinity or NaN there reaches no token that did
+ * not choose it).  x, y: bf16 [tokens, d_model]; w_router: bf16 [experts,
+ * d_model]; expert_bias: float, element e at expert_bias[e * bias_stride];
+ * w_gate, w_up: [experts, d_ff, d_model]; w_down: [experts, d_model, d_ff];
+ * w_dtype ESG_BF16 (the scales are ignored), or ESG_E4M3 with the scales
+ * esg_fp8_quant_tiles gives for these arrays (batch = experts): s_gate, s_up float [experts,
+ * ceil(d_ff/128), ceil(d_model/128)], s_down float [experts, ceil(d_model/128),
+ * ceil(d_ff/128)].  probs: float [tokens, topk]; indices: int64 [tokens, topk].
+ * Sums are float32; probs * SiLU(gate) * up enters the down product as the sum
+ * of two bf16 values (16 bits).
+ * No float atomics: bitwise reproducible.
+ * workspace: esg_moe_decode_workspace_size() bytes, 16-byte aligned, free
+ * between calls.  tokens == 0 enqueues nothing.
+ * esg_moe_decode_supported returns 1 when 0 <= tokens <= 64, 1 <= topk <=
+ * min(32, experts), experts <= 1024, d_model and d_ff are multiples of 16 (at
+ * most 2^20) and w_dtype is one of the two, else 0.
+ * Errors: ESG_ERR_INVALID_ARG (null or misaligned pointer, tokens < 0,
+ * bias_stride < 1), ESG_ERR_UNSUPPORTED (shape outside
+ * esg_moe_decode_supported), ESG_ERR_WORKSPACE.
+ */
+int esg_moe_decode_supported(int tokens, int experts, int topk, int d_model, int d_ff, int w_dtype);
+int esg_moe_decode_workspace_size(int tokens, int experts, int topk, int d_model, int d_ff, size_t* workspace_bytes);
+int esg_moe_decode(const void* x, const void* w_router, const float* expert_bias, int bias_stride, const void* w_gate,
+                   const void* w_up, const void* w_down, const float* s_gate, const float* s_up, const float* s_down,
+                   int w_dtype, int tokens, int experts, int topk, int d_model, int d_ff, float scaling_factor,
+                   int apply_scaling, void* y, float* probs, int64_t* indices, void* workspace,
+                   size_t workspace_bytes, void* stream);
 
 /*
  * Measurement helper (not part of the method): a rate probe of the bf16

@@ -564,7 +564,7 @@ int esg_moe_decode_supported(int tokens, int experts, int topk, int d_model, int
 int esg_moe_decode_workspace_size(int tokens, int experts, int topk, int d_model, int d_ff, size_t* workspace_bytes) {
   if (workspace_bytes == nullptr || tokens < 0) return ESG_ERR_INVALID_ARG;
   if (!esg_moe_decode_supported(tokens, experts, topk, d_model, d_ff, ESG_BF16)) return ESG_ERR_UNSUPPORTED;
-  *workspace_bytes = moe_decode_workspace_bytes(tokens, experts, topk, d_ff);
+  *workspace_bytes = moe_decode_workspace_bytes(tokens, experts, topk, d_model, d_ff);
   return ESG_OK;
 }
 
@@ -580,7 +580,7 @@ int esg_moe_decode(const void* x, const void* w_router, const float* expert_bias
     if (p == nullptr || !aligned16(p)) return ESG_ERR_INVALID_ARG;
   if (expert_bias == nullptr || probs == nullptr || indices == nullptr) return ESG_ERR_INVALID_ARG;
   if (w_dtype == ESG_E4M3 && (s_gate == nullptr || s_up == nullptr || s_down == nullptr)) return ESG_ERR_INVALID_ARG;
-  if (workspace == nullptr || workspace_bytes < moe_decode_workspace_bytes(tokens, experts, topk, d_ff))
+  if (workspace == nullptr || workspace_bytes < moe_decode_workspace_bytes(tokens, experts, topk, d_model, d_ff))
     return ESG_ERR_WORKSPACE;
   if (!aligned16(workspace)) return ESG_ERR_INVALID_ARG;
   const MoeCall c{x,      w_router, expert_bias, bias_stride, w_gate, w_up,           w_down,        s_gate, s_up,  s_down,

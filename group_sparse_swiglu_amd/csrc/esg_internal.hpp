@@ -208,7 +208,7 @@ struct MoeCall {
   float* probs;
   int64_t* indices;
 };
-size_t moe_decode_workspace_bytes(int tokens, int experts, int topk, int d_ff);
+size_t moe_decode_workspace_bytes(int tokens, int experts, int topk, int d_model, int d_ff);
 hipError_t launch_moe_decode(const MoeCall& c, void* workspace, hipStream_t stream);
 
 // Compute units of the current device (cached per device): for launch sizes

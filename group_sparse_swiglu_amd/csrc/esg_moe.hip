@@ -40,7 +40,10 @@ struct MoeArgs {
   bf16_t* y;              // [T][d]
   float* probs;           // [T][k]
   int64_t* indices;       // [T][k]
+  float* part;            // [splits][d/16][T][16]: the parts of y where the down items are split
+  int* arrived;           // [d/16]: workgroups done with a tile of y
   int T, E, k, d, ff, bias_stride, apply_scaling;
+  int splits;             // parts of the down items
   float scaling;
 };
 
@@ -105,44 +108,29 @@ __device__ __forceinline__ void mma_chunk128(f32x4& acc, const Rows16<WT>& a, co
   }
 }
 
-// The same with the columns given as a sum of two, added only in lanes with
-// `in`: the other columns' operand is zero, but zero times an infinite or NaN
-// weight of an expert that their token did not choose is not.
-template <int WT>
-__device__ __forceinline__ void mma_chunk128_masked(f32x4& acc, const Rows16<WT>& a, const Cols16<WT> (&b)[2],
-                                                    float scale, bool in) {
-  f32x4 t = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const uint4 f = a.frag(s);
-    mma_bf16(t, f, b[0].v[s]);
-    mma_bf16(t, f, b[1].v[s]);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float v = WT == W_BF16 ? acc[e] + t[e] : fmaf(t[e], scale, acc[e]);
-    acc[e] = in ? v : acc[e];
-  }
-}
-
 template <int WT>
 __device__ __forceinline__ const void* row_ptr(const void* w, size_t row, int K) {
   return (const char*)w + row * K * (WT == W_BF16 ? 2 : 1);
 }
 
 // ---------------------------------------------------------------------------
-// Scores: 16 experts per workgroup, all tokens; the waves split d.
+// Scores: 16 experts per workgroup, all tokens; the waves split d.  Also clears
+// the arrival counts of the down kernel.
 // ---------------------------------------------------------------------------
+constexpr int kScoreWaves = 16;
+
 template <int MT>
-__global__ __launch_bounds__(kMoeWaves * 64) void moe_scores_kernel(MoeArgs g) {
-  __shared__ f32x4 red[kMoeWaves][MT][64];
+__global__ __launch_bounds__(kScoreWaves * 64) void moe_scores_kernel(MoeArgs g) {
+  __shared__ f32x4 red[kScoreWaves][MT][64];
   const int lane = threadIdx.x & 63, w = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
   const int e0 = blockIdx.x * 16;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < g.d / 16; i += kScoreWaves * 64) g.arrived[i] = 0;
   const void* row = row_ptr<W_BF16>(g.router, min(e0 + lr, g.E - 1), g.d);
   f32x4 acc[MT];
   zero_acc(acc);
-  for (int k0 = w * kChunk; k0 < g.d; k0 += kMoeWaves * kChunk) {
+  for (int k0 = w * kChunk; k0 < g.d; k0 += kScoreWaves * kChunk) {
     Rows16<W_BF16> a;
     a.load(row, k0, g.d, true, lg);
 #pragma unroll
@@ -157,13 +145,14 @@ __global__ __launch_bounds__(kMoeWaves * 64) void moe_scores_kernel(MoeArgs g) {
   for (int j = 0; j < MT; ++j) red[w][j][lane] = acc[j];
   __syncthreads();
   const float* rf = (const float*)red;
-  for (int o = threadIdx.x; o < MT * 256; o += kMoeWaves * 64) {
+  for (int o = threadIdx.x; o < MT * 256; o += kScoreWaves * 64) {
     const int e = o & 15, t = o >> 4;
+    if (t >= g.T || e0 + e >= g.E) continue;
     const int at = ((t >> 4) * 64 + (e >> 2) * 16 + (t & 15)) * 4 + (e & 3);
     float s = rf[at];
 #pragma unroll
-    for (int v = 1; v < kMoeWaves; ++v) s += rf[v * MT * 256 + at];
-    if (t < g.T && e0 + e < g.E) g.scores[(size_t)t * g.E + e0 + e] = exact_sigmoid(s);
+    for (int v = 1; v < kScoreWaves; ++v) s += rf[v * MT * 256 + at];
+    g.scores[(size_t)t * g.E + e0 + e] = exact_sigmoid(s);
   }
 }
 
@@ -177,44 +166,139 @@ struct RouteLds {
   float sel_s[TMAX][kRouteMaxK];
   int sel_e[TMAX][kRouteMaxK];
   float prob[TMAX * kRouteMaxK];         // of each pair
-  uint16_t base[EMAX];                   // first pair of each expert
+  uint16_t base[EMAX];                   // first pair of each expert with tokens
   uint16_t list[EMAX];                   // experts with tokens, ascending
   uint8_t tok[TMAX * kRouteMaxK];        // token of each pair
   int active;
 };
 
-template <int EMAX, int TMAX>
-__device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>& R, bool write) {
+// One data-parallel move inside the vector unit: the value of another lane of
+// the wavefront (ctrl), zero where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, true);
+}
+// lanes 1, 2, 4, 8 below inside a row of 16; then lane 15 of a row to the next row, lane 31 to the upper half
+template <class Op>
+__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v, Op op) {
+  v = op(v, dpp_u32<0x111, 0xf>(v));
+  v = op(v, dpp_u32<0x112, 0xf>(v));
+  v = op(v, dpp_u32<0x114, 0xf>(v));
+  v = op(v, dpp_u32<0x118, 0xf>(v));
+  v = op(v, dpp_u32<0x142, 0xa>(v));
+  v = op(v, dpp_u32<0x143, 0xc>(v));
+  return v;
+}
+// largest value of the wavefront, as a scalar
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = wave_scan_u32(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// sums of the lanes up to each
+__device__ __forceinline__ int wave_prefix_sum(int v) {
+  return (int)wave_scan_u32((uint32_t)v, [](uint32_t a, uint32_t b) { return a + b; });
+}
+
+// Top-k of one token row (the rule of esg_sigmoid_topk_routing).  With the small
+// k of an expert layer, k maxima over the wavefront are quicker than a radix
+// descent over the key bits: each lane keeps its C keys in descending order, so
+// a pick is a maximum over the lanes' first keys (about 150 cycles) and a shift
+// in the lane that held it.  The picks come by descending key, equal keys by
+// ascending expert; lane i keeps the i-th.  Outputs, in lane i < k: the expert
+// and score of the i-th in output order (keys above the k-th largest by
+// ascending expert, then the ones equal to it).
+template <int C>
+__device__ __forceinline__ void topk_row(const float (&sc)[C], const uint32_t (&key)[C], int k, int lane, int& expert,
+                                         float& score) {
+  uint32_t u[C];
+  int c_of[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    u[c] = key[c];
+    c_of[c] = c;
+  }
+#pragma unroll
+  for (int i = 1; i < C; ++i)  // insertion: equal keys keep their order
+#pragma unroll
+    for (int j = i; j > 0; --j) {
+      const bool up = u[j] > u[j - 1];
+      const uint32_t a = u[j - 1];
+      const int b = c_of[j - 1];
+      u[j - 1] = up ? u[j] : a;
+      u[j] = up ? a : u[j];
+      c_of[j - 1] = up ? c_of[j] : b;
+      c_of[j] = up ? b : c_of[j];
+    }
+  int my_e = 0;
+  uint32_t my_key = 0, kth = 0;
+  for (int i = 0; i < k; ++i) {
+    kth = wave_max_u32(u[0]);
+    const int from = __ffsll((unsigned long long)__ballot(u[0] == kth)) - 1;
+    const int e = from * C + __builtin_amdgcn_readlane(c_of[0], from);
+    my_e = lane == i ? e : my_e;
+    my_key = lane == i ? kth : my_key;
+    const bool pop = lane == from;
+#pragma unroll
+    for (int c = 0; c + 1 < C; ++c) {
+      u[c] = pop ? u[c + 1] : u[c];
+      c_of[c] = pop ? c_of[c + 1] : c_of[c];
+    }
+    u[C - 1] = pop ? 0u : u[C - 1];  // candidates' keys are at least 1
+  }
+  float my_s = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const float v = __shfl(sc[c], my_e / C);
+    my_s = my_e % C == c ? v : my_s;
+  }
+  // output order: rank of (equal to the k-th, expert) among the k picks
+  const int id = (my_key == kth ? 1 << 16 : 0) | my_e;
+  int slot = 0;
+  for (int i = 0; i < k; ++i) slot += __builtin_amdgcn_readlane(id, i) < id ? 1 : 0;
+  const int to = lane < k ? slot : lane;
+  expert = __builtin_amdgcn_ds_permute(to * 4, my_e);
+  score = __uint_as_float((uint32_t)__builtin_amdgcn_ds_permute(to * 4, (int)__float_as_uint(my_s)));
+}
+
+// Selection and weights of every token; probabilities and token sets into LDS.
+template <int C, int EMAX, int TMAX>
+__device__ __forceinline__ void select_tokens(const MoeArgs& g, RouteLds<EMAX, TMAX>& R, bool write) {
 #pragma clang fp contract(off)
-  constexpr int C = EMAX / 64;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < g.E; e += kMoeWaves * 64) R.mask[e] = 0;
-  __syncthreads();
+  float bias[C], nxt[C];
+  bool valid[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = lane * C + c;
+    valid[c] = e < g.E;
+    bias[c] = valid[c] ? g.bias[(size_t)e * g.bias_stride] : 0.f;
+  }
+  auto load = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) nxt[c] = valid[c] && t < g.T ? g.scores[(size_t)t * g.E + lane * C + c] : 0.f;
+  };
+  load(w);
   for (int t = w; t < g.T; t += kMoeWaves) {
-    const float* row = g.scores + (size_t)t * g.E;
-    bool valid[C];
-    int ex[C];
     float sc[C];
-    uint32_t u[C];
+    uint32_t key[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      ex[c] = lane * C + c;
-      valid[c] = ex[c] < g.E;
-      sc[c] = valid[c] ? row[ex[c]] : 0.f;
-      u[c] = order_key(sc[c] + (valid[c] ? g.bias[(size_t)ex[c] * g.bias_stride] : 0.f));
+      sc[c] = nxt[c];
+      const uint32_t o = order_key(sc[c] + bias[c]);
+      key[c] = valid[c] ? (o > 1u ? o : 1u) : 0u;
     }
-    int need;
-    const uint32_t tau = kth_largest<C, 32>(u, valid, g.E, g.k, need);
-    place<C>(u, valid, sc, ex, tau, g.k, need, lane, R.sel_s[t], R.sel_e[t]);
-    wave_lds_sync();
+    load(t + kMoeWaves);
+    int e;
+    float s;
+    topk_row<C>(sc, key, g.k, lane, e, s);
     float total = 0.0f;
-    for (int i = 0; i < g.k; ++i) total = total + R.sel_s[t][i];
-    wave_lds_sync();
+    for (int i = 0; i < g.k; ++i)
+      total = total + __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s), i));
     if (lane < g.k) {
-      float p = R.sel_s[t][lane] / (total + 1e-20f);
+      float p = s / (total + 1e-20f);
       if (g.apply_scaling) p = p * g.scaling;
-      const int e = R.sel_e[t][lane];
       R.sel_s[t][lane] = p;
+      R.sel_e[t][lane] = e;
       atomicOr(&R.mask[e], 1ull << t);
       if (write) {
         g.probs[(size_t)t * g.k + lane] = p;
@@ -222,207 +306,306 @@ __device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>
       }
     }
   }
+}
+
+template <int EMAX, int TMAX>
+__device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>& R, bool write) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  for (int e = threadIdx.x; e < EMAX; e += kMoeWaves * 64) R.mask[e] = 0;
   __syncthreads();
-  if (w == 0) {  // active experts and the first pair of each, 64 experts at a time
+  if (EMAX > 256)
+    select_tokens<EMAX / 64>(g, R, write);
+  else if (g.E <= 64)
+    select_tokens<1>(g, R, write);
+  else
+    select_tokens<4>(g, R, write);
+  __syncthreads();
+  if (w == 0) {  // experts with tokens, ascending, and the first pair of each: 64 experts at a time
     int n = 0, pos = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int cnt = e < g.E ? __popcll(R.mask[e]) : 0;
-      const uint64_t on = __ballot(cnt > 0);
-      int incl = cnt;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int up = __shfl_up(incl, off);
-        if (lane >= off) incl += up;
+    for (int c = 0; c < EMAX / 64; ++c) {
+      const int e = c * 64 + lane;
+      const int cnt = __popcll(R.mask[e]);
+      const uint64_t on = __ballot(cnt > 0);
+      const int incl = wave_prefix_sum(cnt);
+      if (cnt > 0) {
+        R.base[e] = (uint16_t)(pos + incl - cnt);
+        R.list[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(on >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)on, 0))] =
+            (uint16_t)e;
       }
-      if (e < g.E) R.base[e] = (uint16_t)(pos + incl - cnt);
-      if (cnt > 0) R.list[n + __popcll(on & ((1ull << lane) - 1ull))] = (uint16_t)e;
       n += __popcll(on);
-      pos += __shfl(incl, 63);
+      pos += __builtin_amdgcn_readlane(incl, 63);
     }
     if (lane == 0) R.active = n;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < g.T * g.k; i += kMoeWaves * 64) {
-    const int t = i / g.k, j = i - t * g.k;
-    const int e = R.sel_e[t][j];
-    const int pos = R.base[e] + __popcll(R.mask[e] & ((1ull << t) - 1ull));
-    R.prob[pos] = R.sel_s[t][j];
-    R.tok[pos] = (uint8_t)t;
+  for (int t = w; t < g.T; t += kMoeWaves) {
+    if (lane < g.k) {
+      const int e = R.sel_e[t][lane];
+      const int pos = R.base[e] + __popcll(R.mask[e] & ((1ull << t) - 1ull));
+      R.prob[pos] = R.sel_s[t][lane];
+      R.tok[pos] = (uint8_t)t;
+    }
   }
   __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
-// Gate and up: 16 neurons of one expert for all its tokens.
+// Gate and up.  A unit is 16 neurons of one expert for all its tokens; the
+// workgroup's waves split d and add their sums in LDS.  The weights of the next
+// step (the rest of d, or the next unit) are requested as soon as the products
+// have taken the current ones, so they are on the way during the reduction.
 // ---------------------------------------------------------------------------
 template <int WT, int MT, int EMAX>
-__device__ __forceinline__ void gate_up_unit(const MoeArgs& g, const RouteLds<EMAX, MT * 16>& R, f32x4* red, int e,
-                                             int n0, int lane, int w) {
+__global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_gate_up_kernel(MoeArgs g) {
+  __shared__ RouteLds<EMAX, MT * 16> R;
+  __shared__ f32x4 red[2][kMoeWaves][2][64];
+  route_all<EMAX, MT * 16>(g, R, blockIdx.x == 0);
+  const int lane = threadIdx.x & 63, w = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
-  const int cnt = __popcll(R.mask[e]), base = R.base[e];
-  const int tiles = (cnt + 15) >> 4;
-  const size_t wrow = (size_t)e * g.ff + n0 + lr;
-  const void* rg = row_ptr<WT>(g.wg, wrow, g.d);
-  const void* ru = row_ptr<WT>(g.wu, wrow, g.d);
-  const int kb = (g.d + kChunk - 1) / kChunk;
-  const size_t srow = WT == W_BF16 ? 0 : ((size_t)e * ((g.ff + kQB - 1) / kQB) + n0 / kQB) * kb;
-  const bf16_t* xr[MT];
-  bool in[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    in[j] = j * 16 + lr < cnt;
-    xr[j] = g.x + (size_t)(in[j] ? R.tok[base + j * 16 + lr] : 0) * g.d;
-  }
-  f32x4 acc[2][MT];
-  zero_acc(acc);
-  constexpr int U = 2;
-  for (int c0 = w; c0 < kb; c0 += kMoeWaves * U) {
-    Rows16<WT> ag[U], au[U];
-    float sg[U], su[U];
+  constexpr int U = WT == W_BF16 && MT > 1 ? 1 : 2;  // K chunks in flight per wave (registers)
+  const int nt = g.ff / 16, units = R.active * nt;
+  const int kb = (g.d + kChunk - 1) / kChunk, fb = (g.ff + kQB - 1) / kQB;
+  const int steps = (kb + kMoeWaves * U - 1) / (kMoeWaves * U);
+
+  Rows16<WT> ag[U], au[U];
+  float sg[U], su[U];
+  auto load = [&](int unit, int step) __attribute__((always_inline)) {
+    const int a = unit / nt, n0 = (unit - a * nt) * 16;
+    const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
+    const size_t wrow = (size_t)e * g.ff + n0 + lr;
+    const void* rg = row_ptr<WT>(g.wg, wrow, g.d);
+    const void* ru = row_ptr<WT>(g.wu, wrow, g.d);
+    const size_t srow = ((size_t)e * fb + n0 / kQB) * kb;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * kMoeWaves;
-      ag[u].load(rg, c * kChunk, g.d, c < kb, lg);
-      au[u].load(ru, c * kChunk, g.d, c < kb, lg);
-      sg[u] = WT != W_BF16 && c < kb ? g.sg[srow + c] : 0.f;
-      su[u] = WT != W_BF16 && c < kb ? g.su[srow + c] : 0.f;
+      const int c = (step * U + u) * kMoeWaves + w;
+      ag[u].load(rg, c * kChunk, g.d, true, lg);  // past d: zeros
+      au[u].load(ru, c * kChunk, g.d, true, lg);
+      if (WT != W_BF16) {
+        sg[u] = c < kb ? g.sg[srow + c] : 0.f;
+        su[u] = c < kb ? g.su[srow + c] : 0.f;
+      }
+    }
+  };
+
+  int unit = blockIdx.x, buf = 0;
+  if (unit < units) load(unit, 0);
+  for (; unit < units; unit += gridDim.x) {
+    const int a = unit / nt, n0 = (unit - a * nt) * 16;
+    const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
+    const int cnt = __builtin_amdgcn_readfirstlane(__popcll(R.mask[e]));
+    const int base = __builtin_amdgcn_readfirstlane((int)R.base[e]);
+    const int tiles = (cnt + 15) >> 4;
+    f32x4 acc[2][MT];
+    zero_acc(acc);
+    for (int step = 0; step < steps; ++step) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        if (j < tiles) {
+          const bool in = j * 16 + lr < cnt;
+          const bf16_t* xr = g.x + (size_t)(in ? R.tok[base + j * 16 + lr] : 0) * g.d;
+          Cols16<WT> b[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) b[u].load(xr, ((step * U + u) * kMoeWaves + w) * kChunk, g.d, in, lg);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            mma_chunk128<WT>(acc[0][j], ag[u], b[u], sg[u]);
+            mma_chunk128<WT>(acc[1][j], au[u], b[u], su[u]);
+          }
+        }
+      }
+      if (step + 1 < steps)
+        load(unit, step + 1);
+      else if (unit + (int)gridDim.x < units)
+        load(unit + gridDim.x, 0);
     }
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      if (j < tiles) {
-        Cols16<WT> b[U];
+      if (j >= tiles) break;
+      // two buffers by turns: a buffer is written again only after the barrier in between
+      red[buf][w][0][lane] = acc[0][j];
+      red[buf][w][1][lane] = acc[1][j];
+      wait_lgkm0();
+      barrier();  // not __syncthreads: that would wait for the weights on their way
+      const float* rf = (const float*)red[buf];
+      buf ^= 1;
+      for (int o = threadIdx.x; o < min(cnt - j * 16, 16) * 16; o += kMoeWaves * 64) {
+        const int n = o & 15, c = o >> 4;  // neuron, column
+        const int at = ((n >> 2) * 16 + c) * 4 + (n & 3);
+        float hg = rf[at], hu = rf[at + 256];
 #pragma unroll
-        for (int u = 0; u < U; ++u) b[u].load(xr[j], (c0 + u * kMoeWaves) * kChunk, g.d, in[j], lg);
+        for (int v = 1; v < kMoeWaves; ++v) {
+          hg += rf[v * 512 + at];
+          hu += rf[v * 512 + at + 256];
+        }
+        // Rounding h to bf16 alone would add an error as large as that of rounding y (together 1.41 times
+        // it); as bf16(h) + bf16(rest) it keeps 16 bits, for one more product per step of the down kernel,
+        // whose matrix cores are idle.
+        const int pair = base + j * 16 + c;
+        const float v = hg / (1.0f + __expf(-hg)) * hu * R.prob[pair];
+        bf16_t* const at_h = g.h + (size_t)pair * g.ff + n0 + n;
+        const uint32_t hi = f32_to_bf16(v);
+        const float rest = v - bf16_to_f32(hi);
+        at_h->bits = (uint16_t)hi;
+        store_elem<bf16_t>(at_h + (size_t)g.T * g.k * g.ff, (hi & 0x7f80u) != 0x7f80u ? rest : 0.f);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Down.  A unit is 16 columns of y for all tokens over one part of the (expert,
+// K chunk) items; its waves take consecutive runs of items and add into sums of
+// their own in LDS, [token][16], by wave.  Where the items are split over
+// several workgroups, each writes its sums and the last to arrive adds them in
+// part order.
+// ---------------------------------------------------------------------------
+template <int WT, int MT, int EMAX>
+__global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_down_kernel(MoeArgs g) {
+  constexpr int TMAX = MT * 16;
+  __shared__ RouteLds<EMAX, TMAX> R;
+  __shared__ f32x4 sums[kMoeWaves][TMAX][4];
+  __shared__ int last;
+  route_all<EMAX, TMAX>(g, R, false);
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int lr = lane & 15, lg = lane >> 4;
+  constexpr int AHEAD = WT == W_BF16 ? 1 : 2;
+  const int kb = (g.ff + kChunk - 1) / kChunk, db = (g.d + kQB - 1) / kQB;
+  const int items = R.active * kb, dtiles = g.d / 16;
+  const size_t plane = (size_t)g.T * g.k * g.ff;
+
+  for (int unit = blockIdx.x; unit < dtiles * g.splits; unit += gridDim.x) {
+    const int part = unit / dtiles, dt = unit - part * dtiles, d0 = dt * 16;
+    const int lo = (int)((long long)items * (part * kMoeWaves + w) / (g.splits * kMoeWaves));
+    const int hi = (int)((long long)items * (part * kMoeWaves + w + 1) / (g.splits * kMoeWaves));
+    for (int i = lane; i < g.T * 4; i += 64) sums[w][i >> 2][i & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // weights of AHEAD items on their way while one is used
+    Rows16<WT> q[AHEAD + 1];
+    float sc[AHEAD + 1];
+    auto load = [&](int i, Rows16<WT>& r, float& scale) __attribute__((always_inline)) {
+      const bool on = i < hi;
+      const int a = (on ? i : lo) / kb, kc = (on ? i : lo) - a * kb;
+      const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
+      r.load(row_ptr<WT>(g.wd, (size_t)e * g.d + d0 + lr, g.ff), kc * kChunk, g.ff, on, lg);
+      scale = WT != W_BF16 ? g.sd[((size_t)e * db + d0 / kQB) * kb + kc] : 1.f;
+    };
+    if (lo < hi)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          mma_chunk128<WT>(acc[0][j], ag[u], b[u], sg[u]);
-          mma_chunk128<WT>(acc[1][j], au[u], b[u], su[u]);
+      for (int u = 0; u < AHEAD; ++u) load(lo + u, q[u], sc[u]);
+    for (int i = lo; i < hi; ++i) {
+      const int a = i / kb, kc = i - a * kb;
+      const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
+      const int cnt = __builtin_amdgcn_readfirstlane(__popcll(R.mask[e]));
+      const int base = __builtin_amdgcn_readfirstlane((int)R.base[e]);
+      Cols16<WT> b[2];
+      int tok;
+      auto cols = [&](int j) __attribute__((always_inline)) {
+        const bool in = j * 16 + lr < cnt;
+        const size_t pair = base + (in ? j * 16 + lr : 0);
+        tok = in ? R.tok[pair] : -1;
+        b[0].load(g.h + pair * g.ff, kc * kChunk, g.ff, in, lg);
+        b[1].load(g.h + plane + pair * g.ff, kc * kChunk, g.ff, in, lg);
+      };
+      auto add = [&]() __attribute__((always_inline)) {
+        f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint4 f = q[0].frag(s);
+          mma_bf16(t, f, b[0].v[s]);
+          mma_bf16(t, f, b[1].v[s]);
+        }
+        if (tok >= 0) {
+          f32x4& at = sums[w][tok][lg];
+          f32x4 v = at;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = fmaf(t[r], sc[0], v[r]);
+          at = v;
+        }
+      };
+      // the columns of this item first, then the weights ahead: the products wait for the former only
+      cols(0);
+      load(i + AHEAD, q[AHEAD], sc[AHEAD]);
+      add();
+      for (int j = 1; j * 16 < cnt; ++j) {
+        cols(j);
+        add();
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        q[u] = q[u + 1];
+        sc[u] = sc[u + 1];
+      }
+    }
+    __syncthreads();
+    const float* sf = (const float*)sums;
+    if (g.splits == 1) {
+      for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64) {
+        float v = sf[o];
+#pragma unroll
+        for (int q = 1; q < kMoeWaves; ++q) v += sf[q * TMAX * 16 + o];
+        store_elem<bf16_t>(g.y + (size_t)(o >> 4) * g.d + d0 + (o & 15), v);
+      }
+    } else {
+      float* mine = g.part + ((size_t)part * dtiles + dt) * g.T * 16;
+      for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64) {
+        float v = sf[o];
+#pragma unroll
+        for (int q = 1; q < kMoeWaves; ++q) v += sf[q * TMAX * 16 + o];
+        __hip_atomic_store(&mine[o], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();  // every wave's stores are done
+      if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(&g.arrived[dt], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == g.splits - 1;
+      __syncthreads();
+      if (last) {
+        for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64) {
+          float v = 0.f;
+          for (int q = 0; q < g.splits; ++q)
+            v += __hip_atomic_load(&g.part[((size_t)q * dtiles + dt) * g.T * 16 + o], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+          store_elem<bf16_t>(g.y + (size_t)(o >> 4) * g.d + d0 + (o & 15), v);
         }
       }
     }
+    __syncthreads();
   }
-#pragma unroll
-  for (int j = 0; j < MT; ++j)
-    if (j < tiles) {
-      red[((w * MT + j) * 2 + 0) * 64 + lane] = acc[0][j];
-      red[((w * MT + j) * 2 + 1) * 64 + lane] = acc[1][j];
-    }
-  __syncthreads();
-  const float* rf = (const float*)red;
-  for (int o = threadIdx.x; o < tiles * 256; o += kMoeWaves * 64) {
-    const int n = o & 15, c = o >> 4;  // neuron, column
-    const int at = (c >> 4) * 512 + ((n >> 2) * 16 + (c & 15)) * 4 + (n & 3);
-    float hg = rf[at], hu = rf[at + 256];
-#pragma unroll
-    for (int v = 1; v < kMoeWaves; ++v) {
-      hg += rf[v * MT * 512 + at];
-      hu += rf[v * MT * 512 + at + 256];
-    }
-    if (c < cnt) {
-      // Rounding h to bf16 alone would add an error as large as that of rounding y (together 1.41 times
-      // it); as bf16(h) + bf16(rest) it keeps 16 bits, for one more product per step of the down kernel,
-      // whose matrix cores are idle.
-      const float a = hg / (1.0f + __expf(-hg)) * hu * R.prob[base + c];
-      bf16_t* const at_h = g.h + (size_t)(base + c) * g.ff + n0 + n;
-      const uint32_t hi = f32_to_bf16(a);
-      const float rest = a - bf16_to_f32(hi);
-      at_h->bits = (uint16_t)hi;
-      store_elem<bf16_t>(at_h + (size_t)g.T * g.k * g.ff, fabsf(a) < __builtin_inff() ? rest : 0.f);
-    }
-  }
-  __syncthreads();
-}
-
-// ---------------------------------------------------------------------------
-// Down: 16 columns of y for all tokens; the waves take (expert, K chunk) items
-// in turn and sum over the experts in the products' accumulators.
-// ---------------------------------------------------------------------------
-template <int WT, int MT, int EMAX>
-__device__ __forceinline__ void down_unit(const MoeArgs& g, const RouteLds<EMAX, MT * 16>& R, f32x4* red, int d0,
-                                          int lane, int w) {
-  const int lr = lane & 15, lg = lane >> 4;
-  const int kb = (g.ff + kChunk - 1) / kChunk, db = (g.d + kQB - 1) / kQB;
-  const int items = R.active * kb;
-  f32x4 acc[MT];
-  zero_acc(acc);
-  constexpr int U = 4;
-  for (int i0 = w; i0 < items; i0 += kMoeWaves * U) {
-    Rows16<WT> a[U];
-    float s[U];
-    int ex[U], kc[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = min(i0 + u * kMoeWaves, items - 1);
-      ex[u] = __builtin_amdgcn_readfirstlane((int)R.list[i / kb]);
-      kc[u] = i % kb;
-      a[u].load(row_ptr<WT>(g.wd, (size_t)ex[u] * g.d + d0 + lr, g.ff), kc[u] * kChunk, g.ff,
-                i0 + u * kMoeWaves < items, lg);
-      s[u] = WT != W_BF16 ? g.sd[((size_t)ex[u] * db + d0 / kQB) * kb + kc[u]] : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i0 + u * kMoeWaves >= items) continue;
-      const unsigned long long mask = R.mask[ex[u]];
-      const int base = R.base[ex[u]];
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        if (((mask >> (j * 16)) & 0xffffull) == 0) continue;
-        const int t = j * 16 + lr;
-        const bool in = (mask >> t) & 1;
-        const int pos = base + __popcll(mask & ((1ull << t) - 1ull));
-        Cols16<WT> b[2];
-        b[0].load(g.h + (size_t)pos * g.ff, kc[u] * kChunk, g.ff, in, lg);
-        b[1].load(g.h + ((size_t)g.T * g.k + pos) * g.ff, kc[u] * kChunk, g.ff, in, lg);
-        mma_chunk128_masked<WT>(acc[j], a[u], b, s[u], in);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < MT; ++j) red[(w * MT + j) * 64 + lane] = acc[j];
-  __syncthreads();
-  const float* rf = (const float*)red;
-  for (int o = threadIdx.x; o < MT * 256; o += kMoeWaves * 64) {
-    const int n = o & 15, t = o >> 4;
-    const int at = ((t >> 4) * 64 + (n >> 2) * 16 + (t & 15)) * 4 + (n & 3);
-    float v = rf[at];
-#pragma unroll
-    for (int q = 1; q < kMoeWaves; ++q) v += rf[q * MT * 256 + at];
-    if (t < g.T) store_elem<bf16_t>(g.y + (size_t)t * g.d + d0 + n, v);
-  }
-  __syncthreads();
-}
-
-template <int WT, int MT, int EMAX>
-__global__ __launch_bounds__(kMoeWaves * 64) void moe_gate_up_kernel(MoeArgs g) {
-  __shared__ RouteLds<EMAX, MT * 16> R;
-  __shared__ f32x4 red[kMoeWaves * MT * 2 * 64];
-  route_all<EMAX, MT * 16>(g, R, blockIdx.x == 0);
-  const int lane = threadIdx.x & 63, w = wave_id();
-  const int nt = g.ff / 16, units = R.active * nt;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int a = u / nt;
-    gate_up_unit<WT, MT, EMAX>(g, R, red, R.list[a], (u - a * nt) * 16, lane, w);
-  }
-}
-
-template <int WT, int MT, int EMAX>
-__global__ __launch_bounds__(kMoeWaves * 64) void moe_down_kernel(MoeArgs g) {
-  __shared__ RouteLds<EMAX, MT * 16> R;
-  __shared__ f32x4 red[kMoeWaves * MT * 64];
-  route_all<EMAX, MT * 16>(g, R, false);
-  const int lane = threadIdx.x & 63, w = wave_id();
-  for (int u = blockIdx.x; u < g.d / 16; u += gridDim.x) down_unit<WT, MT, EMAX>(g, R, red, u * 16, lane, w);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Parts of the down items: the d/16 tiles of y alone would leave workgroup slots
+// (two per CU) empty.  By shape alone, so a shape rounds alike everywhere.
+constexpr int kMaxSplits = 8;
+int down_splits(int d_model, int topk, int d_ff) {
+  const int tiles = d_model / 16;
+  const int items = topk * ((d_ff + kChunk - 1) / kChunk);  // of one token: at least this many
+  int s = std::max(1, 2 * kNominalCUs / tiles);
+  s = std::min(s, std::max(1, items / kMoeWaves));
+  return std::min(s, kMaxSplits);
+}
+
+struct MoeLayout {
+  size_t scores = 0, h = 0, part = 0, arrived = 0, bytes = 0;
+  int splits = 1;
+};
+MoeLayout layout(int tokens, int experts, int topk, int d_model, int d_ff) {
+  MoeLayout L;
+  L.splits = down_splits(d_model, topk, d_ff);
+  L.h = align256((size_t)tokens * experts * 4);
+  L.part = L.h + align256((size_t)tokens * topk * d_ff * 4);
+  L.arrived = L.part + (L.splits > 1 ? align256((size_t)L.splits * tokens * d_model * 4) : 0);
+  L.bytes = L.arrived + align256((size_t)(d_model / 16) * 4);
+  return L;
+}
 
 template <int WT, int MT, int EMAX>
 hipError_t launch_t(const MoeArgs& g, hipStream_t stream) {
   const dim3 block(kMoeWaves * 64);
   {
     LaunchTimer timer("moe_scores", stream);
-    hipLaunchKernelGGL(moe_scores_kernel<MT>, dim3((g.E + 15) / 16), block, 0, stream, g);
+    hipLaunchKernelGGL(moe_scores_kernel<MT>, dim3((g.E + 15) / 16), dim3(kScoreWaves * 64), 0, stream, g);
   }
   const int cus = compute_units();
   {
@@ -432,7 +615,8 @@ hipError_t launch_t(const MoeArgs& g, hipStream_t stream) {
                        0, stream, g);
   }
   LaunchTimer timer("moe_down", stream);
-  hipLaunchKernelGGL((moe_down_kernel<WT, MT, EMAX>), dim3(std::min(g.d / 16, 2 * cus)), block, 0, stream, g);
+  hipLaunchKernelGGL((moe_down_kernel<WT, MT, EMAX>), dim3(std::min(g.d / 16 * g.splits, 2 * cus)), block, 0, stream,
+                     g);
   return hipGetLastError();
 }
 
@@ -443,17 +627,17 @@ hipError_t launch_e(const MoeArgs& g, hipStream_t stream) {
 
 template <int WT>
 hipError_t launch_m(const MoeArgs& g, hipStream_t stream) {
-  if (g.T <= 16) return launch_e<WT, 1>(g, stream);
-  return g.T <= 32 ? launch_e<WT, 2>(g, stream) : launch_e<WT, 4>(g, stream);
+  return g.T <= 16 ? launch_e<WT, 1>(g, stream) : launch_e<WT, 4>(g, stream);
 }
 
 }  // namespace
 
-size_t moe_decode_workspace_bytes(int tokens, int experts, int topk, int d_ff) {
-  return align256((size_t)tokens * experts * 4) + align256((size_t)tokens * topk * d_ff * 4);
+size_t moe_decode_workspace_bytes(int tokens, int experts, int topk, int d_model, int d_ff) {
+  return layout(tokens, experts, topk, d_model, d_ff).bytes;
 }
 
 hipError_t launch_moe_decode(const MoeCall& c, void* workspace, hipStream_t stream) {
+  const MoeLayout L = layout(c.tokens, c.experts, c.topk, c.d_model, c.d_ff);
   MoeArgs g{};
   g.x = (const bf16_t*)c.x;
   g.router = (const bf16_t*)c.w_router;
@@ -465,7 +649,10 @@ hipError_t launch_moe_decode(const MoeCall& c, void* workspace, hipStream_t stre
   g.su = c.s_up;
   g.sd = c.s_down;
   g.scores = (float*)workspace;
-  g.h = (bf16_t*)((char*)workspace + align256((size_t)c.tokens * c.experts * 4));
+  g.h = (bf16_t*)((char*)workspace + L.h);
+  g.part = (float*)((char*)workspace + L.part);
+  g.arrived = (int*)((char*)workspace + L.arrived);
+  g.splits = L.splits;
   g.y = (bf16_t*)c.y;
   g.probs = c.probs;
   g.indices = c.indices;

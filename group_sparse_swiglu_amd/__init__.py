@@ -34,7 +34,7 @@ __all__ = [
     "leaky_mlp_workspace_size", "leaky_mlp_fwd", "leaky_mlp_bwd", "leaky_mlp_saved_views",
     "mhffn_supported", "mhffn_fwd", "mhffn_bwd",
     "fp8_quantize", "fp8_quantize_weight", "fp8_matmul", "fp8_matmul_workspace_size", "fp8_linear",
-    "moe_decode", "moe_decode_supported", "moe_decode_workspace_size",
+    "moe_decode", "moe_decode_supported", "moe_decode_workspace_size", "moe_decode_set_patience",
 ]
 
 ESG_F32 = 0
@@ -102,6 +102,7 @@ _SIGNATURES = {
     "esg_moe_decode": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
                                 _c_int, _c_int, _c_int, _c_int, _c_f, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_size,
                                 _c_vp]),
+    "esg_moe_decode_set_patience": (_c_int, [_c_int]),
     "esg_mfma_rate_probe": (_c_int, [_c_int, _c_int, _c_vp, _c_vp]),
     "esg_timing_enable": (_c_int, [_c_int]),
     "esg_timing_reset": (_c_int, []),
@@ -647,6 +648,12 @@ def moe_decode_workspace_size(tokens: int, experts: int, topk: int, d_model: int
     _check(lib().esg_moe_decode_workspace_size(tokens, experts, topk, d_model, d_ff, ctypes.byref(need)),
            "moe_decode_workspace_size")
     return need.value
+
+
+def moe_decode_set_patience(polls: int = -1) -> None:
+    """Polls after which a workgroup of moe_decode computes results it waits for
+    itself (this host thread's later calls; negative: the default)."""
+    _check(lib().esg_moe_decode_set_patience(polls), "moe_decode_set_patience")
 
 
 def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scaling_factor: Optional[float] = None,

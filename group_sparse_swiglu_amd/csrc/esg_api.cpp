@@ -557,8 +557,17 @@ int esg_fp8_matmul(const void* a, const float* a_scale, const void* b, const flo
 
 int esg_moe_decode_supported(int tokens, int experts, int topk, int d_model, int d_ff, int w_dtype) {
   return tokens >= 0 && tokens <= kMoeMaxTokens && experts >= 1 && experts <= kMoeMaxExperts && topk >= 1 &&
-         topk <= kRouteMaxK && topk <= experts && d_model >= 16 && d_model % 16 == 0 && d_model <= (1 << 20) &&
-         d_ff >= 16 && d_ff % 16 == 0 && d_ff <= (1 << 20) && (w_dtype == ESG_BF16 || w_dtype == ESG_E4M3);
+         topk <= kRouteMaxK && topk <= experts && d_model >= 16 && d_model % 16 == 0 && d_model <= (1 << 17) &&
+         d_ff >= 16 && d_ff % 16 == 0 && d_ff <= (1 << 17) && (w_dtype == ESG_BF16 || w_dtype == ESG_E4M3);
+}
+
+namespace {
+thread_local int moe_patience = kMoePatience;
+}
+
+int esg_moe_decode_set_patience(int polls) {
+  moe_patience = polls < 0 ? kMoePatience : polls;
+  return ESG_OK;
 }
 
 int esg_moe_decode_workspace_size(int tokens, int experts, int topk, int d_model, int d_ff, size_t* workspace_bytes) {
@@ -585,7 +594,7 @@ int esg_moe_decode(const void* x, const void* w_router, const float* expert_bias
   if (!aligned16(workspace)) return ESG_ERR_INVALID_ARG;
   const MoeCall c{x,      w_router, expert_bias, bias_stride, w_gate, w_up,           w_down,        s_gate, s_up,  s_down,
                   w_dtype, tokens,  experts,     topk,        d_model, d_ff,          scaling_factor, apply_scaling, y,
-                  probs,  indices};
+                  probs,  indices, moe_patience};
   return hip_status(launch_moe_decode(c, workspace, (hipStream_t)stream));
 }
 

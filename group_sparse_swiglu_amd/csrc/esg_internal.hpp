@@ -207,7 +207,9 @@ struct MoeCall {
   void* y;
   float* probs;
   int64_t* indices;
+  int patience;  // see esg_moe.hip
 };
+constexpr int kMoePatience = 1000;  // polls of about a microsecond
 size_t moe_decode_workspace_bytes(int tokens, int experts, int topk, int d_model, int d_ff);
 hipError_t launch_moe_decode(const MoeCall& c, void* workspace, hipStream_t stream);
 

@@ -23,6 +23,7 @@ namespace {
 enum { W_BF16 = 0, W_E4M3 = 1 };
 constexpr int kChunk = 128;  // K elements a wave takes at a time: one scale block
 constexpr int kMoeWaves = 8;
+constexpr int kMoeMaxGrid = 1024;  // workgroups of the experts' launch
 
 struct MoeArgs {
   const bf16_t* x;        // [T][d]
@@ -41,26 +42,39 @@ struct MoeArgs {
   float* probs;           // [T][k]
   int64_t* indices;       // [T][k]
   float* part;            // [splits][d/16][T][16]: the parts of y where the down items are split
+  int* flags;             // [kMoeMaxGrid]: workgroup whose gate/up units are done
   int* arrived;           // [d/16]: workgroups done with a tile of y
   int T, E, k, d, ff, bias_stride, apply_scaling;
   int splits;             // parts of the down items
+  int patience;           // polls before a workgroup does others' gate/up units itself
   float scaling;
 };
 
 // One wave's share of 16 weight rows: kChunk consecutive K of each, four MFMA
 // steps of 32.  Lane l holds row l % 16; step s of lane group g = l / 16 covers
-// K elements koff(s, g) .. + 7, the same on the other operand.
+// K elements koff(s, g) .. + 7, the same on the other operand.  Buffer loads:
+// what lies past K, or belongs to no row, is an offset past the buffer and
+// reads zeros, without a branch.
+typedef int v4i32 __attribute__((ext_vector_type(4)));
+constexpr int kDevice = 16;  // sc1 bit of a buffer access: device scope (past the caches that XCDs do not share)
+template <int CPOL = 0>
+__device__ __forceinline__ uint4 load16(rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(uint4, (v4i32)__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, CPOL));
+}
+
 template <int WT>
 struct Rows16;
 template <>
 struct Rows16<W_BF16> {
   uint4 w[4];
   static __device__ __forceinline__ int koff(int s, int g) { return s * 32 + g * 8; }
-  __device__ __forceinline__ void load(const void* row, int k0, int K, bool on, int g) {
-    const bf16_t* p = (const bf16_t*)row + k0;
+  // r: the 16 rows of K elements; row: this lane's
+  __device__ __forceinline__ void load(rsrc_t r, int row, int k0, int K, int g) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      w[s] = on && k0 + koff(s, g) < K ? *(const uint4*)(p + koff(s, g)) : make_uint4(0, 0, 0, 0);
+    for (int s = 0; s < 4; ++s) {
+      const int k = k0 + koff(s, g);
+      w[s] = load16(r, k < K ? (uint32_t)(row * K + k) * 2 : kOOB);
+    }
   }
   __device__ __forceinline__ uint4 frag(int s) const { return w[s]; }
 };
@@ -68,11 +82,12 @@ template <>
 struct Rows16<W_E4M3> {
   uint4 w[2];
   static __device__ __forceinline__ int koff(int s, int g) { return (s >> 1) * 64 + g * 16 + (s & 1) * 8; }
-  __device__ __forceinline__ void load(const void* row, int k0, int K, bool on, int g) {
-    const uint8_t* p = (const uint8_t*)row + k0;
+  __device__ __forceinline__ void load(rsrc_t r, int row, int k0, int K, int g) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      w[i] = on && k0 + koff(2 * i, g) < K ? *(const uint4*)(p + koff(2 * i, g)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+      const int k = k0 + koff(2 * i, g);
+      w[i] = load16(r, k < K ? (uint32_t)(row * K + k) : kOOB);
+    }
   }
   __device__ __forceinline__ uint4 frag(int s) const {
     const uint4& v = w[s >> 1];
@@ -80,15 +95,23 @@ struct Rows16<W_E4M3> {
   }
 };
 
-// The matching chunk of a column operand (bf16 rows; `on` false: zeros).
+// Buffer over 16 weight rows of K elements from row `row` (uniform).
 template <int WT>
+__device__ __forceinline__ rsrc_t rows_rsrc(const void* w, size_t row, int K, int rows = 16) {
+  constexpr int B = WT == W_BF16 ? 2 : 1;
+  return make_rsrc((const char*)w + row * K * B, (uint32_t)(rows * K * B));
+}
+
+// The matching chunk of a column operand: bf16 elements `at` (32-bit, of the
+// buffer's start) and on (`on` false: zeros).
+template <int WT, int CPOL = 0>
 struct Cols16 {
   uint4 v[4];
-  __device__ __forceinline__ void load(const bf16_t* row, int k0, int K, bool on, int g) {
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t at, int k0, int K, bool on, int g) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int k = k0 + Rows16<WT>::koff(s, g);
-      v[s] = on && k < K ? *(const uint4*)(row + k) : make_uint4(0, 0, 0, 0);
+      v[s] = load16<CPOL>(r, on && k < K ? (at + k) * 2 : kOOB);
     }
   }
 };
@@ -108,14 +131,9 @@ __device__ __forceinline__ void mma_chunk128(f32x4& acc, const Rows16<WT>& a, co
   }
 }
 
-template <int WT>
-__device__ __forceinline__ const void* row_ptr(const void* w, size_t row, int K) {
-  return (const char*)w + row * K * (WT == W_BF16 ? 2 : 1);
-}
-
 // ---------------------------------------------------------------------------
 // Scores: 16 experts per workgroup, all tokens; the waves split d.  Also clears
-// the arrival counts of the down kernel.
+// the flags and counts of the launch that follows.
 // ---------------------------------------------------------------------------
 constexpr int kScoreWaves = 16;
 
@@ -126,18 +144,19 @@ __global__ __launch_bounds__(kScoreWaves * 64) void moe_scores_kernel(MoeArgs g)
   const int lr = lane & 15, lg = lane >> 4;
   const int e0 = blockIdx.x * 16;
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < g.d / 16; i += kScoreWaves * 64) g.arrived[i] = 0;
-  const void* row = row_ptr<W_BF16>(g.router, min(e0 + lr, g.E - 1), g.d);
+    for (int i = threadIdx.x; i < kMoeMaxGrid + g.d / 16; i += kScoreWaves * 64) g.flags[i] = 0;
+  const rsrc_t rr = rows_rsrc<W_BF16>(g.router, e0, g.d, min(16, g.E - e0));  // rows past E read zeros
+  const rsrc_t rx = make_rsrc(g.x, (uint32_t)(g.T * g.d * 2));
   f32x4 acc[MT];
   zero_acc(acc);
   for (int k0 = w * kChunk; k0 < g.d; k0 += kScoreWaves * kChunk) {
     Rows16<W_BF16> a;
-    a.load(row, k0, g.d, true, lg);
+    a.load(rr, lr, k0, g.d, lg);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       const int t = j * 16 + lr;
       Cols16<W_BF16> b;
-      b.load(g.x + (size_t)t * g.d, k0, g.d, t < g.T, lg);
+      b.load(rx, t * g.d, k0, g.d, t < g.T, lg);
       mma_chunk128<W_BF16>(acc[j], a, b, 1.0f);
     }
   }
@@ -351,162 +370,204 @@ __device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>
 }
 
 // ---------------------------------------------------------------------------
-// Gate and up.  A unit is 16 neurons of one expert for all its tokens; the
-// workgroup's waves split d and add their sums in LDS.  The weights of the next
-// step (the rest of d, or the next unit) are requested as soon as the products
-// have taken the current ones, so they are on the way during the reduction.
+// The experts, in one launch.  Gate/up units (16 neurons of one expert for all
+// its tokens), then down units (16 columns of y for all tokens over one part of
+// the (expert, K chunk) items), each kind dealt out to the workgroups in turn.
+// A workgroup that has stored the h of its gate/up units raises its flag; before
+// its down units it polls the flags of all.  (Units taken from a counter instead
+// took 13000 to 84000 cycles per ticket: 512 workgroups on one address.)
+//
+// That wait always ends, also when some workgroups cannot start because others
+// wait (launches on several streams that share the device): a workgroup that
+// has polled `patience` times computes the missing units itself, one owner
+// after another.  They give the same bits whoever computes them, so it does no
+// harm if their owner does so too.
+//
+// What a workgroup hands to others in the same launch (h, parts of y, flags) is
+// written through to memory (device-scope stores) and waited for before the
+// flag or count that announces it, and read at device scope.  (Fences by every
+// workgroup work on whole caches instead: 22 us for the release, 27 us for the
+// acquire over 512 workgroups.)
 // ---------------------------------------------------------------------------
 template <int WT, int MT, int EMAX>
-__global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_gate_up_kernel(MoeArgs g) {
-  __shared__ RouteLds<EMAX, MT * 16> R;
-  __shared__ f32x4 red[2][kMoeWaves][2][64];
-  route_all<EMAX, MT * 16>(g, R, blockIdx.x == 0);
-  const int lane = threadIdx.x & 63, w = wave_id();
-  const int lr = lane & 15, lg = lane >> 4;
-  constexpr int U = WT == W_BF16 && MT > 1 ? 1 : 2;  // K chunks in flight per wave (registers)
-  const int nt = g.ff / 16, units = R.active * nt;
-  const int kb = (g.d + kChunk - 1) / kChunk, fb = (g.ff + kQB - 1) / kQB;
-  const int steps = (kb + kMoeWaves * U - 1) / (kMoeWaves * U);
-
-  Rows16<WT> ag[U], au[U];
-  float sg[U], su[U];
-  auto load = [&](int unit, int step) __attribute__((always_inline)) {
-    const int a = unit / nt, n0 = (unit - a * nt) * 16;
-    const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
-    const size_t wrow = (size_t)e * g.ff + n0 + lr;
-    const void* rg = row_ptr<WT>(g.wg, wrow, g.d);
-    const void* ru = row_ptr<WT>(g.wu, wrow, g.d);
-    const size_t srow = ((size_t)e * fb + n0 / kQB) * kb;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = (step * U + u) * kMoeWaves + w;
-      ag[u].load(rg, c * kChunk, g.d, true, lg);  // past d: zeros
-      au[u].load(ru, c * kChunk, g.d, true, lg);
-      if (WT != W_BF16) {
-        sg[u] = c < kb ? g.sg[srow + c] : 0.f;
-        su[u] = c < kb ? g.su[srow + c] : 0.f;
-      }
-    }
-  };
-
-  int unit = blockIdx.x, buf = 0;
-  if (unit < units) load(unit, 0);
-  for (; unit < units; unit += gridDim.x) {
-    const int a = unit / nt, n0 = (unit - a * nt) * 16;
-    const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
-    const int cnt = __builtin_amdgcn_readfirstlane(__popcll(R.mask[e]));
-    const int base = __builtin_amdgcn_readfirstlane((int)R.base[e]);
-    const int tiles = (cnt + 15) >> 4;
-    f32x4 acc[2][MT];
-    zero_acc(acc);
-    for (int step = 0; step < steps; ++step) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        if (j < tiles) {
-          const bool in = j * 16 + lr < cnt;
-          const bf16_t* xr = g.x + (size_t)(in ? R.tok[base + j * 16 + lr] : 0) * g.d;
-          Cols16<WT> b[U];
-#pragma unroll
-          for (int u = 0; u < U; ++u) b[u].load(xr, ((step * U + u) * kMoeWaves + w) * kChunk, g.d, in, lg);
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            mma_chunk128<WT>(acc[0][j], ag[u], b[u], sg[u]);
-            mma_chunk128<WT>(acc[1][j], au[u], b[u], su[u]);
-          }
-        }
-      }
-      if (step + 1 < steps)
-        load(unit, step + 1);
-      else if (unit + (int)gridDim.x < units)
-        load(unit + gridDim.x, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      if (j >= tiles) break;
-      // two buffers by turns: a buffer is written again only after the barrier in between
-      red[buf][w][0][lane] = acc[0][j];
-      red[buf][w][1][lane] = acc[1][j];
-      wait_lgkm0();
-      barrier();  // not __syncthreads: that would wait for the weights on their way
-      const float* rf = (const float*)red[buf];
-      buf ^= 1;
-      for (int o = threadIdx.x; o < min(cnt - j * 16, 16) * 16; o += kMoeWaves * 64) {
-        const int n = o & 15, c = o >> 4;  // neuron, column
-        const int at = ((n >> 2) * 16 + c) * 4 + (n & 3);
-        float hg = rf[at], hu = rf[at + 256];
-#pragma unroll
-        for (int v = 1; v < kMoeWaves; ++v) {
-          hg += rf[v * 512 + at];
-          hu += rf[v * 512 + at + 256];
-        }
-        // Rounding h to bf16 alone would add an error as large as that of rounding y (together 1.41 times
-        // it); as bf16(h) + bf16(rest) it keeps 16 bits, for one more product per step of the down kernel,
-        // whose matrix cores are idle.
-        const int pair = base + j * 16 + c;
-        const float v = hg / (1.0f + __expf(-hg)) * hu * R.prob[pair];
-        bf16_t* const at_h = g.h + (size_t)pair * g.ff + n0 + n;
-        const uint32_t hi = f32_to_bf16(v);
-        const float rest = v - bf16_to_f32(hi);
-        at_h->bits = (uint16_t)hi;
-        store_elem<bf16_t>(at_h + (size_t)g.T * g.k * g.ff, (hi & 0x7f80u) != 0x7f80u ? rest : 0.f);
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Down.  A unit is 16 columns of y for all tokens over one part of the (expert,
-// K chunk) items; its waves take consecutive runs of items and add into sums of
-// their own in LDS, [token][16], by wave.  Where the items are split over
-// several workgroups, each writes its sums and the last to arrive adds them in
-// part order.
-// ---------------------------------------------------------------------------
-template <int WT, int MT, int EMAX>
-__global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_down_kernel(MoeArgs g) {
+__global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs g) {
   constexpr int TMAX = MT * 16;
   __shared__ RouteLds<EMAX, TMAX> R;
-  __shared__ f32x4 sums[kMoeWaves][TMAX][4];
-  __shared__ int last;
-  route_all<EMAX, TMAX>(g, R, false);
+  __shared__ union {
+    f32x4 red[2][kMoeWaves][2][64];      // gate/up: sums of the waves
+    f32x4 sums[kMoeWaves][TMAX][4];      // down: [token][16] sums, by wave
+  } L;
+  __shared__ int shared_int;
   const int lane = threadIdx.x & 63, w = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
-  constexpr int AHEAD = WT == W_BF16 ? 1 : 2;
-  const int kb = (g.ff + kChunk - 1) / kChunk, db = (g.d + kQB - 1) / kQB;
-  const int items = R.active * kb, dtiles = g.d / 16;
+  route_all<EMAX, TMAX>(g, R, blockIdx.x == 0);
+
+  const int nt = g.ff / 16, dtiles = g.d / 16, grid = gridDim.x;
+  const int gu_units = R.active * nt, d_units = dtiles * g.splits;
+  const int kb = (g.d + kChunk - 1) / kChunk, fb = (g.ff + kQB - 1) / kQB;
   const size_t plane = (size_t)g.T * g.k * g.ff;
+  const rsrc_t rh = make_rsrc(g.h, (uint32_t)(plane * 4));
+  const rsrc_t rx = make_rsrc(g.x, (uint32_t)(g.T * g.d * 2));
 
-  for (int unit = blockIdx.x; unit < dtiles * g.splits; unit += gridDim.x) {
-    const int part = unit / dtiles, dt = unit - part * dtiles, d0 = dt * 16;
-    const int lo = (int)((long long)items * (part * kMoeWaves + w) / (g.splits * kMoeWaves));
-    const int hi = (int)((long long)items * (part * kMoeWaves + w + 1) / (g.splits * kMoeWaves));
-    for (int i = lane; i < g.T * 4; i += 64) sums[w][i >> 2][i & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    // weights of AHEAD items on their way while one is used
-    Rows16<WT> q[AHEAD + 1];
-    float sc[AHEAD + 1];
-    auto load = [&](int i, Rows16<WT>& r, float& scale) __attribute__((always_inline)) {
-      const bool on = i < hi;
-      const int a = (on ? i : lo) / kb, kc = (on ? i : lo) - a * kb;
-      const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
-      r.load(row_ptr<WT>(g.wd, (size_t)e * g.d + d0 + lr, g.ff), kc * kChunk, g.ff, on, lg);
-      scale = WT != W_BF16 ? g.sd[((size_t)e * db + d0 / kQB) * kb + kc] : 1.f;
-    };
-    if (lo < hi)
+  // ---- down, first half: a unit's items and the weights of its first ones ----
+  constexpr int AHEAD = WT == W_BF16 ? 1 : 2;  // items whose weights are on their way while one is used
+  const int items = R.active * fb;
+  Rows16<WT> q[AHEAD + 1];
+  float sc[AHEAD + 1];
+  int part, dt, lo, hi;
+  auto load_item = [&](int i, Rows16<WT>& r, float& scale) __attribute__((always_inline)) {
+    const bool on = i < hi;
+    const int a = on ? i / fb : 0, kc = i - a * fb;
+    const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
+    r.load(rows_rsrc<WT>(g.wd, (size_t)e * g.d + dt * 16, g.ff), lr, on ? kc * kChunk : g.ff, g.ff, lg);
+    scale = WT != W_BF16 ? g.sd[((size_t)e * kb + dt * 16 / kQB) * fb + (on ? kc : 0)] : 1.f;
+  };
+  auto begin_down = [&](int unit) __attribute__((always_inline)) {
+    part = unit / dtiles;
+    dt = unit - part * dtiles;
+    // this wave's run of the part's items
+    lo = (int)((long long)items * (part * kMoeWaves + w) / (g.splits * kMoeWaves));
+    hi = (int)((long long)items * (part * kMoeWaves + w + 1) / (g.splits * kMoeWaves));
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) load(lo + u, q[u], sc[u]);
-    for (int i = lo; i < hi; ++i) {
-      const int a = i / kb, kc = i - a * kb;
+    for (int u = 0; u < AHEAD; ++u) load_item(lo + u, q[u], sc[u]);
+  };
+
+  for (int owner = blockIdx.x, polls = 0; owner >= 0;) {
+    // ---- gate and up units of `owner`: the waves split d and add their sums in
+    // LDS.  The weights of the next step (the rest of d, or the next unit) are
+    // requested as soon as the products have taken the current ones, so they are
+    // on the way during the reduction. ----
+    constexpr int U = WT == W_BF16 && MT > 1 ? 1 : 2;  // K chunks in flight per wave (registers)
+    const int steps = (kb + kMoeWaves * U - 1) / (kMoeWaves * U);
+    Rows16<WT> ag[U], au[U];
+    float sg[U], su[U];
+    auto load = [&](int unit, int step) __attribute__((always_inline)) {
+      const int d = unit < gu_units ? g.d : 0;  // no such unit: zeros, without a branch
+      const int a = d ? unit / nt : 0, n0 = d ? (unit - a * nt) * 16 : 0;
+      const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
+      const rsrc_t rg = rows_rsrc<WT>(g.wg, (size_t)e * g.ff + n0, g.d);
+      const rsrc_t ru = rows_rsrc<WT>(g.wu, (size_t)e * g.ff + n0, g.d);
+      const size_t srow = ((size_t)e * fb + n0 / kQB) * kb;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = (step * U + u) * kMoeWaves + w;
+        ag[u].load(rg, lr, c * kChunk, d, lg);
+        au[u].load(ru, lr, c * kChunk, d, lg);
+        if (WT != W_BF16) {
+          sg[u] = c < kb ? g.sg[srow + c] : 0.f;
+          su[u] = c < kb ? g.su[srow + c] : 0.f;
+        }
+      }
+    };
+    int buf = 0;
+    load(owner, 0);
+    for (int unit = owner; unit < gu_units; unit += grid) {
+      const int a = unit / nt, n0 = (unit - a * nt) * 16;
       const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
       const int cnt = __builtin_amdgcn_readfirstlane(__popcll(R.mask[e]));
       const int base = __builtin_amdgcn_readfirstlane((int)R.base[e]);
-      Cols16<WT> b[2];
+      const int tiles = (cnt + 15) >> 4;
+      f32x4 acc[2][MT];
+      zero_acc(acc);
+      for (int step = 0; step < steps; ++step) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          if (j < tiles) {
+            const bool in = j * 16 + lr < cnt;
+            const uint32_t xr = (in ? R.tok[base + j * 16 + lr] : 0) * g.d;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              Cols16<WT> b;
+              b.load(rx, xr, ((step * U + u) * kMoeWaves + w) * kChunk, g.d, in, lg);
+              mma_chunk128<WT>(acc[0][j], ag[u], b, sg[u]);
+              mma_chunk128<WT>(acc[1][j], au[u], b, su[u]);
+            }
+          }
+        }
+        const bool more = step + 1 < steps;
+        load(more ? unit : unit + grid, more ? step + 1 : 0);
+      }
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        if (j >= tiles) break;
+        // two buffers by turns: a buffer is written again only after the barrier in between
+        L.red[buf][w][0][lane] = acc[0][j];
+        L.red[buf][w][1][lane] = acc[1][j];
+        wait_lgkm0();
+        barrier();  // not __syncthreads: that would wait for the weights on their way
+        const float* rf = (const float*)L.red[buf];
+        buf ^= 1;
+        const int o = threadIdx.x;  // two neurons of one column
+        if (o < min(cnt - j * 16, 16) * 8) {
+          const int n = (o & 7) * 2, c = o >> 3;
+          const int at = ((n >> 2) * 16 + c) * 4 + (n & 3);
+          float hv[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float hg = rf[at + r], hu = rf[at + r + 256];
+#pragma unroll
+            for (int v = 1; v < kMoeWaves; ++v) {
+              hg += rf[v * 512 + at + r];
+              hu += rf[v * 512 + at + r + 256];
+            }
+            hv[r] = hg / (1.0f + __expf(-hg)) * hu * R.prob[base + j * 16 + c];
+          }
+          // Rounding h to bf16 alone would add an error as large as that of rounding y (together 1.41 times
+          // it); as bf16(h) + bf16(rest) it keeps 16 bits, for one more product per step of the down part,
+          // whose matrix cores are idle.
+          const uint32_t hh = pack_bf16x2(hv[0], hv[1]);
+          const float r0 = (hh & 0x7f80u) != 0x7f80u ? hv[0] - __uint_as_float(hh << 16) : 0.f;
+          const float r1 = (hh & 0x7f800000u) != 0x7f800000u ? hv[1] - __uint_as_float(hh & 0xffff0000u) : 0.f;
+          const uint32_t at_h = (uint32_t)(base + j * 16 + c) * g.ff + n0 + n;
+          __builtin_amdgcn_raw_buffer_store_b32(hh, rh, at_h * 2, 0, kDevice);
+          __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(r0, r1), rh, ((uint32_t)plane + at_h) * 2, 0,
+                                                kDevice);
+        }
+      }
+    }
+    wait_vmcnt<0>();
+    barrier();  // every wave's h is stored
+    if (threadIdx.x == 0)
+      __hip_atomic_store(g.flags + owner, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if ((int)blockIdx.x >= d_units) return;
+    begin_down(blockIdx.x);
+    for (;; ++polls) {  // threads watch different flags
+      int missing = -1;
+      for (int b = threadIdx.x; b < min(grid, gu_units); b += kMoeWaves * 64)
+        if (__hip_atomic_load(g.flags + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0) missing = b;
+      owner = -1;
+      if (!__syncthreads_or(missing >= 0)) break;
+      if (polls >= g.patience) {  // uniform: help one of the owners that some thread misses
+        if (missing >= 0) shared_int = missing;
+        __syncthreads();
+        owner = __builtin_amdgcn_readfirstlane(shared_int);
+        __syncthreads();
+        break;
+      }
+      __builtin_amdgcn_s_sleep(2);
+    }
+  }
+
+  // ---- down, second half: a wave takes a run of consecutive items and adds into
+  // sums of its own; where the items are split over several workgroups, each
+  // writes its sums and the last to arrive adds them in part order. ----
+  for (int unit = blockIdx.x; unit < d_units; unit += grid) {
+    if (unit != (int)blockIdx.x) begin_down(unit);
+    const int d0 = dt * 16;
+    for (int i = lane; i < g.T * 4; i += 64) L.sums[w][i >> 2][i & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = lo; i < hi; ++i) {
+      const int a = i / fb, kc = i - a * fb;
+      const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
+      const int cnt = __builtin_amdgcn_readfirstlane(__popcll(R.mask[e]));
+      const int base = __builtin_amdgcn_readfirstlane((int)R.base[e]);
+      Cols16<WT, kDevice> b[2];
       int tok;
       auto cols = [&](int j) __attribute__((always_inline)) {
         const bool in = j * 16 + lr < cnt;
-        const size_t pair = base + (in ? j * 16 + lr : 0);
+        const int pair = base + (in ? j * 16 + lr : 0);
         tok = in ? R.tok[pair] : -1;
-        b[0].load(g.h + pair * g.ff, kc * kChunk, g.ff, in, lg);
-        b[1].load(g.h + plane + pair * g.ff, kc * kChunk, g.ff, in, lg);
+        b[0].load(rh, pair * g.ff, kc * kChunk, g.ff, in, lg);
+        b[1].load(rh, (uint32_t)plane + pair * g.ff, kc * kChunk, g.ff, in, lg);
       };
       auto add = [&]() __attribute__((always_inline)) {
         f32x4 t = {0.f, 0.f, 0.f, 0.f};
@@ -517,7 +578,7 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_down_kernel(MoeArgs g) 
           mma_bf16(t, f, b[1].v[s]);
         }
         if (tok >= 0) {
-          f32x4& at = sums[w][tok][lg];
+          f32x4& at = L.sums[w][tok][lg];
           f32x4 v = at;
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[r] = fmaf(t[r], sc[0], v[r]);
@@ -526,7 +587,7 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_down_kernel(MoeArgs g) 
       };
       // the columns of this item first, then the weights ahead: the products wait for the former only
       cols(0);
-      load(i + AHEAD, q[AHEAD], sc[AHEAD]);
+      load_item(i + AHEAD, q[AHEAD], sc[AHEAD]);
       add();
       for (int j = 1; j * 16 < cnt; ++j) {
         cols(j);
@@ -539,32 +600,31 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_down_kernel(MoeArgs g) 
       }
     }
     __syncthreads();
-    const float* sf = (const float*)sums;
+    const float* sf = (const float*)L.sums;
+    auto sum = [&](int o) __attribute__((always_inline)) {
+      float v = sf[o];
+#pragma unroll
+      for (int r = 1; r < kMoeWaves; ++r) v += sf[r * TMAX * 16 + o];
+      return v;
+    };
     if (g.splits == 1) {
-      for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64) {
-        float v = sf[o];
-#pragma unroll
-        for (int q = 1; q < kMoeWaves; ++q) v += sf[q * TMAX * 16 + o];
-        store_elem<bf16_t>(g.y + (size_t)(o >> 4) * g.d + d0 + (o & 15), v);
-      }
+      for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64)
+        store_elem<bf16_t>(g.y + (size_t)(o >> 4) * g.d + d0 + (o & 15), sum(o));
     } else {
-      float* mine = g.part + ((size_t)part * dtiles + dt) * g.T * 16;
-      for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64) {
-        float v = sf[o];
-#pragma unroll
-        for (int q = 1; q < kMoeWaves; ++q) v += sf[q * TMAX * 16 + o];
-        __hip_atomic_store(&mine[o], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+      float* parts = g.part + (size_t)dt * g.T * 16;
+      const size_t pstride = (size_t)dtiles * g.T * 16;
+      for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64)
+        __hip_atomic_store(&parts[part * pstride + o], sum(o), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();  // every wave's stores are done
       if (threadIdx.x == 0)
-        last = __hip_atomic_fetch_add(&g.arrived[dt], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == g.splits - 1;
+        shared_int =
+            __hip_atomic_fetch_add(g.arrived + dt, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == g.splits - 1;
       __syncthreads();
-      if (last) {
+      if (shared_int) {
         for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64) {
           float v = 0.f;
-          for (int q = 0; q < g.splits; ++q)
-            v += __hip_atomic_load(&g.part[((size_t)q * dtiles + dt) * g.T * 16 + o], __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
+          for (int r = 0; r < g.splits; ++r)
+            v += __hip_atomic_load(&parts[r * pstride + o], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
           store_elem<bf16_t>(g.y + (size_t)(o >> 4) * g.d + d0 + (o & 15), v);
         }
       }
@@ -587,7 +647,7 @@ int down_splits(int d_model, int topk, int d_ff) {
 }
 
 struct MoeLayout {
-  size_t scores = 0, h = 0, part = 0, arrived = 0, bytes = 0;
+  size_t scores = 0, h = 0, part = 0, flags = 0, bytes = 0;
   int splits = 1;
 };
 MoeLayout layout(int tokens, int experts, int topk, int d_model, int d_ff) {
@@ -595,28 +655,23 @@ MoeLayout layout(int tokens, int experts, int topk, int d_model, int d_ff) {
   L.splits = down_splits(d_model, topk, d_ff);
   L.h = align256((size_t)tokens * experts * 4);
   L.part = L.h + align256((size_t)tokens * topk * d_ff * 4);
-  L.arrived = L.part + (L.splits > 1 ? align256((size_t)L.splits * tokens * d_model * 4) : 0);
-  L.bytes = L.arrived + align256((size_t)(d_model / 16) * 4);
+  L.flags = L.part + (L.splits > 1 ? align256((size_t)L.splits * tokens * d_model * 4) : 0);
+  L.bytes = L.flags + align256((size_t)(kMoeMaxGrid + d_model / 16) * 4);
   return L;
 }
 
 template <int WT, int MT, int EMAX>
 hipError_t launch_t(const MoeArgs& g, hipStream_t stream) {
-  const dim3 block(kMoeWaves * 64);
   {
     LaunchTimer timer("moe_scores", stream);
     hipLaunchKernelGGL(moe_scores_kernel<MT>, dim3((g.E + 15) / 16), dim3(kScoreWaves * 64), 0, stream, g);
   }
-  const int cus = compute_units();
-  {
-    LaunchTimer timer("moe_gate_up", stream);
-    const long long most = (long long)std::min(g.E, g.T * g.k) * (g.ff / 16);
-    hipLaunchKernelGGL((moe_gate_up_kernel<WT, MT, EMAX>), dim3((unsigned)std::min<long long>(most, 2 * cus)), block,
-                       0, stream, g);
-  }
-  LaunchTimer timer("moe_down", stream);
-  hipLaunchKernelGGL((moe_down_kernel<WT, MT, EMAX>), dim3(std::min(g.d / 16 * g.splits, 2 * cus)), block, 0, stream,
-                     g);
+  // two workgroups per CU; more than there can be units of either kind would find none
+  const int slots = std::min(2 * compute_units(), kMoeMaxGrid);
+  const long long most = std::max<long long>((long long)std::min(g.E, g.T * g.k) * (g.ff / 16), g.d / 16 * g.splits);
+  LaunchTimer timer("moe_experts", stream);
+  hipLaunchKernelGGL((moe_experts_kernel<WT, MT, EMAX>), dim3((unsigned)std::min<long long>(most, slots)),
+                     dim3(kMoeWaves * 64), 0, stream, g);
   return hipGetLastError();
 }
 
@@ -651,7 +706,9 @@ hipError_t launch_moe_decode(const MoeCall& c, void* workspace, hipStream_t stre
   g.scores = (float*)workspace;
   g.h = (bf16_t*)((char*)workspace + L.h);
   g.part = (float*)((char*)workspace + L.part);
-  g.arrived = (int*)((char*)workspace + L.arrived);
+  g.flags = (int*)((char*)workspace + L.flags);
+  g.arrived = g.flags + kMoeMaxGrid;
+  g.patience = c.patience;
   g.splits = L.splits;
   g.y = (bf16_t*)c.y;
   g.probs = c.probs;

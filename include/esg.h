@@ -462,7 +462,7 @@ int esg_fp8_matmul(const void* a, const float* a_scale, const void* b, const flo
  * between calls.  tokens == 0 enqueues nothing.
  * esg_moe_decode_supported returns 1 when 0 <= tokens <= 64, 1 <= topk <=
  * min(32, experts), experts <= 1024, d_model and d_ff are multiples of 16 (at
- * most 2^20) and w_dtype is one of the two, else 0.
+ * most 2^17) and w_dtype is one of the two, else 0.
  * Errors: ESG_ERR_INVALID_ARG (null or misaligned pointer, tokens < 0,
  * bias_stride < 1), ESG_ERR_UNSUPPORTED (shape outside
  * esg_moe_decode_supported), ESG_ERR_WORKSPACE.
@@ -474,6 +474,15 @@ int esg_moe_decode(const void* x, const void* w_router, const float* expert_bias
                    int w_dtype, int tokens, int experts, int topk, int d_model, int d_ff, float scaling_factor,
                    int apply_scaling, void* y, float* probs, int64_t* indices, void* workspace,
                    size_t workspace_bytes, void* stream);
+/*
+ * Workgroups of esg_moe_decode wait for each other's gate/up results inside one
+ * launch.  One that has polled for them `polls` times computes the missing ones
+ * itself, so the call ends whatever else runs on the device; the results are
+ * bitwise the same.  This sets that number for later calls of the calling host
+ * thread (negative: the default, 1000 polls, about a millisecond; 0: at once,
+ * which exercises that path).
+ */
+int esg_moe_decode_set_patience(int polls);
 
 /*
  * Measurement helper (not part of the method): a rate probe of the bf16

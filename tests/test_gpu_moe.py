@@ -195,6 +195,41 @@ def test_on_another_stream_and_in_a_graph():
         assert all(torch.equal(a, c) for a, c in zip(out, eager))
 
 
+@pytest.mark.parametrize("weights", ["bf16", "fp8"])
+def test_workgroups_that_do_not_wait_give_the_same(weights):
+    """Without patience a workgroup computes the gate/up units it misses itself."""
+    require_gpu()
+    for T, Ex, k, d, ff in ((1, 256, 8, 1024, 512), (40, 32, 4, 512, 272)):
+        note(f"moe patience {T} {weights}")
+        x, r, b, ws = _inputs(T, Ex, d, ff, 7)
+        got, _, (dev, scales) = _run(x, r, b, ws, k, None, weights)
+        try:
+            for polls in (0, 1, 3):
+                E.moe_decode_set_patience(polls)
+                again = E.moe_decode(x.to(DEV), r.to(DEV), b.to(DEV), *dev, k, scales=scales)
+                assert all(torch.equal(a, c) for a, c in zip(again, got))
+        finally:
+            E.moe_decode_set_patience()
+
+
+def test_concurrent_calls_on_two_streams():
+    require_gpu()
+    note("moe two streams")
+    x, r, b, ws = _inputs(8, 64, 2048, 512, 11)
+    got, _, (dev, _) = _run(x, r, b, ws, 8, None, "bf16")
+    args = (x.to(DEV), r.to(DEV), b.to(DEV), *dev, 8)
+    streams, outs = [torch.cuda.Stream() for _ in range(3)], []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(E.moe_decode(*args))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(a, c) for a, c in zip(o, got))
+
+
 def test_arguments_are_refused():
     require_gpu()
     x, r, b, ws = _inputs(4, 8, 64, 32, 1)

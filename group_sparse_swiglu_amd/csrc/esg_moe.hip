@@ -186,7 +186,7 @@ struct RouteLds {
   int sel_e[TMAX][kRouteMaxK];
   float prob[TMAX * kRouteMaxK];         // of each pair
   uint16_t base[EMAX];                   // first pair of each expert with tokens
-  uint16_t list[EMAX];                   // experts with tokens, ascending
+  uint2 act[EMAX];                       // experts with tokens, ascending: expert | first pair << 16, pairs
   uint8_t tok[TMAX * kRouteMaxK];        // token of each pair
   int active;
 };
@@ -327,6 +327,16 @@ __device__ __forceinline__ void select_tokens(const MoeArgs& g, RouteLds<EMAX, T
   }
 }
 
+struct Active {
+  int e, base, cnt;  // an expert with tokens, its first pair, its pairs (all wave-uniform)
+};
+template <int EMAX, int TMAX>
+__device__ __forceinline__ Active active(const RouteLds<EMAX, TMAX>& R, int a) {
+  const uint2 v = R.act[a];
+  const uint32_t x = (uint32_t)__builtin_amdgcn_readfirstlane((int)v.x);
+  return {(int)(x & 0xffffu), (int)(x >> 16), __builtin_amdgcn_readfirstlane((int)v.y)};
+}
+
 template <int EMAX, int TMAX>
 __device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>& R, bool write) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -349,8 +359,8 @@ __device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>
       const int incl = wave_prefix_sum(cnt);
       if (cnt > 0) {
         R.base[e] = (uint16_t)(pos + incl - cnt);
-        R.list[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(on >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)on, 0))] =
-            (uint16_t)e;
+        R.act[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(on >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)on, 0))] =
+            make_uint2((uint32_t)e | (uint32_t)(pos + incl - cnt) << 16, (uint32_t)cnt);
       }
       n += __popcll(on);
       pos += __builtin_amdgcn_readlane(incl, 63);
@@ -409,27 +419,51 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
   const rsrc_t rh = make_rsrc(g.h, (uint32_t)(plane * 4));
   const rsrc_t rx = make_rsrc(g.x, (uint32_t)(g.T * g.d * 2));
 
-  // ---- down, first half: a unit's items and the weights of its first ones ----
-  constexpr int AHEAD = WT == W_BF16 ? 1 : 2;  // items whose weights are on their way while one is used
+  // ---- down, first half.  A unit's items are (expert, K chunk) pairs; each wave
+  // takes a run of them.  P are on their way or in use, each with its weights and
+  // its columns: h of up to 8 pairs, the upper bf16 values in columns 0..7 and the
+  // rest in columns 8..15 (one product for both; their sums are added below). ----
+  constexpr int P = WT == W_BF16 ? 2 : 3;
   const int items = R.active * fb;
-  Rows16<WT> q[AHEAD + 1];
-  float sc[AHEAD + 1];
-  int part, dt, lo, hi;
-  auto load_item = [&](int i, Rows16<WT>& r, float& scale) __attribute__((always_inline)) {
+  struct Item {
+    Rows16<WT> w;
+    Cols16<WT, kDevice> h;
+    float scale;
+    int cnt, base, kc, tok;  // tok: of this lane's column (-1: none)
+  } q[P];
+  int d0 = 0, lo = 0, hi = 0;
+  int at_a = 0, at_kc = 0;  // the next item to request
+  Active at = {0, 0, 0};
+  auto weights = [&](int i, Item& t) __attribute__((always_inline)) {
     const bool on = i < hi;
-    const int a = on ? i / fb : 0, kc = i - a * fb;
-    const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
-    r.load(rows_rsrc<WT>(g.wd, (size_t)e * g.d + dt * 16, g.ff), lr, on ? kc * kChunk : g.ff, g.ff, lg);
-    scale = WT != W_BF16 ? g.sd[((size_t)e * kb + dt * 16 / kQB) * fb + (on ? kc : 0)] : 1.f;
+    t.cnt = on ? at.cnt : 0;
+    t.base = at.base;
+    t.kc = at_kc;
+    t.w.load(rows_rsrc<WT>(g.wd, (size_t)at.e * g.d + d0, g.ff), lr, on ? at_kc * kChunk : g.ff, g.ff, lg);
+    t.scale = WT != W_BF16 ? g.sd[((size_t)at.e * kb + d0 / kQB) * fb + at_kc] : 1.f;
+    if (++at_kc == fb) {
+      at_kc = 0;
+      at_a = min(at_a + 1, R.active - 1);
+      at = active(R, at_a);
+    }
+  };
+  auto columns = [&](int j, Item& t) __attribute__((always_inline)) {
+    const int col = j * 8 + (lr & 7);
+    const bool in = col < t.cnt;
+    const int pair = t.base + (in ? col : 0);
+    t.tok = in ? R.tok[pair] : -1;
+    t.h.load(rh, (uint32_t)(lr < 8 ? 0 : plane) + pair * g.ff, t.kc * kChunk, g.ff, in, lg);
   };
   auto begin_down = [&](int unit) __attribute__((always_inline)) {
-    part = unit / dtiles;
-    dt = unit - part * dtiles;
-    // this wave's run of the part's items
+    const int part = unit / dtiles;
+    d0 = (unit - part * dtiles) * 16;
     lo = (int)((long long)items * (part * kMoeWaves + w) / (g.splits * kMoeWaves));
     hi = (int)((long long)items * (part * kMoeWaves + w + 1) / (g.splits * kMoeWaves));
+    at_a = min(lo / fb, R.active - 1);
+    at_kc = lo - lo / fb * fb;
+    at = active(R, at_a);
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) load_item(lo + u, q[u], sc[u]);
+    for (int u = 0; u < P; ++u) weights(lo + u, q[u]);
   };
 
   for (int owner = blockIdx.x, polls = 0; owner >= 0;) {
@@ -441,10 +475,11 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
     const int steps = (kb + kMoeWaves * U - 1) / (kMoeWaves * U);
     Rows16<WT> ag[U], au[U];
     float sg[U], su[U];
-    auto load = [&](int unit, int step) __attribute__((always_inline)) {
-      const int d = unit < gu_units ? g.d : 0;  // no such unit: zeros, without a branch
-      const int a = d ? unit / nt : 0, n0 = d ? (unit - a * nt) * 16 : 0;
-      const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
+    // units go by (place in the list of active experts, 16-neuron tile); a workgroup's next one is `grid` further
+    const int da = grid / nt, dn = grid - da * nt;
+    auto load = [&](int a, int n0, int step) __attribute__((always_inline)) {
+      const int d = a < R.active ? g.d : 0;  // no such unit: zeros, without a branch
+      const int e = active(R, d ? a : 0).e;
       const rsrc_t rg = rows_rsrc<WT>(g.wg, (size_t)e * g.ff + n0, g.d);
       const rsrc_t ru = rows_rsrc<WT>(g.wu, (size_t)e * g.ff + n0, g.d);
       const size_t srow = ((size_t)e * fb + n0 / kQB) * kb;
@@ -460,13 +495,17 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
       }
     };
     int buf = 0;
-    load(owner, 0);
-    for (int unit = owner; unit < gu_units; unit += grid) {
-      const int a = unit / nt, n0 = (unit - a * nt) * 16;
-      const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
-      const int cnt = __builtin_amdgcn_readfirstlane(__popcll(R.mask[e]));
-      const int base = __builtin_amdgcn_readfirstlane((int)R.base[e]);
+    int a = owner / nt, tile = owner - a * nt;
+    load(a, tile * 16, 0);
+    while (a < R.active) {
+      const Active act = active(R, a);
+      const int cnt = act.cnt, base = act.base, n0 = tile * 16;
       const int tiles = (cnt + 15) >> 4;
+      int next_a = a + da, next_tile = tile + dn;
+      if (next_tile >= nt) {
+        ++next_a;
+        next_tile -= nt;
+      }
       f32x4 acc[2][MT];
       zero_acc(acc);
       for (int step = 0; step < steps; ++step) {
@@ -485,8 +524,10 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
           }
         }
         const bool more = step + 1 < steps;
-        load(more ? unit : unit + grid, more ? step + 1 : 0);
+        load(more ? a : next_a, more ? n0 : next_tile * 16, more ? step + 1 : 0);
       }
+      a = next_a;
+      tile = next_tile;
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
         if (j >= tiles) break;
@@ -553,50 +594,38 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
   // writes its sums and the last to arrive adds them in part order. ----
   for (int unit = blockIdx.x; unit < d_units; unit += grid) {
     if (unit != (int)blockIdx.x) begin_down(unit);
-    const int d0 = dt * 16;
+    const int part = unit / dtiles, dt = unit - part * dtiles;
     for (int i = lane; i < g.T * 4; i += 64) L.sums[w][i >> 2][i & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int i = lo; i < hi; ++i) {
-      const int a = i / fb, kc = i - a * fb;
-      const int e = __builtin_amdgcn_readfirstlane((int)R.list[a]);
-      const int cnt = __builtin_amdgcn_readfirstlane(__popcll(R.mask[e]));
-      const int base = __builtin_amdgcn_readfirstlane((int)R.base[e]);
-      Cols16<WT, kDevice> b[2];
-      int tok;
-      auto cols = [&](int j) __attribute__((always_inline)) {
-        const bool in = j * 16 + lr < cnt;
-        const int pair = base + (in ? j * 16 + lr : 0);
-        tok = in ? R.tok[pair] : -1;
-        b[0].load(rh, pair * g.ff, kc * kChunk, g.ff, in, lg);
-        b[1].load(rh, (uint32_t)plane + pair * g.ff, kc * kChunk, g.ff, in, lg);
-      };
-      auto add = [&]() __attribute__((always_inline)) {
-        f32x4 t = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](const Item& t) __attribute__((always_inline)) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const uint4 f = q[0].frag(s);
-          mma_bf16(t, f, b[0].v[s]);
-          mma_bf16(t, f, b[1].v[s]);
-        }
-        if (tok >= 0) {
-          f32x4& at = L.sums[w][tok][lg];
-          f32x4 v = at;
+      for (int s = 0; s < 4; ++s) mma_bf16(v, t.w.frag(s), t.h.v[s]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = fmaf(t[r], sc[0], v[r]);
-          at = v;
-        }
-      };
-      // the columns of this item first, then the weights ahead: the products wait for the former only
-      cols(0);
-      load_item(i + AHEAD, q[AHEAD], sc[AHEAD]);
-      add();
-      for (int j = 1; j * 16 < cnt; ++j) {
-        cols(j);
-        add();
+      for (int r = 0; r < 4; ++r)  // columns c and c + 8
+        v[r] += __uint_as_float(dpp_u32<0x128, 0xf>(__float_as_uint(v[r])));
+      if (t.tok >= 0 && lr < 8) {
+        f32x4& sum = L.sums[w][t.tok][lg];
+        f32x4 y = sum;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = fmaf(v[r], t.scale, y[r]);
+        sum = y;
       }
+    };
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        q[u] = q[u + 1];
-        sc[u] = sc[u + 1];
+    for (int u = 0; u < P; ++u) columns(0, q[u]);
+    // registers by turns, not moved: a move would wait for the load on its way
+    for (int i0 = lo; i0 < hi; i0 += P) {
+#pragma unroll
+      for (int u = 0; u < P; ++u) {
+        if (i0 + u < hi) {
+          add(q[u]);
+          for (int j = 1; j * 8 < q[u].cnt; ++j) {
+            columns(j, q[u]);
+            add(q[u]);
+          }
+          weights(i0 + u + P, q[u]);
+          columns(0, q[u]);
+        }
       }
     }
     __syncthreads();

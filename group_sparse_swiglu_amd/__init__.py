@@ -19,6 +19,7 @@ expert layer for a few tokens (moe_decode).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -34,6 +35,7 @@ __all__ = [
     "leaky_mlp_workspace_size", "leaky_mlp_fwd", "leaky_mlp_bwd", "leaky_mlp_saved_views",
     "mhffn_supported", "mhffn_fwd", "mhffn_bwd",
     "fp8_quantize", "fp8_quantize_weight", "fp8_matmul", "fp8_matmul_workspace_size", "fp8_linear",
+    "fp8_linear_workspace_size", "fp8_linear_fwd", "fp8_linear_bwd",
     "moe_decode", "moe_decode_supported", "moe_decode_workspace_size", "moe_decode_set_patience",
 ]
 
@@ -97,6 +99,12 @@ _SIGNATURES = {
     "esg_fp8_matmul_workspace_size": (_c_int, [_c_int, _c_int, _c_int, ctypes.POINTER(_c_size)]),
     "esg_fp8_matmul": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_vp, _c_vp,
                                 _c_size, _c_vp]),
+    "esg_fp8_linear_workspace_size": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_c_size),
+                                               ctypes.POINTER(_c_size), ctypes.POINTER(_c_size)]),
+    "esg_fp8_linear_fwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_vp, _c_vp,
+                                    _c_size, _c_vp, _c_size, _c_vp]),
+    "esg_fp8_linear_bwd": (_c_int, [_c_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_vp, _c_size, _c_vp, _c_vp, _c_vp,
+                                    _c_size, _c_vp]),
     "esg_moe_decode_supported": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
     "esg_moe_decode_workspace_size": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_c_size)]),
     "esg_moe_decode": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
@@ -163,7 +171,8 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
 
 
 def _stream(device: torch.device):
-    return torch.cuda.current_stream(device).cuda_stream
+    # the raw handle of torch.cuda.current_stream(device), without building its Stream object (1.8 us)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def make_subsample_index(d_ff: int, group_size: int, samples_per_group: int, seed: int):
@@ -554,6 +563,7 @@ def fp8_quantize_weight(w, transposed: bool = False):
     return (q, scale, qt, scale_t) if transposed else (q, scale)
 
 
+@functools.lru_cache(maxsize=4096)
 def fp8_matmul_workspace_size(M: int, N: int, K: int) -> int:
     """Bytes of scratch esg_fp8_matmul needs for this shape (0 for most)."""
     need = _c_size()
@@ -592,33 +602,75 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, works
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def fp8_linear_workspace_size(tokens: int, d_in: int, d_out: int, need_dx: bool = True, need_dw: bool = True):
+    """(saved_bytes, fwd_scratch_bytes, bwd_scratch_bytes) of the 8-bit linear layer."""
+    sv, fw, bw = _c_size(), _c_size(), _c_size()
+    _check(lib().esg_fp8_linear_workspace_size(tokens, d_in, d_out, int(need_dx), int(need_dw), ctypes.byref(sv),
+                                               ctypes.byref(fw), ctypes.byref(bw)), "fp8_linear_workspace_size")
+    return sv.value, fw.value, bw.value
+
+
+def fp8_linear_fwd(x, w, need_dx: bool = True, need_dw: bool = True, workspace: Optional[dict] = None, out=None):
+    """y = x W^T with x and W quantised -> (y [T, N], saved) (see fp8_linear).
+
+    x: [T, K], w: [N, K], float32 or bfloat16.  ``saved`` holds what
+    fp8_linear_bwd needs for the gradients asked for (None for none).
+    ``workspace``: optional dict reused across calls to hold the scratch buffer."""
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise EsgError("x must be [T, K] and w [N, K]")
+    (T, K), N, dev = x.shape, w.shape[0], x.device
+    sv, fw, _ = fp8_linear_workspace_size(T, K, N, need_dx, need_dw)
+    xc, wc = _dtype_code(x), _dtype_code(w)
+    if out is None:
+        out = torch.empty(T, N, dtype=x.dtype, device=dev)
+    elif out.shape != (T, N) or out.dtype != x.dtype:
+        raise EsgError("out must be [T, N] in the dtype of x")
+    saved = torch.empty(sv, dtype=torch.uint8, device=dev) if sv else None
+    scratch = _ws(fw, dev, workspace, "fp8_linear_fwd")
+    _check(lib().esg_fp8_linear_fwd(_dev(x, "x"), xc, _dev(w, "w"), wc, T, K, N, int(need_dx), int(need_dw),
+                                    _dev(out, "out"), None if saved is None else saved.data_ptr(), sv,
+                                    scratch.data_ptr(), scratch.numel(), _stream(dev)), "fp8_linear_fwd")
+    return out, saved
+
+
+def fp8_linear_bwd(dy, saved, d_in: int, w_dtype, need_dx: bool = True, need_dw: bool = True,
+                   workspace: Optional[dict] = None):
+    """(dx [T, K] in the dtype of dy, dw [N, K] in w_dtype) from the forward's ``saved``
+    (None where not asked for; need_dx and need_dw as in the forward)."""
+    if dy.dim() != 2:
+        raise EsgError("dy must be [T, N]")
+    (T, N), K, dev = dy.shape, d_in, dy.device
+    sv, _, bw = fp8_linear_workspace_size(T, K, N, need_dx, need_dw)
+    if (0 if saved is None else saved.numel()) != sv:
+        raise EsgError("saved is not that of a forward with these sizes and gradients")
+    dx = torch.empty(T, K, dtype=dy.dtype, device=dev) if need_dx else None
+    dw = torch.empty(N, K, dtype=w_dtype, device=dev) if need_dw else None
+    code = _dtype_code(dy)
+    wcode = _dtype_code(dw) if need_dw else ESG_BF16
+    scratch = _ws(bw, dev, workspace, "fp8_linear_bwd")
+    _check(lib().esg_fp8_linear_bwd(_dev(dy, "dy"), code, wcode, T, K, N, _dev(saved, "saved"), sv,
+                                    None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
+                                    scratch.data_ptr(), scratch.numel(), _stream(dev)), "fp8_linear_bwd")
+    return dx, dw
+
+
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     def forward(fctx, x, w):
         need_x, need_w = fctx.needs_input_grad
-        x2 = x.reshape(-1, x.shape[-1]).contiguous()
-        xq = fp8_quantize(x2, transposed=need_w)
-        wq = fp8_quantize_weight(w.contiguous(), transposed=need_x)
-        y = fp8_matmul(xq[0], xq[1], wq[0], wq[1], out_dtype=x.dtype)
-        fctx.save_for_backward(*(xq[2:] if need_w else (None, None)), *(wq[2:] if need_x else (None, None)))
-        fctx.esg = (x.shape, x.dtype, w.shape, w.dtype)
-        return y.view(*x.shape[:-1], w.shape[0])
+        y, saved = fp8_linear_fwd(x.reshape(-1, x.shape[-1]).contiguous(), w.contiguous(), need_x, need_w)
+        fctx.save_for_backward(saved)
+        fctx.esg = (x.shape, w.dtype, need_x, need_w)
+        return y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(fctx, dy):
-        xqt, xst, wqt, wst = fctx.saved_tensors
-        xshape, xdtype, wshape, wdtype = fctx.esg
-        dq = fp8_quantize(dy.reshape(-1, wshape[0]).contiguous(), transposed=xqt is not None)
-        dx = dw = None
-        if wqt is not None:
-            dx = fp8_matmul(dq[0], dq[1], wqt, wst, out_dtype=xdtype).view(xshape)
-        if xqt is not None:
-            if xqt.shape[1] == 0:
-                dw = torch.zeros(wshape, dtype=wdtype, device=dy.device)
-            else:
-                dw = fp8_matmul(dq[2], dq[3], xqt, xst, out_dtype=wdtype)
-        return dx, dw
+        xshape, wdtype, need_x, need_w = fctx.esg
+        dx, dw = fp8_linear_bwd(dy.reshape(-1, dy.shape[-1]).contiguous(), fctx.saved_tensors[0], xshape[-1], wdtype,
+                                need_x, need_w)
+        return dx if dx is None or len(xshape) == 2 else dx.view(xshape), dw
 
 
 def fp8_linear(x, w):
@@ -643,6 +695,7 @@ def moe_decode_supported(tokens: int, experts: int, topk: int, d_model: int, d_f
     return bool(lib().esg_moe_decode_supported(tokens, experts, topk, d_model, d_ff, code))
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_decode_workspace_size(tokens: int, experts: int, topk: int, d_model: int, d_ff: int) -> int:
     need = _c_size()
     _check(lib().esg_moe_decode_workspace_size(tokens, experts, topk, d_model, d_ff, ctypes.byref(need)),

@@ -555,6 +555,123 @@ int esg_fp8_matmul(const void* a, const float* a_scale, const void* b, const flo
                                       (hipStream_t)stream));
 }
 
+namespace {
+// Buffers of the linear layer: what the backward needs (the transposes), and scratch.
+struct LinearLayout {
+  size_t xqt = 0, xst = 0, wqt = 0, wst = 0, saved = 0;             // saved
+  size_t xq = 0, xs = 0, wq = 0, ws = 0, fmm = 0, fwd = 0;          // forward scratch
+  size_t dq = 0, ds = 0, dqt = 0, dst = 0, bmm = 0, bwd = 0;        // backward scratch
+};
+int linear_shape(int tokens, int d_in, int d_out) {
+  if (tokens < 0 || d_in <= 0 || d_out <= 0) return ESG_ERR_INVALID_ARG;
+  if (d_out % 16) return ESG_ERR_UNSUPPORTED;
+  int e = quant_shape(ESG_BF16, 1, tokens, d_in);
+  if (e == ESG_OK) e = quant_shape(ESG_BF16, 1, tokens, d_out);
+  if (e == ESG_OK) e = fp8_shape(tokens, d_out, d_in);
+  if (e == ESG_OK) e = fp8_shape(tokens, d_in, d_out);
+  if (e == ESG_OK && tokens > 0) e = fp8_shape(d_out, d_in, (tokens + 15) / 16 * 16);
+  return e;
+}
+LinearLayout linear_layout(int tokens, int d_in, int d_out, int need_dx, int need_dw) {
+  LinearLayout L;
+  const size_t T = tokens, T16 = (T + 15) / 16 * 16, K = d_in, N = d_out;
+  const size_t tb = (T + 127) / 128, kb = (K + 127) / 128, nb = (N + 127) / 128;
+  auto put = [](size_t& end, size_t bytes) {
+    const size_t at = end;
+    end += align256(bytes);
+    return at;
+  };
+  if (need_dw) L.xqt = put(L.saved, K * T16), L.xst = put(L.saved, K * tb * 4);
+  if (need_dx) L.wqt = put(L.saved, K * N), L.wst = put(L.saved, kb * nb * 4);
+  L.xq = put(L.fwd, T * K);
+  L.xs = put(L.fwd, T * kb * 4);
+  L.wq = put(L.fwd, N * K);
+  L.ws = put(L.fwd, nb * kb * 4);
+  L.fmm = put(L.fwd, fp8_matmul_workspace_bytes(tokens, d_out, d_in));
+  L.dq = put(L.bwd, T * N);
+  L.ds = put(L.bwd, T * nb * 4);
+  if (need_dw) L.dqt = put(L.bwd, N * T16), L.dst = put(L.bwd, N * tb * 4);
+  const size_t a = need_dx ? fp8_matmul_workspace_bytes(tokens, d_in, d_out) : 0;
+  const size_t b = need_dw ? fp8_matmul_workspace_bytes(d_out, d_in, (int)T16) : 0;
+  L.bmm = put(L.bwd, a > b ? a : b);
+  return L;
+}
+}  // namespace
+
+int esg_fp8_linear_workspace_size(int tokens, int d_in, int d_out, int need_dx, int need_dw, size_t* saved_bytes,
+                                  size_t* fwd_scratch_bytes, size_t* bwd_scratch_bytes) {
+  if (saved_bytes == nullptr || fwd_scratch_bytes == nullptr || bwd_scratch_bytes == nullptr)
+    return ESG_ERR_INVALID_ARG;
+  const int e = linear_shape(tokens, d_in, d_out);
+  if (e != ESG_OK) return e;
+  const LinearLayout L = linear_layout(tokens, d_in, d_out, need_dx, need_dw);
+  *saved_bytes = L.saved;
+  *fwd_scratch_bytes = L.fwd;
+  *bwd_scratch_bytes = L.bwd;
+  return ESG_OK;
+}
+
+int esg_fp8_linear_fwd(const void* x, int x_dtype, const void* w, int w_dtype, int tokens, int d_in, int d_out,
+                       int need_dx, int need_dw, void* y, void* saved, size_t saved_bytes, void* scratch,
+                       size_t scratch_bytes, void* stream) {
+  int e = linear_shape(tokens, d_in, d_out);
+  if (e != ESG_OK) return e;
+  const LinearLayout L = linear_layout(tokens, d_in, d_out, need_dx, need_dw);
+  if ((x_dtype != ESG_F32 && x_dtype != ESG_BF16) || (w_dtype != ESG_F32 && w_dtype != ESG_BF16))
+    return ESG_ERR_UNSUPPORTED;
+  if (w == nullptr || !aligned16(w)) return ESG_ERR_INVALID_ARG;
+  if (tokens > 0)
+    for (const void* p : {x, (const void*)y})
+      if (p == nullptr || !aligned16(p)) return ESG_ERR_INVALID_ARG;
+  if ((L.saved > 0 && (saved == nullptr || saved_bytes < L.saved)) || scratch == nullptr || scratch_bytes < L.fwd)
+    return ESG_ERR_WORKSPACE;
+  if (!aligned16(scratch) || !aligned16(saved)) return ESG_ERR_INVALID_ARG;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t h = launch_quant_tiles(w_dtype, w, 1, d_out, d_in, at<char>(scratch, L.wq), at<float>(scratch, L.ws),
+                                    need_dx ? at<char>(saved, L.wqt) : nullptr,
+                                    need_dx ? at<float>(saved, L.wst) : nullptr, st);
+  if (h != hipSuccess || tokens == 0) return hip_status(h);
+  h = launch_quant_rows(x_dtype, x, tokens, d_in, at<char>(scratch, L.xq), at<float>(scratch, L.xs),
+                        need_dw ? at<char>(saved, L.xqt) : nullptr, need_dw ? at<float>(saved, L.xst) : nullptr, st);
+  if (h == hipSuccess)
+    h = launch_fp8_matmul(at<char>(scratch, L.xq), at<float>(scratch, L.xs), at<char>(scratch, L.wq),
+                          at<float>(scratch, L.ws), 0, x_dtype, tokens, d_out, d_in, y, at<char>(scratch, L.fmm), st);
+  return hip_status(h);
+}
+
+int esg_fp8_linear_bwd(const void* dy, int x_dtype, int w_dtype, int tokens, int d_in, int d_out, const void* saved,
+                       size_t saved_bytes, void* dx, void* dw, void* scratch, size_t scratch_bytes, void* stream) {
+  int e = linear_shape(tokens, d_in, d_out);
+  if (e != ESG_OK) return e;
+  if ((x_dtype != ESG_F32 && x_dtype != ESG_BF16) || (w_dtype != ESG_F32 && w_dtype != ESG_BF16))
+    return ESG_ERR_UNSUPPORTED;
+  const int need_dx = dx != nullptr, need_dw = dw != nullptr;
+  if (!need_dx && !need_dw) return ESG_OK;
+  hipStream_t st = (hipStream_t)stream;
+  if (!aligned16(dx) || !aligned16(dw)) return ESG_ERR_INVALID_ARG;
+  if (tokens == 0) {  // no tokens: the weight gradient is zero
+    if (!need_dw) return ESG_OK;
+    const size_t words = (size_t)d_out * d_in * (w_dtype == ESG_F32 ? 4 : 2) / 4;
+    return hip_status(launch_fill_i32((int32_t*)dw, 0, words, st));
+  }
+  const LinearLayout L = linear_layout(tokens, d_in, d_out, need_dx, need_dw);
+  if (dy == nullptr || !aligned16(dy)) return ESG_ERR_INVALID_ARG;
+  if (saved == nullptr || saved_bytes < L.saved || scratch == nullptr || scratch_bytes < L.bwd)
+    return ESG_ERR_WORKSPACE;
+  if (!aligned16(scratch) || !aligned16(saved)) return ESG_ERR_INVALID_ARG;
+  hipError_t h = launch_quant_rows(x_dtype, dy, tokens, d_out, at<char>(scratch, L.dq), at<float>(scratch, L.ds),
+                                   need_dw ? at<char>(scratch, L.dqt) : nullptr,
+                                   need_dw ? at<float>(scratch, L.dst) : nullptr, st);
+  if (h == hipSuccess && need_dx)
+    h = launch_fp8_matmul(at<char>(scratch, L.dq), at<float>(scratch, L.ds), at<char>(saved, L.wqt),
+                          at<float>(saved, L.wst), 0, x_dtype, tokens, d_in, d_out, dx, at<char>(scratch, L.bmm), st);
+  if (h == hipSuccess && need_dw)
+    h = launch_fp8_matmul(at<char>(scratch, L.dqt), at<float>(scratch, L.dst), at<char>(saved, L.xqt),
+                          at<float>(saved, L.xst), 1, w_dtype, d_out, d_in, (tokens + 15) / 16 * 16, dw,
+                          at<char>(scratch, L.bmm), st);
+  return hip_status(h);
+}
+
 int esg_moe_decode_supported(int tokens, int experts, int topk, int d_model, int d_ff, int w_dtype) {
   return tokens >= 0 && tokens <= kMoeMaxTokens && experts >= 1 && experts <= kMoeMaxExperts && topk >= 1 &&
          topk <= kRouteMaxK && topk <= experts && d_model >= 16 && d_model % 16 == 0 && d_model <= (1 << 17) &&

@@ -285,62 +285,81 @@ __global__ __launch_bounds__(256) void fp8_reduce_kernel(const float* __restrict
 
 // ---------------------------------------------------------------------------
 // Few rows: a workgroup takes 16 rows of b and all of a (MT tiles of 16 rows);
-// its waves take the K blocks in turn, b straight from memory into the
-// products' operand registers, and add their sums in LDS in wave order.
+// its NW waves take the K blocks in turn, b straight from memory into the
+// products' operand registers, and add their sums in LDS in wave order.  The
+// read of b bounds it; P blocks per wave are on their way or in use, in
+// registers that take turns (moving them would wait for the loads), and what
+// lies outside is an offset past its buffer, which reads zeros without a branch.
 // ---------------------------------------------------------------------------
 constexpr int kSkinnyM = 64;
-constexpr int kSkinnyWaves = 8;
 
-template <int MT, int SB, int OUT>
-__global__ __launch_bounds__(kSkinnyWaves * 64) void fp8_skinny_kernel(Fp8Args g) {
-  __shared__ f32x4 red[kSkinnyWaves][MT][64];
+typedef int v4i32_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 buffer16(rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(uint4, (v4i32_t)__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ float buffer4(rsrc_t r, uint32_t off) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+
+template <int MT, int NW, int SB, int OUT>
+__global__ __launch_bounds__(NW * 64) void fp8_skinny_kernel(Fp8Args g) {
+  constexpr int P = MT == 1 ? 4 : MT * NW >= 48 ? 1 : 2;  // within 128 registers for 16 waves
+  __shared__ f32x4 red[NW][MT][64];
   const int lane = threadIdx.x & 63, w = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
-  const int n0 = blockIdx.x * 16;
-  const uint8_t* brow = g.b + (size_t)min(n0 + lr, g.N - 1) * g.K;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  f32x4 acc[MT];
-  zero_acc(acc);
-  constexpr int U = MT == 1 ? 4 : 2;  // K blocks in flight
-  for (int kb0 = w; kb0 < g.KB; kb0 += kSkinnyWaves * U) {
-    uint4 b[U][2], a[U][MT][2];
-    float fm[U][MT];
-    f32x4 fn[U];
+  const int n0 = blockIdx.x * 16, nrows = min(16, g.N - n0);
+  const rsrc_t rb = make_rsrc(g.b + (size_t)n0 * g.K, (uint32_t)(nrows * g.K));
+  const rsrc_t ra = make_rsrc(g.a, (uint32_t)(g.M * g.K));
+  const rsrc_t rsa = make_rsrc(g.sa, (uint32_t)(g.M * g.KB * 4));
+  const rsrc_t rsb = SB == SB_TILES ? make_rsrc(g.sb + (size_t)(n0 / kQB) * g.KB, (uint32_t)(g.KB * 4))
+                                    : make_rsrc(g.sb + (size_t)n0 * g.KB, (uint32_t)(nrows * g.KB * 4));
+  struct Block {
+    uint4 b[2], a[MT][2];
+    float fa[MT], fb[SB == SB_TILES ? 1 : 4];
+  } q[P];
+  auto request = [&](int kb, Block& t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = kb0 + u * kSkinnyWaves;
-      const int k = kb * kQB + lg * 16;
-      const bool on = kb < g.KB;
-      b[u][0] = on && k < g.K ? *(const uint4*)(brow + k) : zero;
-      b[u][1] = on && k + 64 < g.K ? *(const uint4*)(brow + k + 64) : zero;
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const int m = j * 16 + lr;
-        const uint8_t* arow = g.a + (size_t)m * g.K;
-        const bool in = on && m < g.M;
-        a[u][j][0] = in && k < g.K ? *(const uint4*)(arow + k) : zero;
-        a[u][j][1] = in && k + 64 < g.K ? *(const uint4*)(arow + k + 64) : zero;
-        fm[u][j] = in ? g.sa[(size_t)m * g.KB + kb] : 0.f;
-      }
-      if constexpr (SB == SB_TILES) {
-        const float s = on ? g.sb[(size_t)(n0 / kQB) * g.KB + kb] : 0.f;
-        fn[u] = f32x4{s, s, s, s};
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          fn[u][e] = on && n0 + lg * 4 + e < g.N ? g.sb[(size_t)(n0 + lg * 4 + e) * g.KB + kb] : 0.f;
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int k = kb * kQB + h * 64 + lg * 16;
+      t.b[h] = buffer16(rb, k < g.K ? (uint32_t)(lr * g.K + k) : kOOB);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (kb0 + u * kSkinnyWaves >= g.KB) continue;
-      const Frag<fine(OUT)> bn(b[u][0], b[u][1]);
+    for (int j = 0; j < MT; ++j) {
+      const int m = j * 16 + lr;
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const Frag<fine(OUT)> am(a[u][j][0], a[u][j][1]);
-        const f32x4 d = mma_block(bn, am);
+      for (int h = 0; h < 2; ++h) {
+        const int k = kb * kQB + h * 64 + lg * 16;
+        t.a[j][h] = buffer16(ra, k < g.K && m < g.M ? (uint32_t)(m * g.K + k) : kOOB);
+      }
+      t.fa[j] = buffer4(rsa, kb < g.KB && m < g.M ? (uint32_t)(m * g.KB + kb) * 4 : kOOB);
+    }
+    if constexpr (SB == SB_TILES) {
+      t.fb[0] = buffer4(rsb, kb < g.KB ? (uint32_t)kb * 4 : kOOB);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(d[e], fm[u][j] * fn[u][e], acc[j][e]);
+      for (int e = 0; e < 4; ++e)
+        t.fb[e] = buffer4(rsb, kb < g.KB && lg * 4 + e < nrows ? (uint32_t)((lg * 4 + e) * g.KB + kb) * 4 : kOOB);
+    }
+  };
+  f32x4 acc[MT];
+  zero_acc(acc);
+#pragma unroll
+  for (int u = 0; u < P; ++u) request(w + u * NW, q[u]);
+  for (int kb0 = w; kb0 < g.KB; kb0 += NW * P) {
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      const int kb = kb0 + u * NW;
+      if (kb < g.KB) {
+        const Frag<fine(OUT)> bn(q[u].b[0], q[u].b[1]);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const Frag<fine(OUT)> am(q[u].a[j][0], q[u].a[j][1]);
+          const f32x4 d = mma_block(bn, am);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[j][e] = fmaf(d[e], q[u].fa[j] * q[u].fb[SB == SB_TILES ? 0 : e], acc[j][e]);
+        }
+        if (kb + NW * P < g.KB) request(kb + NW * P, q[u]);
       }
     }
   }
@@ -349,13 +368,13 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void fp8_skinny_kernel(Fp8Args g
   __syncthreads();
   // output o: n = o % 16 of row m = o / 16; it sits in lane (n / 4) * 16 + m % 16, element n % 4
   const float* rf = (const float*)red;
-  for (int o = threadIdx.x; o < MT * 256; o += kSkinnyWaves * 64) {
+  for (int o = threadIdx.x; o < min(MT * 16, g.M) * 16; o += NW * 64) {
     const int n = o & 15, m = o >> 4;
     const int at = ((m >> 4) * 64 + (n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
     float s = rf[at];
 #pragma unroll
-    for (int v = 1; v < kSkinnyWaves; ++v) s += rf[v * MT * 256 + at];
-    if (m < g.M && n0 + n < g.N) {
+    for (int v = 1; v < NW; ++v) s += rf[v * MT * 256 + at];
+    if (n < nrows) {
       const size_t out = (size_t)m * g.N + n0 + n;
       if constexpr (OUT == OUT_BF16)
         store_elem<bf16_t>((bf16_t*)g.y + out, s);
@@ -365,17 +384,28 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void fp8_skinny_kernel(Fp8Args g
   }
 }
 
+template <int MT, int SB, int OUT>
+hipError_t launch_skinny_m(const Fp8Args& g, hipStream_t stream) {
+  // Waves per workgroup: about four blocks of K each, more waves where the rows
+  // of b give few workgroups (2048 waves: eight per CU).  By shape alone.
+  const int tiles = (g.N + 15) / 16;
+  int nw = 4;
+  while (nw < 16 && nw < g.KB && (g.KB > 4 * nw || (long long)tiles * nw < 8 * kNominalCUs)) nw *= 2;
+  LaunchTimer timer("fp8_skinny", stream);
+  if (nw == 4)
+    hipLaunchKernelGGL((fp8_skinny_kernel<MT, 4, SB, OUT>), dim3(tiles), dim3(4 * 64), 0, stream, g);
+  else if (nw == 8)
+    hipLaunchKernelGGL((fp8_skinny_kernel<MT, 8, SB, OUT>), dim3(tiles), dim3(8 * 64), 0, stream, g);
+  else
+    hipLaunchKernelGGL((fp8_skinny_kernel<MT, 16, SB, OUT>), dim3(tiles), dim3(16 * 64), 0, stream, g);
+  return hipGetLastError();
+}
+
 template <int SB, int OUT>
 hipError_t launch_skinny(const Fp8Args& g, hipStream_t stream) {
-  const dim3 grid((g.N + 15) / 16), block(kSkinnyWaves * 64);
-  LaunchTimer timer("fp8_skinny", stream);
-  if (g.M <= 16)
-    hipLaunchKernelGGL((fp8_skinny_kernel<1, SB, OUT>), grid, block, 0, stream, g);
-  else if (g.M <= 32)
-    hipLaunchKernelGGL((fp8_skinny_kernel<2, SB, OUT>), grid, block, 0, stream, g);
-  else
-    hipLaunchKernelGGL((fp8_skinny_kernel<4, SB, OUT>), grid, block, 0, stream, g);
-  return hipGetLastError();
+  if (g.M <= 16) return launch_skinny_m<1, SB, OUT>(g, stream);
+  if (g.M <= 32) return launch_skinny_m<2, SB, OUT>(g, stream);
+  return g.M <= 48 ? launch_skinny_m<3, SB, OUT>(g, stream) : launch_skinny_m<4, SB, OUT>(g, stream);
 }
 
 template <int BM, int BN, int SB, int OUT>

@@ -441,6 +441,30 @@ int esg_fp8_matmul(const void* a, const float* a_scale, const void* b, const flo
                    void* stream);
 
 /*
+ * The linear layer y = x W^T made of the calls above, with its gradients.
+ * x: x_dtype [tokens, d_in]; w: w_dtype [d_out, d_in]; y, dy: x_dtype [tokens,
+ * d_out]; dx: x_dtype; dw: w_dtype (ESG_F32 or ESG_BF16 each).  Forward: x in
+ * rows and w in tiles.  Backward: dy in rows against the transposed tiles of w
+ * gives dx; dy and x in blocks of 128 tokens give dw.  `saved` holds the
+ * transposed e4m3 x (need_dw) and w (need_dx) with their scales, written by the
+ * forward for the backward.  The backward computes the gradients whose pointer
+ * is not NULL; they have to be exactly those whose need_ the forward set (both
+ * buffers' layout goes by them).  dx and dw are overwritten (tokens == 0: dw is
+ * zero).
+ * Sizes: esg_fp8_linear_workspace_size; buffers 16-byte aligned.
+ * Errors: ESG_ERR_INVALID_ARG (null or misaligned pointer, negative size),
+ * ESG_ERR_UNSUPPORTED (d_in or d_out not a multiple of 16, the limits of the
+ * calls above, a dtype), ESG_ERR_WORKSPACE.
+ */
+int esg_fp8_linear_workspace_size(int tokens, int d_in, int d_out, int need_dx, int need_dw, size_t* saved_bytes,
+                                  size_t* fwd_scratch_bytes, size_t* bwd_scratch_bytes);
+int esg_fp8_linear_fwd(const void* x, int x_dtype, const void* w, int w_dtype, int tokens, int d_in, int d_out,
+                       int need_dx, int need_dw, void* y, void* saved, size_t saved_bytes, void* scratch,
+                       size_t scratch_bytes, void* stream);
+int esg_fp8_linear_bwd(const void* dy, int x_dtype, int w_dtype, int tokens, int d_in, int d_out, const void* saved,
+                       size_t saved_bytes, void* dx, void* dw, void* scratch, size_t scratch_bytes, void* stream);
+
+/*
  * A whole mixture-of-experts feed-forward layer for a few tokens (decode):
  *   s[t,e] = sigmoid(x[t] . w_router[e])  (the fp32 sum's fp64 sigmoid, rounded once to fp32);
  *   indices, probs: the top-k rule of esg_sigmoid_topk_routing on s and expert_bias;

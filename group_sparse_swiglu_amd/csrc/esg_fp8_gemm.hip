@@ -182,6 +182,17 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
   const int lr = lane & 15, lg = lane >> 4;
   f32x4 acc[C::FN][C::FM];
   zero_acc(acc);
+  f32x4 dp[C::FM], sp = {0.f, 0.f, 0.f, 0.f};  // products not added yet, and their scales
+  float fp[C::FM];
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j) {
+    dp[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    fp[j] = 0.f;
+  }
+  auto add_scaled = [](f32x4& to, const f32x4& d, float f, const f32x4& s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[e] = fmaf(d[e], SB == SB_ROWS ? f * s[e] : f, to[e]);
+  };
 
   load_scales(kb0);
   issue(0);
@@ -197,8 +208,22 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
     const ESG_LDS char* ta = lds + (t & 1) * C::STAGE;
     const ESG_LDS char* tb = ta + C::A_BYTES;
     const ESG_LDS float* sc = slots + ((t >> 2) & 1) * C::SLOT + (t & 3) * C::SROWS;
+    // The products of row fragment i run while the results of fragment i - 1 are
+    // scaled and added (the last fragment's in the next step) and fragment i + 1
+    // is read: without this order the compiler waits out every product's latency
+    // (MFMA busy 34 %).
     Frag<fine(OUT)> am[C::FM];
     float fm[C::FM];
+    f32x4 sn = {0.f, 0.f, 0.f, 0.f};
+    auto rows = [&](int i) __attribute__((always_inline)) {
+      const int r = wn * C::WN + i * 16 + lr;
+      return Frag<fine(OUT)>(frag_krow(tb, r, lg), frag_krow(tb, r, lg + 4));
+    };
+    auto rows_scale = [&](int i) __attribute__((always_inline)) {
+      return SB == SB_ROWS ? *(const ESG_LDS f32x4*)(sc + BM + wn * C::WN + i * 16 + lg * 4) : f32x4{1.f, 1.f, 1.f, 1.f};
+    };
+    Frag<fine(OUT)> bn = rows(0);
+    sn = rows_scale(0);
 #pragma unroll
     for (int j = 0; j < C::FM; ++j) {
       const int r = wm * C::WM + j * 16 + lr;
@@ -208,21 +233,32 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
     }
 #pragma unroll
     for (int i = 0; i < C::FN; ++i) {
-      const int r = wn * C::WN + i * 16 + lr;
-      const Frag<fine(OUT)> bn(frag_krow(tb, r, lg), frag_krow(tb, r, lg + 4));
-      f32x4 sn = {0.f, 0.f, 0.f, 0.f};
-      if constexpr (SB == SB_ROWS) sn = *(const ESG_LDS f32x4*)(sc + BM + wn * C::WN + i * 16 + lg * 4);
+      Frag<fine(OUT)> bnext;
+      f32x4 snext = sn;
+      if (i + 1 < C::FN) {
+        bnext = rows(i + 1);
+        snext = rows_scale(i + 1);
+      }
+      f32x4 d[C::FM];
 #pragma unroll
       for (int j = 0; j < C::FM; ++j) {
-        const f32x4 d = mma_block(bn, am[j]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = SB == SB_ROWS ? fm[j] * sn[e] : fm[j];
-          acc[i][j][e] = fmaf(d[e], f, acc[i][j][e]);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        d[j] = mma_block(bn, am[j]);
+        add_scaled(acc[(i + C::FN - 1) % C::FN][j], dp[j], fp[j], sp);
       }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j) {
+        dp[j] = d[j];
+        fp[j] = fm[j];
+      }
+      sp = sn;
+      bn = bnext;
+      sn = snext;
     }
   }
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j) add_scaled(acc[C::FN - 1][j], dp[j], fp[j], sp);
 
   // a lane holds n = 4 consecutive of one m
   const bool vec = (g.N & 3) == 0;

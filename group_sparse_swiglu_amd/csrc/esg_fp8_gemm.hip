@@ -76,10 +76,20 @@ struct Fp8Args {
 };
 
 // ---------------------------------------------------------------------------
-// Tiles.  BM x BN outputs per workgroup; K in steps of one block (128 bytes
-// per row) through two direct-to-LDS stages of K-row tiles.  The scales of
-// four K blocks at a time go through registers to LDS, [4][BM + BN] floats in
-// two alternating slots.
+// Tiles.  BM x BN outputs per workgroup; K in steps of one block (128 bytes per
+// row) through two direct-to-LDS stages of K-row tiles.
+//
+// One step of a wave: FN row fragments of b against FM column fragments of a.
+// The products of row fragment i run while the results of fragment i - 1 are
+// scaled and added (the last one's in the next step) and fragment i + 1 is read.
+// The barrier sits before the last fragment, whose operands are in registers:
+// under its products the next step's first fragments are read and the loads of
+// the step after that are issued.  (The compiler's own order waited out every
+// product's latency: MFMA busy 34 %.)
+//
+// The scales of four K blocks at a time go through registers to LDS, [4][BM +
+// BN] floats in two alternating slots.  Results go through LDS, so that whole
+// lines are written.
 // ---------------------------------------------------------------------------
 template <int BM, int BN>
 struct Tile {
@@ -93,7 +103,7 @@ struct Tile {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int SROWS = BM + BN;
   static constexpr int SLOT = 4 * SROWS;                // floats of one scale slot
-  static constexpr int LDS = 2 * STAGE + 2 * SLOT * 4;
+  static constexpr int LDS = 2 * STAGE + 2 * SLOT * 4;  // one workgroup per CU, or two
   static_assert(SROWS == NTH, "one scale row per thread");
   static_assert(WN <= 128, "the n range of a wave lies in one 128-row block");
 };
@@ -102,21 +112,20 @@ template <int ROWS, int NW>
 struct RowDma {
   static constexpr int NI = ROWS / 8 / NW;  // 1 KB instructions (8 rows of 128 bytes) per wave and stage
   uint32_t base[NI];
-  int koff;
+  __device__ __forceinline__ static int koff(int lane) { return ((lane & 7) ^ (lane >> 3)) * 16; }
   __device__ __forceinline__ void init(int w, int lane, int rows, int K) {
-    const int c = (lane & 7) ^ (lane >> 3);
-    koff = c * 16;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = (w * NI + i) * 8 + (lane >> 3);
-      base[i] = r < rows ? (uint32_t)r * (uint32_t)K + koff : kOOB;
+      base[i] = r < rows ? (uint32_t)r * (uint32_t)K + koff(lane) : kOOB;
     }
   }
   // k0: first K element of the step; chunks at or past K read zeros
-  __device__ __forceinline__ void issue(const DmaSrc& src, ESG_LDS char* st, int w, int k0, int K) {
+  __device__ __forceinline__ void issue(const DmaSrc& src, ESG_LDS char* st, int w, int lane, int k0, int K) {
+    const bool in = k0 + koff(lane) < K;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-      dma16(src, st + (w * NI + i) * 1024, base[i] != kOOB && k0 + koff < K ? base[i] + (uint32_t)k0 : kOOB);
+    for (int i = 0; i < NI; ++i)  // kOOB + k0 stays past every buffer
+      dma16(src, st + (w * NI + i) * 1024, in ? base[i] + (uint32_t)k0 : kOOB);
   }
 };
 
@@ -136,10 +145,13 @@ __device__ __forceinline__ void tile_of(int id, int total, int nm, int nn, int& 
 template <int BM, int BN, int SB, int OUT>
 __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Args g) {
   using C = Tile<BM, BN>;
+  using F = Frag<fine(OUT)>;
   __shared__ __attribute__((aligned(1024))) char lds_[C::LDS];
   ESG_LDS char* const lds = (ESG_LDS char*)lds_;
   ESG_LDS float* const slots = (ESG_LDS float*)(lds + 2 * C::STAGE);
   const int lane = threadIdx.x & 63, w = wave_id();
+  const int wm = w % C::NWM, wn = w / C::NWM;
+  const int lr = lane & 15, lg = lane >> 4;
   int tm, tn;
   tile_of(blockIdx.x, g.nm * g.nn, g.nm, g.nn, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
@@ -153,6 +165,12 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
   RowDma<BN, C::NW> db;
   da.init(w, lane, mrows, g.K);
   db.init(w, lane, nrows, g.K);
+  const int kend = min(g.K, kb1 * kQB);  // blocks past the part read nothing
+  auto issue = [&](int t) __attribute__((always_inline)) {
+    ESG_LDS char* st = lds + (t & 1) * C::STAGE;
+    da.issue(ra, st, w, lane, (kb0 + t) * kQB, kend);
+    db.issue(rb, st + C::A_BYTES, w, lane, (kb0 + t) * kQB, kend);
+  };
 
   // this thread's row of scales (rows outside the matrix take the last one; their outputs are not stored)
   const float* srow;
@@ -165,25 +183,20 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
   float sreg[4];
   auto load_scales = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sreg[e] = kb + e < kb1 ? srow[kb + e] : 0.f;
+    for (int e = 0; e < 4; ++e) sreg[e] = srow[min(kb + e, kb1 - 1)];
   };
   auto put_scales = [&](int slot) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) slots[slot * C::SLOT + e * C::SROWS + threadIdx.x] = sreg[e];
   };
-  auto issue = [&](int t) __attribute__((always_inline)) {
-    const int k0 = (kb0 + t) * kQB;
-    ESG_LDS char* st = lds + (t & 1) * C::STAGE;
-    da.issue(ra, st, w, k0, g.K);
-    db.issue(rb, st + C::A_BYTES, w, k0, g.K);
-  };
 
-  const int wm = w % C::NWM, wn = w / C::NWM;
-  const int lr = lane & 15, lg = lane >> 4;
   f32x4 acc[C::FN][C::FM];
-  zero_acc(acc);
   f32x4 dp[C::FM], sp = {0.f, 0.f, 0.f, 0.f};  // products not added yet, and their scales
   float fp[C::FM];
+  F am[C::FM], bn;
+  float fm[C::FM];
+  f32x4 sn;
+  zero_acc(acc);
 #pragma unroll
   for (int j = 0; j < C::FM; ++j) {
     dp[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -193,51 +206,60 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
 #pragma unroll
     for (int e = 0; e < 4; ++e) to[e] = fmaf(d[e], SB == SB_ROWS ? f * s[e] : f, to[e]);
   };
+  // fragments and scales of the step in stage st, scale line sc
+  auto read_a = [&](const ESG_LDS char* st, int j) __attribute__((always_inline)) {
+    const int r = wm * C::WM + j * 16 + lr;
+    am[j] = F(frag_krow(st, r, lg), frag_krow(st, r, lg + 4));
+  };
+  auto read_fa = [&](const ESG_LDS float* sc, int j) __attribute__((always_inline)) {
+    fm[j] = sc[wm * C::WM + j * 16 + lr];
+    if constexpr (SB == SB_TILES) fm[j] *= sc[BM + wn * C::WN];
+  };
+  auto read_b = [&](const ESG_LDS char* st, int i) __attribute__((always_inline)) {
+    const int r = wn * C::WN + i * 16 + lr;
+    return F(frag_krow(st + C::A_BYTES, r, lg), frag_krow(st + C::A_BYTES, r, lg + 4));
+  };
+  auto read_sb = [&](const ESG_LDS float* sc, int i) __attribute__((always_inline)) {
+    return SB == SB_ROWS ? *(const ESG_LDS f32x4*)(sc + BM + wn * C::WN + i * 16 + lg * 4) : f32x4{1.f, 1.f, 1.f, 1.f};
+  };
 
   load_scales(kb0);
   issue(0);
+  issue(1);
   put_scales(0);
-  for (int t = 0; t < nk; ++t) {
-    wait_vmcnt<0>();
-    wait_lgkm0();
-    barrier();
-    // the scales' wait comes before this step's loads: nothing is in flight here
-    if ((t & 3) == 2 && t + 2 < nk) put_scales(((t >> 2) + 1) & 1);
-    if (t + 1 < nk) issue(t + 1);
-    if ((t & 3) == 0 && t + 4 < nk) load_scales(kb0 + t + 4);
-    const ESG_LDS char* ta = lds + (t & 1) * C::STAGE;
-    const ESG_LDS char* tb = ta + C::A_BYTES;
-    const ESG_LDS float* sc = slots + ((t >> 2) & 1) * C::SLOT + (t & 3) * C::SROWS;
-    // The products of row fragment i run while the results of fragment i - 1 are
-    // scaled and added (the last fragment's in the next step) and fragment i + 1
-    // is read: without this order the compiler waits out every product's latency
-    // (MFMA busy 34 %).
-    Frag<fine(OUT)> am[C::FM];
-    float fm[C::FM];
-    f32x4 sn = {0.f, 0.f, 0.f, 0.f};
-    auto rows = [&](int i) __attribute__((always_inline)) {
-      const int r = wn * C::WN + i * 16 + lr;
-      return Frag<fine(OUT)>(frag_krow(tb, r, lg), frag_krow(tb, r, lg + 4));
-    };
-    auto rows_scale = [&](int i) __attribute__((always_inline)) {
-      return SB == SB_ROWS ? *(const ESG_LDS f32x4*)(sc + BM + wn * C::WN + i * 16 + lg * 4) : f32x4{1.f, 1.f, 1.f, 1.f};
-    };
-    Frag<fine(OUT)> bn = rows(0);
-    sn = rows_scale(0);
+  wait_vmcnt<0>();
+  wait_lgkm0();
+  barrier();
+  bn = read_b(lds, 0);
+  sn = read_sb(slots, 0);
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j) {
-      const int r = wm * C::WM + j * 16 + lr;
-      am[j] = Frag<fine(OUT)>(frag_krow(ta, r, lg), frag_krow(ta, r, lg + 4));
-      fm[j] = sc[r];
-      if constexpr (SB == SB_TILES) fm[j] *= sc[BM + wn * C::WN];
-    }
+  for (int j = 0; j < C::FM; ++j) {
+    read_a(lds, j);
+    read_fa(slots, j);
+  }
+  for (int t = 0; t < nk; ++t) {
+    // the next four blocks' scales: requested at a group's first step, written two steps later
+    if ((t & 3) == 0 && t + 4 < nk) load_scales(kb0 + t + 4);
+    if ((t & 3) == 2 && t + 2 < nk) put_scales(((t >> 2) + 1) & 1);
+    const ESG_LDS char* st = lds + (t & 1) * C::STAGE;
+    const ESG_LDS float* sc = slots + ((t >> 2) & 1) * C::SLOT + (t & 3) * C::SROWS;
+    const ESG_LDS char* st2 = lds + ((t + 1) & 1) * C::STAGE;  // the next step's (past the last: read, not used)
+    const ESG_LDS float* sc2 = slots + (((t + 1) >> 2) & 1) * C::SLOT + ((t + 1) & 3) * C::SROWS;
 #pragma unroll
     for (int i = 0; i < C::FN; ++i) {
-      Frag<fine(OUT)> bnext;
-      f32x4 snext = sn;
+      F bnext;
+      f32x4 snext;
       if (i + 1 < C::FN) {
-        bnext = rows(i + 1);
-        snext = rows_scale(i + 1);
+        bnext = read_b(st, i + 1);
+        snext = read_sb(sc, i + 1);
+      } else {
+        // this step's operands are all in registers; the next step's have landed
+        wait_lgkm0();
+        wait_vmcnt<0>();
+        barrier();
+        issue(t + 2);
+        bnext = read_b(st2, 0);
+        snext = read_sb(sc2, 0);
       }
       f32x4 d[C::FM];
 #pragma unroll
@@ -245,6 +267,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
         __builtin_amdgcn_sched_barrier(0);
         d[j] = mma_block(bn, am[j]);
         add_scaled(acc[(i + C::FN - 1) % C::FN][j], dp[j], fp[j], sp);
+        if (i + 1 == C::FN) read_a(st2, j);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -256,39 +279,62 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
       bn = bnext;
       sn = snext;
     }
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) read_fa(sc2, j);
   }
 #pragma unroll
   for (int j = 0; j < C::FM; ++j) add_scaled(acc[C::FN - 1][j], dp[j], fp[j], sp);
+  wait_lgkm0();
+  wait_vmcnt<0>();
+  barrier();  // the stages are free
 
-  // a lane holds n = 4 consecutive of one m
-  const bool vec = (g.N & 3) == 0;
+  // ---- results: a lane holds 4 consecutive n of one m.  A wave takes 16 rows at
+  // a time through 8 KB of its own (16 rows of 512 bytes at most), in 16-byte
+  // chunks swizzled by row, and stores whole rows of its WN columns. ----
+  constexpr int ES = OUT == OUT_BF16 ? 2 : 4;
+  constexpr int NCH = C::WN * ES / 16;  // chunks per row
+  char* y = OUT == OUT_BF16 || OUT == OUT_F32 ? (char*)g.y : (char*)(g.part + (size_t)blockIdx.y * g.M * g.N);
+  const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WN;
+  if (g.N * ES % 16 == 0) {
+    static_assert(16 * NCH * 16 * C::NW <= 2 * C::STAGE, "the pieces lie in the stages");
+    ESG_LDS char* out = lds + w * (16 * NCH * 16);
 #pragma unroll
-  for (int j = 0; j < C::FM; ++j) {
-    const int m = m0 + wm * C::WM + j * 16 + lr;
-    if (m >= g.M) continue;
+    for (int j = 0; j < C::FM; ++j) {
 #pragma unroll
-    for (int i = 0; i < C::FN; ++i) {
-      const int n = n0 + wn * C::WN + i * 16 + lg * 4;
-      const size_t at = (size_t)m * g.N + n;
-      if constexpr (OUT == OUT_BF16) {
-        bf16_t* y = (bf16_t*)g.y + at;
-        if (vec && n < g.N) {
-          *(uint2*)y = make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < g.N) store_elem<bf16_t>(y + e, acc[i][j][e]);
-        }
-      } else {
-        float* y = (OUT != OUT_F32 ? g.part + (size_t)blockIdx.y * g.M * g.N : (float*)g.y) + at;
-        if (vec && n < g.N) {
-          *(float4*)y = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < g.N) y[e] = acc[i][j][e];
-        }
+      for (int i = 0; i < C::FN; ++i) {
+        const f32x4& v = acc[i][j];
+        if constexpr (ES == 2)
+          lds_write8(out + (lr * NCH + ((i * 2 + (lg >> 1)) ^ (lr & (NCH - 1)))) * 16 + (lg & 1) * 8,
+                     pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        else
+          *(ESG_LDS f32x4*)(out + (lr * NCH + ((i * 4 + lg) ^ (lr & (NCH - 1)))) * 16) = v;
       }
+      wait_lgkm0();
+#pragma unroll
+      for (int h = 0; h < 16 * NCH / 64; ++h) {
+        const int r = (h * 64 + lane) / NCH, c = lane % NCH;
+        const u32x4_t v = *(const ESG_LDS u32x4_t*)(out + (r * NCH + (c ^ (r & (NCH - 1)))) * 16);
+        const int m = mw + j * 16 + r, n = nw + c * (16 / ES);
+        if (m < g.M && n < g.N) *(u32x4_t*)(y + ((size_t)m * g.N + n) * ES) = v;
+      }
+      wait_lgkm0();  // read before the next rows are written
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) {
+      const int m = mw + j * 16 + lr;
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = nw + i * 16 + lg * 4 + e;
+          if (m < g.M && n < g.N) {
+            if constexpr (ES == 2)
+              store_elem<bf16_t>((bf16_t*)y + (size_t)m * g.N + n, acc[i][j][e]);
+            else
+              ((float*)y)[(size_t)m * g.N + n] = acc[i][j][e];
+          }
+        }
     }
   }
 }
@@ -458,7 +504,7 @@ struct Plan {
   int nm = 0, nn = 0, splits = 1, kb_split = 0;
 };
 
-Plan plan(int M, int N, int K) {
+Plan plan(int M, int N, int K, bool f32_out = false) {
   Plan p;
   const int KB = (K + kQB - 1) / kQB;
   p.kb_split = KB;
@@ -467,7 +513,8 @@ Plan plan(int M, int N, int K) {
     return p;
   }
   const long long big = (long long)((M + 255) / 256) * ((N + 255) / 256);
-  p.big = big >= kNominalCUs;
+  // float32 results: the widened operands of a 256 x 256 tile do not fit the registers (61 spilled)
+  p.big = big >= kNominalCUs && !f32_out;
   const int t = p.big ? 256 : 128;
   p.nm = (M + t - 1) / t;
   p.nn = (N + t - 1) / t;
@@ -495,7 +542,7 @@ template <int SB>
 static hipError_t run(Fp8Args& g, const Plan& p, int out_bf16, hipStream_t stream) {
   if (p.skinny) return out_bf16 ? launch_skinny<SB, OUT_BF16>(g, stream) : launch_skinny<SB, OUT_F32>(g, stream);
   if (p.big)
-    return out_bf16 ? launch_tiles<256, 256, SB, OUT_BF16>(g, stream) : launch_tiles<256, 256, SB, OUT_F32>(g, stream);
+    return launch_tiles<256, 256, SB, OUT_BF16>(g, stream);
   if (p.splits == 1)
     return out_bf16 ? launch_tiles<128, 128, SB, OUT_BF16>(g, stream) : launch_tiles<128, 128, SB, OUT_F32>(g, stream);
   const hipError_t e = out_bf16 ? launch_tiles<128, 128, SB, OUT_PART>(g, stream)
@@ -515,7 +562,7 @@ static hipError_t run(Fp8Args& g, const Plan& p, int out_bf16, hipStream_t strea
 
 hipError_t launch_fp8_matmul(const void* a, const float* sa, const void* b, const float* sb, int sb_rows, int out_dtype,
                              int M, int N, int K, void* y, void* workspace, hipStream_t stream) {
-  const Plan p = plan(M, N, K);
+  const Plan p = plan(M, N, K, out_dtype == 0);
   Fp8Args g{};
   g.a = (const uint8_t*)a;
   g.b = (const uint8_t*)b;

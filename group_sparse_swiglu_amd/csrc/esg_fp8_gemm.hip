@@ -108,6 +108,15 @@ struct Tile {
   static_assert(WN <= 128, "the n range of a wave lies in one 128-row block");
 };
 
+// One lane's 16-byte direct-to-LDS load (see dma16) at voff + soff, soff scalar.
+// The range check compares voff with the buffer's size less soff, so soff must
+// not be past the buffer.
+__device__ __forceinline__ void dma16_at(const DmaSrc& s, ESG_LDS char* wave_base, uint32_t voff, uint32_t soff) {
+  const int m = __builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)wave_base);
+  const int so = __builtin_amdgcn_readfirstlane((int)soff);
+  asm volatile("buffer_load_dwordx4 %0, %1, %3 offen lds" : : "v"(voff), "s"(s.d), "{m0}"(m), "s"(so) : "memory");
+}
+
 template <int ROWS, int NW>
 struct RowDma {
   static constexpr int NI = ROWS / 8 / NW;  // 1 KB instructions (8 rows of 128 bytes) per wave and stage
@@ -120,12 +129,15 @@ struct RowDma {
       base[i] = r < rows ? (uint32_t)r * (uint32_t)K + koff(lane) : kOOB;
     }
   }
-  // k0: first K element of the step; chunks at or past K read zeros
-  __device__ __forceinline__ void issue(const DmaSrc& src, ESG_LDS char* st, int w, int lane, int k0, int K) {
-    const bool in = k0 + koff(lane) < K;
+  // before the block from k0 is issued that K cuts short: chunks at or past K read zeros from here on
+  __device__ __forceinline__ void cut(int lane, int k0, int K) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)  // kOOB + k0 stays past every buffer
-      dma16(src, st + (w * NI + i) * 1024, in ? base[i] + (uint32_t)k0 : kOOB);
+    for (int i = 0; i < NI; ++i) base[i] = k0 + koff(lane) < K ? base[i] : kOOB;
+  }
+  // k0: first K element of the step, below K
+  __device__ __forceinline__ void issue(const DmaSrc& src, ESG_LDS char* st, int w, int k0) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) dma16_at(src, st + (w * NI + i) * 1024, base[i], (uint32_t)k0);
   }
 };
 
@@ -165,11 +177,18 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
   RowDma<BN, C::NW> db;
   da.init(w, lane, mrows, g.K);
   db.init(w, lane, nrows, g.K);
-  const int kend = min(g.K, kb1 * kQB);  // blocks past the part read nothing
-  auto issue = [&](int t) __attribute__((always_inline)) {
-    ESG_LDS char* st = lds + (t & 1) * C::STAGE;
-    da.issue(ra, st, w, lane, (kb0 + t) * kQB, kend);
-    db.issue(rb, st + C::A_BYTES, w, lane, (kb0 + t) * kQB, kend);
+  // loads of step t into stage S; past the last step: its block again (not used)
+  auto issue = [&](int t, ESG_LDS char* st) __attribute__((always_inline)) {
+    const int k0 = min(kb0 + t, kb1 - 1) * kQB;
+    da.issue(ra, st, w, k0);
+    db.issue(rb, st + C::A_BYTES, w, k0);
+  };
+  auto cut = [&](int t) __attribute__((always_inline)) {  // before issue(t)
+    const int k0 = (kb0 + t) * kQB;
+    if (k0 < g.K && k0 + kQB > g.K) {
+      da.cut(lane, k0, g.K);
+      db.cut(lane, k0, g.K);
+    }
   };
 
   // this thread's row of scales (rows outside the matrix take the last one; their outputs are not stored)
@@ -206,47 +225,113 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
 #pragma unroll
     for (int e = 0; e < 4; ++e) to[e] = fmaf(d[e], SB == SB_ROWS ? f * s[e] : f, to[e]);
   };
-  // fragments and scales of the step in stage st, scale line sc
-  auto read_a = [&](const ESG_LDS char* st, int j) __attribute__((always_inline)) {
-    const int r = wm * C::WM + j * 16 + lr;
-    am[j] = F(frag_krow(st, r, lg), frag_krow(st, r, lg + 4));
+  // This lane's chunks lg and lg + 4 of the first column and row fragment in stage 0 (krow_off); the others lie
+  // at constant distances, so the reads need no address arithmetic.
+  const ESG_LDS char* const a_lo = lds + krow_off(wm * C::WM + lr, lg);
+  const ESG_LDS char* const a_hi = lds + krow_off(wm * C::WM + lr, lg + 4);
+  const ESG_LDS char* const b_lo = lds + C::A_BYTES + krow_off(wn * C::WN + lr, lg);
+  const ESG_LDS char* const b_hi = lds + C::A_BYTES + krow_off(wn * C::WN + lr, lg + 4);
+  struct Raw {
+    uint4 v[2];
   };
+  auto read16 = [](const ESG_LDS char* p) __attribute__((always_inline)) {
+    return __builtin_bit_cast(uint4, *(const ESG_LDS u32x4_t*)p);
+  };
+  auto raw_a = [&](int st, int j) __attribute__((always_inline)) {
+    return Raw{{read16(a_lo + st * C::STAGE + j * 2048), read16(a_hi + st * C::STAGE + j * 2048)}};
+  };
+  auto raw_b = [&](int st, int i) __attribute__((always_inline)) {
+    return Raw{{read16(b_lo + st * C::STAGE + i * 2048), read16(b_hi + st * C::STAGE + i * 2048)}};
+  };
+  auto read_a = [&](int st, int j) __attribute__((always_inline)) {
+    const Raw r = raw_a(st, j);
+    am[j] = F(r.v[0], r.v[1]);
+  };
+  auto read_b = [&](int st, int i) __attribute__((always_inline)) {
+    const Raw r = raw_b(st, i);
+    return F(r.v[0], r.v[1]);
+  };
+  // scales of the step whose line is sc
   auto read_fa = [&](const ESG_LDS float* sc, int j) __attribute__((always_inline)) {
     fm[j] = sc[wm * C::WM + j * 16 + lr];
     if constexpr (SB == SB_TILES) fm[j] *= sc[BM + wn * C::WN];
-  };
-  auto read_b = [&](const ESG_LDS char* st, int i) __attribute__((always_inline)) {
-    const int r = wn * C::WN + i * 16 + lr;
-    return F(frag_krow(st + C::A_BYTES, r, lg), frag_krow(st + C::A_BYTES, r, lg + 4));
   };
   auto read_sb = [&](const ESG_LDS float* sc, int i) __attribute__((always_inline)) {
     return SB == SB_ROWS ? *(const ESG_LDS f32x4*)(sc + BM + wn * C::WN + i * 16 + lg * 4) : f32x4{1.f, 1.f, 1.f, 1.f};
   };
 
   load_scales(kb0);
-  issue(0);
-  issue(1);
+  cut(0);
+  issue(0, lds);
+  if (nk > 1) cut(1);
+  issue(1, lds + C::STAGE);
   put_scales(0);
   wait_vmcnt<0>();
   wait_lgkm0();
   barrier();
-  bn = read_b(lds, 0);
+  bn = read_b(0, 0);
   sn = read_sb(slots, 0);
 #pragma unroll
   for (int j = 0; j < C::FM; ++j) {
-    read_a(lds, j);
+    read_a(0, j);
     read_fa(slots, j);
   }
-  for (int t = 0; t < nk; ++t) {
+  // step t, in stage S (a constant at each of its two places)
+  auto step = [&](int t, int S) __attribute__((always_inline)) {
+    if (t + 2 < nk) cut(t + 2);
     // the next four blocks' scales: requested at a group's first step, written two steps later
     if ((t & 3) == 0 && t + 4 < nk) load_scales(kb0 + t + 4);
     if ((t & 3) == 2 && t + 2 < nk) put_scales(((t >> 2) + 1) & 1);
-    const ESG_LDS char* st = lds + (t & 1) * C::STAGE;
+    const int st = S, st2 = S ^ 1;  // st2: the next step's stage (past the last step: read, not used)
     const ESG_LDS float* sc = slots + ((t >> 2) & 1) * C::SLOT + (t & 3) * C::SROWS;
-    const ESG_LDS char* st2 = lds + ((t + 1) & 1) * C::STAGE;  // the next step's (past the last: read, not used)
     const ESG_LDS float* sc2 = slots + (((t + 1) >> 2) & 1) * C::SLOT + ((t + 1) & 3) * C::SROWS;
 #pragma unroll
-    for (int i = 0; i < C::FN; ++i) {
+    for (int i = 0; i < C::FN && fine(OUT); ++i) {
+      // The same order for widened operands: the four products of a block go through all column fragments in
+      // turn (each depends on the one before), and what is read for the next fragment is widened under the
+      // last of them, when it has arrived.
+      Raw braw, araw[C::FM];
+      F bnext;
+      f32x4 snext;
+      if (i + 1 < C::FN) {
+        braw = raw_b(st, i + 1);
+        snext = read_sb(sc, i + 1);
+      } else {
+        wait_lgkm0();
+        wait_vmcnt<0>();
+        barrier();
+        issue(t + 2, lds + S * C::STAGE);
+        braw = raw_b(st2, 0);
+        snext = read_sb(sc2, 0);
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j) araw[j] = raw_a(st2, j);
+      }
+      f32x4 d[C::FM];
+      static_assert(C::FM == 4, "one of the four products per column fragment's sums");
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j) {
+          if (s == 0) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+          mma_bf16(d[j], bn.v[s % (fine(OUT) ? 4 : 2)], am[j].v[s % (fine(OUT) ? 4 : 2)]);
+        }
+        add_scaled(acc[(i + C::FN - 1) % C::FN][s], dp[s], fp[s], sp);
+      }
+      bnext = F(braw.v[0], braw.v[1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j) {
+        dp[j] = d[j];
+        fp[j] = fm[j];
+        if (i + 1 == C::FN) am[j] = F(araw[j].v[0], araw[j].v[1]);
+      }
+      sp = sn;
+      bn = bnext;
+      sn = snext;
+    }
+#pragma unroll
+    for (int i = 0; i < C::FN && !fine(OUT); ++i) {
       F bnext;
       f32x4 snext;
       if (i + 1 < C::FN) {
@@ -257,7 +342,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
         wait_lgkm0();
         wait_vmcnt<0>();
         barrier();
-        issue(t + 2);
+        issue(t + 2, lds + S * C::STAGE);
         bnext = read_b(st2, 0);
         snext = read_sb(sc2, 0);
       }
@@ -281,6 +366,10 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
     }
 #pragma unroll
     for (int j = 0; j < C::FM; ++j) read_fa(sc2, j);
+  };
+  for (int t = 0; t < nk; t += 2) {
+    step(t, 0);
+    if (t + 1 < nk) step(t + 1, 1);
   }
 #pragma unroll
   for (int j = 0; j < C::FM; ++j) add_scaled(acc[C::FN - 1][j], dp[j], fp[j], sp);

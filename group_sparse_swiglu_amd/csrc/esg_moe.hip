@@ -42,10 +42,12 @@ struct MoeArgs {
   float* probs;           // [T][k]
   int64_t* indices;       // [T][k]
   float* part;            // [splits][d/16][T][16]: the parts of y where the down items are split
-  int* flags;             // [kMoeMaxGrid]: workgroup whose gate/up units are done
+  int* flags;             // [kMoeMaxGrid]: workgroups whose gate/up units are done
+  int* tickets;           // [kMoeMaxGrid]: units taken, of each team
   int* arrived;           // [d/16]: workgroups done with a tile of y
   int T, E, k, d, ff, bias_stride, apply_scaling;
   int splits;             // parts of the down items
+  int teams;              // workgroups that run on CUs of their own
   int patience;           // polls before a workgroup does others' gate/up units itself
   float scaling;
 };
@@ -132,47 +134,39 @@ __device__ __forceinline__ void mma_chunk128(f32x4& acc, const Rows16<WT>& a, co
 }
 
 // ---------------------------------------------------------------------------
-// Scores: 16 experts per workgroup, all tokens; the waves split d.  Also clears
-// the flags and counts of the launch that follows.
+// Scores: 16 experts and 16 tokens per workgroup; the waves split d.  Also clears
+// the counters of the launch that follows.
 // ---------------------------------------------------------------------------
 constexpr int kScoreWaves = 16;
 
-template <int MT>
 __global__ __launch_bounds__(kScoreWaves * 64) void moe_scores_kernel(MoeArgs g) {
-  __shared__ f32x4 red[kScoreWaves][MT][64];
+  __shared__ f32x4 red[kScoreWaves][64];
   const int lane = threadIdx.x & 63, w = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
-  const int e0 = blockIdx.x * 16;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < kMoeMaxGrid + g.d / 16; i += kScoreWaves * 64) g.flags[i] = 0;
+  const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < 2 * kMoeMaxGrid + g.d / 16; i += kScoreWaves * 64) g.flags[i] = 0;
   const rsrc_t rr = rows_rsrc<W_BF16>(g.router, e0, g.d, min(16, g.E - e0));  // rows past E read zeros
   const rsrc_t rx = make_rsrc(g.x, (uint32_t)(g.T * g.d * 2));
-  f32x4 acc[MT];
-  zero_acc(acc);
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   for (int k0 = w * kChunk; k0 < g.d; k0 += kScoreWaves * kChunk) {
     Rows16<W_BF16> a;
+    Cols16<W_BF16> b;
     a.load(rr, lr, k0, g.d, lg);
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int t = j * 16 + lr;
-      Cols16<W_BF16> b;
-      b.load(rx, t * g.d, k0, g.d, t < g.T, lg);
-      mma_chunk128<W_BF16>(acc[j], a, b, 1.0f);
-    }
+    b.load(rx, (t0 + lr) * g.d, k0, g.d, t0 + lr < g.T, lg);
+    mma_chunk128<W_BF16>(acc, a, b, 1.0f);
   }
-#pragma unroll
-  for (int j = 0; j < MT; ++j) red[w][j][lane] = acc[j];
+  red[w][lane] = acc;
   __syncthreads();
+  if (threadIdx.x >= 256) return;
+  const int e = threadIdx.x & 15, t = threadIdx.x >> 4;
+  if (t0 + t >= g.T || e0 + e >= g.E) return;
   const float* rf = (const float*)red;
-  for (int o = threadIdx.x; o < MT * 256; o += kScoreWaves * 64) {
-    const int e = o & 15, t = o >> 4;
-    if (t >= g.T || e0 + e >= g.E) continue;
-    const int at = ((t >> 4) * 64 + (e >> 2) * 16 + (t & 15)) * 4 + (e & 3);
-    float s = rf[at];
+  const int at = ((e >> 2) * 16 + t) * 4 + (e & 3);
+  float s = rf[at];
 #pragma unroll
-    for (int v = 1; v < kScoreWaves; ++v) s += rf[v * MT * 256 + at];
-    g.scores[(size_t)t * g.E + e0 + e] = exact_sigmoid(s);
-  }
+  for (int v = 1; v < kScoreWaves; ++v) s += rf[v * 256 + at];
+  g.scores[(size_t)(t0 + t) * g.E + e0 + e] = exact_sigmoid(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -382,18 +376,22 @@ __device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>
 // ---------------------------------------------------------------------------
 // The experts, in one launch.  Gate/up units (16 neurons of one expert for all
 // its tokens), then down units (16 columns of y for all tokens over one part of
-// the (expert, K chunk) items), each kind dealt out to the workgroups in turn.
-// A workgroup that has stored the h of its gate/up units raises its flag; before
-// its down units it polls the flags of all.  (Units taken from a counter instead
-// took 13000 to 84000 cycles per ticket: 512 workgroups on one address.)
+// the (expert, K chunk) items), each kind dealt out in turn: the gate/up units to
+// teams of the workgroups that share a CU (b and b + teams), which take them
+// from a counter of the team.  (With every workgroup's units fixed, the second
+// workgroup of a CU, which gets less of it, ended at 45 us and the first at 30
+// us of a 70 us launch; with one counter for all, 512 workgroups on one address,
+// a ticket took 13000 to 84000 cycles.)  A workgroup raises a flag when the h of
+// all gate/up units that it took is stored and its team has no more, and polls
+// the flags of all before its down units.
 //
 // That wait always ends, also when some workgroups cannot start because others
 // wait (launches on several streams that share the device): a workgroup that
-// has polled `patience` times computes the missing units itself, one owner
-// after another.  They give the same bits whoever computes them, so it does no
-// harm if their owner does so too.
+// has polled `patience` times computes the missing units itself, one team after
+// another.  They give the same bits whoever computes them, so it does no harm if
+// their owner does so too.
 //
-// What a workgroup hands to others in the same launch (h, parts of y, flags) is
+// What a workgroup hands to others in the same launch (h, parts of y) is
 // written through to memory (device-scope stores) and waited for before the
 // flag or count that announces it, and read at device scope.  (Fences by every
 // workgroup work on whole caches instead: 22 us for the release, 27 us for the
@@ -408,9 +406,17 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
     f32x4 sums[kMoeWaves][TMAX][4];      // down: [token][16] sums, by wave
   } L;
   __shared__ int shared_int;
+  __shared__ int ticket[2];
   const int lane = threadIdx.x & 63, w = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
+  const int team = blockIdx.x % g.teams;
+  auto take = [&]() __attribute__((always_inline)) {
+    return __hip_atomic_fetch_add(g.tickets + team, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  if (threadIdx.x == 0) ticket[0] = take();
   route_all<EMAX, TMAX>(g, R, blockIdx.x == 0);
+  int ahead = 0;  // thread 0: the ticket after the next
+  if (threadIdx.x == 0) ahead = take();
 
   const int nt = g.ff / 16, dtiles = g.d / 16, grid = gridDim.x;
   const int gu_units = R.active * nt, d_units = dtiles * g.splits;
@@ -466,8 +472,9 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
     for (int u = 0; u < P; ++u) weights(lo + u, q[u]);
   };
 
-  for (int owner = blockIdx.x, polls = 0; owner >= 0;) {
-    // ---- gate and up units of `owner`: the waves split d and add their sums in
+  bool own = true;  // this workgroup's share of its team's units; else all units of a team that is missed
+  for (int owner = team, polls = 0; owner >= 0; own = false) {
+    // ---- gate and up units of team `owner`: the waves split d and add their sums in
     // LDS.  The weights of the next step (the rest of d, or the next unit) are
     // requested as soon as the products have taken the current ones, so they are
     // on the way during the reduction. ----
@@ -475,10 +482,11 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
     const int steps = (kb + kMoeWaves * U - 1) / (kMoeWaves * U);
     Rows16<WT> ag[U], au[U];
     float sg[U], su[U];
-    // units go by (place in the list of active experts, 16-neuron tile); a workgroup's next one is `grid` further
-    const int da = grid / nt, dn = grid - da * nt;
-    auto load = [&](int a, int n0, int step) __attribute__((always_inline)) {
-      const int d = a < R.active ? g.d : 0;  // no such unit: zeros, without a branch
+    // unit t of the team: number owner + t * teams, by active expert, then 16-neuron tile
+    auto load = [&](int t, int step) __attribute__((always_inline)) {
+      const int unit = owner + t * g.teams;
+      const int d = unit < gu_units ? g.d : 0;  // no such unit: zeros, without a branch
+      const int a = d ? unit / nt : 0, n0 = d ? (unit - a * nt) * 16 : 0;
       const int e = active(R, d ? a : 0).e;
       const rsrc_t rg = rows_rsrc<WT>(g.wg, (size_t)e * g.ff + n0, g.d);
       const rsrc_t ru = rows_rsrc<WT>(g.wu, (size_t)e * g.ff + n0, g.d);
@@ -494,18 +502,18 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
         }
       }
     };
-    int buf = 0;
-    int a = owner / nt, tile = owner - a * nt;
-    load(a, tile * 16, 0);
-    while (a < R.active) {
+    int buf = 0, turn = 0;
+    int cur = own ? ticket[0] : 0;
+    load(cur, 0);
+    if (own && threadIdx.x == 0) ticket[1] = ahead;
+    __syncthreads();
+    int nxt = own ? ticket[1] : 1;
+    while (owner + cur * g.teams < gu_units) {
+      const int unit = owner + cur * g.teams, a = unit / nt, n0 = (unit - a * nt) * 16;
       const Active act = active(R, a);
-      const int cnt = act.cnt, base = act.base, n0 = tile * 16;
+      const int cnt = act.cnt, base = act.base;
       const int tiles = (cnt + 15) >> 4;
-      int next_a = a + da, next_tile = tile + dn;
-      if (next_tile >= nt) {
-        ++next_a;
-        next_tile -= nt;
-      }
+      if (own && threadIdx.x == 0) ahead = take();
       f32x4 acc[2][MT];
       zero_acc(acc);
       for (int step = 0; step < steps; ++step) {
@@ -524,10 +532,10 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
           }
         }
         const bool more = step + 1 < steps;
-        load(more ? a : next_a, more ? n0 : next_tile * 16, more ? step + 1 : 0);
+        load(more ? cur : nxt, more ? step + 1 : 0);
       }
-      a = next_a;
-      tile = next_tile;
+      if (own && threadIdx.x == 0) ticket[turn] = ahead;
+      int after = nxt + 1;
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
         if (j >= tiles) break;
@@ -536,6 +544,7 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
         L.red[buf][w][1][lane] = acc[1][j];
         wait_lgkm0();
         barrier();  // not __syncthreads: that would wait for the weights on their way
+        if (j == 0 && own) after = ticket[turn];
         const float* rf = (const float*)L.red[buf];
         buf ^= 1;
         const int o = threadIdx.x;  // two neurons of one column
@@ -565,20 +574,25 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
                                                 kDevice);
         }
       }
+      cur = nxt;
+      nxt = after;
+      turn ^= 1;
     }
     wait_vmcnt<0>();
     barrier();  // every wave's h is stored
+    // this workgroup has done its share of the team's units, or all of them for the whole team
     if (threadIdx.x == 0)
-      __hip_atomic_store(g.flags + owner, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int b = own ? blockIdx.x : owner; b < grid; b += own ? grid : g.teams)
+        __hip_atomic_store(g.flags + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if ((int)blockIdx.x >= d_units) return;
     begin_down(blockIdx.x);
     for (;; ++polls) {  // threads watch different flags
       int missing = -1;
-      for (int b = threadIdx.x; b < min(grid, gu_units); b += kMoeWaves * 64)
-        if (__hip_atomic_load(g.flags + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0) missing = b;
+      for (int b = threadIdx.x; b < grid; b += kMoeWaves * 64)
+        if (__hip_atomic_load(g.flags + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0) missing = b % g.teams;
       owner = -1;
       if (!__syncthreads_or(missing >= 0)) break;
-      if (polls >= g.patience) {  // uniform: help one of the owners that some thread misses
+      if (polls >= g.patience) {  // uniform: help one of the teams that some thread misses
         if (missing >= 0) shared_int = missing;
         __syncthreads();
         owner = __builtin_amdgcn_readfirstlane(shared_int);
@@ -685,22 +699,24 @@ MoeLayout layout(int tokens, int experts, int topk, int d_model, int d_ff) {
   L.h = align256((size_t)tokens * experts * 4);
   L.part = L.h + align256((size_t)tokens * topk * d_ff * 4);
   L.flags = L.part + (L.splits > 1 ? align256((size_t)L.splits * tokens * d_model * 4) : 0);
-  L.bytes = L.flags + align256((size_t)(kMoeMaxGrid + d_model / 16) * 4);
+  L.bytes = L.flags + align256((size_t)(2 * kMoeMaxGrid + d_model / 16) * 4);
   return L;
 }
 
 template <int WT, int MT, int EMAX>
-hipError_t launch_t(const MoeArgs& g, hipStream_t stream) {
+hipError_t launch_t(MoeArgs g, hipStream_t stream) {
   {
     LaunchTimer timer("moe_scores", stream);
-    hipLaunchKernelGGL(moe_scores_kernel<MT>, dim3((g.E + 15) / 16), dim3(kScoreWaves * 64), 0, stream, g);
+    hipLaunchKernelGGL(moe_scores_kernel, dim3((g.E + 15) / 16, (g.T + 15) / 16), dim3(kScoreWaves * 64), 0, stream,
+                       g);
   }
   // two workgroups per CU; more than there can be units of either kind would find none
   const int slots = std::min(2 * compute_units(), kMoeMaxGrid);
   const long long most = std::max<long long>((long long)std::min(g.E, g.T * g.k) * (g.ff / 16), g.d / 16 * g.splits);
+  const int grid = (int)std::min<long long>(most, slots);
+  g.teams = std::min(grid, slots / 2);
   LaunchTimer timer("moe_experts", stream);
-  hipLaunchKernelGGL((moe_experts_kernel<WT, MT, EMAX>), dim3((unsigned)std::min<long long>(most, slots)),
-                     dim3(kMoeWaves * 64), 0, stream, g);
+  hipLaunchKernelGGL((moe_experts_kernel<WT, MT, EMAX>), dim3(grid), dim3(kMoeWaves * 64), 0, stream, g);
   return hipGetLastError();
 }
 
@@ -736,7 +752,8 @@ hipError_t launch_moe_decode(const MoeCall& c, void* workspace, hipStream_t stre
   g.h = (bf16_t*)((char*)workspace + L.h);
   g.part = (float*)((char*)workspace + L.part);
   g.flags = (int*)((char*)workspace + L.flags);
-  g.arrived = g.flags + kMoeMaxGrid;
+  g.tickets = g.flags + kMoeMaxGrid;
+  g.arrived = g.tickets + kMoeMaxGrid;
   g.patience = c.patience;
   g.splits = L.splits;
   g.y = (bf16_t*)c.y;

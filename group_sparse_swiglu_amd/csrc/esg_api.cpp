@@ -484,13 +484,13 @@ int esg_sigmoid_topk_routing(const float* logits, const float* expert_bias, int 
 
 namespace {
 // rows of cols elements quantised in blocks of 128: cols a multiple of 16, and
-// the launch's workgroups (one per 128 x 128 tile at most) within 2^31
+// the launch's threads (256 per 128 x 128 tile at most) within 2^32
 int quant_shape(int dtype, int batch, int rows, int cols) {
   if (dtype != ESG_F32 && dtype != ESG_BF16) return ESG_ERR_UNSUPPORTED;
   if (batch < 0 || rows < 0 || cols <= 0) return ESG_ERR_INVALID_ARG;
   if (cols % 16 || rows > (1 << 30) || cols > (1 << 22)) return ESG_ERR_UNSUPPORTED;
   const double tiles = (double)batch * ((rows + 127) / 128) * ((cols + 127) / 128);
-  return tiles < 2147483647.0 ? ESG_OK : ESG_ERR_UNSUPPORTED;
+  return tiles < 16777216.0 ? ESG_OK : ESG_ERR_UNSUPPORTED;
 }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 }  // namespace
@@ -522,10 +522,9 @@ int esg_fp8_quant_tiles(const void* w, int dtype, int batch, int rows, int cols,
 namespace {
 int fp8_shape(int M, int N, int K) {
   if (M < 0 || N < 0 || K <= 0) return ESG_ERR_INVALID_ARG;
-  if (K % 16 || K > (1 << 22) || M > (1 << 30) || N > (1 << 30)) return ESG_ERR_UNSUPPORTED;
-  // one workgroup per output tile of at least 16 x 128
-  if ((double)((M + 127) / 128) * ((N + 15) / 16) >= 2147483647.0) return ESG_ERR_UNSUPPORTED;
-  return ESG_OK;
+  if (K % 16 || K > (1 << 22) || M > (1 << 30) || N > (1 << 25)) return ESG_ERR_UNSUPPORTED;
+  // a launch's threads within 2^32: 512 per output tile of 128 x 128 at most, 1024 per 16 rows of b for few rows
+  return (double)((M + 127) / 128) * ((N + 127) / 128) < 8388608.0 ? ESG_OK : ESG_ERR_UNSUPPORTED;
 }
 }  // namespace
 

@@ -409,7 +409,7 @@ int esg_sigmoid_topk_routing(const float* logits, const float* expert_bias, int 
  * Errors: ESG_ERR_INVALID_ARG (null pointer, x, w, q or qt not 16-byte aligned,
  * a scale not 4-byte aligned, one of qt and scale_t without the other, negative
  * size, cols <= 0), ESG_ERR_UNSUPPORTED (dtype, cols not a multiple of 16, cols
- * above 2^22, rows above 2^30, or 2^31 tiles of 128 x 128 or more).
+ * above 2^22, rows above 2^30, or 2^24 tiles of 128 x 128 or more).
  */
 int esg_fp8_quant_rows(const void* x, int dtype, int rows, int cols, void* q, float* scale, void* qt, float* scale_t,
                        void* stream);
@@ -423,8 +423,12 @@ int esg_fp8_quant_tiles(const void* w, int dtype, int batch, int rows, int cols,
  * b_scale_rows == 0: B(n, j) = b_scale[n/128, j], b_scale float
  * [ceil(N/128), ceil(K/128)] (weights quantised in tiles); else B(n, j) =
  * b_scale[n, j], b_scale float [N, ceil(K/128)].  y: [M, N], out_dtype ESG_F32
- * or ESG_BF16, overwritten.  Products and sums are float32; the order of a sum
- * depends on the shape only, and no atomics are used (bitwise reproducible).
+ * or ESG_BF16, overwritten.  Sums are float32; the order of a sum depends on the
+ * shape and out_dtype only, and no atomics are used (bitwise reproducible).  For
+ * an ESG_BF16 result the products run on the 8-bit matrix cores, which drop what
+ * lies far below the largest term of a sum (2e-5 to 3e-5 of a result's norm
+ * measured, a hundredth of its rounding); for ESG_F32 the operands are widened
+ * to bf16, exactly, and float32 accuracy is kept at half the rate.
  * The three products of a linear layer y = x W^T, with x and dy quantised in
  * rows (and transposed), W in tiles (and transposed):
  *   y = (xq, wq); dx = (dyq, wqt); dW = (dyqt, xqt, b_scale_rows = 1).
@@ -433,7 +437,8 @@ int esg_fp8_quant_tiles(const void* w, int dtype, int batch, int rows, int cols,
  * workspace may be NULL).  M == 0 or N == 0 enqueues nothing.
  * Errors: ESG_ERR_INVALID_ARG (null pointer, a, b or y not 16-byte aligned,
  * negative size, K <= 0), ESG_ERR_UNSUPPORTED (out_dtype, K not a multiple of 16 or above
- * 2^22, M or N above 2^30, or 2^31 output tiles), ESG_ERR_WORKSPACE.
+ * 2^22, M above 2^30, N above 2^25, or 2^23 output tiles of 128 x 128 or more),
+ * ESG_ERR_WORKSPACE.
  */
 int esg_fp8_matmul_workspace_size(int M, int N, int K, size_t* workspace_bytes);
 int esg_fp8_matmul(const void* a, const float* a_scale, const void* b, const float* b_scale, int b_scale_rows,

@@ -66,7 +66,7 @@ def test_matmul_refusals_and_workspace():
         assert call(**{name: P + 2}) == 1
     assert call(M=-1) == 1 and call(K=0) == 1 and call(N=-3) == 1
     assert call(K=100) == 2 and call(K=(1 << 22) + 16) == 2 and call(out=2) == 2
-    assert call(M=1 << 30, N=1 << 30) == 2
+    assert call(M=1 << 30, N=1 << 24) == 2 and call(N=(1 << 25) + 1) == 2   # more threads than a launch may have
     assert E.lib().esg_fp8_matmul_workspace_size(4, 4, 128, None) == 1
     assert _ws(4, 4, 100)[0] == 2
     assert _ws(4, 4096, 2048) == (0, 0)
@@ -77,6 +77,40 @@ def test_matmul_refusals_and_workspace():
     assert call(M=128, N=128, K=16384, bytes=need - 1) == 3
     assert call(M=128, N=128, K=16384, ws=NULL) == 3
     assert call(M=128, N=128, K=16384, ws=P + 8) == 1
+
+
+def test_linear_refusals_and_sizes():
+    lib = E.lib()
+
+    def sizes(*args):
+        out = [ctypes.c_size_t() for _ in range(3)]
+        return lib.esg_fp8_linear_workspace_size(*args, *map(ctypes.byref, out)), *(o.value for o in out)
+
+    st, sv, fw, bw = sizes(100, 256, 512, 1, 1)
+    assert st == 0 and sv >= 256 * 112 + 256 * 512 and fw >= 100 * 256 + 512 * 256 and bw >= 100 * 512 + 512 * 112
+    assert sizes(100, 256, 512, 0, 0)[1] == 0
+    assert sizes(100, 256, 512, 1, 0)[1] < sv and sizes(100, 256, 512, 0, 1)[1] < sv
+    assert sizes(0, 256, 512, 1, 1)[0] == 0
+    assert sizes(4, 250, 512, 1, 1)[0] == 2 and sizes(4, 256, 500, 1, 1)[0] == 2
+    assert sizes(-1, 256, 512, 1, 1)[0] == 1 and sizes(4, 0, 512, 1, 1)[0] == 1
+    assert lib.esg_fp8_linear_workspace_size(4, 256, 512, 1, 1, None, None, None) == 1
+    f, big = lib.esg_fp8_linear_fwd, 1 << 40
+    assert f(NULL, 1, P, 1, 4, 256, 512, 1, 1, P, P, big, P, big, NULL) == 1
+    assert f(P, 1, NULL, 1, 4, 256, 512, 1, 1, P, P, big, P, big, NULL) == 1
+    assert f(P, 1, P, 1, 4, 256, 512, 1, 1, P + 8, P, big, P, big, NULL) == 1
+    assert f(P, 2, P, 1, 4, 256, 512, 1, 1, P, P, big, P, big, NULL) == 2
+    assert f(P, 1, P, 2, 4, 256, 512, 1, 1, P, P, big, P, big, NULL) == 2
+    assert f(P, 1, P, 1, 4, 256, 512, 1, 1, P, NULL, 0, P, big, NULL) == 3
+    assert f(P, 1, P, 1, 4, 256, 512, 1, 1, P, P, 16, P, big, NULL) == 3
+    assert f(P, 1, P, 1, 4, 256, 512, 1, 1, P, P, big, P, 16, NULL) == 3
+    assert f(P, 1, P, 1, 4, 256, 512, 1, 1, P, P + 8, big, P, big, NULL) == 1
+    b = lib.esg_fp8_linear_bwd
+    assert b(P, 1, 1, 4, 256, 512, P, big, NULL, NULL, P, big, NULL) == 0        # nothing asked for
+    assert b(NULL, 1, 1, 4, 256, 512, P, big, P, P, P, big, NULL) == 1
+    assert b(P, 1, 1, 4, 256, 512, P, 16, P, P, P, big, NULL) == 3
+    assert b(P, 1, 1, 4, 256, 512, P, big, P, P, P, 16, NULL) == 3
+    assert b(P, 1, 1, 4, 256, 512, P, big, P + 8, P, P, big, NULL) == 1
+    assert b(P, 3, 1, 4, 256, 512, P, big, P, P, P, big, NULL) == 2
 
 
 def test_moe_refusals_and_workspace():

@@ -279,6 +279,31 @@ def test_linear_single_gradients_and_leading_dims():
     assert torch.equal(s, torch.autograd.grad(E.fp8_linear(x, w), x, torch.ones_like(dy))[0])
 
 
+def test_linear_calls_agree_with_the_parts_and_autograd():
+    require_gpu()
+    note("linear calls")
+    T, K, N = 200, 272, 144
+    x, w, dy = _x(T, K, BF, 1).to(DEV), _x(N, K, F32, 2).to(DEV), _x(T, N, BF, 3).to(DEV)
+    ws = {}
+    y, saved = E.fp8_linear_fwd(x, w, workspace=ws)
+    dx, dw = E.fp8_linear_bwd(dy, saved, K, F32, workspace=ws)
+    xq, xs, xqt, xst = E.fp8_quantize(x, transposed=True)
+    wq, wsc, wqt, wst = E.fp8_quantize_weight(w, transposed=True)
+    dq, ds, dqt, dst = E.fp8_quantize(dy, transposed=True)
+    assert torch.equal(y, E.fp8_matmul(xq, xs, wq, wsc))
+    assert torch.equal(dx, E.fp8_matmul(dq, ds, wqt, wst))
+    assert torch.equal(dw, E.fp8_matmul(dqt, dst, xqt, xst, out_dtype=F32))
+    y2, none = E.fp8_linear_fwd(x, w, False, False, workspace=ws)
+    assert none is None and torch.equal(y2, y)
+    _, half = E.fp8_linear_fwd(x, w, True, False, workspace=ws)
+    only = E.fp8_linear_bwd(dy, half, K, F32, True, False, workspace=ws)
+    assert torch.equal(only[0], dx) and only[1] is None
+    with pytest.raises(E.EsgError):
+        E.fp8_linear_bwd(dy, half, K, F32, workspace=ws)      # saved without the weight gradient's part
+    with pytest.raises(E.EsgError):
+        E.fp8_linear_fwd(x, w[:, :256].contiguous())
+
+
 def test_on_another_stream_and_in_a_graph():
     require_gpu()
     note("fp8 graph")

@@ -18,8 +18,9 @@
 // can hold, so its operands are widened to bf16 (exactly) on the way into bf16
 // products, at half the matrix rate.
 //
-// Two kernels: tile_kernel for M > kSkinnyM (operand tiles staged through LDS),
-// skinny_kernel for few rows, where the product is a read of b.
+// Two kernels: fp8_rows_kernel for few rows and small products, where latency and
+// the read of b count, fp8_tile_kernel (128 x 128 or 256 x 256 tiles) for the rest;
+// plan() chooses between them.
 #include <algorithm>
 
 #include "esg_fp8.hpp"
@@ -455,128 +456,155 @@ __global__ __launch_bounds__(256) void fp8_reduce_kernel(const float* __restrict
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: a workgroup takes 16 rows of b and all of a (MT tiles of 16 rows);
-// its NW waves take the K blocks in turn, b straight from memory into the
-// products' operand registers, and add their sums in LDS in wave order.  The
-// read of b bounds it; P blocks per wave are on their way or in use, in
-// registers that take turns (moving them would wait for the loads), and what
-// lies outside is an offset past its buffer, which reads zeros without a branch.
+// Few rows: a workgroup takes 16 rows of b and up to 64 rows of a (MT tiles of
+// 16); its NW waves take the K blocks in turn and add their sums in LDS in wave
+// order.  The read of b bounds it, with a's rows from L2 beside it (each
+// workgroup reads them all, so the time grows with M).
+//
+// Everything goes through LDS: loads into the products' registers touch 16 rows,
+// one per lane, in every quarter of a wave and come at about 15 bytes per clock
+// and CU; direct-to-LDS loads of whole 128-byte rows come at about 40 (37 rows,
+// N = 2048, K = 5504: 11.7 us from registers, 6.9 through LDS).  Each wave has P
+// slots of its own, with a block of b, of a and their scales, and waits for its
+// own loads only, never for another wave.
+//
+// Measured (graph of 30 calls, 16-bit results): N = 2048, K = 5504: 4.1 us for one
+// row, 6.9 for 37, 9.2 for 64; N = 11008, K = 2048: 6.1, 9.6 and 10.9 us (3.8 us
+// is the read of b at 6 TB/s); N = K = 8192: 11.8 us for one row (5.7 TB/s).
 // ---------------------------------------------------------------------------
-constexpr int kSkinnyM = 64;
+constexpr int kFewRows = 64;
 
-typedef int v4i32_t __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ uint4 buffer16(rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(uint4, (v4i32_t)__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-__device__ __forceinline__ float buffer4(rsrc_t r, uint32_t off) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-}
+template <int MT, int P>
+struct SlotLayout {
+  static constexpr int A_AT = 2048, SA_AT = A_AT + MT * 2048, SB_AT = SA_AT + 256, BYTES = SB_AT + 256;
+  static constexpr int NI = 2 + 2 * MT + 2;  // load instructions of a block
+  static_assert((P - 1) * NI < 64, "vmcnt range");
+};
 
-template <int MT, int NW, int SB, int OUT>
-__global__ __launch_bounds__(NW * 64) void fp8_skinny_kernel(Fp8Args g) {
-  constexpr int P = MT == 1 ? 4 : MT * NW >= 48 ? 1 : 2;  // within 128 registers for 16 waves
-  __shared__ f32x4 red[NW][MT][64];
+template <int MT, int NW, int P, int SB, int OUT>
+__global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(Fp8Args g) {
+  using S = SlotLayout<MT, P>;
+  constexpr int RED = NW * MT * 1024, RING = NW * P * S::BYTES;
+  __shared__ __attribute__((aligned(1024))) char lds_[RED > RING ? RED : RING];
   const int lane = threadIdx.x & 63, w = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
+  ESG_LDS char* const ring = (ESG_LDS char*)lds_ + w * P * S::BYTES;
   const int n0 = blockIdx.x * 16, nrows = min(16, g.N - n0);
-  const rsrc_t rb = make_rsrc(g.b + (size_t)n0 * g.K, (uint32_t)(nrows * g.K));
-  const rsrc_t ra = make_rsrc(g.a, (uint32_t)(g.M * g.K));
-  const rsrc_t rsa = make_rsrc(g.sa, (uint32_t)(g.M * g.KB * 4));
-  const rsrc_t rsb = SB == SB_TILES ? make_rsrc(g.sb + (size_t)(n0 / kQB) * g.KB, (uint32_t)(g.KB * 4))
-                                    : make_rsrc(g.sb + (size_t)n0 * g.KB, (uint32_t)(nrows * g.KB * 4));
-  struct Block {
-    uint4 b[2], a[MT][2];
-    float fa[MT], fb[SB == SB_TILES ? 1 : 4];
-  } q[P];
-  auto request = [&](int kb, Block& t) __attribute__((always_inline)) {
+  const int kb0 = blockIdx.y * g.kb_split, kb1 = min(g.KB, kb0 + g.kb_split);
+  const int m0 = blockIdx.z * kFewRows, mrows = min(kFewRows, g.M - m0);
+  const DmaSrc rb = make_dma_src(g.b + (size_t)n0 * g.K, (uint32_t)(nrows * g.K));
+  const DmaSrc ra = make_dma_src(g.a + (size_t)m0 * g.K, (uint32_t)(mrows * g.K));
+  const DmaSrc rsa = make_dma_src(g.sa + (size_t)m0 * g.KB, (uint32_t)(mrows * g.KB * 4));
+  const DmaSrc rsb = SB == SB_TILES ? make_dma_src(g.sb + (size_t)(n0 / kQB) * g.KB, (uint32_t)(g.KB * 4))
+                                    : make_dma_src(g.sb + (size_t)n0 * g.KB, (uint32_t)(nrows * g.KB * 4));
+  // rows of eight, 16-byte chunks in the K-row swizzle; offsets of K block 0
+  const int koff = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t ob[2], oa[2 * MT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = kb * kQB + h * 64 + lg * 16;
-      t.b[h] = buffer16(rb, k < g.K ? (uint32_t)(lr * g.K + k) : kOOB);
-    }
+  for (int i = 0; i < 2; ++i) {
+    const int r = i * 8 + (lane >> 3);
+    ob[i] = r < nrows ? (uint32_t)(r * g.K + koff) : kOOB;
+  }
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int m = j * 16 + lr;
+  for (int i = 0; i < 2 * MT; ++i) {
+    const int r = i * 8 + (lane >> 3);
+    oa[i] = r < mrows ? (uint32_t)(r * g.K + koff) : kOOB;
+  }
+  const uint32_t osa = lane < mrows ? (uint32_t)(lane * g.KB) * 4 : kOOB;
+  const uint32_t osb = SB == SB_TILES ? 0u : lane < nrows ? (uint32_t)(lane * g.KB) * 4 : kOOB;
+  // block kb into a slot; past the last block: zeros (so every block is the same number of loads).  kOOB plus an
+  // offset below 2^31 stays past every buffer.
+  auto request = [&](int kb, ESG_LDS char* slot) __attribute__((always_inline)) {
+    const int k0 = kb * kQB;
+    const bool in = kb < kb1 && k0 + koff < g.K;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = kb * kQB + h * 64 + lg * 16;
-        t.a[j][h] = buffer16(ra, k < g.K && m < g.M ? (uint32_t)(m * g.K + k) : kOOB);
-      }
-      t.fa[j] = buffer4(rsa, kb < g.KB && m < g.M ? (uint32_t)(m * g.KB + kb) * 4 : kOOB);
-    }
-    if constexpr (SB == SB_TILES) {
-      t.fb[0] = buffer4(rsb, kb < g.KB ? (uint32_t)kb * 4 : kOOB);
-    } else {
+    for (int i = 0; i < 2; ++i) dma16(rb, slot + i * 1024, in ? ob[i] + (uint32_t)k0 : kOOB);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        t.fb[e] = buffer4(rsb, kb < g.KB && lg * 4 + e < nrows ? (uint32_t)((lg * 4 + e) * g.KB + kb) * 4 : kOOB);
-    }
+    for (int i = 0; i < 2 * MT; ++i) dma16(ra, slot + S::A_AT + i * 1024, in ? oa[i] + (uint32_t)k0 : kOOB);
+    dma4(rsa, slot + S::SA_AT, kb < kb1 ? osa + (uint32_t)kb * 4 : kOOB);
+    dma4(rsb, slot + S::SB_AT, kb < kb1 ? osb + (uint32_t)kb * 4 : kOOB);
   };
   f32x4 acc[MT];
   zero_acc(acc);
 #pragma unroll
-  for (int u = 0; u < P; ++u) request(w + u * NW, q[u]);
-  for (int kb0 = w; kb0 < g.KB; kb0 += NW * P) {
+  for (int u = 0; u < P; ++u) request(kb0 + w + u * NW, ring + u * S::BYTES);
+  int at = 0;
+  for (int kb = kb0 + w; kb < kb1; kb += NW) {
+    ESG_LDS char* slot = ring + at * S::BYTES;
+    at = at + 1 == P ? 0 : at + 1;
+    wait_vmcnt<(P - 1) * S::NI>();
+    __builtin_amdgcn_sched_barrier(0);
+    const Frag<fine(OUT)> bn(frag_krow(slot, lr, lg), frag_krow(slot, lr, lg + 4));
+    const ESG_LDS float* fa = (const ESG_LDS float*)(slot + S::SA_AT);
+    const ESG_LDS float* fb = (const ESG_LDS float*)(slot + S::SB_AT);
+    f32x4 sn;
+    if constexpr (SB == SB_ROWS)
+      sn = *(const ESG_LDS f32x4*)(fb + lg * 4);
+    else
+      sn = f32x4{fb[0], fb[0], fb[0], fb[0]};
 #pragma unroll
-    for (int u = 0; u < P; ++u) {
-      const int kb = kb0 + u * NW;
-      if (kb < g.KB) {
-        const Frag<fine(OUT)> bn(q[u].b[0], q[u].b[1]);
+    for (int j = 0; j < MT; ++j) {
+      const ESG_LDS char* a = slot + S::A_AT;
+      const Frag<fine(OUT)> am(frag_krow(a, j * 16 + lr, lg), frag_krow(a, j * 16 + lr, lg + 4));
+      const f32x4 d = mma_block(bn, am);
+      const float f = fa[j * 16 + lr];
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const Frag<fine(OUT)> am(q[u].a[j][0], q[u].a[j][1]);
-          const f32x4 d = mma_block(bn, am);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[j][e] = fmaf(d[e], q[u].fa[j] * q[u].fb[SB == SB_TILES ? 0 : e], acc[j][e]);
-        }
-        if (kb + NW * P < g.KB) request(kb + NW * P, q[u]);
-      }
+      for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(d[e], f * sn[e], acc[j][e]);
     }
+    wait_lgkm0();  // the slot has been read
+    __builtin_amdgcn_sched_barrier(0);
+    request(kb + P * NW, slot);
   }
+  wait_vmcnt<0>();
+  __syncthreads();  // the slots become the sums of the waves
+  f32x4* red = (f32x4*)lds_;
 #pragma unroll
-  for (int j = 0; j < MT; ++j) red[w][j][lane] = acc[j];
+  for (int j = 0; j < MT; ++j) red[(w * MT + j) * 64 + lane] = acc[j];
   __syncthreads();
-  // output o: n = o % 16 of row m = o / 16; it sits in lane (n / 4) * 16 + m % 16, element n % 4
   const float* rf = (const float*)red;
-  for (int o = threadIdx.x; o < min(MT * 16, g.M) * 16; o += NW * 64) {
+  for (int o = threadIdx.x; o < mrows * 16; o += NW * 64) {
     const int n = o & 15, m = o >> 4;
-    const int at = ((m >> 4) * 64 + (n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
-    float s = rf[at];
+    const int at_o = ((m >> 4) * 64 + (n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+    float s = rf[at_o];
 #pragma unroll
-    for (int v = 1; v < NW; ++v) s += rf[v * MT * 256 + at];
+    for (int v = 1; v < NW; ++v) s += rf[v * MT * 256 + at_o];
     if (n < nrows) {
-      const size_t out = (size_t)m * g.N + n0 + n;
+      const size_t out = (size_t)(m0 + m) * g.N + n0 + n;
       if constexpr (OUT == OUT_BF16)
         store_elem<bf16_t>((bf16_t*)g.y + out, s);
-      else
+      else if constexpr (OUT == OUT_F32)
         ((float*)g.y)[out] = s;
+      else
+        g.part[(size_t)blockIdx.y * g.M * g.N + out] = s;
     }
   }
 }
 
-template <int MT, int SB, int OUT>
-hipError_t launch_skinny_m(const Fp8Args& g, hipStream_t stream) {
-  // Waves per workgroup: about four blocks of K each, more waves where the rows
-  // of b give few workgroups (2048 waves: eight per CU).  By shape alone.
-  const int tiles = (g.N + 15) / 16;
-  int nw = 4;
-  while (nw < 16 && nw < g.KB && (g.KB > 4 * nw || (long long)tiles * nw < 8 * kNominalCUs)) nw *= 2;
-  LaunchTimer timer("fp8_skinny", stream);
-  if (nw == 4)
-    hipLaunchKernelGGL((fp8_skinny_kernel<MT, 4, SB, OUT>), dim3(tiles), dim3(4 * 64), 0, stream, g);
-  else if (nw == 8)
-    hipLaunchKernelGGL((fp8_skinny_kernel<MT, 8, SB, OUT>), dim3(tiles), dim3(8 * 64), 0, stream, g);
-  else
-    hipLaunchKernelGGL((fp8_skinny_kernel<MT, 16, SB, OUT>), dim3(tiles), dim3(16 * 64), 0, stream, g);
+template <int MT, int NW, int P, int SB, int OUT>
+hipError_t launch_rows(const Fp8Args& g, hipStream_t stream) {
+  LaunchTimer timer("fp8_rows", stream);
+  hipLaunchKernelGGL((fp8_rows_kernel<MT, NW, P, SB, OUT>), dim3((g.N + 15) / 16, g.splits, g.nm),
+                     dim3(NW * 64), 0, stream, g);
   return hipGetLastError();
 }
 
+// Four waves where there is more than a workgroup for each CU, eight otherwise
+// (us, four against eight waves: one row of N = 2048, K = 5504 5.0 / 4.2, of
+// N = 11008, K = 2048 6.1 / 6.9; 37 rows: 7.7 / 6.8 and 9.4 / 9.6).  A slot per wave
+// where slots are large, or two workgroups of a CU would not fit (64 rows of
+// N = 11008: 10.9 us with one slot, 13.4 with two).
 template <int SB, int OUT>
-hipError_t launch_skinny(const Fp8Args& g, hipStream_t stream) {
-  if (g.M <= 16) return launch_skinny_m<1, SB, OUT>(g, stream);
-  if (g.M <= 32) return launch_skinny_m<2, SB, OUT>(g, stream);
-  return g.M <= 48 ? launch_skinny_m<3, SB, OUT>(g, stream) : launch_skinny_m<4, SB, OUT>(g, stream);
+hipError_t launch_few_rows(const Fp8Args& g, hipStream_t stream) {
+  if ((g.N + 15) / 16 * g.splits * g.nm > kNominalCUs) {
+    if (g.M > 48) return launch_rows<4, 4, 1, SB, OUT>(g, stream);
+    if (g.M > 32) return launch_rows<3, 4, 2, SB, OUT>(g, stream);
+    if (g.M > 16) return launch_rows<2, 4, 2, SB, OUT>(g, stream);
+    return launch_rows<1, 4, 2, SB, OUT>(g, stream);
+  }
+  if (g.M > 48) return launch_rows<4, 8, 1, SB, OUT>(g, stream);
+  if (g.M > 32) return launch_rows<3, 8, 1, SB, OUT>(g, stream);
+  if (g.M > 16) return launch_rows<2, 8, 2, SB, OUT>(g, stream);
+  return launch_rows<1, 8, 2, SB, OUT>(g, stream);
 }
 
 template <int BM, int BN, int SB, int OUT>
@@ -587,9 +615,9 @@ hipError_t launch_tiles(const Fp8Args& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Tile size and K splits by shape alone (so a shape rounds alike everywhere).
+// Kernel, tile size and K splits by shape alone (so a shape rounds alike everywhere).
 struct Plan {
-  bool skinny = false, big = false;
+  bool rows = false, big = false;
   int nm = 0, nn = 0, splits = 1, kb_split = 0;
 };
 
@@ -597,8 +625,23 @@ Plan plan(int M, int N, int K, bool f32_out = false) {
   Plan p;
   const int KB = (K + kQB - 1) / kQB;
   p.kb_split = KB;
-  if (M <= kSkinnyM) {
-    p.skinny = true;
+  auto split_k = [&](int s) {
+    s = std::min(std::max(s, 1), 16);
+    p.kb_split = (KB + s - 1) / s;
+    p.splits = (KB + p.kb_split - 1) / p.kb_split;
+  };
+  // The few-rows kernel, in chunks of 64 rows, while its workgroups are one round of the CUs, or two with a short K
+  // (us, few rows / 128 x 128 tiles: 128 rows of N = 2048, K = 5504 9.7 / 14.3; 512 rows of N = 512, K = 2048
+  // 5.1 / 11.5; 256 rows of N = K = 2048, two rounds, 7.1 / 12.2, of N = 2048, K = 16384 38 / 25).
+  const long long wgs = (long long)((N + 15) / 16) * ((M + kFewRows - 1) / kFewRows);
+  if (M <= kFewRows || wgs <= kNominalCUs || (wgs <= 2 * kNominalCUs && KB <= 32)) {
+    p.rows = true;
+    p.nm = (M + kFewRows - 1) / kFewRows;
+    // Few workgroups with much work in each: split K.  The second launch costs 2 us (N = 512, K = 16384, whole / split:
+    // one row 6.4 / 5.4 us, 64 rows 19.8 / 9.9; N = 512, K = 7168: 4.1 / 4.8 and 8.4 / 7.2).
+    const int work = KB * ((std::min(M, kFewRows) + 15) / 16);
+    if (wgs <= kNominalCUs / 2 && work >= (wgs <= kNominalCUs / 4 ? 128 : 256))
+      split_k(std::min({std::max(4, work / 64), std::max(4, kNominalCUs / (int)wgs), KB / 8}));
     return p;
   }
   const long long big = (long long)((M + 255) / 256) * ((N + 255) / 256);
@@ -610,11 +653,7 @@ Plan plan(int M, int N, int K, bool f32_out = false) {
   if (!p.big) {
     const long long tiles = (long long)p.nm * p.nn;
     // split K while the tiles leave slots idle (two workgroups per CU) and a split keeps eight blocks or more
-    int s = (int)std::max<long long>(1, 2 * kNominalCUs / std::max<long long>(1, tiles));
-    s = std::min(s, std::max(1, KB / 8));
-    s = std::min(s, 16);
-    p.kb_split = (KB + s - 1) / s;
-    p.splits = (KB + p.kb_split - 1) / p.kb_split;
+    split_k(std::min((int)(2 * kNominalCUs / std::max<long long>(1, tiles)), KB / 8));
   }
   return p;
 }
@@ -627,15 +666,20 @@ size_t fp8_matmul_workspace_bytes(int M, int N, int K) {
   return p.splits > 1 ? (size_t)p.splits * M * N * 4 : 0;
 }
 
+template <int SB, int OUT>
+static hipError_t launch_products(const Fp8Args& g, const Plan& p, hipStream_t stream) {
+  if (p.rows) return launch_few_rows<SB, OUT>(g, stream);
+  if constexpr (OUT == OUT_BF16)
+    if (p.big) return launch_tiles<256, 256, SB, OUT>(g, stream);
+  return launch_tiles<128, 128, SB, OUT>(g, stream);
+}
+
 template <int SB>
 static hipError_t run(Fp8Args& g, const Plan& p, int out_bf16, hipStream_t stream) {
-  if (p.skinny) return out_bf16 ? launch_skinny<SB, OUT_BF16>(g, stream) : launch_skinny<SB, OUT_F32>(g, stream);
-  if (p.big)
-    return launch_tiles<256, 256, SB, OUT_BF16>(g, stream);
   if (p.splits == 1)
-    return out_bf16 ? launch_tiles<128, 128, SB, OUT_BF16>(g, stream) : launch_tiles<128, 128, SB, OUT_F32>(g, stream);
-  const hipError_t e = out_bf16 ? launch_tiles<128, 128, SB, OUT_PART>(g, stream)
-                                : launch_tiles<128, 128, SB, OUT_PART_FINE>(g, stream);
+    return out_bf16 ? launch_products<SB, OUT_BF16>(g, p, stream) : launch_products<SB, OUT_F32>(g, p, stream);
+  const hipError_t e = out_bf16 ? launch_products<SB, OUT_PART>(g, p, stream)
+                                : launch_products<SB, OUT_PART_FINE>(g, p, stream);
   if (e != hipSuccess) return e;
   const size_t n = (size_t)g.M * g.N;
   const unsigned blocks = (unsigned)std::min<size_t>((n + 1023) / 1024, 2048);

@@ -124,6 +124,20 @@ def test_matmul(M, N, K, out, form):
     assert torch.equal(E.fp8_matmul(*a, *b, out_dtype=out).view(torch.uint8), y.view(torch.uint8))
 
 
+# chunks of 64 rows, one to many; K split over workgroups, into uneven parts and with a partial last block; the
+# smallest products that the tile kernel takes, ragged, with and without a split
+MATMUL_ROUTES = [(70, 16, 144), (130, 2050, 400), (448, 100, 5136), (1025, 33, 272), (4096, 16, 128), (3, 40, 16400),
+                 (64, 513, 4112), (48, 64, 30000), (127, 129, 12304), (70, 4111, 144), (2000, 300, 176),
+                 (300, 1700, 2064), (1100, 777, 4240)]
+
+
+@pytest.mark.parametrize("form", ["tiles", "rows"])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,N,K", MATMUL_ROUTES)
+def test_matmul_routes(M, N, K, out, form):
+    test_matmul(M, N, K, out, form)
+
+
 @pytest.mark.parametrize("form", ["tiles", "rows"])
 @pytest.mark.parametrize("out", [BF, F32])
 def test_matmul_large_tiles_sampled(out, form):

@@ -11,6 +11,7 @@
 // into the operand registers, and up to 16 tokens on its column side.  8-bit
 // weights are widened to bf16 (exactly) in registers; x stays bf16.
 #include <algorithm>
+#include <type_traits>
 
 #include "esg_fp8.hpp"
 #include "esg_internal.hpp"
@@ -24,6 +25,9 @@ enum { W_BF16 = 0, W_E4M3 = 1 };
 constexpr int kChunk = 128;  // K elements a wave takes at a time: one scale block
 constexpr int kMoeWaves = 8;
 constexpr int kMoeMaxGrid = 1024;  // workgroups of the experts' launch
+constexpr int kMaxSplits = 8;      // parts of the down items
+// 16-row tiles of a down unit: they share the loads of h, which go past the L2.
+__host__ __device__ constexpr int down_tiles(bool e4m3, bool many) { return e4m3 && many ? 2 : 1; }
 
 struct MoeArgs {
   const bf16_t* x;        // [T][d]
@@ -175,15 +179,19 @@ __global__ __launch_bounds__(kScoreWaves * 64) void moe_scores_kernel(MoeArgs g)
 // ---------------------------------------------------------------------------
 template <int EMAX, int TMAX>
 struct RouteLds {
-  unsigned long long mask[EMAX];         // tokens of each expert
-  float sel_s[TMAX][kRouteMaxK];
-  int sel_e[TMAX][kRouteMaxK];
   float prob[TMAX * kRouteMaxK];         // of each pair
-  uint16_t base[EMAX];                   // first pair of each expert with tokens
-  uint2 act[EMAX];                       // experts with tokens, ascending: expert | first pair << 16, pairs
+  uint32_t act[EMAX];                    // experts with tokens, ascending: expert | first pair << 10 | pairs << 21
   uint8_t tok[TMAX * kRouteMaxK];        // token of each pair
   int active;
 };
+template <int EMAX, int TMAX>
+struct RouteScratch {                    // during the routing only
+  unsigned long long mask[EMAX];         // tokens of each expert
+  float sel_s[TMAX][kRouteMaxK];
+  int sel_e[TMAX][kRouteMaxK];
+  uint16_t base[EMAX];                   // first pair of each expert with tokens
+};
+static_assert(kMoeMaxExperts <= 1 << 10 && 64 * kRouteMaxK <= 1 << 11, "fields of act");
 
 // One data-parallel move inside the vector unit: the value of another lane of
 // the wavefront (ctrl), zero where there is none.
@@ -202,10 +210,25 @@ __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v, Op op) {
   v = op(v, dpp_u32<0x143, 0xc>(v));
   return v;
 }
-// largest value of the wavefront, as a scalar
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  v = wave_scan_u32(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+// largest value of the wavefront, as a scalar, of each of N rows
+template <int N>
+__device__ __forceinline__ void wave_max_rows(uint32_t (&v)[N]) {
+  auto step = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t o = dpp_u32<decltype(ctrl)::value, decltype(rows)::value>(v[i]);
+      v[i] = o > v[i] ? o : v[i];
+    }
+  };
+  using std::integral_constant;
+  step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
+  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = (uint32_t)__builtin_amdgcn_readlane((int)v[i], 63);
 }
 // sums of the lanes up to each
 __device__ __forceinline__ int wave_prefix_sum(int v) {
@@ -220,65 +243,85 @@ __device__ __forceinline__ int wave_prefix_sum(int v) {
 // ascending expert; lane i keeps the i-th.  Outputs, in lane i < k: the expert
 // and score of the i-th in output order (keys above the k-th largest by
 // ascending expert, then the ones equal to it).
-template <int C>
-__device__ __forceinline__ void topk_row(const float (&sc)[C], const uint32_t (&key)[C], int k, int lane, int& expert,
-                                         float& score) {
-  uint32_t u[C];
-  int c_of[C];
+// RW rows at a time: their chains of dependent instructions fill each other's waits.
+template <int C, int RW>
+__device__ __forceinline__ void topk_rows(const float (&sc)[RW][C], const uint32_t (&key)[RW][C], int k, int lane,
+                                          int (&expert)[RW], float (&score)[RW]) {
+  uint32_t u[RW][C];
+  int c_of[RW][C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    u[c] = key[c];
-    c_of[c] = c;
-  }
+  for (int r = 0; r < RW; ++r) {
 #pragma unroll
-  for (int i = 1; i < C; ++i)  // insertion: equal keys keep their order
-#pragma unroll
-    for (int j = i; j > 0; --j) {
-      const bool up = u[j] > u[j - 1];
-      const uint32_t a = u[j - 1];
-      const int b = c_of[j - 1];
-      u[j - 1] = up ? u[j] : a;
-      u[j] = up ? a : u[j];
-      c_of[j - 1] = up ? c_of[j] : b;
-      c_of[j] = up ? b : c_of[j];
+    for (int c = 0; c < C; ++c) {
+      u[r][c] = key[r][c];
+      c_of[r][c] = c;
     }
-  int my_e = 0;
-  uint32_t my_key = 0, kth = 0;
+#pragma unroll
+    for (int i = 1; i < C; ++i)  // insertion: equal keys keep their order
+#pragma unroll
+      for (int j = i; j > 0; --j) {
+        const bool up = u[r][j] > u[r][j - 1];
+        const uint32_t a = u[r][j - 1];
+        const int b = c_of[r][j - 1];
+        u[r][j - 1] = up ? u[r][j] : a;
+        u[r][j] = up ? a : u[r][j];
+        c_of[r][j - 1] = up ? c_of[r][j] : b;
+        c_of[r][j] = up ? b : c_of[r][j];
+      }
+  }
+  int my_e[RW] = {};
+  uint32_t my_key[RW] = {}, kth[RW] = {};
   for (int i = 0; i < k; ++i) {
-    kth = wave_max_u32(u[0]);
-    const int from = __ffsll((unsigned long long)__ballot(u[0] == kth)) - 1;
-    const int e = from * C + __builtin_amdgcn_readlane(c_of[0], from);
-    my_e = lane == i ? e : my_e;
-    my_key = lane == i ? kth : my_key;
-    const bool pop = lane == from;
+    uint32_t best[RW];
 #pragma unroll
-    for (int c = 0; c + 1 < C; ++c) {
-      u[c] = pop ? u[c + 1] : u[c];
-      c_of[c] = pop ? c_of[c + 1] : c_of[c];
+    for (int r = 0; r < RW; ++r) best[r] = u[r][0];
+    wave_max_rows(best);
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      kth[r] = best[r];
+      const int from = __ffsll((unsigned long long)__ballot(u[r][0] == kth[r])) - 1;
+      const int e = from * C + __builtin_amdgcn_readlane(c_of[r][0], from);
+      my_e[r] = lane == i ? e : my_e[r];
+      my_key[r] = lane == i ? kth[r] : my_key[r];
+      const bool pop = lane == from;
+#pragma unroll
+      for (int c = 0; c + 1 < C; ++c) {
+        u[r][c] = pop ? u[r][c + 1] : u[r][c];
+        c_of[r][c] = pop ? c_of[r][c + 1] : c_of[r][c];
+      }
+      u[r][C - 1] = pop ? 0u : u[r][C - 1];  // candidates' keys are at least 1
     }
-    u[C - 1] = pop ? 0u : u[C - 1];  // candidates' keys are at least 1
   }
-  float my_s = 0.f;
+  int id[RW], slot[RW] = {};
+  float my_s[RW] = {};
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const float v = __shfl(sc[c], my_e / C);
-    my_s = my_e % C == c ? v : my_s;
+  for (int r = 0; r < RW; ++r) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float v = __shfl(sc[r][c], my_e[r] / C);
+      my_s[r] = my_e[r] % C == c ? v : my_s[r];
+    }
+    // output order: rank of (equal to the k-th, expert) among the k picks
+    id[r] = (my_key[r] == kth[r] ? 1 << 16 : 0) | my_e[r];
   }
-  // output order: rank of (equal to the k-th, expert) among the k picks
-  const int id = (my_key == kth ? 1 << 16 : 0) | my_e;
-  int slot = 0;
-  for (int i = 0; i < k; ++i) slot += __builtin_amdgcn_readlane(id, i) < id ? 1 : 0;
-  const int to = lane < k ? slot : lane;
-  expert = __builtin_amdgcn_ds_permute(to * 4, my_e);
-  score = __uint_as_float((uint32_t)__builtin_amdgcn_ds_permute(to * 4, (int)__float_as_uint(my_s)));
+  for (int i = 0; i < k; ++i)
+#pragma unroll
+    for (int r = 0; r < RW; ++r) slot[r] += __builtin_amdgcn_readlane(id[r], i) < id[r] ? 1 : 0;
+#pragma unroll
+  for (int r = 0; r < RW; ++r) {
+    const int to = (lane < k ? slot[r] : lane) * 4;
+    expert[r] = __builtin_amdgcn_ds_permute(to, my_e[r]);
+    score[r] = __uint_as_float((uint32_t)__builtin_amdgcn_ds_permute(to, (int)__float_as_uint(my_s[r])));
+  }
 }
 
 // Selection and weights of every token; probabilities and token sets into LDS.
 template <int C, int EMAX, int TMAX>
-__device__ __forceinline__ void select_tokens(const MoeArgs& g, RouteLds<EMAX, TMAX>& R, bool write) {
+__device__ __forceinline__ void select_tokens(const MoeArgs& g, RouteScratch<EMAX, TMAX>& S, bool write) {
 #pragma clang fp contract(off)
+  constexpr int RW = TMAX == 16 || C > 4 ? 1 : C > 1 ? 2 : 4;  // tokens of a wave at a time (registers)
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  float bias[C], nxt[C];
+  float bias[C], nxt[RW][C];
   bool valid[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -286,36 +329,48 @@ __device__ __forceinline__ void select_tokens(const MoeArgs& g, RouteLds<EMAX, T
     valid[c] = e < g.E;
     bias[c] = valid[c] ? g.bias[(size_t)e * g.bias_stride] : 0.f;
   }
-  auto load = [&](int t) __attribute__((always_inline)) {
+  auto load = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) nxt[c] = valid[c] && t < g.T ? g.scores[(size_t)t * g.E + lane * C + c] : 0.f;
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int t = t0 + r * kMoeWaves;
+        nxt[r][c] = valid[c] && t < g.T ? g.scores[(size_t)t * g.E + lane * C + c] : 0.f;
+      }
   };
   load(w);
-  for (int t = w; t < g.T; t += kMoeWaves) {
-    float sc[C];
-    uint32_t key[C];
+  for (int t0 = w; t0 < g.T; t0 += RW * kMoeWaves) {
+    float sc[RW][C];
+    uint32_t key[RW][C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      sc[c] = nxt[c];
-      const uint32_t o = order_key(sc[c] + bias[c]);
-      key[c] = valid[c] ? (o > 1u ? o : 1u) : 0u;
-    }
-    load(t + kMoeWaves);
-    int e;
-    float s;
-    topk_row<C>(sc, key, g.k, lane, e, s);
-    float total = 0.0f;
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        sc[r][c] = nxt[r][c];
+        const uint32_t o = order_key(sc[r][c] + bias[c]);
+        key[r][c] = valid[c] ? (o > 1u ? o : 1u) : 0u;
+      }
+    load(t0 + RW * kMoeWaves);
+    int e[RW];
+    float s[RW], total[RW] = {};
+    topk_rows<C, RW>(sc, key, g.k, lane, e, s);
     for (int i = 0; i < g.k; ++i)
-      total = total + __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s), i));
-    if (lane < g.k) {
-      float p = s / (total + 1e-20f);
-      if (g.apply_scaling) p = p * g.scaling;
-      R.sel_s[t][lane] = p;
-      R.sel_e[t][lane] = e;
-      atomicOr(&R.mask[e], 1ull << t);
-      if (write) {
-        g.probs[(size_t)t * g.k + lane] = p;
-        g.indices[(size_t)t * g.k + lane] = e;
+#pragma unroll
+      for (int r = 0; r < RW; ++r)
+        total[r] = total[r] + __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s[r]), i));
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const int t = t0 + r * kMoeWaves;
+      if (lane < g.k && t < g.T) {
+        float p = s[r] / (total[r] + 1e-20f);
+        if (g.apply_scaling) p = p * g.scaling;
+        S.sel_s[t][lane] = p;
+        S.sel_e[t][lane] = e[r];
+        atomicOr(&S.mask[e[r]], 1ull << t);
+        if (write) {
+          g.probs[(size_t)t * g.k + lane] = p;
+          g.indices[(size_t)t * g.k + lane] = e[r];
+        }
       }
     }
   }
@@ -326,35 +381,35 @@ struct Active {
 };
 template <int EMAX, int TMAX>
 __device__ __forceinline__ Active active(const RouteLds<EMAX, TMAX>& R, int a) {
-  const uint2 v = R.act[a];
-  const uint32_t x = (uint32_t)__builtin_amdgcn_readfirstlane((int)v.x);
-  return {(int)(x & 0xffffu), (int)(x >> 16), __builtin_amdgcn_readfirstlane((int)v.y)};
+  const uint32_t v = (uint32_t)__builtin_amdgcn_readfirstlane((int)R.act[a]);
+  return {(int)(v & 0x3ffu), (int)(v >> 10 & 0x7ffu), (int)(v >> 21)};
 }
 
 template <int EMAX, int TMAX>
-__device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>& R, bool write) {
+__device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>& R,
+                                           RouteScratch<EMAX, TMAX>& S, bool write) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < EMAX; e += kMoeWaves * 64) R.mask[e] = 0;
+  for (int e = threadIdx.x; e < EMAX; e += kMoeWaves * 64) S.mask[e] = 0;
   __syncthreads();
   if (EMAX > 256)
-    select_tokens<EMAX / 64>(g, R, write);
+    select_tokens<EMAX / 64>(g, S, write);
   else if (g.E <= 64)
-    select_tokens<1>(g, R, write);
+    select_tokens<1>(g, S, write);
   else
-    select_tokens<4>(g, R, write);
+    select_tokens<4>(g, S, write);
   __syncthreads();
   if (w == 0) {  // experts with tokens, ascending, and the first pair of each: 64 experts at a time
     int n = 0, pos = 0;
 #pragma unroll
     for (int c = 0; c < EMAX / 64; ++c) {
       const int e = c * 64 + lane;
-      const int cnt = __popcll(R.mask[e]);
+      const int cnt = __popcll(S.mask[e]);
       const uint64_t on = __ballot(cnt > 0);
       const int incl = wave_prefix_sum(cnt);
       if (cnt > 0) {
-        R.base[e] = (uint16_t)(pos + incl - cnt);
+        S.base[e] = (uint16_t)(pos + incl - cnt);
         R.act[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(on >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)on, 0))] =
-            make_uint2((uint32_t)e | (uint32_t)(pos + incl - cnt) << 16, (uint32_t)cnt);
+            (uint32_t)e | (uint32_t)(pos + incl - cnt) << 10 | (uint32_t)cnt << 21;
       }
       n += __popcll(on);
       pos += __builtin_amdgcn_readlane(incl, 63);
@@ -364,9 +419,9 @@ __device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>
   __syncthreads();
   for (int t = w; t < g.T; t += kMoeWaves) {
     if (lane < g.k) {
-      const int e = R.sel_e[t][lane];
-      const int pos = R.base[e] + __popcll(R.mask[e] & ((1ull << t) - 1ull));
-      R.prob[pos] = R.sel_s[t][lane];
+      const int e = S.sel_e[t][lane];
+      const int pos = S.base[e] + __popcll(S.mask[e] & ((1ull << t) - 1ull));
+      R.prob[pos] = S.sel_s[t][lane];
       R.tok[pos] = (uint8_t)t;
     }
   }
@@ -399,11 +454,12 @@ __device__ __forceinline__ void route_all(const MoeArgs& g, RouteLds<EMAX, TMAX>
 // ---------------------------------------------------------------------------
 template <int WT, int MT, int EMAX>
 __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs g) {
-  constexpr int TMAX = MT * 16;
+  constexpr int TMAX = MT * 16, DT = down_tiles(WT == W_E4M3, MT > 1), DN = DT * 16;
   __shared__ RouteLds<EMAX, TMAX> R;
   __shared__ union {
+    RouteScratch<EMAX, TMAX> route;
     f32x4 red[2][kMoeWaves][2][64];      // gate/up: sums of the waves
-    f32x4 sums[kMoeWaves][TMAX][4];      // down: [token][16] sums, by wave
+    f32x4 sums[kMoeWaves][TMAX][DT * 4];  // down: [token][DN] sums, by wave
   } L;
   __shared__ int shared_int;
   __shared__ int ticket[2];
@@ -414,11 +470,11 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
     return __hip_atomic_fetch_add(g.tickets + team, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
   if (threadIdx.x == 0) ticket[0] = take();
-  route_all<EMAX, TMAX>(g, R, blockIdx.x == 0);
+  route_all<EMAX, TMAX>(g, R, L.route, blockIdx.x == 0);
   int ahead = 0;  // thread 0: the ticket after the next
   if (threadIdx.x == 0) ahead = take();
 
-  const int nt = g.ff / 16, dtiles = g.d / 16, grid = gridDim.x;
+  const int nt = g.ff / 16, dtiles = (g.d + DN - 1) / DN, grid = gridDim.x;
   const int gu_units = R.active * nt, d_units = dtiles * g.splits;
   const int kb = (g.d + kChunk - 1) / kChunk, fb = (g.ff + kQB - 1) / kQB;
   const size_t plane = (size_t)g.T * g.k * g.ff;
@@ -429,10 +485,10 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
   // takes a run of them.  P are on their way or in use, each with its weights and
   // its columns: h of up to 8 pairs, the upper bf16 values in columns 0..7 and the
   // rest in columns 8..15 (one product for both; their sums are added below). ----
-  constexpr int P = WT == W_BF16 ? 2 : 3;
+  constexpr int P = WT == W_BF16 || DT > 1 ? 2 : 3;
   const int items = R.active * fb;
   struct Item {
-    Rows16<WT> w;
+    Rows16<WT> w[DT];
     Cols16<WT, kDevice> h;
     float scale;
     int cnt, base, kc, tok;  // tok: of this lane's column (-1: none)
@@ -445,7 +501,9 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
     t.cnt = on ? at.cnt : 0;
     t.base = at.base;
     t.kc = at_kc;
-    t.w.load(rows_rsrc<WT>(g.wd, (size_t)at.e * g.d + d0, g.ff), lr, on ? at_kc * kChunk : g.ff, g.ff, lg);
+    const rsrc_t rw = rows_rsrc<WT>(g.wd, (size_t)at.e * g.d + d0, g.ff, min(DN, g.d - d0));
+#pragma unroll
+    for (int v = 0; v < DT; ++v) t.w[v].load(rw, v * 16 + lr, on ? at_kc * kChunk : g.ff, g.ff, lg);
     t.scale = WT != W_BF16 ? g.sd[((size_t)at.e * kb + d0 / kQB) * fb + at_kc] : 1.f;
     if (++at_kc == fb) {
       at_kc = 0;
@@ -462,7 +520,7 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
   };
   auto begin_down = [&](int unit) __attribute__((always_inline)) {
     const int part = unit / dtiles;
-    d0 = (unit - part * dtiles) * 16;
+    d0 = (unit - part * dtiles) * DN;
     lo = (int)((long long)items * (part * kMoeWaves + w) / (g.splits * kMoeWaves));
     hi = (int)((long long)items * (part * kMoeWaves + w + 1) / (g.splits * kMoeWaves));
     at_a = min(lo / fb, R.active - 1);
@@ -609,20 +667,23 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
   for (int unit = blockIdx.x; unit < d_units; unit += grid) {
     if (unit != (int)blockIdx.x) begin_down(unit);
     const int part = unit / dtiles, dt = unit - part * dtiles;
-    for (int i = lane; i < g.T * 4; i += 64) L.sums[w][i >> 2][i & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = lane; i < g.T * DT * 4; i += 64) ((f32x4*)L.sums[w])[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto add = [&](const Item& t) __attribute__((always_inline)) {
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < 4; ++s) mma_bf16(v, t.w.frag(s), t.h.v[s]);
+      for (int c = 0; c < DT; ++c) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int r = 0; r < 4; ++r)  // columns c and c + 8
-        v[r] += __uint_as_float(dpp_u32<0x128, 0xf>(__float_as_uint(v[r])));
-      if (t.tok >= 0 && lr < 8) {
-        f32x4& sum = L.sums[w][t.tok][lg];
-        f32x4 y = sum;
+        for (int s = 0; s < 4; ++s) mma_bf16(v, t.w[c].frag(s), t.h.v[s]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) y[r] = fmaf(v[r], t.scale, y[r]);
-        sum = y;
+        for (int r = 0; r < 4; ++r)  // columns c and c + 8
+          v[r] += __uint_as_float(dpp_u32<0x128, 0xf>(__float_as_uint(v[r])));
+        if (t.tok >= 0 && lr < 8) {
+          f32x4& sum = L.sums[w][t.tok][c * 4 + lg];
+          f32x4 y = sum;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y[r] = fmaf(v[r], t.scale, y[r]);
+          sum = y;
+        }
       }
     };
 #pragma unroll
@@ -643,32 +704,42 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
       }
     }
     __syncthreads();
-    const float* sf = (const float*)L.sums;
+    // four columns of a token at a time
+    const int quads = g.T * (DN / 4);
     auto sum = [&](int o) __attribute__((always_inline)) {
-      float v = sf[o];
+      f32x4 v = (&L.sums[0][0][0])[o];
 #pragma unroll
-      for (int r = 1; r < kMoeWaves; ++r) v += sf[r * TMAX * 16 + o];
+      for (int r = 1; r < kMoeWaves; ++r) v += (&L.sums[r][0][0])[o];
       return v;
     };
+    auto store = [&](int o, const f32x4& v) __attribute__((always_inline)) {
+      const int t = o / (DN / 4), n = d0 + o % (DN / 4) * 4;
+      const float out[4] = {v[0], v[1], v[2], v[3]};
+      if (n < g.d) Quad<bf16_t>::store(g.y + (size_t)t * g.d + n, out);
+    };
     if (g.splits == 1) {
-      for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64)
-        store_elem<bf16_t>(g.y + (size_t)(o >> 4) * g.d + d0 + (o & 15), sum(o));
+      for (int o = threadIdx.x; o < quads; o += kMoeWaves * 64) store(o, sum(o));
     } else {
-      float* parts = g.part + (size_t)dt * g.T * 16;
-      const size_t pstride = (size_t)dtiles * g.T * 16;
-      for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64)
-        __hip_atomic_store(&parts[part * pstride + o], sum(o), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const uint32_t tile = quads * 16, pstride = dtiles * tile;  // bytes
+      const rsrc_t rp = make_rsrc((const char*)g.part + (size_t)dt * tile, (g.splits - 1) * pstride + tile);
+      for (int o = threadIdx.x; o < quads; o += kMoeWaves * 64)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i32, sum(o)), rp, part * pstride + o * 16, 0,
+                                               kDevice);
+      wait_vmcnt<0>();
       __syncthreads();  // every wave's stores are done
       if (threadIdx.x == 0)
         shared_int =
             __hip_atomic_fetch_add(g.arrived + dt, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == g.splits - 1;
       __syncthreads();
       if (shared_int) {
-        for (int o = threadIdx.x; o < g.T * 16; o += kMoeWaves * 64) {
-          float v = 0.f;
-          for (int r = 0; r < g.splits; ++r)
-            v += __hip_atomic_load(&parts[r * pstride + o], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          store_elem<bf16_t>(g.y + (size_t)(o >> 4) * g.d + d0 + (o & 15), v);
+        for (int o = threadIdx.x; o < quads; o += kMoeWaves * 64) {
+          f32x4 v[kMaxSplits];
+#pragma unroll
+          for (int r = 0; r < kMaxSplits; ++r)  // all on their way together; past the last part: zeros
+            v[r] = __builtin_bit_cast(f32x4, load16<kDevice>(rp, r < g.splits ? r * pstride + o * 16 : kOOB));
+#pragma unroll
+          for (int r = 1; r < kMaxSplits; ++r) v[0] += v[r];
+          store(o, v[0]);
         }
       }
     }
@@ -680,9 +751,8 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Parts of the down items: the d/16 tiles of y alone would leave workgroup slots
 // (two per CU) empty.  By shape alone, so a shape rounds alike everywhere.
-constexpr int kMaxSplits = 8;
-int down_splits(int d_model, int topk, int d_ff) {
-  const int tiles = d_model / 16;
+int down_splits(int d_model, int topk, int d_ff, int dt) {
+  const int tiles = (d_model + dt * 16 - 1) / (dt * 16);
   const int items = topk * ((d_ff + kChunk - 1) / kChunk);  // of one token: at least this many
   int s = std::max(1, 2 * kNominalCUs / tiles);
   s = std::min(s, std::max(1, items / kMoeWaves));
@@ -691,20 +761,26 @@ int down_splits(int d_model, int topk, int d_ff) {
 
 struct MoeLayout {
   size_t scores = 0, h = 0, part = 0, flags = 0, bytes = 0;
-  int splits = 1;
 };
 MoeLayout layout(int tokens, int experts, int topk, int d_model, int d_ff) {
   MoeLayout L;
-  L.splits = down_splits(d_model, topk, d_ff);
+  // the parts of y, with either type of weights
+  size_t part = 0;
+  for (const int dt : {down_tiles(false, tokens > 16), down_tiles(true, tokens > 16)}) {
+    const int splits = down_splits(d_model, topk, d_ff, dt);
+    if (splits > 1) part = std::max(part, (size_t)splits * tokens * ((d_model + dt * 16 - 1) / (dt * 16) * dt * 16) * 4);
+  }
   L.h = align256((size_t)tokens * experts * 4);
   L.part = L.h + align256((size_t)tokens * topk * d_ff * 4);
-  L.flags = L.part + (L.splits > 1 ? align256((size_t)L.splits * tokens * d_model * 4) : 0);
+  L.flags = L.part + align256(part);
   L.bytes = L.flags + align256((size_t)(2 * kMoeMaxGrid + d_model / 16) * 4);
   return L;
 }
 
 template <int WT, int MT, int EMAX>
 hipError_t launch_t(MoeArgs g, hipStream_t stream) {
+  constexpr int DT = down_tiles(WT == W_E4M3, MT > 1);
+  g.splits = down_splits(g.d, g.k, g.ff, DT);
   {
     LaunchTimer timer("moe_scores", stream);
     hipLaunchKernelGGL(moe_scores_kernel, dim3((g.E + 15) / 16, (g.T + 15) / 16), dim3(kScoreWaves * 64), 0, stream,
@@ -712,7 +788,7 @@ hipError_t launch_t(MoeArgs g, hipStream_t stream) {
   }
   // two workgroups per CU; more than there can be units of either kind would find none
   const int slots = std::min(2 * compute_units(), kMoeMaxGrid);
-  const long long most = std::max<long long>((long long)std::min(g.E, g.T * g.k) * (g.ff / 16), g.d / 16 * g.splits);
+  const long long most = std::max<long long>((long long)std::min(g.E, g.T * g.k) * (g.ff / 16), (g.d + DT * 16 - 1) / (DT * 16) * g.splits);
   const int grid = (int)std::min<long long>(most, slots);
   g.teams = std::min(grid, slots / 2);
   LaunchTimer timer("moe_experts", stream);
@@ -755,7 +831,6 @@ hipError_t launch_moe_decode(const MoeCall& c, void* workspace, hipStream_t stre
   g.tickets = g.flags + kMoeMaxGrid;
   g.arrived = g.tickets + kMoeMaxGrid;
   g.patience = c.patience;
-  g.splits = L.splits;
   g.y = (bf16_t*)c.y;
   g.probs = c.probs;
   g.indices = c.indices;

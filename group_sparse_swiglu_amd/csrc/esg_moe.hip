@@ -749,14 +749,18 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Parts of the down items: the d/16 tiles of y alone would leave workgroup slots
-// (two per CU) empty.  By shape alone, so a shape rounds alike everywhere.
-int down_splits(int d_model, int topk, int d_ff, int dt) {
+// Parts of the down items: the tiles of y alone would leave workgroup slots (two
+// per CU) empty.  A part is worth its adding (2 to 4 us) where each wave has an
+// item, counted as one token's experts, or four, counted as every expert that
+// the tokens can choose (us, without / with the second: 32 tokens, 8 of 256
+// experts, d = 1024, d_ff = 512, 8-bit, 88.6 / 80.3; with one item in place of four,
+// 4 tokens, 11 of 43 experts, d = 2048, d_ff = 128, 26.5 / 30.8).  By shape alone, so a
+// shape rounds alike everywhere.
+int down_splits(int tokens, int experts, int topk, int d_model, int d_ff, int dt) {
   const int tiles = (d_model + dt * 16 - 1) / (dt * 16);
-  const int items = topk * ((d_ff + kChunk - 1) / kChunk);  // of one token: at least this many
-  int s = std::max(1, 2 * kNominalCUs / tiles);
-  s = std::min(s, std::max(1, items / kMoeWaves));
-  return std::min(s, kMaxSplits);
+  const int chunks = (d_ff + kChunk - 1) / kChunk, all = std::min(experts, tokens * topk);
+  const int worth = std::max(topk * chunks / kMoeWaves, all * chunks / (4 * kMoeWaves));
+  return std::max(1, std::min({2 * kNominalCUs / tiles, worth, kMaxSplits}));
 }
 
 struct MoeLayout {
@@ -767,7 +771,7 @@ MoeLayout layout(int tokens, int experts, int topk, int d_model, int d_ff) {
   // the parts of y, with either type of weights
   size_t part = 0;
   for (const int dt : {down_tiles(false, tokens > 16), down_tiles(true, tokens > 16)}) {
-    const int splits = down_splits(d_model, topk, d_ff, dt);
+    const int splits = down_splits(tokens, experts, topk, d_model, d_ff, dt);
     if (splits > 1) part = std::max(part, (size_t)splits * tokens * ((d_model + dt * 16 - 1) / (dt * 16) * dt * 16) * 4);
   }
   L.h = align256((size_t)tokens * experts * 4);
@@ -780,7 +784,7 @@ MoeLayout layout(int tokens, int experts, int topk, int d_model, int d_ff) {
 template <int WT, int MT, int EMAX>
 hipError_t launch_t(MoeArgs g, hipStream_t stream) {
   constexpr int DT = down_tiles(WT == W_E4M3, MT > 1);
-  g.splits = down_splits(g.d, g.k, g.ff, DT);
+  g.splits = down_splits(g.T, g.E, g.k, g.d, g.ff, DT);
   {
     LaunchTimer timer("moe_scores", stream);
     hipLaunchKernelGGL(moe_scores_kernel, dim3((g.E + 15) / 16, (g.T + 15) / 16), dim3(kScoreWaves * 64), 0, stream,

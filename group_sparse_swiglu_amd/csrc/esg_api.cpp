@@ -523,7 +523,7 @@ namespace {
 int fp8_shape(int M, int N, int K) {
   if (M < 0 || N < 0 || K <= 0) return ESG_ERR_INVALID_ARG;
   if (K % 16 || K > (1 << 22) || M > (1 << 30) || N > (1 << 25)) return ESG_ERR_UNSUPPORTED;
-  // a launch's threads within 2^32: 512 per output tile of 128 x 128 at most, 1024 per 16 rows of b for few rows
+  // a launch's threads within 2^32: 512 per output tile of 128 x 128 at most, 512 per 16 rows of b for few rows
   return (double)((M + 127) / 128) * ((N + 127) / 128) < 8388608.0 ? ESG_OK : ESG_ERR_UNSUPPORTED;
 }
 }  // namespace

@@ -10,6 +10,13 @@
 // bf16 one with 16 weight rows on its row side, loaded straight from memory
 // into the operand registers, and up to 16 tokens on its column side.  8-bit
 // weights are widened to bf16 (exactly) in registers; x stays bf16.
+//
+// Two launches: the scores, and everything else.  Measured (both, bytes of the
+// chosen experts' weights over the whole time): one token, 8 of 256 experts, d =
+// 2048, d_ff = 1024, bf16: 37.5 us, 2.7 TB/s; five tokens, d_ff = 1008, 8-bit: 70 us,
+// 3.4 TB/s; 64 tokens, 6 of 64 experts, d_ff = 1408, 8-bit: 155 us, 3.6 TB/s.  The gate
+// and up products themselves read at 5.2 TB/s; the rest is the way between the
+// parts: scores 5 us, start and routing 4 to 12, waiting for the last h 3 to 10.
 #include <algorithm>
 #include <type_traits>
 
@@ -26,7 +33,9 @@ constexpr int kChunk = 128;  // K elements a wave takes at a time: one scale blo
 constexpr int kMoeWaves = 8;
 constexpr int kMoeMaxGrid = 1024;  // workgroups of the experts' launch
 constexpr int kMaxSplits = 8;      // parts of the down items
-// 16-row tiles of a down unit: they share the loads of h, which go past the L2.
+// 16-row tiles of a down unit: they share the loads of h, which go past the L2 (64 tokens, 6 of 64 experts, d = 2048,
+// d_ff = 1408, 8-bit: down part 62 us with one tile, 44 with two).  One where h is small beside the weights (up to 16
+// tokens), and with 16-bit weights, where two tiles in flight do not fit the registers.
 __host__ __device__ constexpr int down_tiles(bool e4m3, bool many) { return e4m3 && many ? 2 : 1; }
 
 struct MoeArgs {
@@ -139,7 +148,8 @@ __device__ __forceinline__ void mma_chunk128(f32x4& acc, const Rows16<WT>& a, co
 
 // ---------------------------------------------------------------------------
 // Scores: 16 experts and 16 tokens per workgroup; the waves split d.  Also clears
-// the counters of the launch that follows.
+// the counters of the launch that follows.  Bound by latency: 5.3 us for one token
+// and 256 experts (1 MB), 6.3 for 64 tokens and 64 experts.
 // ---------------------------------------------------------------------------
 constexpr int kScoreWaves = 16;
 

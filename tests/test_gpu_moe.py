@@ -83,6 +83,16 @@ def test_layer_matches_oracle(T, Ex, k, d, ff, weights):
     assert all(torch.equal(a, c) for a, c in zip(again, got))
 
 
+# more than 16 tokens with an odd number of 16-column tiles of y, more experts than 256, parts of y by either count
+MANY = [(20, 12, 3, 272, 144), (64, 40, 6, 784, 400), (33, 300, 4, 48, 272), (17, 1, 1, 16, 16), (64, 64, 6, 1040, 272)]
+
+
+@pytest.mark.parametrize("weights", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,Ex,k,d,ff", MANY)
+def test_many_tokens(T, Ex, k, d, ff, weights):
+    test_layer_matches_oracle(T, Ex, k, d, ff, weights)
+
+
 @pytest.mark.parametrize("weights", ["bf16", "fp8"])
 def test_wide_layer(weights):
     require_gpu()

@@ -626,12 +626,19 @@ int esg_fp8_linear_fwd(const void* x, int x_dtype, const void* w, int w_dtype, i
     return ESG_ERR_WORKSPACE;
   if (!aligned16(scratch) || !aligned16(saved)) return ESG_ERR_INVALID_ARG;
   hipStream_t st = (hipStream_t)stream;
-  hipError_t h = launch_quant_tiles(w_dtype, w, 1, d_out, d_in, at<char>(scratch, L.wq), at<float>(scratch, L.ws),
-                                    need_dx ? at<char>(saved, L.wqt) : nullptr,
-                                    need_dx ? at<float>(saved, L.wst) : nullptr, st);
-  if (h != hipSuccess || tokens == 0) return hip_status(h);
-  h = launch_quant_rows(x_dtype, x, tokens, d_in, at<char>(scratch, L.xq), at<float>(scratch, L.xs),
-                        need_dw ? at<char>(saved, L.xqt) : nullptr, need_dw ? at<float>(saved, L.xst) : nullptr, st);
+  void* const wqt = need_dx ? at<char>(saved, L.wqt) : nullptr;
+  float* const wst = need_dx ? at<float>(saved, L.wst) : nullptr;
+  hipError_t h;
+  if (need_dw && tokens > 0) {
+    h = launch_quant_pair(w_dtype, w, d_out, at<char>(scratch, L.wq), at<float>(scratch, L.ws), wqt, wst, x_dtype, x,
+                          tokens, at<char>(scratch, L.xq), at<float>(scratch, L.xs), at<char>(saved, L.xqt),
+                          at<float>(saved, L.xst), d_in, st);
+  } else {
+    h = launch_quant_tiles(w_dtype, w, 1, d_out, d_in, at<char>(scratch, L.wq), at<float>(scratch, L.ws), wqt, wst, st);
+    if (h != hipSuccess || tokens == 0) return hip_status(h);
+    h = launch_quant_rows(x_dtype, x, tokens, d_in, at<char>(scratch, L.xq), at<float>(scratch, L.xs), nullptr, nullptr,
+                          st);
+  }
   if (h == hipSuccess)
     h = launch_fp8_matmul(at<char>(scratch, L.xq), at<float>(scratch, L.xs), at<char>(scratch, L.wq),
                           at<float>(scratch, L.ws), 0, x_dtype, tokens, d_out, d_in, y, at<char>(scratch, L.fmm), st);

@@ -186,6 +186,10 @@ hipError_t launch_quant_rows(int dtype, const void* x, int rows, int cols, void*
                              float* scale_t, hipStream_t stream);
 hipError_t launch_quant_tiles(int dtype, const void* w, int batch, int rows, int cols, void* q, float* scale, void* qt,
                               float* scale_t, hipStream_t stream);
+// launch_quant_tiles of one w and launch_quant_rows of x in both directions (xqt not null), of equal columns
+hipError_t launch_quant_pair(int w_dtype, const void* w, int w_rows, void* wq, float* w_scale, void* wqt,
+                             float* w_scale_t, int x_dtype, const void* x, int x_rows, void* xq, float* x_scale,
+                             void* xqt, float* x_scale_t, int cols, hipStream_t stream);
 size_t fp8_matmul_workspace_bytes(int M, int N, int K);
 hipError_t launch_fp8_matmul(const void* a, const float* sa, const void* b, const float* sb, int sb_rows, int out_dtype,
                              int M, int N, int K, void* y, void* workspace, hipStream_t stream);

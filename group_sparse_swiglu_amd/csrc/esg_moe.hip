@@ -147,20 +147,22 @@ __device__ __forceinline__ void mma_chunk128(f32x4& acc, const Rows16<WT>& a, co
 }
 
 // ---------------------------------------------------------------------------
-// Scores: 16 experts and 16 tokens per workgroup; the waves split d.  Also clears
-// the counters of the launch that follows.  Bound by latency: 5.3 us for one token
-// and 256 experts (1 MB), 6.3 for 64 tokens and 64 experts.
+// Scores: 4 experts and 16 tokens per workgroup (the other rows of the products
+// are zeros); the waves split d.  Also clears the counters of the launch that
+// follows.  Bound by latency: 5.3 us for one token and 256 experts (1 MB), 5.5 for
+// 64 tokens and 64 experts (6.3 with 16 experts per workgroup, whose few CUs read
+// too much each).
 // ---------------------------------------------------------------------------
-constexpr int kScoreWaves = 16;
+constexpr int kScoreWaves = 16, kScoreRows = 4;
 
 __global__ __launch_bounds__(kScoreWaves * 64) void moe_scores_kernel(MoeArgs g) {
   __shared__ f32x4 red[kScoreWaves][64];
   const int lane = threadIdx.x & 63, w = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
-  const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+  const int e0 = blockIdx.x * kScoreRows, t0 = blockIdx.y * 16;
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < 2 * kMoeMaxGrid + g.d / 16; i += kScoreWaves * 64) g.flags[i] = 0;
-  const rsrc_t rr = rows_rsrc<W_BF16>(g.router, e0, g.d, min(16, g.E - e0));  // rows past E read zeros
+  const rsrc_t rr = rows_rsrc<W_BF16>(g.router, e0, g.d, min(kScoreRows, g.E - e0));  // the other rows read zeros
   const rsrc_t rx = make_rsrc(g.x, (uint32_t)(g.T * g.d * 2));
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   for (int k0 = w * kChunk; k0 < g.d; k0 += kScoreWaves * kChunk) {
@@ -172,8 +174,8 @@ __global__ __launch_bounds__(kScoreWaves * 64) void moe_scores_kernel(MoeArgs g)
   }
   red[w][lane] = acc;
   __syncthreads();
-  if (threadIdx.x >= 256) return;
-  const int e = threadIdx.x & 15, t = threadIdx.x >> 4;
+  if (threadIdx.x >= kScoreRows * 16) return;
+  const int e = threadIdx.x % kScoreRows, t = threadIdx.x / kScoreRows;
   if (t0 + t >= g.T || e0 + e >= g.E) return;
   const float* rf = (const float*)red;
   const int at = ((e >> 2) * 16 + t) * 4 + (e & 3);
@@ -797,7 +799,7 @@ hipError_t launch_t(MoeArgs g, hipStream_t stream) {
   g.splits = down_splits(g.T, g.E, g.k, g.d, g.ff, DT);
   {
     LaunchTimer timer("moe_scores", stream);
-    hipLaunchKernelGGL(moe_scores_kernel, dim3((g.E + 15) / 16, (g.T + 15) / 16), dim3(kScoreWaves * 64), 0, stream,
+    hipLaunchKernelGGL(moe_scores_kernel, dim3((g.E + kScoreRows - 1) / kScoreRows, (g.T + 15) / 16), dim3(kScoreWaves * 64), 0, stream,
                        g);
   }
   // two workgroups per CU; more than there can be units of either kind would find none

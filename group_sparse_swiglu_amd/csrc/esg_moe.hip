@@ -13,8 +13,8 @@
 //
 // Two launches: the scores, and everything else.  Measured (both, bytes of the
 // chosen experts' weights over the whole time): one token, 8 of 256 experts, d =
-// 2048, d_ff = 1024, bf16: 37.5 us, 2.7 TB/s; five tokens, d_ff = 1008, 8-bit: 70 us,
-// 3.4 TB/s; 64 tokens, 6 of 64 experts, d_ff = 1408, 8-bit: 155 us, 3.6 TB/s.  The gate
+// 2048, d_ff = 1024, bf16: 37.4 us, 2.7 TB/s; five tokens, d_ff = 1008, 8-bit: 70 us,
+// 3.4 TB/s; 64 tokens, 6 of 64 experts, d_ff = 1408, 8-bit: 152 us, 3.6 TB/s.  The gate
 // and up products themselves read at 5.2 TB/s; the rest is the way between the
 // parts: scores 5 us, start and routing 4 to 12, waiting for the last h 3 to 10.
 #include <algorithm>

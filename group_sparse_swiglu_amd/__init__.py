@@ -264,21 +264,26 @@ class FfnContext:
 
 
 def _ws(nbytes: int, dev, cache: Optional[dict], key: str) -> torch.Tensor:
+    """Scratch of a call.  ``cache`` keeps one buffer per operator, device and stream: calls on different streams may
+    run side by side, and what a call on the same stream outgrew is free for it in stream order.  A captured graph
+    keeps the addresses that it saw, so a call under capture takes its scratch from the graph's own memory instead,
+    which lives as long as the graph and which no call outside it gets."""
     nbytes = max(int(nbytes), 256)
-    if cache is not None:
-        buf = cache.get(key)
-        if buf is None or buf.numel() < nbytes or buf.device != dev:
-            buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            cache[key] = buf
-        return buf
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if cache is None or dev.type != "cuda" or torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    slot = (key, dev, _stream(dev))
+    buf = cache.get(slot)
+    if buf is None or buf.numel() < nbytes:
+        buf = cache[slot] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return buf
 
 
 def sparse_swiglu_fwd(x, w_gate, w_up, w_down, group_idx, group_size: int, status=None, workspace=None,
                       out=None, saved=None, for_backward: bool = True):
     """Forward -> (y [T, d], FfnContext).  group_idx None = every group active.
 
-    ``workspace``: optional dict reused across calls to hold scratch buffers.
+    ``workspace``: optional dict reused across calls to hold scratch buffers
+    (one per stream).
     ``for_backward=False``: inference, nothing is saved (the context then cannot
     be passed to the backward)."""
     T, d = x.shape
@@ -577,7 +582,7 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, works
     a, a_scale: [M, K] and [M, ceil(K/128)] as fp8_quantize gives them; b: [N, K]
     with b_scale [ceil(N/128), ceil(K/128)] (fp8_quantize_weight) or
     [N, ceil(K/128)] (fp8_quantize).  ``workspace``: optional dict reused across
-    calls to hold the scratch buffer."""
+    calls to hold the scratch buffer (one per stream)."""
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise EsgError("a must be [M, K] and b [N, K]")
     (M, K), N = a.shape, b.shape[0]
@@ -616,7 +621,8 @@ def fp8_linear_fwd(x, w, need_dx: bool = True, need_dw: bool = True, workspace: 
 
     x: [T, K], w: [N, K], float32 or bfloat16.  ``saved`` holds what
     fp8_linear_bwd needs for the gradients asked for (None for none).
-    ``workspace``: optional dict reused across calls to hold the scratch buffer."""
+    ``workspace``: optional dict reused across calls to hold the scratch buffer
+    (one per stream)."""
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise EsgError("x must be [T, K] and w [N, K]")
     (T, K), N, dev = x.shape, w.shape[0], x.device
@@ -719,7 +725,7 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
     fp8_quantize_weight.  Routing as sigmoid_topk_routing on x w_router^T; y:
     bfloat16 [T, d], probs: float32 [T, topk], indices: int64 [T, topk].
     ``out`` may supply the three; ``workspace``: optional dict reused across
-    calls to hold the scratch buffer."""
+    calls to hold the scratch buffer (one per stream)."""
     if x.dim() != 2 or w_gate.dim() != 3:
         raise EsgError("x must be [T, d] and the expert weights [E, rows, cols]")
     T, d = x.shape

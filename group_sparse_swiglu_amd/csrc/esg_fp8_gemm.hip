@@ -63,7 +63,6 @@ __device__ __forceinline__ f32x4 mma_block(const Frag<true>& a, const Frag<true>
   return d;
 }
 
-
 struct Fp8Args {
   const uint8_t* a;
   const uint8_t* b;
@@ -75,6 +74,47 @@ struct Fp8Args {
   int nm, nn;     // tiles along m and n
   int splits, kb_split;  // K splits, blocks of K in one
 };
+
+// ---------------------------------------------------------------------------
+// Range.  The kernels multiply the two scales of a block with each other before
+// they meet its sum, one operation per element.  With both scales below 2^64 that
+// product is finite.  Above, it may not be though the block adds nothing (large
+// values of one side against zeros of the other) or something finite: those
+// blocks are scaled in 64 bits.  (A product below the normal range is off by
+// 2^-150 at most, and the sum of a block is below 2^25: 2^-125 of the result.)
+// ---------------------------------------------------------------------------
+constexpr float kFarScale = 0x1p64f;
+__device__ __forceinline__ float top4(float top, float a, float b, float c, float d) {
+  return fmaxf(fmaxf(fmaxf(top, fabsf(a)), fabsf(b)), fmaxf(fabsf(c), fabsf(d)));
+}
+__device__ __forceinline__ float add_far(float acc, float d, float sa, float sb) {
+  return acc + (float)((double)d * (double)sa * (double)sb);
+}
+
+// A 16 x 16 piece of the product over every kstep-th of the blocks kb0 .. kb1 - 1, straight from memory and scaled in
+// 64 bits: element i of lane l is row n0 + (l / 16) * 4 + i of b and row m0 + l % 16 of a.
+template <bool FINE, int SB>
+__device__ __forceinline__ f32x4 far_piece(const Fp8Args& g, int m0, int n0, int kb0, int kb1, int kstep,
+                                           int lr, int lg) {
+  const int m = m0 + lr, n = n0 + lr;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int kb = kb0; kb < kb1; kb += kstep) {
+    auto chunk = [&](const uint8_t* p, int row, int rows, int k) __attribute__((always_inline)) {
+      return row < rows && k < g.K ? *(const uint4*)(p + (size_t)row * g.K + k) : make_uint4(0, 0, 0, 0);
+    };
+    const int k = kb * kQB + lg * 16;
+    const Frag<FINE> a(chunk(g.a, m, g.M, k), chunk(g.a, m, g.M, k + 64));
+    const Frag<FINE> b(chunk(g.b, n, g.N, k), chunk(g.b, n, g.N, k + 64));
+    const f32x4 d = mma_block(b, a);
+    const float sa = g.sa[(size_t)min(m, g.M - 1) * g.KB + kb];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int ne = min(n0 + lg * 4 + e, g.N - 1);
+      acc[e] = add_far(acc[e], d[e], sa, g.sb[(size_t)(SB == SB_ROWS ? ne : ne / kQB) * g.KB + kb]);
+    }
+  }
+  return acc;
+}
 
 // ---------------------------------------------------------------------------
 // Tiles.  BM x BN outputs per workgroup; K in steps of one block (128 bytes per
@@ -113,7 +153,8 @@ struct Tile {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int SROWS = BM + BN;
   static constexpr int SLOT = 4 * SROWS;                // floats of one scale slot
-  static constexpr int LDS = 2 * STAGE + 2 * SLOT * 4;  // one workgroup per CU, or two
+  static constexpr int FAR_AT = 2 * STAGE + 2 * SLOT * 4;  // a word per wave: it has met a scale of kFarScale or more
+  static constexpr int LDS = FAR_AT + NW * 4;           // one workgroup per CU, or two
   static_assert(SROWS == NTH, "one scale row per thread");
   static_assert(WN <= 128, "the n range of a wave lies in one 128-row block");
 };
@@ -210,6 +251,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
     srow = g.sb + (size_t)(SB == SB_ROWS ? n : n / kQB) * g.KB;
   }
   float sreg[4];
+  float top = 0.f;  // largest |scale| of this thread's row so far
   auto load_scales = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) sreg[e] = srow[min(kb + e, kb1 - 1)];
@@ -217,6 +259,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
   auto put_scales = [&](int slot) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) slots[slot * C::SLOT + e * C::SROWS + threadIdx.x] = sreg[e];
+    top = top4(top, sreg[0], sreg[1], sreg[2], sreg[3]);
   };
 
   f32x4 acc[C::FN][C::FM];
@@ -383,6 +426,10 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
   }
 #pragma unroll
   for (int j = 0; j < C::FM; ++j) add_scaled(acc[C::FN - 1][j], dp[j], fp[j], sp);
+  ESG_LDS int* const met = (ESG_LDS int*)(lds + C::FAR_AT);
+  // a row with an infinite scale needs no second look: all of it is NaN in either form
+  const bool far = __ballot(top >= kFarScale && top < INFINITY) != 0;
+  if (lane == 0) met[w] = far;
   wait_lgkm0();
   wait_vmcnt<0>();
   barrier();  // the stages are free
@@ -394,6 +441,24 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
   constexpr int NCH = C::WN * ES / 16;  // chunks per row
   char* y = OUT == OUT_BF16 || OUT == OUT_F32 ? (char*)g.y : (char*)(g.part + (size_t)blockIdx.y * g.M * g.N);
   const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WN;
+  auto store1 = [&](int m, int n, float v) __attribute__((always_inline)) {
+    if (m < g.M && n < g.N) {
+      if constexpr (ES == 2)
+        store_elem<bf16_t>((bf16_t*)y + (size_t)m * g.N + n, v);
+      else
+        ((float*)y)[(size_t)m * g.N + n] = v;
+    }
+  };
+  if (__ballot(met[lane % C::NW] != 0) != 0) {
+    // a scale of kFarScale or more in this tile: all of it again, a piece of 16 x 16 at a time
+    for (int f = 0; f < C::FM * C::FN; ++f) {
+      const int mp = mw + f % C::FM * 16, np = nw + f / C::FM * 16;
+      const f32x4 v = far_piece<fine(OUT), SB>(g, mp, np, kb0, kb1, 1, lr, lg);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) store1(mp + lr, np + lg * 4 + e, v[e]);
+    }
+    return;
+  }
   if (g.N * ES % 16 == 0) {
     static_assert(16 * NCH * 16 * C::NW <= 2 * C::STAGE, "the pieces lie in the stages");
     ESG_LDS char* out = lds + w * (16 * NCH * 16);
@@ -425,15 +490,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void fp8_tile_kernel(Fp8Arg
 #pragma unroll
       for (int i = 0; i < C::FN; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int n = nw + i * 16 + lg * 4 + e;
-          if (m < g.M && n < g.N) {
-            if constexpr (ES == 2)
-              store_elem<bf16_t>((bf16_t*)y + (size_t)m * g.N + n, acc[i][j][e]);
-            else
-              ((float*)y)[(size_t)m * g.N + n] = acc[i][j][e];
-          }
-        }
+        for (int e = 0; e < 4; ++e) store1(m, nw + i * 16 + lg * 4 + e, acc[i][j][e]);
     }
   }
 }
@@ -535,6 +592,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(Fp8Args g) {
     dma4(rsb, slot + S::SB_AT, kb < kb1 ? osb + (uint32_t)kb * 4 : kOOB);
   };
   f32x4 acc[MT];
+  float top = 0.f;  // largest |scale| that this wave has met
   zero_acc(acc);
 #pragma unroll
   for (int u = 0; u < P; ++u) request(kb0 + w + u * NW, ring + u * S::BYTES);
@@ -552,18 +610,24 @@ __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(Fp8Args g) {
       sn = *(const ESG_LDS f32x4*)(fb + lg * 4);
     else
       sn = f32x4{fb[0], fb[0], fb[0], fb[0]};
+    top = top4(top, sn[0], sn[1], sn[2], sn[3]);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       const ESG_LDS char* a = slot + S::A_AT;
       const Frag<fine(OUT)> am(frag_krow(a, j * 16 + lr, lg), frag_krow(a, j * 16 + lr, lg + 4));
       const f32x4 d = mma_block(bn, am);
       const float f = fa[j * 16 + lr];
+      top = fmaxf(top, fabsf(f));
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(d[e], f * sn[e], acc[j][e]);
     }
     wait_lgkm0();  // the slot has been read
     __builtin_amdgcn_sched_barrier(0);
     request(kb + P * NW, slot);
+  }
+  if (__ballot(top >= kFarScale) != 0) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[j] = far_piece<fine(OUT), SB>(g, m0 + j * 16, n0, kb0 + w, kb1, NW, lr, lg);
   }
   wait_vmcnt<0>();
   __syncthreads();  // the slots become the sums of the waves

@@ -429,6 +429,9 @@ int esg_fp8_quant_tiles(const void* w, int dtype, int batch, int rows, int cols,
  * lies far below the largest term of a sum (2e-5 to 3e-5 of a result's norm
  * measured, a hundredth of its rounding); for ESG_F32 the operands are widened
  * to bf16, exactly, and float32 accuracy is kept at half the rate.
+ * The scales are any float32 values; where the product of two leaves float32's
+ * range, a block still adds what the formula says (a product below the normal
+ * range may be off by 2^-125 of the result per block).
  * The three products of a linear layer y = x W^T, with x and dy quantised in
  * rows (and transposed), W in tiles (and transposed):
  *   y = (xq, wq); dx = (dyq, wqt); dW = (dyqt, xqt, b_scale_rows = 1).

@@ -661,11 +661,17 @@ def fp8_linear_bwd(dy, saved, d_in: int, w_dtype, need_dx: bool = True, need_dw:
     return dx, dw
 
 
+def _rows(t):
+    """t as contiguous rows at a 16-byte aligned address: itself, or a copy (of a slice of a flat buffer, say)."""
+    t = t.reshape(-1, t.shape[-1]).contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     def forward(fctx, x, w):
         need_x, need_w = fctx.needs_input_grad
-        y, saved = fp8_linear_fwd(x.reshape(-1, x.shape[-1]).contiguous(), w.contiguous(), need_x, need_w)
+        y, saved = fp8_linear_fwd(_rows(x), _rows(w), need_x, need_w)
         fctx.save_for_backward(saved)
         fctx.esg = (x.shape, w.dtype, need_x, need_w)
         return y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])
@@ -674,8 +680,7 @@ class _Fp8Linear(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(fctx, dy):
         xshape, wdtype, need_x, need_w = fctx.esg
-        dx, dw = fp8_linear_bwd(dy.reshape(-1, dy.shape[-1]).contiguous(), fctx.saved_tensors[0], xshape[-1], wdtype,
-                                need_x, need_w)
+        dx, dw = fp8_linear_bwd(_rows(dy), fctx.saved_tensors[0], xshape[-1], wdtype, need_x, need_w)
         return dx if dx is None or len(xshape) == 2 else dx.view(xshape), dw
 
 
@@ -692,7 +697,7 @@ def fp8_linear(x, w):
     if w.shape[0] % 16 or w.shape[1] % 16:
         raise EsgError("both dimensions of w must be multiples of 16")
     if not torch.is_grad_enabled():  # the function's needs_input_grad reports requires_grad here too
-        y, _ = fp8_linear_fwd(x.reshape(-1, x.shape[-1]).contiguous(), w.contiguous(), False, False)
+        y, _ = fp8_linear_fwd(_rows(x), _rows(w), False, False)
         return y.view(*x.shape[:-1], w.shape[0])
     return _Fp8Linear.apply(x, w)
 

@@ -35,3 +35,31 @@ def test_nothing_is_kept_without_gradients(calls, mode):
     assert [c[:3] for c in calls] == [("fwd", False, False)]
     assert torch.equal(y, E.fp8_linear(x, w).detach())
     assert [c[:3] for c in calls] == [("fwd", False, False), ("fwd", False, True)]
+
+
+def _off(*shape):
+    """A contiguous tensor one element past an aligned address."""
+    n = torch.Size(shape).numel()
+    t = torch.randn(n + 1)[1:].view(shape)
+    assert t.is_contiguous() and t.data_ptr() % 16
+    return t
+
+
+def test_tensors_at_unaligned_addresses_are_copied(calls):
+    x, w, dy = _off(5, 32), _off(16, 32), _off(5, 16)
+    y = E.fp8_linear(x.requires_grad_(), w.requires_grad_())
+    dx, dw = torch.autograd.grad(y, (x, w), dy)
+    with torch.no_grad():
+        E.fp8_linear(x, w)
+    assert len(calls) == 3
+    for c in calls:
+        for t in c[3:]:
+            assert t.data_ptr() % 16 == 0 and t.is_contiguous()
+    assert torch.allclose(dx, dy @ w) and torch.allclose(dw, dy.t() @ x)
+
+
+def test_aligned_tensors_are_not_copied(calls):
+    x, w, dy = torch.randn(5, 32), torch.randn(16, 32), torch.randn(5, 16)
+    y = E.fp8_linear(x, w.requires_grad_())
+    torch.autograd.grad(y, w, dy)
+    assert [t.data_ptr() for c in calls for t in c[3:]] == [x.data_ptr(), w.data_ptr(), dy.data_ptr()]

@@ -157,12 +157,14 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise EsgError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
 
 
-def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
-    """Device pointer of a contiguous GPU tensor (None -> NULL)."""
+def _dev(t: Optional[torch.Tensor], name: str, dtype=None, on: Optional[torch.device] = None):
+    """Device pointer of a contiguous GPU tensor (None -> NULL), which has to be on the GPU ``on`` if that is given."""
     if t is None:
         return None
     if not t.is_cuda:
         raise EsgError(f"{name} must be a GPU tensor")
+    if on is not None and t.device != on:
+        raise EsgError(f"{name} must be on {on} like the other tensors, it is on {t.device}")
     if not t.is_contiguous():
         raise EsgError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -585,7 +587,7 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, works
     calls to hold the scratch buffer (one per stream)."""
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise EsgError("a must be [M, K] and b [N, K]")
-    (M, K), N = a.shape, b.shape[0]
+    (M, K), N, dev = a.shape, b.shape[0], a.device
     kb = (K + 127) // 128
     e4m3, f32 = torch.float8_e4m3fn, torch.float32
     if a_scale.shape != (M, kb):
@@ -594,16 +596,16 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, works
     if not rows and b_scale.shape != ((N + 127) // 128, kb):
         raise EsgError("b_scale must be [ceil(N/128), ceil(K/128)] or [N, ceil(K/128)]")
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype, device=a.device)
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
     elif out.shape != (M, N):
         raise EsgError("out must be [M, N]")
     code = _dtype_code(out)
     need = fp8_matmul_workspace_size(M, N, K)
-    ws = _ws(need, a.device, workspace, "fp8_matmul") if need else None
-    _check(lib().esg_fp8_matmul(_dev(a, "a", e4m3), _dev(a_scale, "a_scale", f32), _dev(b, "b", e4m3),
-                                _dev(b_scale, "b_scale", f32), int(rows), code, M, N, K, _dev(out, "out"),
-                                None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                _stream(a.device)), "fp8_matmul")
+    ws = _ws(need, dev, workspace, "fp8_matmul") if need else None
+    _check(lib().esg_fp8_matmul(_dev(a, "a", e4m3), _dev(a_scale, "a_scale", f32, dev), _dev(b, "b", e4m3, dev),
+                                _dev(b_scale, "b_scale", f32, dev), int(rows), code, M, N, K,
+                                _dev(out, "out", None, dev), None if ws is None else ws.data_ptr(),
+                                0 if ws is None else ws.numel(), _stream(dev)), "fp8_matmul")
     return out
 
 
@@ -634,8 +636,8 @@ def fp8_linear_fwd(x, w, need_dx: bool = True, need_dw: bool = True, workspace: 
         raise EsgError("out must be [T, N] in the dtype of x")
     saved = torch.empty(sv, dtype=torch.uint8, device=dev) if sv else None
     scratch = _ws(fw, dev, workspace, "fp8_linear_fwd")
-    _check(lib().esg_fp8_linear_fwd(_dev(x, "x"), xc, _dev(w, "w"), wc, T, K, N, int(need_dx), int(need_dw),
-                                    _dev(out, "out"), None if saved is None else saved.data_ptr(), sv,
+    _check(lib().esg_fp8_linear_fwd(_dev(x, "x"), xc, _dev(w, "w", None, dev), wc, T, K, N, int(need_dx),
+                                    int(need_dw), _dev(out, "out", None, dev), None if saved is None else saved.data_ptr(), sv,
                                     scratch.data_ptr(), scratch.numel(), _stream(dev)), "fp8_linear_fwd")
     return out, saved
 
@@ -655,7 +657,7 @@ def fp8_linear_bwd(dy, saved, d_in: int, w_dtype, need_dx: bool = True, need_dw:
     code = _dtype_code(dy)
     wcode = _dtype_code(dw) if need_dw else ESG_BF16
     scratch = _ws(bw, dev, workspace, "fp8_linear_bwd")
-    _check(lib().esg_fp8_linear_bwd(_dev(dy, "dy"), code, wcode, T, K, N, _dev(saved, "saved"), sv,
+    _check(lib().esg_fp8_linear_bwd(_dev(dy, "dy"), code, wcode, T, K, N, _dev(saved, "saved", None, dev), sv,
                                     None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
                                     scratch.data_ptr(), scratch.numel(), _stream(dev)), "fp8_linear_bwd")
     return dx, dw
@@ -752,7 +754,7 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
         for s, shape in zip(scales, ((E, fb, db), (E, fb, db), (E, db, fb))):
             if s.shape != shape:
                 raise EsgError("scales must be [E, ceil(rows/128), ceil(cols/128)] of each weight")
-        code, sc = ESG_E4M3, tuple(_dev(s, "scales", f32) for s in scales)
+        code, sc = ESG_E4M3, tuple(_dev(s, "scales", f32, dev) for s in scales)
     else:
         raise EsgError(f"unsupported weight dtype {wt}; use bfloat16 or float8_e4m3fn")
     if expert_bias.dim() != 1 or expert_bias.shape[0] != E or expert_bias.dtype != f32:
@@ -772,11 +774,11 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
         if y.shape != (T, d) or probs.shape != (T, topk) or indices.shape != (T, topk):
             raise EsgError("out must be [T, d], [T, topk] and [T, topk]")
     _check(lib().esg_moe_decode(
-        _dev(x, "x", bf), _dev(w_router, "w_router", bf), expert_bias.data_ptr(), stride, _dev(w_gate, "w_gate", wt),
-        _dev(w_up, "w_up", wt), _dev(w_down, "w_down", wt), *sc, code, T, E, topk, d, ff,
-        1.0 if scaling_factor is None else float(scaling_factor), int(scaling_factor is not None), _dev(y, "y", bf),
-        _dev(probs, "probs", f32), _dev(indices, "indices", torch.int64), ws.data_ptr(), ws.numel(), _stream(dev)),
-        "moe_decode")
+        _dev(x, "x", bf), _dev(w_router, "w_router", bf, dev), expert_bias.data_ptr(), stride,
+        _dev(w_gate, "w_gate", wt, dev), _dev(w_up, "w_up", wt, dev), _dev(w_down, "w_down", wt, dev), *sc, code, T, E,
+        topk, d, ff, 1.0 if scaling_factor is None else float(scaling_factor), int(scaling_factor is not None),
+        _dev(y, "y", bf, dev), _dev(probs, "probs", f32, dev), _dev(indices, "indices", torch.int64, dev),
+        ws.data_ptr(), ws.numel(), _stream(dev)), "moe_decode")
     return y, probs, indices
 
 

@@ -174,7 +174,11 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, on: Optional[torch.de
 
 def _stream(device: torch.device):
     # the raw handle of torch.cuda.current_stream(device), without building its Stream object (1.8 us)
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    handle = torch._C._cuda_getCurrentRawStream(device.index)
+    # the default stream has the same handle, 0, on every GPU: a launch on it goes to the current one
+    if not handle and torch._C._cuda_getDevice() != device.index:
+        raise EsgError(f"the tensors are on {device}, which is not the current GPU (torch.cuda.set_device)")
+    return handle
 
 
 def make_subsample_index(d_ff: int, group_size: int, samples_per_group: int, seed: int):

@@ -752,8 +752,8 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
     if wt == bf:
         code, sc = ESG_BF16, (None, None, None)
     elif wt == torch.float8_e4m3fn:
-        if scales is None:
-            raise EsgError("float8 expert weights need their scales")
+        if scales is None or len(scales) != 3:
+            raise EsgError("float8 expert weights need their three scales (gate, up, down)")
         fb, db = (ff + 127) // 128, (d + 127) // 128
         for s, shape in zip(scales, ((E, fb, db), (E, fb, db), (E, db, fb))):
             if s.shape != shape:

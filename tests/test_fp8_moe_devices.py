@@ -86,3 +86,12 @@ def test_experts(launches):
                 scales=tuple(Stub((Ex, 1, 1), F32) for _ in range(3)),
                 out=(Stub((T, d), BF), Stub((T, k), F32), Stub((T, k), I64)))
     _each_elsewhere(lambda **kw: E.moe_decode(topk=k, **kw), args, launches)
+
+
+@pytest.mark.parametrize("n", [0, 2, 4])
+def test_experts_take_three_scales(launches, n):
+    w, wd = Stub((8, 64, 128), E4M3), Stub((8, 128, 64), E4M3)
+    with pytest.raises(E.EsgError, match="three"):
+        E.moe_decode(Stub((4, 128), BF), Stub((8, 128), BF), Stub((8,), F32), w, w, wd, 2,
+                     scales=tuple(Stub((8, 1, 1), F32) for _ in range(n)))
+    assert not launches

@@ -157,14 +157,15 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise EsgError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
 
 
-def _dev(t: Optional[torch.Tensor], name: str, dtype=None, on: Optional[torch.device] = None):
-    """Device pointer of a contiguous GPU tensor (None -> NULL), which has to be on the GPU ``on`` if that is given."""
+def _dev(t: Optional[torch.Tensor], name: str, dtype=None, on: Optional[int] = None):
+    """Device pointer of a contiguous GPU tensor (None -> NULL), which has to be on GPU ``on`` if that is given."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise EsgError(f"{name} must be a GPU tensor")
-    if on is not None and t.device != on:
-        raise EsgError(f"{name} must be on {on} like the other tensors, it is on {t.device}")
+    if on is None:
+        if not t.is_cuda:
+            raise EsgError(f"{name} must be a GPU tensor")
+    elif t.get_device() != on:
+        raise EsgError(f"{name} must be on cuda:{on} like the other tensors, it is on {t.device}")
     if not t.is_contiguous():
         raise EsgError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -172,11 +173,16 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, on: Optional[torch.de
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=None)
+def _several_gpus() -> bool:
+    return torch.cuda.device_count() > 1
+
+
 def _stream(device: torch.device):
     # the raw handle of torch.cuda.current_stream(device), without building its Stream object (1.8 us)
     handle = torch._C._cuda_getCurrentRawStream(device.index)
     # the default stream has the same handle, 0, on every GPU: a launch on it goes to the current one
-    if not handle and torch._C._cuda_getDevice() != device.index:
+    if not handle and _several_gpus() and torch._C._cuda_getDevice() != device.index:
         raise EsgError(f"the tensors are on {device}, which is not the current GPU (torch.cuda.set_device)")
     return handle
 
@@ -591,7 +597,7 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, works
     calls to hold the scratch buffer (one per stream)."""
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise EsgError("a must be [M, K] and b [N, K]")
-    (M, K), N, dev = a.shape, b.shape[0], a.device
+    (M, K), N, dev, gpu = a.shape, b.shape[0], a.device, a.get_device()
     kb = (K + 127) // 128
     e4m3, f32 = torch.float8_e4m3fn, torch.float32
     if a_scale.shape != (M, kb):
@@ -606,9 +612,9 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, works
     code = _dtype_code(out)
     need = fp8_matmul_workspace_size(M, N, K)
     ws = _ws(need, dev, workspace, "fp8_matmul") if need else None
-    _check(lib().esg_fp8_matmul(_dev(a, "a", e4m3), _dev(a_scale, "a_scale", f32, dev), _dev(b, "b", e4m3, dev),
-                                _dev(b_scale, "b_scale", f32, dev), int(rows), code, M, N, K,
-                                _dev(out, "out", None, dev), None if ws is None else ws.data_ptr(),
+    _check(lib().esg_fp8_matmul(_dev(a, "a", e4m3), _dev(a_scale, "a_scale", f32, gpu), _dev(b, "b", e4m3, gpu),
+                                _dev(b_scale, "b_scale", f32, gpu), int(rows), code, M, N, K,
+                                _dev(out, "out", None, gpu), None if ws is None else ws.data_ptr(),
                                 0 if ws is None else ws.numel(), _stream(dev)), "fp8_matmul")
     return out
 
@@ -631,7 +637,7 @@ def fp8_linear_fwd(x, w, need_dx: bool = True, need_dw: bool = True, workspace: 
     (one per stream)."""
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise EsgError("x must be [T, K] and w [N, K]")
-    (T, K), N, dev = x.shape, w.shape[0], x.device
+    (T, K), N, dev, gpu = x.shape, w.shape[0], x.device, x.get_device()
     sv, fw, _ = fp8_linear_workspace_size(T, K, N, need_dx, need_dw)
     xc, wc = _dtype_code(x), _dtype_code(w)
     if out is None:
@@ -640,8 +646,8 @@ def fp8_linear_fwd(x, w, need_dx: bool = True, need_dw: bool = True, workspace: 
         raise EsgError("out must be [T, N] in the dtype of x")
     saved = torch.empty(sv, dtype=torch.uint8, device=dev) if sv else None
     scratch = _ws(fw, dev, workspace, "fp8_linear_fwd")
-    _check(lib().esg_fp8_linear_fwd(_dev(x, "x"), xc, _dev(w, "w", None, dev), wc, T, K, N, int(need_dx),
-                                    int(need_dw), _dev(out, "out", None, dev), None if saved is None else saved.data_ptr(), sv,
+    _check(lib().esg_fp8_linear_fwd(_dev(x, "x"), xc, _dev(w, "w", None, gpu), wc, T, K, N, int(need_dx), int(need_dw),
+                                    _dev(out, "out", None, gpu), None if saved is None else saved.data_ptr(), sv,
                                     scratch.data_ptr(), scratch.numel(), _stream(dev)), "fp8_linear_fwd")
     return out, saved
 
@@ -652,7 +658,7 @@ def fp8_linear_bwd(dy, saved, d_in: int, w_dtype, need_dx: bool = True, need_dw:
     (None where not asked for; need_dx and need_dw as in the forward)."""
     if dy.dim() != 2:
         raise EsgError("dy must be [T, N]")
-    (T, N), K, dev = dy.shape, d_in, dy.device
+    (T, N), K, dev, gpu = dy.shape, d_in, dy.device, dy.get_device()
     sv, _, bw = fp8_linear_workspace_size(T, K, N, need_dx, need_dw)
     if (0 if saved is None else saved.numel()) != sv:
         raise EsgError("saved is not that of a forward with these sizes and gradients")
@@ -661,7 +667,7 @@ def fp8_linear_bwd(dy, saved, d_in: int, w_dtype, need_dx: bool = True, need_dw:
     code = _dtype_code(dy)
     wcode = _dtype_code(dw) if need_dw else ESG_BF16
     scratch = _ws(bw, dev, workspace, "fp8_linear_bwd")
-    _check(lib().esg_fp8_linear_bwd(_dev(dy, "dy"), code, wcode, T, K, N, _dev(saved, "saved", None, dev), sv,
+    _check(lib().esg_fp8_linear_bwd(_dev(dy, "dy"), code, wcode, T, K, N, _dev(saved, "saved", None, gpu), sv,
                                     None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
                                     scratch.data_ptr(), scratch.numel(), _stream(dev)), "fp8_linear_bwd")
     return dx, dw
@@ -744,6 +750,7 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
         raise EsgError("x must be [T, d] and the expert weights [E, rows, cols]")
     T, d = x.shape
     E, ff, _ = w_gate.shape
+    gpu = x.get_device()
     if w_gate.shape != (E, ff, d) or w_up.shape != (E, ff, d) or w_down.shape != (E, d, ff) or \
             w_router.shape != (E, d):
         raise EsgError("shapes: w_router [E,d], w_gate/w_up [E,ff,d], w_down [E,d,ff]")
@@ -758,7 +765,7 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
         for s, shape in zip(scales, ((E, fb, db), (E, fb, db), (E, db, fb))):
             if s.shape != shape:
                 raise EsgError("scales must be [E, ceil(rows/128), ceil(cols/128)] of each weight")
-        code, sc = ESG_E4M3, tuple(_dev(s, "scales", f32, dev) for s in scales)
+        code, sc = ESG_E4M3, tuple(_dev(s, "scales", f32, gpu) for s in scales)
     else:
         raise EsgError(f"unsupported weight dtype {wt}; use bfloat16 or float8_e4m3fn")
     if expert_bias.dim() != 1 or expert_bias.shape[0] != E or expert_bias.dtype != f32:
@@ -778,10 +785,10 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
         if y.shape != (T, d) or probs.shape != (T, topk) or indices.shape != (T, topk):
             raise EsgError("out must be [T, d], [T, topk] and [T, topk]")
     _check(lib().esg_moe_decode(
-        _dev(x, "x", bf), _dev(w_router, "w_router", bf, dev), expert_bias.data_ptr(), stride,
-        _dev(w_gate, "w_gate", wt, dev), _dev(w_up, "w_up", wt, dev), _dev(w_down, "w_down", wt, dev), *sc, code, T, E,
+        _dev(x, "x", bf), _dev(w_router, "w_router", bf, gpu), expert_bias.data_ptr(), stride,
+        _dev(w_gate, "w_gate", wt, gpu), _dev(w_up, "w_up", wt, gpu), _dev(w_down, "w_down", wt, gpu), *sc, code, T, E,
         topk, d, ff, 1.0 if scaling_factor is None else float(scaling_factor), int(scaling_factor is not None),
-        _dev(y, "y", bf, dev), _dev(probs, "probs", f32, dev), _dev(indices, "indices", torch.int64, dev),
+        _dev(y, "y", bf, gpu), _dev(probs, "probs", f32, gpu), _dev(indices, "indices", torch.int64, gpu),
         ws.data_ptr(), ws.numel(), _stream(dev)), "moe_decode")
     return y, probs, indices
 

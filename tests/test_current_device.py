@@ -9,6 +9,7 @@ import group_sparse_swiglu_amd as E
 def gpu(monkeypatch):
     state = dict(current=0, streams={0: 0, 1: 0})
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: state["streams"][i], raising=False)
+    monkeypatch.setattr(E, "_several_gpus", lambda: True, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["current"], raising=False)
     return state
 

@@ -17,6 +17,9 @@ class Stub:
     def __init__(self, shape, dtype, device=HERE):
         self.shape, self.dtype, self.device = torch.Size(shape), dtype, device
 
+    def get_device(self):
+        return self.device.index
+
     def dim(self):
         return len(self.shape)
 

@@ -593,8 +593,10 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, works
 
     a, a_scale: [M, K] and [M, ceil(K/128)] as fp8_quantize gives them; b: [N, K]
     with b_scale [ceil(N/128), ceil(K/128)] (fp8_quantize_weight) or
-    [N, ceil(K/128)] (fp8_quantize).  ``workspace``: optional dict reused across
-    calls to hold the scratch buffer (one per stream)."""
+    [N, ceil(K/128)] (fp8_quantize).  A bfloat16 result comes from the 8-bit matrix
+    cores, whose sums are off by up to 7 * 2^-14 of the sum of the |terms|; a float32
+    result keeps float32 accuracy, at half the rate.  ``workspace``: optional dict
+    reused across calls to hold the scratch buffer (one per stream)."""
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise EsgError("a must be [M, K] and b [N, K]")
     (M, K), N, dev, gpu = a.shape, b.shape[0], a.device, a.get_device()

@@ -70,11 +70,10 @@ struct MoeArgs {
 // K elements koff(s, g) .. + 7, the same on the other operand.  Buffer loads:
 // what lies past K, or belongs to no row, is an offset past the buffer and
 // reads zeros, without a branch.
-typedef int v4i32 __attribute__((ext_vector_type(4)));
 constexpr int kDevice = 16;  // sc1 bit of a buffer access: device scope (past the caches that XCDs do not share)
 template <int CPOL = 0>
 __device__ __forceinline__ uint4 load16(rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(uint4, (v4i32)__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, CPOL));
+  return __builtin_bit_cast(uint4, (i32x4_t)__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, CPOL));
 }
 
 template <int WT>
@@ -735,7 +734,7 @@ __global__ __launch_bounds__(kMoeWaves * 64, 4) void moe_experts_kernel(MoeArgs 
       const uint32_t tile = quads * 16, pstride = dtiles * tile;  // bytes
       const rsrc_t rp = make_rsrc((const char*)g.part + (size_t)dt * tile, (g.splits - 1) * pstride + tile);
       for (int o = threadIdx.x; o < quads; o += kMoeWaves * 64)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i32, sum(o)), rp, part * pstride + o * 16, 0,
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, sum(o)), rp, part * pstride + o * 16, 0,
                                                kDevice);
       wait_vmcnt<0>();
       __syncthreads();  // every wave's stores are done

@@ -34,12 +34,6 @@ def quantize(x: np.ndarray, rows: int, cols: int):
     return q, scale
 
 
-def pad_rows16(x: np.ndarray) -> np.ndarray:
-    out = np.zeros(((x.shape[0] + 15) // 16 * 16,) + x.shape[1:], x.dtype)
-    out[: x.shape[0]] = x
-    return out
-
-
 def values(q: np.ndarray, scale: np.ndarray, rows: int, cols: int) -> np.ndarray:
     """What q and its scales stand for, float64."""
     s = np.repeat(np.repeat(scale.astype(np.float64), rows, 0), cols, 1)

@@ -1,0 +1,457 @@
+"""What is measured of the operators around and inside an expert feed-forward
+block: the norm before it, the routing of its tokens, and its products in 4 bits.
+
+Five operators, each in a plain form (elementary torch operations in 32 bits, 64
+for the scores of the routing) and as a user calls it from
+``group_sparse_swiglu_amd``:
+
+- ``norm``: root-mean-square norm after adding the residual, h = x + residual
+  (rounded to their type), y = h (mean h^2 + eps)^-1/2 w; with its gradients, or
+  with y in 8-bit floating point (e4m3, one float32 scale per 1 x 128 block);
+- ``route``: softmax or sigmoid scores (rounded once to float32), a bias for the
+  choice, groups of experts ranked by the sum of their two largest keys, the k
+  experts with the largest keys in ascending order, their weights; with the
+  gradient of the logits;
+- ``quant``: rows to 4-bit floating point (e2m1) with a power of two per 32
+  elements, and the values that these stand for;
+- ``matmul``: y = A B^T of two such operands;
+- ``experts``: the same for rows in the order of their experts, taken from the
+  tokens through an index, each expert with its own B.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+EPS = 1e-6
+MX = 32                # elements of a 4-bit block
+E4M3 = torch.float8_e4m3fn
+
+
+# --------------------------------------------------------------------- cases
+def listed():
+    return [
+        # before an 8-bit projection of a decode batch at the 1.3B width: latency
+        dict(name="norm_decode64", op="norm", form="fp8", T=64, d=2048, dtype="bf16", wdtype="bf16", residual=True),
+        # a training step's norm at the 1.3B shape, both directions
+        dict(name="norm_train", op="norm", form="train", T=32768, d=2048, dtype="bf16", wdtype="f32", residual=True),
+        # a small ragged float32 batch at the 128M width, first layer (no residual yet)
+        dict(name="norm_333", op="norm", form="train", T=333, d=768, dtype="f32", wdtype="f32", residual=False),
+        # one decode step's routing over 256 experts in 8 groups
+        dict(name="route_decode64", op="route", form="fwd", T=64, E=256, k=8, dtype="f32", scoring="sigmoid", bias=True,
+             groups=8, topk_groups=4, normalize=True, scaling=2.5),
+        # the same router over a training batch, with the gradient of its logits
+        dict(name="route_train", op="route", form="train", T=32768, E=256, k=8, dtype="bf16", scoring="sigmoid", bias=True,
+             groups=8, topk_groups=4, normalize=True, scaling=2.5),
+        # softmax over the 1.3B layer's 43 groups as experts, 11 active, an odd prompt
+        dict(name="route_softmax43", op="route", form="train", T=8197, E=43, k=11, dtype="f32", scoring="softmax", bias=False,
+             groups=1, topk_groups=1, normalize=True, scaling=0.0),
+        # a training batch's activations at the 1.3B width
+        dict(name="quant_tokens", op="quant", M=32768, K=2048, dtype="bf16"),
+        # float32 weights of the 1.3B layer's down projection
+        dict(name="quant_weights", op="quant", M=2048, K=5504, dtype="f32"),
+        # gate and up projections stacked (2 x 5504), one token
+        dict(name="matmul_token1", op="matmul", M=1, N=11008, K=2048, out="bf16"),
+        # the 1.3B layer's gate projection over a whole training batch
+        dict(name="matmul_train", op="matmul", M=32768, N=5504, K=2048, out="bf16"),
+        # gate and up of 64 experts for a decode batch of 64 tokens, 6 experts each
+        dict(name="experts_decode64", op="experts", T=64, E=64, k=6, N=2816, K=2048, out="bf16"),
+        # their down projection for an odd prompt
+        dict(name="experts_prompt", op="experts", T=8191, E=64, k=6, N=2048, K=1408, out="bf16"),
+    ]
+
+
+def _log(rng, lo, hi, step=1):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi))) / step)) * step))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "norm", "route", "route", "quant", "matmul", "matmul", "experts", "experts"])
+    while True:
+        if op == "norm":
+            c = dict(op=op, form=rng.choice(["fp8", "fwd", "train", "train"]), T=_log(rng, 1, 32768), d=_log(rng, 128, 16384, 16),
+                     dtype=rng.choice(["bf16", "bf16", "f32"]), wdtype=rng.choice(["bf16", "f32"]),
+                     residual=rng.random() < 0.7)
+            if c["T"] * c["d"] * (2 if c["dtype"] == "f32" else 1) <= 32768 * 2048:
+                return c
+        elif op == "route":
+            per = _log(rng, 4, 64)
+            groups = rng.choice([1, 1, 4, 6, 8])
+            E = per * groups
+            top = rng.randint(1, groups)
+            c = dict(op=op, form=rng.choice(["fwd", "train"]), T=_log(rng, 1, 32768), E=E, k=rng.randint(1, min(12, per * top)),
+                     dtype=rng.choice(["f32", "bf16"]), scoring=rng.choice(["softmax", "sigmoid"]), bias=rng.random() < 0.5,
+                     groups=groups, topk_groups=top, normalize=rng.random() < 0.7, scaling=rng.choice([0.0, 2.5]))
+            if c["T"] * E <= 32768 * 256:
+                return c
+        elif op == "quant":
+            c = dict(op=op, M=_log(rng, 1, 65536), K=_log(rng, 32, 16384, 32), dtype=rng.choice(["bf16", "f32"]))
+            if c["M"] * c["K"] * (2 if c["dtype"] == "f32" else 1) <= 32768 * 2048:
+                return c
+        elif op == "matmul":
+            c = dict(op=op, M=_log(rng, 1, 32768), N=_log(rng, 16, 16384), K=_log(rng, 64, 16384, 32),
+                     out=rng.choice(["bf16", "bf16", "f32"]))
+            if c["M"] * c["N"] * c["K"] <= 32768 * 5504 * 2048 and c["M"] * c["N"] <= 32768 * 5504 // 2:
+                return c
+        else:
+            E = _log(rng, 4, 128)
+            c = dict(op=op, T=_log(rng, 1, 8192), E=E, k=rng.randint(1, min(E, 8)), N=_log(rng, 64, 4096, 4),
+                     K=_log(rng, 64, 4096, 32), out=rng.choice(["bf16", "bf16", "f32"]))
+            if E * c["N"] * c["K"] <= 64 * 2816 * 2048 and c["T"] * c["k"] * c["N"] * c["K"] <= 32768 * 5504 * 2048:
+                return c
+
+
+# ------------------------------------------------------------------- inputs
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed))
+    return g
+
+
+def _activations(g, rows, cols, dtype=torch.bfloat16):
+    """Normal values whose channels differ in size, a few of them by much."""
+    size = torch.exp(0.7 * torch.randn(cols, device=DEV, generator=g))
+    return (torch.randn(rows, cols, device=DEV, generator=g) * size).to(dtype)
+
+
+def _weights(g, *shape, dtype=torch.bfloat16):
+    return (torch.randn(*shape, device=DEV, generator=g) * shape[-1] ** -0.5).to(dtype)
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    op = case["op"]
+    if op == "norm":
+        t, T, d = TYPES[case["dtype"]], case["T"], case["d"]
+        s = dict(case=case, x=_activations(g, T, d, t), residual=None, dh=None, workspace={})
+        s["w"] = (1.0 + 0.2 * torch.randn(d, device=DEV, generator=g)).to(TYPES[case["wdtype"]])
+        if case["residual"]:
+            s["residual"] = _activations(g, T, d, t)
+        if case["form"] == "train":
+            s["dy"] = _activations(g, T, d, t) * 1e-3
+            s["x"].requires_grad_()
+            s["w"].requires_grad_()
+            if case["residual"]:
+                s["dh"] = _activations(g, T, d, t) * 1e-3
+                s["residual"].requires_grad_()
+        return s
+    if op == "route":
+        T, E = case["T"], case["E"]
+        skill = 0.5 * torch.randn(E, device=DEV, generator=g)  # some experts are asked for more than others
+        z = (torch.randn(T, E, device=DEV, generator=g) + skill).to(TYPES[case["dtype"]])
+        s = dict(case=case, z=z, bias=None)
+        if case["bias"]:
+            unit = 1.0 / E if case["scoring"] == "softmax" else 1.0
+            s["bias"] = unit * (0.1 * torch.rand(E, device=DEV, generator=g) - 0.05)
+        if case["form"] == "train":
+            s["dp"] = torch.randn(T, case["k"], device=DEV, generator=g) * 1e-2
+            s["z"].requires_grad_()
+        return s
+    if op == "quant":
+        return dict(case=case, x=_activations(g, case["M"], case["K"], TYPES[case["dtype"]]))
+    K, N = case["K"], case["N"]
+    if op == "matmul":
+        a, sa = _mx_quantize(_activations(g, case["M"], K))
+        b, sb = _mx_quantize(_weights(g, N, K))
+        return dict(case=case, a=a, sa=sa, b=b, sb=sb, workspace={})
+    T, E, k = case["T"], case["E"], case["k"]
+    a, sa = _mx_quantize(_activations(g, T, K))
+    b, sb = _mx_quantize(_weights(g, E, N, K))
+    skill = torch.randn(E, device=DEV, generator=g) * 0.5
+    chosen = (torch.randn(T, E, device=DEV, generator=g) + skill).sort(dim=1, descending=True).indices[:, :k]
+    order = chosen.reshape(-1).sort(stable=True)
+    rows = (order.indices // k).int()                       # token of each sorted row
+    offsets = torch.searchsorted(order.values, torch.arange(E + 1, device=DEV)).int()
+    cap = int((offsets[1:] - offsets[:-1]).max())
+    return dict(case=case, a=a, sa=sa, b=b, sb=sb, rows=rows, offsets=offsets, cap=cap, workspace={})
+
+
+# -------------------------------------------------------------- plain forms
+def _blocks8(y):
+    """float32 [T, d] -> e4m3 values and float32 scales of 1 x 128 blocks."""
+    T, d = y.shape
+    n = -(-d // 128)
+    full = y.new_zeros(T, n * 128)
+    full[:, :d] = y
+    full = full.view(T, n, 128)
+    top = full.abs().amax(-1).clamp(min=2.0 ** -100)
+    m = torch.full_like(top, 448.0)  # two tensors: a division by a number may go by its rounded reciprocal
+    return (full * (m / top)[..., None]).view(T, -1)[:, :d].to(E4M3).contiguous(), top / m
+
+
+def _plain_norm(s):
+    c = s["case"]
+    t = s["x"].dtype
+    h = s["x"] if s["residual"] is None else (s["x"].float() + s["residual"].float()).to(t)
+    hf, w = h.float(), s["w"].float()
+    r = 1.0 / torch.sqrt((hf * hf).mean(-1, keepdim=True) + EPS)
+    y = hf * r * w
+    new = () if s["residual"] is None else (h,)
+    if c["form"] == "fp8":
+        return (*_blocks8(y), *new)
+    if c["form"] == "fwd":
+        return (y.to(t), h) if new else y.to(t)
+    dy = s["dy"].float()
+    g = dy * w
+    dx = r * (g - hf * (r * r * (g * hf).mean(-1, keepdim=True)))
+    if s["dh"] is not None:
+        dx = dx + s["dh"].float()
+    dx = dx.to(t)
+    dw = (dy * hf * r).sum(0).to(s["w"].dtype)
+    return (y.to(t), *new, dx, *((dx,) if new else ()), dw)
+
+
+def _plain_route(s):
+    c = s["case"]
+    T, E, k, G = c["T"], c["E"], c["k"], c["groups"]
+    z = s["z"].double()
+    if c["scoring"] == "sigmoid":
+        score = 1.0 / (1.0 + torch.exp(-z))
+    else:
+        e = torch.exp(z - z.amax(-1, keepdim=True))
+        score = e / e.sum(-1, keepdim=True)
+    score = score.float()
+    key = score if s["bias"] is None else score + s["bias"]
+    if c["topk_groups"] < G:
+        of = key.view(T, G, E // G).sort(dim=-1, descending=True).values
+        rank = of[..., 0] + of[..., 1] if E // G > 1 else of[..., 0]
+        best = rank.sort(dim=-1, descending=True, stable=True).indices[:, : c["topk_groups"]]
+        keep = torch.zeros(T, G, dtype=torch.bool, device=z.device).scatter_(1, best, True)
+        key = key.masked_fill(~keep.repeat_interleave(E // G, 1), -math.inf)
+    idx = key.sort(dim=-1, descending=True, stable=True).indices[:, :k].sort(dim=-1).values
+    sel = score.gather(1, idx)
+    scale = c["scaling"] or 1.0
+    total = sel.sum(-1, keepdim=True) + 1e-20
+    p = sel / total * scale if c["normalize"] else sel * scale
+    if c["form"] == "fwd":
+        return p, idx.int()
+    dp = s["dp"]
+    ds = (dp - (dp * sel).sum(-1, keepdim=True) / total) * (scale / total) if c["normalize"] else dp * scale
+    if c["scoring"] == "sigmoid":
+        dz = torch.zeros(T, E, device=z.device).scatter_(1, idx, ds * sel * (1.0 - sel))
+    else:
+        dz = -score * (sel * ds).sum(-1, keepdim=True)
+        dz = dz.scatter_add_(1, idx, sel * ds)
+    return p, idx.int(), dz.to(s["z"].dtype)
+
+
+def _mx_quantize(x):
+    """[..., K] -> two e2m1 codes a byte (the lower half first), a biased exponent per 32."""
+    xb = x.float().reshape(*x.shape[:-1], -1, MX)
+    top = xb.abs().amax(-1)
+    e = ((top.view(torch.int32) >> 23) - 2).clamp(min=0)
+    v = xb * torch.exp2((127 - e).float())[..., None]
+    m = v.abs()
+    step = 0.5 + 0.5 * (m >= 2).float() + (m >= 4).float()
+    m = (torch.round(m / step) * step).clamp(max=6.0)
+    # 0, .5, 1, 1.5, 2, 3, 4, 6 are the codes 0 .. 7
+    code = torch.where(m < 2, 2 * m, torch.where(m < 4, m + 2, m / 2 + 4)).to(torch.uint8)
+    code = code + 8 * torch.signbit(v).to(torch.uint8)
+    code = code.view(*x.shape[:-1], -1, 2)
+    return code[..., 0] + 16 * code[..., 1], e.to(torch.uint8)
+
+
+def _mx_values(q, scale):
+    """float32 values of the codes."""
+    code = torch.stack((q & 15, q >> 4), -1).view(*q.shape[:-1], -1).int()
+    m = (code & 7).float()
+    m = torch.where(m < 4, 0.5 * m, torch.where(m < 6, m - 2, 2 * m - 8)) * (1 - 2 * (code >> 3)).float()
+    return (m.view(*scale.shape, MX) * torch.exp2(scale.float() - 127)[..., None]).view(code.shape)
+
+
+def _plain_experts(s):
+    c = s["case"]
+    E, cap, rows, off = c["E"], s["cap"], s["rows"].long(), s["offsets"].long()
+    a = _mx_values(s["a"], s["sa"])[rows]
+    at = torch.arange(rows.numel(), device=a.device)
+    e = torch.searchsorted(off, at, right=True) - 1
+    place = e * cap + at - off[e]                            # each expert's rows in a block of the largest count
+    block = a.new_zeros(E * cap, a.shape[1]).index_copy_(0, place, a).view(E, cap, -1)
+    y = torch.bmm(block, _mx_values(s["b"], s["sb"]).transpose(1, 2).contiguous())
+    return y.view(E * cap, -1)[place].to(TYPES[c["out"]])
+
+
+# ----------------------------------------------------------------- one pass
+def run(s):
+    c = s["case"]
+    op = c["op"]
+    if not own:
+        with torch.no_grad():
+            if op == "norm":
+                return _plain_norm(s)
+            if op == "route":
+                return _plain_route(s)
+            if op == "quant":
+                return _mx_values(*_mx_quantize(s["x"])).to(torch.bfloat16)
+            if op == "matmul":
+                return (_mx_values(s["a"], s["sa"]) @ _mx_values(s["b"], s["sb"]).t()).to(TYPES[c["out"]])
+            return _plain_experts(s)
+    import group_sparse_swiglu_amd as E
+    if op == "norm":
+        if c["form"] == "fp8":
+            return E.rms_norm_quantize(s["x"], s["w"], s["residual"], eps=EPS)
+        out = E.rms_norm(s["x"], s["w"], s["residual"], eps=EPS)
+        if c["form"] == "fwd":
+            return out
+        if s["residual"] is None:
+            return (out, *torch.autograd.grad(out, (s["x"], s["w"]), s["dy"]))
+        return (*out, *torch.autograd.grad(out, (s["x"], s["residual"], s["w"]), (s["dy"], s["dh"])))
+    if op == "route":
+        p, idx = E.topk_routing(s["z"], c["k"], scoring=c["scoring"], expert_bias=s["bias"], groups=c["groups"],
+                                topk_groups=c["topk_groups"], normalize=c["normalize"],
+                                scaling_factor=c["scaling"] or None)
+        return (p, idx) if c["form"] == "fwd" else (p, idx, *torch.autograd.grad(p, s["z"], s["dp"]))
+    if op == "quant":
+        return E.mxfp4_dequantize(*E.mxfp4_quantize(s["x"]))
+    if op == "matmul":
+        return E.mxfp4_matmul(s["a"], s["sa"], s["b"], s["sb"], out_dtype=TYPES[c["out"]], workspace=s["workspace"])
+    return E.mxfp4_grouped_matmul(s["a"], s["sa"], s["b"], s["sb"], s["offsets"], rows=s["rows"],
+                                  out_dtype=TYPES[c["out"]], workspace=s["workspace"])
+
+
+def work(case):
+    op = case["op"]
+    if op == "norm":
+        T, d = case["T"], case["d"]
+        n, size, wsize = T * d, 4 if case["dtype"] == "f32" else 2, 4 if case["wdtype"] == "f32" else 2
+        io = n * size * (3 if case["residual"] else 1) + d * wsize  # x, residual, h; w
+        if case["form"] == "fp8":
+            return {"bytes": io + n + 4 * T * -(-d // 128), "flops": 8 * n}
+        if case["form"] == "fwd":
+            return {"bytes": io + n * size, "flops": 5 * n}
+        back = n * size * (3 if case["residual"] else 2) + d * wsize  # dy, dh, dx; dw
+        return {"bytes": io + n * size + back, "flops": 16 * n}
+    if op == "route":
+        T, E, k = case["T"], case["E"], case["k"]
+        size = 4 if case["dtype"] == "f32" else 2
+        n = T * E
+        train = case["form"] == "train"
+        return {"bytes": n * size * (2 if train else 1) + 8 * T * k + (4 * T * k if train else 0) + (4 * E if case["bias"] else 0),
+                "flops": 4 * n + (6 * n if train else 0)}
+    if op == "quant":
+        n = case["M"] * case["K"]
+        return {"bytes": n * ((4 if case["dtype"] == "f32" else 2) + 2), "flops": 4 * n}
+    N, K, size = case["N"], case["K"], 4 if case["out"] == "f32" else 2
+    held = K / 2 + K / MX  # bytes of a row
+    if op == "matmul":
+        M = case["M"]
+        return {"bytes": (M + N) * held + M * N * size, "flops": 2 * M * N * K}
+    T, E, k = case["T"], case["E"], case["k"]
+    active = E * (1.0 - (1.0 - k / E) ** T)
+    return {"bytes": (T + active * N) * held + T * k * N * size + 4 * T * k + 4 * E, "flops": 2 * T * k * N * K}
+
+
+# ------------------------------------------------------------------ 64 bits
+def _round8(v):
+    """float64 to the nearest e4m3 value, ties to even."""
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    return (torch.round(v / step) * step).clamp(-448.0, 448.0)
+
+
+def _norm64(s):
+    c = s["case"]
+    h = s["x"].double()
+    if s["residual"] is not None:
+        h = (h + s["residual"].double()).to(s["x"].dtype).double()
+    w = s["w"].double()
+    r = torch.rsqrt(h.square().sum(1) / c["d"] + EPS).unsqueeze(1)
+    y = h * w * r
+    new = [] if s["residual"] is None else [h]
+    if c["form"] == "fp8":
+        parts = torch.split(y, 128, dim=1)
+        tops = [p.abs().amax(1, keepdim=True).clamp(min=2.0 ** -100) for p in parts]
+        q = torch.cat([_round8(p * (448.0 / t)) for p, t in zip(parts, tops)], dim=1)
+        return (q, torch.cat(tops, dim=1) / 448.0, *new)
+    if c["form"] == "fwd":
+        return y if not new else (y, *new)
+    dy = s["dy"].double()
+    n = h * r
+    gw = dy * w
+    dx = (gw - n * ((gw * n).sum(1, keepdim=True) / c["d"])) * r
+    if s["dh"] is not None:
+        dx = dx + s["dh"].double()
+    return (y, *new, dx, *([dx] if new else []), torch.sum(dy * n, dim=0))
+
+
+def _route64(s):
+    c = s["case"]
+    z = s["z"].double()
+    T, E, k, G = c["T"], c["E"], c["k"], c["groups"]
+    sc = torch.sigmoid(z) if c["scoring"] == "sigmoid" else torch.softmax(z, dim=1)
+    key = sc.float()
+    if s["bias"] is not None:
+        key = key + s["bias"]
+    if c["topk_groups"] < G:
+        two = torch.topk(key.reshape(T, G, -1), min(2, E // G), dim=2).values.sum(2)
+        order = torch.argsort(two, dim=1, descending=True, stable=True)
+        worst = torch.argsort(order, dim=1) >= c["topk_groups"]
+        key = torch.where(worst.unsqueeze(2), -math.inf, key.reshape(T, G, -1)).reshape(T, E)
+    idx = torch.argsort(key, dim=1, descending=True, stable=True)[:, :k]
+    idx = torch.sort(idx, dim=1).values
+    hot = torch.zeros(T, E, dtype=torch.float64, device=z.device)
+    hot[torch.arange(T, device=z.device).unsqueeze(1), idx] = 1.0
+    part = sc * hot
+    mass = part.sum(1, keepdim=True) + 1e-20
+    scale = c["scaling"] if c["scaling"] else 1.0
+    weight = part * scale / (mass if c["normalize"] else 1.0)
+    p = torch.gather(weight, 1, idx)
+    if c["form"] == "fwd":
+        return p, None
+    up = torch.zeros_like(sc).scatter(1, idx, s["dp"].double())
+    if c["normalize"]:
+        dsc = hot * scale * (up * mass - (up * part).sum(1, keepdim=True)) / mass.square()
+    else:
+        dsc = hot * scale * up
+    if c["scoring"] == "sigmoid":
+        return p, None, dsc * sc * (1.0 - sc)
+    return p, None, sc * dsc - sc * (sc * dsc).sum(1, keepdim=True)
+
+
+def _quant64(x):
+    """The values that x stands for in 4 bits, by the nearest of the eight magnitudes (of two equally near, the one with the even code)."""
+    v = x.double().reshape(-1, MX)
+    top = v.abs().amax(1, keepdim=True)
+    scale = torch.exp2((torch.floor(torch.log2(top.clamp(min=2.0 ** -126))) - 2).clamp(min=-127.0))
+    u = (v / scale).abs()
+    mags = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+    out = torch.zeros_like(u)
+    for i in range(1, 8):  # up from the value below at the middle between them: at it where this code is even
+        mid = (mags[i - 1] + mags[i]) / 2
+        out = torch.where(u >= mid if i % 2 == 0 else u > mid, mags[i], out)
+    return (torch.copysign(out, v) * scale).reshape(x.shape)
+
+
+_MAGS = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0)
+
+
+def _decode64(q, scale):
+    table = torch.tensor(_MAGS, dtype=torch.float64, device=q.device)
+    v = torch.empty(*q.shape[:-1], 2 * q.shape[-1], dtype=torch.float64, device=q.device)
+    v[..., 0::2] = table[(q % 16).long()]
+    v[..., 1::2] = table[(q // 16).long()]
+    return v * torch.repeat_interleave(torch.pow(2.0, scale.double() - 127.0), MX, dim=-1)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    with torch.no_grad():
+        if op == "norm":
+            return _norm64(s)
+        if op == "route":
+            return _route64(s)
+        if op == "quant":
+            return _quant64(s["x"])
+        a = _decode64(s["a"], s["sa"])
+        if op == "matmul":
+            return torch.matmul(a, _decode64(s["b"], s["sb"]).t().contiguous())
+        off = s["offsets"].tolist()
+        y = torch.empty(s["rows"].numel(), case["N"], dtype=torch.float64, device=a.device)
+        for e in range(case["E"]):
+            if off[e + 1] > off[e]:
+                b = _decode64(s["b"][e], s["sb"][e]).t().contiguous()
+                y[off[e]:off[e + 1]] = torch.matmul(a[s["rows"][off[e]:off[e + 1]].long()], b)
+        return y

@@ -13,8 +13,11 @@ parameter-golf pull request 1105 page, the LeakyReLU(0.5)^2 MLP with a stored
 activation gradient (leaky_mlp_fwd / leaky_mlp_bwd); and, from the FlashFFN
 README, the multi-head sub-network FFN core (mhffn_fwd / mhffn_bwd).  Beside
 them: the feed-forward products in 8-bit floating point with block scales
-(fp8_quantize, fp8_quantize_weight, fp8_matmul, fp8_linear) and the whole
-expert layer for a few tokens (moe_decode).
+(fp8_quantize, fp8_quantize_weight, fp8_matmul, fp8_linear), the whole expert
+layer for a few tokens (moe_decode), and the steps around and inside an expert
+block of any size: the norm before it (rms_norm, rms_norm_quantize), routing
+with groups and a gradient (topk_routing), and 4-bit values with a power of two
+per 32 (mxfp4_quantize, mxfp4_dequantize).
 """
 from __future__ import annotations
 
@@ -37,11 +40,15 @@ __all__ = [
     "fp8_quantize", "fp8_quantize_weight", "fp8_matmul", "fp8_matmul_workspace_size", "fp8_linear",
     "fp8_linear_workspace_size", "fp8_linear_fwd", "fp8_linear_bwd",
     "moe_decode", "moe_decode_supported", "moe_decode_workspace_size", "moe_decode_set_patience",
+    "rms_norm", "rms_norm_fwd", "rms_norm_bwd", "rms_norm_bwd_workspace_size", "rms_norm_quantize",
+    "topk_routing", "topk_routing_fwd", "topk_routing_bwd", "topk_routing_supported",
+    "mxfp4_quantize", "mxfp4_dequantize",
 ]
 
 ESG_F32 = 0
 ESG_BF16 = 1
 ESG_E4M3 = 2
+ESG_E2M1 = 3
 STATUS_GROUP_OUT_OF_RANGE = 1
 STATUS_GROUP_DUPLICATE = 2
 
@@ -50,6 +57,7 @@ _LIB = None
 
 _c_int, _c_size, _c_vp, _c_f = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
 _c_i32p = ctypes.POINTER(ctypes.c_int32)
+_c_i64 = ctypes.c_int64
 
 # name -> (restype, argtypes)
 _SIGNATURES = {
@@ -111,6 +119,20 @@ _SIGNATURES = {
                                 _c_int, _c_int, _c_int, _c_int, _c_f, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_size,
                                 _c_vp]),
     "esg_moe_decode_set_patience": (_c_int, [_c_int]),
+    "esg_rms_norm_fwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_f, _c_vp, _c_vp, _c_vp,
+                                  _c_vp]),
+    "esg_rms_norm_quant": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_f, _c_int, _c_vp, _c_vp,
+                                    _c_vp, _c_vp]),
+    "esg_rms_norm_bwd_workspace_size": (_c_int, [_c_int, _c_int, ctypes.POINTER(_c_size)]),
+    "esg_rms_norm_bwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_vp, _c_vp,
+                                  _c_vp, _c_size, _c_vp]),
+    "esg_topk_routing_supported": (_c_int, [_c_int, _c_int, _c_int, _c_int]),
+    "esg_topk_routing_fwd": (_c_int, [_c_vp, _c_int, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                      _c_int, _c_f, _c_vp, _c_vp, _c_vp]),
+    "esg_topk_routing_bwd": (_c_int, [_c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_f, _c_vp,
+                                      _c_vp]),
+    "esg_mxfp4_quant": (_c_int, [_c_vp, _c_int, _c_i64, _c_int, _c_vp, _c_vp, _c_vp]),
+    "esg_mxfp4_dequant": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_int, _c_vp, _c_vp]),
     "esg_mfma_rate_probe": (_c_int, [_c_int, _c_int, _c_vp, _c_vp]),
     "esg_timing_enable": (_c_int, [_c_int]),
     "esg_timing_reset": (_c_int, []),
@@ -793,6 +815,270 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
         _dev(y, "y", bf, gpu), _dev(probs, "probs", f32, gpu), _dev(indices, "indices", torch.int64, gpu),
         ws.data_ptr(), ws.numel(), _stream(dev)), "moe_decode")
     return y, probs, indices
+
+
+def _norm_args(x, weight, residual):
+    """(tokens, d, device, GPU) of a norm's inputs, checked."""
+    if x.dim() < 1 or weight.dim() != 1 or x.shape[-1] != weight.shape[0]:
+        raise EsgError("x must be [..., d] and weight [d]")
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+        raise EsgError("residual must have the shape and dtype of x")
+    d = x.shape[-1]
+    return x.numel() // d if d else 0, d, x.device, x.get_device()
+
+
+def _like(out, x, name):
+    if out is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise EsgError(f"{name} must have the shape and dtype of x")
+    return out
+
+
+def rms_norm_fwd(x, weight, residual=None, eps: float = 1e-6, need_rstd: bool = True, out=None, residual_out=None):
+    """RMS norm after the residual's addition -> (y, h, rstd) (see rms_norm).
+
+    x, residual: [..., d] and weight: [d], float32 or bfloat16.  h = x + residual is
+    the new residual (x itself without one); rstd: float32 [tokens] for
+    rms_norm_bwd (None without ``need_rstd``).  ``out`` may be x, and ``residual_out``
+    residual or x."""
+    T, d, dev, gpu = _norm_args(x, weight, residual)
+    y = _like(out, x, "out")
+    h = None
+    if residual is not None:
+        h = _like(residual_out, x, "residual_out")
+    elif residual_out is not None:
+        raise EsgError("residual_out needs a residual")
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if need_rstd else None
+    _check(lib().esg_rms_norm_fwd(
+        _dev(x, "x"), _dev(residual, "residual", None, gpu), _dev(weight, "weight", None, gpu), _dtype_code(x),
+        _dtype_code(weight), T, d, eps, _dev(y, "out", None, gpu), _dev(h, "residual_out", None, gpu),
+        None if rstd is None else rstd.data_ptr(), _stream(dev)), "rms_norm_fwd")
+    return y, x if h is None else h, rstd
+
+
+@functools.lru_cache(maxsize=4096)
+def rms_norm_bwd_workspace_size(tokens: int, d_model: int) -> int:
+    """Bytes of scratch the weight gradient of rms_norm needs."""
+    need = _c_size()
+    _check(lib().esg_rms_norm_bwd_workspace_size(tokens, d_model, ctypes.byref(need)), "rms_norm_bwd_workspace_size")
+    return need.value
+
+
+def rms_norm_bwd(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspace: Optional[dict] = None):
+    """(dx, dw) of rms_norm: dx (of x and of the residual alike) in the dtype of h, dw in
+    that of weight (None without ``need_dw``).
+
+    h, rstd: of the forward (h: x where there was no residual); dh: the gradient of
+    the new residual (None: zero).  ``workspace``: optional dict reused across calls to
+    hold the scratch buffer (one per stream)."""
+    T, d, dev, gpu = _norm_args(h, weight, None)
+    for name, t in (("dy", dy), ("dh", dh)):
+        if t is not None and (t.shape != h.shape or t.dtype != h.dtype):
+            raise EsgError(f"{name} must have the shape and dtype of h")
+    if rstd.shape != (T,):
+        raise EsgError("rstd must be [tokens]")
+    dx = torch.empty_like(h, memory_format=torch.contiguous_format)
+    dw = ws = None
+    if need_dw:
+        dw = torch.empty_like(weight)
+        ws = _ws(rms_norm_bwd_workspace_size(T, d), dev, workspace, "rms_norm_bwd")
+    _check(lib().esg_rms_norm_bwd(
+        _dev(dy, "dy", None, gpu), _dev(dh, "dh", None, gpu), _dev(h, "h"), _dev(weight, "weight", None, gpu),
+        _dev(rstd, "rstd", torch.float32, gpu), _dtype_code(h), _dtype_code(weight), T, d, dx.data_ptr(),
+        None if dw is None else dw.data_ptr(), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+        _stream(dev)), "rms_norm_bwd")
+    return dx, dw
+
+
+def _whole(t):
+    """t, or a copy where it is not contiguous at a 16-byte aligned address."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(fctx, x, weight, residual, eps):
+        y, h, rstd = rms_norm_fwd(_whole(x), _whole(weight), None if residual is None else _whole(residual), eps)
+        fctx.save_for_backward(h, weight, rstd)
+        fctx.set_materialize_grads(False)
+        return y if residual is None else (y, h)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(fctx, dy, dh=None):
+        h, weight, rstd = fctx.saved_tensors
+        need_x, need_w, need_r, _ = fctx.needs_input_grad
+        if dy is None:  # only the new residual was used
+            return dh if need_x else None, None, dh if need_r else None, None
+        dx, dw = rms_norm_bwd(_whole(dy), h, _whole(weight), rstd, None if dh is None else _whole(dh), need_w)
+        return dx if need_x else None, dw, dx if need_r else None, None
+
+
+def rms_norm(x, weight, residual=None, eps: float = 1e-6):
+    """Differentiable root-mean-square norm after the residual's addition.
+
+    h = x + residual (rounded to their dtype), y = h (mean h^2 + eps)^-1/2 weight -> y,
+    or (y, h) with a residual: h is the new one.  x, residual: [..., d], float32 or
+    bfloat16, d a multiple of 16, at most 16384; weight: [d], float32 or bfloat16."""
+    _norm_args(x, weight, residual)
+    if not torch.is_grad_enabled():
+        y, h, _ = rms_norm_fwd(_whole(x), _whole(weight), None if residual is None else _whole(residual), eps, False)
+        return y if residual is None else (y, h)
+    return _RmsNorm.apply(x, weight, residual, eps)
+
+
+def rms_norm_quantize(x, weight, residual=None, eps: float = 1e-6, format: str = "fp8", residual_out=None):
+    """rms_norm whose float32 y leaves quantised -> (q, scale), or (q, scale, h) with a residual.
+
+    ``format`` "fp8": q float8_e4m3fn [..., d], scale float32 [..., ceil(d/128)] as of
+    fp8_quantize; "mxfp4": q uint8 [..., d/2], scale uint8 [..., d/32] as of
+    mxfp4_quantize (d a multiple of 32).  No gradient.  ``residual_out`` may be
+    residual or x."""
+    T, d, dev, gpu = _norm_args(x, weight, residual)
+    lead = x.shape[:-1]
+    if format == "fp8":
+        code = ESG_E4M3
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        scale = torch.empty(*lead, _ceil128(d), dtype=torch.float32, device=dev)
+    elif format == "mxfp4":
+        code = ESG_E2M1
+        q = torch.empty(*lead, d // 2, dtype=torch.uint8, device=dev)
+        scale = torch.empty(*lead, d // 32, dtype=torch.uint8, device=dev)
+    else:
+        raise EsgError('format must be "fp8" or "mxfp4"')
+    h = None
+    if residual is not None:
+        h = _like(residual_out, x, "residual_out")
+    elif residual_out is not None:
+        raise EsgError("residual_out needs a residual")
+    _check(lib().esg_rms_norm_quant(
+        _dev(x, "x"), _dev(residual, "residual", None, gpu), _dev(weight, "weight", None, gpu), _dtype_code(x),
+        _dtype_code(weight), T, d, eps, code, q.data_ptr(), scale.data_ptr(), _dev(h, "residual_out", None, gpu),
+        _stream(dev)), "rms_norm_quantize")
+    return (q, scale) if residual is None else (q, scale, h)
+
+
+_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def topk_routing_supported(num_experts: int, topk: int, groups: int = 1, topk_groups: Optional[int] = None) -> bool:
+    """Whether topk_routing takes this shape (topk <= 32, at most 1024 experts and 64 groups; see include/esg.h)."""
+    return bool(lib().esg_topk_routing_supported(num_experts, topk, groups, groups if topk_groups is None else topk_groups))
+
+
+def _scoring_code(scoring: str) -> int:
+    if scoring not in _SCORES:
+        raise EsgError('scoring must be "softmax" or "sigmoid"')
+    return _SCORES[scoring]
+
+
+def topk_routing_fwd(logits, topk: int, scoring: str = "softmax", expert_bias=None, groups: int = 1,
+                     topk_groups: Optional[int] = None, normalize: bool = True, scaling_factor: Optional[float] = None,
+                     out=None):
+    """(probs float32 [T, topk], indices int32 [T, topk]) of topk_routing; ``out`` may supply both."""
+    if logits.dim() != 2:
+        raise EsgError("logits must be [tokens, num_experts]")
+    T, E = logits.shape
+    dev, gpu = logits.device, logits.get_device()
+    stride = 1
+    if expert_bias is not None:
+        if expert_bias.dim() != 1 or expert_bias.shape[0] != E or expert_bias.dtype != torch.float32:
+            raise EsgError("expert_bias must be float32 [num_experts]")
+        if not expert_bias.is_cuda or expert_bias.get_device() != gpu:
+            raise EsgError("expert_bias must be on the logits' GPU")
+        stride = expert_bias.stride(0) if E > 1 else 1
+        if stride < 1:
+            raise EsgError("expert_bias must have a positive stride")
+    code = _scoring_code(scoring)
+    if out is None:
+        probs = torch.empty(T, topk, dtype=torch.float32, device=dev)
+        indices = torch.empty(T, topk, dtype=torch.int32, device=dev)
+    else:
+        probs, indices = out
+        if probs.shape != (T, topk) or indices.shape != (T, topk):
+            raise EsgError("out must be two [tokens, topk] tensors")
+    _check(lib().esg_topk_routing_fwd(
+        _dev(logits, "logits"), _dtype_code(logits), None if expert_bias is None else expert_bias.data_ptr(), stride, T, E,
+        topk, code, groups, groups if topk_groups is None else topk_groups, int(normalize),
+        1.0 if scaling_factor is None else float(scaling_factor), _dev(probs, "probs", torch.float32, gpu),
+        _dev(indices, "indices", torch.int32, gpu), _stream(dev)), "topk_routing")
+    return probs, indices
+
+
+def topk_routing_bwd(dprobs, logits, indices, scoring: str = "softmax", normalize: bool = True,
+                     scaling_factor: Optional[float] = None):
+    """dlogits [T, E] (the dtype of logits) from the gradient of topk_routing's probs and its indices."""
+    if logits.dim() != 2 or indices.dim() != 2 or indices.shape[0] != logits.shape[0] or dprobs.shape != indices.shape:
+        raise EsgError("logits must be [tokens, num_experts], dprobs and indices [tokens, topk]")
+    T, E = logits.shape
+    dev, gpu = logits.device, logits.get_device()
+    dz = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    _check(lib().esg_topk_routing_bwd(
+        _dev(dprobs, "dprobs", torch.float32, gpu), _dev(logits, "logits"), _dtype_code(logits),
+        _dev(indices, "indices", torch.int32, gpu), T, E, indices.shape[1], _scoring_code(scoring), int(normalize),
+        1.0 if scaling_factor is None else float(scaling_factor), dz.data_ptr(), _stream(dev)), "topk_routing_bwd")
+    return dz
+
+
+class _TopkRouting(torch.autograd.Function):
+    @staticmethod
+    def forward(fctx, logits, topk, scoring, expert_bias, groups, topk_groups, normalize, scaling_factor):
+        logits = logits.contiguous()
+        probs, indices = topk_routing_fwd(logits, topk, scoring, expert_bias, groups, topk_groups, normalize,
+                                          scaling_factor)
+        fctx.save_for_backward(logits, indices)
+        fctx.esg = (scoring, normalize, scaling_factor)
+        fctx.mark_non_differentiable(indices)
+        return probs, indices
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(fctx, dprobs, _):
+        logits, indices = fctx.saved_tensors
+        return (topk_routing_bwd(dprobs.contiguous(), logits, indices, *fctx.esg),) + (None,) * 7
+
+
+def topk_routing(logits, topk: int, scoring: str = "softmax", expert_bias=None, groups: int = 1,
+                 topk_groups: Optional[int] = None, normalize: bool = True, scaling_factor: Optional[float] = None):
+    """Differentiable routing -> (probs float32 [T, topk], indices int32 [T, topk]).
+
+    Per row of logits (float32 or bfloat16 [T, E]): the topk experts with the largest
+    score + bias, in ascending order, of the ``topk_groups`` groups whose two largest keys
+    have the largest sum (all groups by default), ties to the lower number; their scores
+    (``scoring`` "softmax" or "sigmoid"), divided by their sum with ``normalize`` and times
+    ``scaling_factor``.  expert_bias: float32 [E] (a strided view is accepted), for the
+    choice only.  The gradient goes through the weights to the logits."""
+    if not torch.is_grad_enabled() or not logits.requires_grad:
+        return topk_routing_fwd(logits.contiguous(), topk, scoring, expert_bias, groups, topk_groups, normalize,
+                                scaling_factor)
+    return _TopkRouting.apply(logits, topk, scoring, expert_bias, groups, topk_groups, normalize, scaling_factor)
+
+
+def mxfp4_quantize(x):
+    """x (float32 or bfloat16 [..., K], K a multiple of 32) to 4-bit floating point with a power
+    of two per 32 elements -> (q uint8 [..., K/2], two codes a byte, the first in the low half;
+    scale uint8 [..., K/32], a biased exponent each)."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise EsgError("x must be [..., K]")
+    K, dev = x.shape[-1], x.device
+    q = torch.empty(*x.shape[:-1], K // 2, dtype=torch.uint8, device=dev)
+    scale = torch.empty(*x.shape[:-1], K // 32, dtype=torch.uint8, device=dev)
+    _check(lib().esg_mxfp4_quant(_dev(x, "x"), _dtype_code(x), x.numel() // K, K, q.data_ptr(), scale.data_ptr(),
+                                 _stream(dev)), "mxfp4_quantize")
+    return q, scale
+
+
+def mxfp4_dequantize(q, scale, dtype=torch.bfloat16):
+    """The values that mxfp4_quantize's q and scale stand for, [..., K] in float32 or bfloat16 (exact in both)."""
+    if q.dim() < 1 or q.dim() != scale.dim() or q.shape[:-1] != scale.shape[:-1] or q.shape[-1] != 16 * scale.shape[-1]:
+        raise EsgError("q must be [..., K/2] and scale [..., K/32]")
+    K, dev, u8 = 2 * q.shape[-1], q.device, torch.uint8
+    y = torch.empty(*q.shape[:-1], K, dtype=dtype, device=dev)
+    _check(lib().esg_mxfp4_dequant(_dev(q, "q", u8), _dev(scale, "scale", u8, q.get_device()), _dtype_code(y),
+                                   q.numel() * 2 // K if K else 0, K, y.data_ptr(), _stream(dev)), "mxfp4_dequantize")
+    return y
 
 
 def mfma_rate_probe(blocks: int, iters: int, out: torch.Tensor) -> None:

@@ -678,6 +678,142 @@ int esg_fp8_linear_bwd(const void* dy, int x_dtype, int w_dtype, int tokens, int
   return hip_status(h);
 }
 
+// ---- root-mean-square norm -------------------------------------------------------
+namespace {
+bool float_dtype(int t) { return t == ESG_F32 || t == ESG_BF16; }
+int norm_shape(int dtype, int w_dtype, int tokens, int d) {
+  if (tokens < 0 || d <= 0) return ESG_ERR_INVALID_ARG;
+  if (!float_dtype(dtype) || !float_dtype(w_dtype)) return ESG_ERR_UNSUPPORTED;
+  return d % 16 != 0 || d > kNormMaxWidth ? ESG_ERR_UNSUPPORTED : ESG_OK;
+}
+// x, w and y present, residual and h together, everything aligned
+int norm_args(const void* x, const void* residual, const void* w, const void* y, const void* h) {
+  if (x == nullptr || w == nullptr || y == nullptr || (residual == nullptr) != (h == nullptr)) return ESG_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, w, y, h})
+    if (!aligned16(p)) return ESG_ERR_INVALID_ARG;
+  return ESG_OK;
+}
+}  // namespace
+
+int esg_rms_norm_fwd(const void* x, const void* residual, const void* w, int dtype, int w_dtype, int tokens, int d_model,
+                     float eps, void* y, void* h, float* rstd, void* stream) {
+  int e = norm_shape(dtype, w_dtype, tokens, d_model);
+  if (e != ESG_OK || tokens == 0) return e;
+  e = norm_args(x, residual, w, y, h);
+  if (e != ESG_OK) return e;
+  if (((uintptr_t)rstd & 3u) != 0) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_rms_norm(dtype, w_dtype, x, residual, w, tokens, d_model, eps, kNormSame, y, nullptr, h, rstd,
+                                    (hipStream_t)stream));
+}
+
+int esg_rms_norm_quant(const void* x, const void* residual, const void* w, int dtype, int w_dtype, int tokens,
+                       int d_model, float eps, int q_dtype, void* q, void* scale, void* h, void* stream) {
+  int e = norm_shape(dtype, w_dtype, tokens, d_model);
+  if (e != ESG_OK) return e;
+  if ((q_dtype != ESG_E4M3 && q_dtype != ESG_E2M1) || (q_dtype == ESG_E2M1 && d_model % 32 != 0))
+    return ESG_ERR_UNSUPPORTED;
+  if (tokens == 0) return ESG_OK;
+  e = norm_args(x, residual, w, q, h);
+  if (e != ESG_OK) return e;
+  if (scale == nullptr || (q_dtype == ESG_E4M3 && ((uintptr_t)scale & 3u) != 0)) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_rms_norm(dtype, w_dtype, x, residual, w, tokens, d_model, eps,
+                                    q_dtype == ESG_E4M3 ? kNormE4m3 : kNormMx, q, scale, h, nullptr,
+                                    (hipStream_t)stream));
+}
+
+int esg_rms_norm_bwd_workspace_size(int tokens, int d_model, size_t* workspace_bytes) {
+  if (workspace_bytes == nullptr) return ESG_ERR_INVALID_ARG;
+  const int e = norm_shape(ESG_BF16, ESG_BF16, tokens, d_model);
+  if (e != ESG_OK) return e;
+  *workspace_bytes = rms_norm_bwd_bytes(tokens, d_model);
+  return ESG_OK;
+}
+
+int esg_rms_norm_bwd(const void* dy, const void* dh, const void* h, const void* w, const float* rstd, int dtype,
+                     int w_dtype, int tokens, int d_model, void* dx, void* dw, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  const int e = norm_shape(dtype, w_dtype, tokens, d_model);
+  if (e != ESG_OK) return e;
+  if (tokens > 0) {
+    if (dy == nullptr || h == nullptr || w == nullptr || rstd == nullptr || dx == nullptr) return ESG_ERR_INVALID_ARG;
+    for (const void* p : {dy, dh, h, w, (const void*)dx})
+      if (!aligned16(p)) return ESG_ERR_INVALID_ARG;
+    if (((uintptr_t)rstd & 3u) != 0) return ESG_ERR_INVALID_ARG;
+    if (dw != nullptr && (workspace == nullptr || workspace_bytes < rms_norm_bwd_bytes(tokens, d_model)))
+      return ESG_ERR_WORKSPACE;
+  }
+  if (!aligned16(dw) || !aligned16(workspace)) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_rms_norm_bwd(dtype, w_dtype, dy, dh, h, w, rstd, tokens, d_model, dx, dw, workspace,
+                                        (hipStream_t)stream));
+}
+
+// ---- routing with groups and gradients --------------------------------------------
+namespace {
+int routing_shape(int dtype, int tokens, int experts, int topk, int scoring, int groups, int topk_groups) {
+  if (tokens < 0) return ESG_ERR_INVALID_ARG;
+  if (!float_dtype(dtype) || (scoring != ESG_SCORE_SIGMOID && scoring != ESG_SCORE_SOFTMAX)) return ESG_ERR_UNSUPPORTED;
+  if (!topk_routing_supported(experts, topk, groups, topk_groups)) return ESG_ERR_UNSUPPORTED;
+  // positions are int32; a row takes 16 threads, or 64 above 256 experts' slots, and a launch fewer than 2^32
+  return (long long)tokens * topk >= (1ll << 31) || tokens >= (1 << 26) ? ESG_ERR_UNSUPPORTED : ESG_OK;
+}
+}  // namespace
+
+int esg_topk_routing_supported(int num_experts, int topk, int groups, int topk_groups) {
+  return topk_routing_supported(num_experts, topk, groups, topk_groups) ? 1 : 0;
+}
+
+int esg_topk_routing_fwd(const void* logits, int dtype, const float* expert_bias, int bias_stride, int tokens,
+                         int num_experts, int topk, int scoring, int groups, int topk_groups, int normalize,
+                         float scaling_factor, float* probs, int32_t* indices, void* stream) {
+  const int e = routing_shape(dtype, tokens, num_experts, topk, scoring, groups, topk_groups);
+  if (e != ESG_OK || tokens == 0) return e;
+  if (logits == nullptr || probs == nullptr || indices == nullptr || (expert_bias != nullptr && bias_stride < 1))
+    return ESG_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)expert_bias, (const void*)probs, (const void*)indices})
+    if (((uintptr_t)p & 3u) != 0) return ESG_ERR_INVALID_ARG;
+  if (((uintptr_t)logits & (dtype == ESG_F32 ? 3u : 1u)) != 0) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_topk_routing(dtype, logits, expert_bias, bias_stride, tokens, num_experts, topk, scoring,
+                                        groups, topk_groups, normalize != 0, scaling_factor, probs, indices,
+                                        (hipStream_t)stream));
+}
+
+int esg_topk_routing_bwd(const float* dprobs, const void* logits, int dtype, const int32_t* indices, int tokens,
+                         int num_experts, int topk, int scoring, int normalize, float scaling_factor, void* dlogits,
+                         void* stream) {
+  const int e = routing_shape(dtype, tokens, num_experts, topk, scoring, 1, 1);
+  if (e != ESG_OK || tokens == 0) return e;
+  if (dprobs == nullptr || logits == nullptr || indices == nullptr || dlogits == nullptr) return ESG_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)dprobs, (const void*)indices})
+    if (((uintptr_t)p & 3u) != 0) return ESG_ERR_INVALID_ARG;
+  for (const void* p : {logits, (const void*)dlogits})
+    if (((uintptr_t)p & (dtype == ESG_F32 ? 3u : 1u)) != 0) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_topk_routing_bwd(dprobs, dtype, logits, indices, tokens, num_experts, topk, scoring,
+                                            normalize != 0, scaling_factor, dlogits, (hipStream_t)stream));
+}
+
+// ---- 4-bit floating point ------------------------------------------------------------
+namespace {
+int mx_rows(int dtype, int64_t rows, int cols) {
+  if (rows < 0 || cols <= 0) return ESG_ERR_INVALID_ARG;
+  if (!float_dtype(dtype)) return ESG_ERR_UNSUPPORTED;
+  return cols % 32 != 0 || cols > (1 << 22) || rows > (1ll << 40) / cols ? ESG_ERR_UNSUPPORTED : ESG_OK;
+}
+}  // namespace
+
+int esg_mxfp4_quant(const void* x, int dtype, int64_t rows, int cols, void* q, void* scale, void* stream) {
+  const int e = mx_rows(dtype, rows, cols);
+  if (e != ESG_OK || rows == 0) return e;
+  if (x == nullptr || q == nullptr || scale == nullptr || !aligned16(x) || !aligned16(q)) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_mx_quant(dtype, x, rows * (cols / 32), q, scale, (hipStream_t)stream));
+}
+
+int esg_mxfp4_dequant(const void* q, const void* scale, int dtype, int64_t rows, int cols, void* y, void* stream) {
+  const int e = mx_rows(dtype, rows, cols);
+  if (e != ESG_OK || rows == 0) return e;
+  if (y == nullptr || q == nullptr || scale == nullptr || !aligned16(y) || !aligned16(q)) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_mx_dequant(dtype, q, scale, rows * (cols / 32), y, (hipStream_t)stream));
+}
+
 int esg_moe_decode_supported(int tokens, int experts, int topk, int d_model, int d_ff, int w_dtype) {
   return tokens >= 0 && tokens <= kMoeMaxTokens && experts >= 1 && experts <= kMoeMaxExperts && topk >= 1 &&
          topk <= kRouteMaxK && topk <= experts && d_model >= 16 && d_model % 16 == 0 && d_model <= (1 << 17) &&

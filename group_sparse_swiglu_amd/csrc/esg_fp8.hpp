@@ -1,5 +1,5 @@
-// Device building blocks of the 8-bit (e4m3) kernels: conversions, the block
-// scale, and the 16 x 16 x 128 matrix product.
+// Device building blocks of the 8-bit (e4m3) kernels: reads of eight elements,
+// conversions, the block scale, and the 16 x 16 x 128 matrix product.
 #pragma once
 
 #include "esg_device.hpp"
@@ -29,6 +29,76 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
   return (uint32_t)w;
+}
+
+// Eight consecutive elements as floats, and the largest magnitude's bits.
+template <typename T>
+struct Oct;
+template <>
+struct Oct<bf16_t> {
+  uint4 w;
+  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const bf16_t* p) { w = *(const uint4*)p; }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Oct<float> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = *(const float4*)p;
+    b = *(const float4*)(p + 4);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]);
+template <>
+__device__ __forceinline__ void store8<bf16_t>(bf16_t* p, const float (&v)[8]) {
+  *(uint4*)p = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                          pack_bf16x2(v[6], v[7]));
+}
+template <>
+__device__ __forceinline__ void store8<float>(float* p, const float (&v)[8]) {
+  *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+  *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+__device__ __forceinline__ uint32_t max8(const float (&v)[8]) {
+  uint32_t m = mag(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = umax(m, mag(v[i]));
+  return m;
+}
+
+// Maximum over the 16 lanes of a row group (lanes 16g .. 16g + 15), left in all
+// of them: exchanges inside quads (xor 1, xor 2), then mirrored half rows and
+// rows, all in the vector unit's data-parallel moves.
+__device__ __forceinline__ uint32_t max_lanes16(uint32_t m) {
+  m = umax(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, true));
+  m = umax(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, true));
+  m = umax(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xf, 0xf, true));
+  m = umax(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xf, 0xf, true));
+  return m;
+}
+
+__device__ __forceinline__ uint2 scale_pack8(const float (&v)[8], float inv) {
+  return make_uint2(pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    pack_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
 
 // 16 x 16 x 128 product of e4m3 operands on zero: lane l gives 32 bytes of row

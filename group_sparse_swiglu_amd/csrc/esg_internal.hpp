@@ -194,6 +194,31 @@ size_t fp8_matmul_workspace_bytes(int M, int N, int K);
 hipError_t launch_fp8_matmul(const void* a, const float* sa, const void* b, const float* sb, int sb_rows, int out_dtype,
                              int M, int N, int K, void* y, void* workspace, hipStream_t stream);
 
+// ---- root-mean-square norm with the residual's addition (esg_norm.hip) ----------
+enum { kNormSame = 0, kNormE4m3 = 1, kNormMx = 2 };  // form of y
+constexpr int kNormMaxWidth = 16384;                 // a row in the registers of 256 threads
+hipError_t launch_rms_norm(int dtype, int w_dtype, const void* x, const void* residual, const void* w, int rows, int d,
+                           float eps, int y_format, void* y, void* scale, void* h, float* rstd, hipStream_t stream);
+size_t rms_norm_bwd_bytes(int rows, int d);
+// dw NULL: not computed, and no workspace needed
+hipError_t launch_rms_norm_bwd(int dtype, int w_dtype, const void* dy, const void* dh, const void* h, const void* w,
+                               const float* rstd, int rows, int d, void* dx, void* dw, void* workspace,
+                               hipStream_t stream);
+
+// ---- routing with groups and gradients (esg_topk.hip) ----------------------------
+bool topk_routing_supported(int experts, int topk, int groups, int topk_groups);
+hipError_t launch_topk_routing(int dtype, const void* logits, const float* bias, int bias_stride, int tokens,
+                               int experts, int topk, int scoring, int groups, int topk_groups, int normalize,
+                               float scaling, float* probs, int32_t* idx, hipStream_t stream);
+hipError_t launch_topk_routing_bwd(const float* dprobs, int dtype, const void* logits, const int32_t* idx, int tokens,
+                                   int experts, int topk, int scoring, int normalize, float scaling, void* dlogits,
+                                   hipStream_t stream);
+
+// ---- 4-bit floating point in blocks of 32 (esg_mx_quant.hip) -----------------------
+hipError_t launch_mx_quant(int dtype, const void* x, int64_t blocks, void* q, void* scale, hipStream_t stream);
+hipError_t launch_mx_dequant(int dtype, const void* q, const void* scale, int64_t blocks, void* y,
+                             hipStream_t stream);
+
 // ---- whole expert layer for a few tokens (esg_moe.hip) --------------------------
 constexpr int kMoeMaxTokens = 64;     // a 64-bit token set per expert
 constexpr int kMoeMaxExperts = 1024;

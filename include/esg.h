@@ -52,6 +52,12 @@ extern "C" {
 #define ESG_BF16 1
 #define ESG_E4M3 2  /* 8-bit floating point (1 sign, 4 exponent, 3 fraction bits, no infinity); only where a call says so */
 
+#define ESG_E2M1 3  /* 4-bit floating point (1 sign, 2 exponent, 1 fraction bits: 0 to 6), two to a byte; only where a call says so */
+
+/* scores of esg_topk_routing_* */
+#define ESG_SCORE_SIGMOID 0
+#define ESG_SCORE_SOFTMAX 1
+
 /* bits OR-ed into the optional device status word by the bucketing pass */
 #define ESG_STATUS_GROUP_OUT_OF_RANGE 1   /* an id < 0 or >= G was skipped */
 #define ESG_STATUS_GROUP_DUPLICATE 2      /* a repeated id in one token was skipped */
@@ -473,6 +479,109 @@ int esg_fp8_linear_fwd(const void* x, int x_dtype, const void* w, int w_dtype, i
                        size_t scratch_bytes, void* stream);
 int esg_fp8_linear_bwd(const void* dy, int x_dtype, int w_dtype, int tokens, int d_in, int d_out, const void* saved,
                        size_t saved_bytes, void* dx, void* dw, void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * Root-mean-square norm after the residual's addition:
+ *   h = x + residual, rounded to dtype (without a residual h = x);
+ *   r = (mean over d_model of h^2 + eps)^(-1/2);  y = h r w.
+ * x, residual, y, h: dtype [tokens, d_model]; w: w_dtype [d_model] (ESG_F32 or
+ * ESG_BF16 each, and not the same one necessarily).  residual NULL: h has to be
+ * NULL.  rstd (or NULL): float [tokens], r for the backward.  y may be x, and h
+ * may be residual or x (buffers that overlap otherwise are not allowed).
+ * The sum of squares, r and y's products are float32 (where the squares leave its
+ * range, those of 2^-80 h); each output is rounded once.  A row's result does not
+ * depend on the others (bitwise).
+ *
+ * esg_rms_norm_quant gives the same float32 y in q_dtype instead, as the products
+ * take it: ESG_E4M3, q e4m3 [tokens, d_model] with scale float [tokens,
+ * ceil(d_model/128)] as of esg_fp8_quant_rows; ESG_E2M1, q [tokens, d_model/2]
+ * bytes with scale [tokens, d_model/32] bytes as of esg_mxfp4_quant (d_model a
+ * multiple of 32).
+ *
+ * esg_rms_norm_bwd: with dy = dL/dy and dh = dL/dh (dtype; dh NULL: zero), h (x
+ * where there was no residual) and rstd of the forward, g = dy w:
+ *   dx = dh + r (g - h r^2 mean(g h))   (the gradient of x and of residual alike);
+ *   dw = sum over tokens of dy h r      (w_dtype [d_model]; NULL: not computed).
+ * dx may be dy or dh.  Both are overwritten (tokens == 0: dw is zero).  The sum of g h
+ * over a row has to stay in float32's range.  dw's sum is
+ * float32 in a fixed order (bitwise reproducible).  workspace (16-byte aligned):
+ * esg_rms_norm_bwd_workspace_size() bytes, needed for dw only.
+ * Errors: ESG_ERR_INVALID_ARG (null or misaligned pointer, h without residual or
+ * the reverse, negative tokens, d_model <= 0), ESG_ERR_UNSUPPORTED (a dtype, d_model
+ * not a multiple of 16 or above 16384), ESG_ERR_WORKSPACE.
+ */
+int esg_rms_norm_fwd(const void* x, const void* residual, const void* w, int dtype, int w_dtype, int tokens, int d_model,
+                     float eps, void* y, void* h, float* rstd, void* stream);
+int esg_rms_norm_quant(const void* x, const void* residual, const void* w, int dtype, int w_dtype, int tokens,
+                       int d_model, float eps, int q_dtype, void* q, void* scale, void* h, void* stream);
+int esg_rms_norm_bwd_workspace_size(int tokens, int d_model, size_t* workspace_bytes);
+int esg_rms_norm_bwd(const void* dy, const void* dh, const void* h, const void* w, const float* rstd, int dtype,
+                     int w_dtype, int tokens, int d_model, void* dx, void* dw, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
+ * Routing of tokens to experts, with a gradient.  Per token row of logits z:
+ *   s_e = sigmoid(z_e) (ESG_SCORE_SIGMOID) or softmax(z)_e (ESG_SCORE_SOFTMAX), the
+ *         fp64 value rounded once to fp32;
+ *   key_e = s_e + expert_bias[e * bias_stride], one fp32 addition (expert_bias NULL: s_e);
+ *   the num_experts / groups experts of a group follow each other; a group's rank
+ *   is by the sum of its two largest keys (one fp32 addition; its only key if it has
+ *   one), and the topk_groups best ones stay, equal ones by lower group (all of them
+ *   for topk_groups == groups);
+ *   indices = the topk experts of these with the largest keys, equal ones by lower
+ *   expert, in ascending order;
+ *   probs_j = s_j / (sum of the chosen s + 1e-20) * scaling_factor with normalize, else
+ *   s_j * scaling_factor (float32, to about 2^-20 of its value).
+ * The bias serves the choice only.  A logit of -infinity is an expert of score 0 (a
+ * row of nothing else: softmax scores of 0).  A NaN logit, or with softmax +infinity,
+ * counts as -infinity for the choice and makes its row's probs NaN; a NaN bias counts
+ * as -infinity.  The indices of a row are always topk different experts.  Rows are
+ * independent (bitwise).
+ * logits: dtype (ESG_F32 or ESG_BF16) [tokens, num_experts]; probs: float [tokens,
+ * topk]; indices: int32 [tokens, topk], as esg_bucket_by_group takes them.
+ *
+ * esg_topk_routing_bwd: dlogits (dtype, like logits, overwritten) from dprobs =
+ * dL/dprobs (float, like probs) and the forward's indices.  The choice has no gradient,
+ * the bias none either.  With ds_j the gradient of a chosen score: sigmoid dz_j = ds_j
+ * s_j (1 - s_j), 0 for the others; softmax dz_e = s_e (ds_e - sum over j of s_j ds_j).
+ * An index outside 0..num_experts-1 is skipped; the indices of a row have to differ.
+ *
+ * esg_topk_routing_supported returns 1 when 1 <= topk <= 32, topk_groups is in
+ * 1..groups, num_experts is a multiple of groups, topk <= topk_groups * num_experts /
+ * groups, num_experts <= 1024 and, for topk_groups < groups, groups <= 64 and a group
+ * has at most 16 * 64 / (groups rounded up to a power of two) experts; else 0.
+ * tokens == 0 enqueues nothing.
+ * Errors: ESG_ERR_INVALID_ARG (null pointer, one not aligned to its elements, tokens <
+ * 0, bias_stride < 1), ESG_ERR_UNSUPPORTED (dtype, scoring, a shape outside
+ * esg_topk_routing_supported, tokens * topk >= 2^31 or tokens >= 2^26).
+ */
+int esg_topk_routing_supported(int num_experts, int topk, int groups, int topk_groups);
+int esg_topk_routing_fwd(const void* logits, int dtype, const float* expert_bias, int bias_stride, int tokens,
+                         int num_experts, int topk, int scoring, int groups, int topk_groups, int normalize,
+                         float scaling_factor, float* probs, int32_t* indices, void* stream);
+int esg_topk_routing_bwd(const float* dprobs, const void* logits, int dtype, const int32_t* indices, int tokens,
+                         int num_experts, int topk, int scoring, int normalize, float scaling_factor, void* dlogits,
+                         void* stream);
+
+/*
+ * 4-bit floating point (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives, codes 0
+ * to 7 and, with the sign, 8 to 15) in blocks of 32 elements along a row, each with a
+ * power of two held as a biased exponent byte (2^(byte - 127); 255 is NaN).  With a
+ * the largest magnitude of a block:
+ *   byte = max(biased float32 exponent of a - 2, 0);  q = e2m1(x * 2^(127 - byte)),
+ * to nearest even, at most 6 in magnitude.  A block that holds an infinity or NaN gets
+ * the byte 255 and codes 0.
+ * x: dtype (ESG_F32 or ESG_BF16) [rows, cols]; q: [rows, cols/2] bytes, element 2i in
+ * the low half of byte i; scale: [rows, cols/32] bytes.
+ * esg_mxfp4_dequant gives the values, y: dtype [rows, cols] (exact in both types; NaN
+ * for the byte 255, infinite where 2^(byte - 127) times the element leaves the range).
+ * rows == 0 enqueues nothing.
+ * Errors: ESG_ERR_INVALID_ARG (null pointer, x, y or q not 16-byte aligned, negative
+ * rows, cols <= 0), ESG_ERR_UNSUPPORTED (dtype, cols not a multiple of 32 or above 2^22,
+ * rows * cols above 2^40).
+ */
+int esg_mxfp4_quant(const void* x, int dtype, int64_t rows, int cols, void* q, void* scale, void* stream);
+int esg_mxfp4_dequant(const void* q, const void* scale, int dtype, int64_t rows, int cols, void* y, void* stream);
 
 /*
  * A whole mixture-of-experts feed-forward layer for a few tokens (decode):

@@ -17,7 +17,8 @@ them: the feed-forward products in 8-bit floating point with block scales
 layer for a few tokens (moe_decode), and the steps around and inside an expert
 block of any size: the norm before it (rms_norm, rms_norm_quantize), routing
 with groups and a gradient (topk_routing), and 4-bit values with a power of two
-per 32 (mxfp4_quantize, mxfp4_dequantize).
+per 32 with their products, also by expert (mxfp4_quantize, mxfp4_dequantize,
+mxfp4_matmul, mxfp4_grouped_matmul).
 """
 from __future__ import annotations
 
@@ -42,7 +43,7 @@ __all__ = [
     "moe_decode", "moe_decode_supported", "moe_decode_workspace_size", "moe_decode_set_patience",
     "rms_norm", "rms_norm_fwd", "rms_norm_bwd", "rms_norm_bwd_workspace_size", "rms_norm_quantize",
     "topk_routing", "topk_routing_fwd", "topk_routing_bwd", "topk_routing_supported",
-    "mxfp4_quantize", "mxfp4_dequantize",
+    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_matmul", "mxfp4_matmul_workspace_size", "mxfp4_grouped_matmul",
 ]
 
 ESG_F32 = 0
@@ -133,6 +134,11 @@ _SIGNATURES = {
                                       _c_vp]),
     "esg_mxfp4_quant": (_c_int, [_c_vp, _c_int, _c_i64, _c_int, _c_vp, _c_vp, _c_vp]),
     "esg_mxfp4_dequant": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_int, _c_vp, _c_vp]),
+    "esg_mxfp4_matmul_workspace_size": (_c_int, [_c_int, _c_int, _c_int, ctypes.POINTER(_c_size)]),
+    "esg_mxfp4_matmul": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_vp, _c_vp, _c_size,
+                                  _c_vp]),
+    "esg_mxfp4_grouped_matmul": (_c_int, [_c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_int,
+                                          _c_int, _c_int, _c_vp, _c_vp]),
     "esg_mfma_rate_probe": (_c_int, [_c_int, _c_int, _c_vp, _c_vp]),
     "esg_timing_enable": (_c_int, [_c_int]),
     "esg_timing_reset": (_c_int, []),
@@ -1079,6 +1085,67 @@ def mxfp4_dequantize(q, scale, dtype=torch.bfloat16):
     _check(lib().esg_mxfp4_dequant(_dev(q, "q", u8), _dev(scale, "scale", u8, q.get_device()), _dtype_code(y),
                                    q.numel() * 2 // K if K else 0, K, y.data_ptr(), _stream(dev)), "mxfp4_dequantize")
     return y
+
+
+@functools.lru_cache(maxsize=4096)
+def mxfp4_matmul_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of scratch esg_mxfp4_matmul needs for this shape (0 for most)."""
+    need = _c_size()
+    _check(lib().esg_mxfp4_matmul_workspace_size(M, N, K, ctypes.byref(need)), "mxfp4_matmul_workspace_size")
+    return need.value
+
+
+def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, workspace: Optional[dict] = None):
+    """y = A B^T of 4-bit operands with a power of two per 32 elements -> [M, N] (bfloat16 or float32).
+
+    a, a_scale: [M, K/2] and [M, K/32]; b, b_scale: [N, K/2] and [N, K/32], uint8 as
+    mxfp4_quantize gives them.  ``workspace``: optional dict reused across calls to hold the
+    scratch buffer (one per stream)."""
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise EsgError("a must be [M, K/2] and b [N, K/2]")
+    (M, KH), N, dev, gpu, u8 = a.shape, b.shape[0], a.device, a.get_device(), torch.uint8
+    if a_scale.shape != (M, KH // 16) or b_scale.shape != (N, KH // 16):
+        raise EsgError("a_scale must be [M, K/32] and b_scale [N, K/32]")
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    elif out.shape != (M, N):
+        raise EsgError("out must be [M, N]")
+    code = _dtype_code(out)
+    need = mxfp4_matmul_workspace_size(M, N, 2 * KH)
+    ws = _ws(need, dev, workspace, "mxfp4_matmul") if need else None
+    _check(lib().esg_mxfp4_matmul(_dev(a, "a", u8), _dev(a_scale, "a_scale", u8, gpu), _dev(b, "b", u8, gpu),
+                                  _dev(b_scale, "b_scale", u8, gpu), code, M, N, 2 * KH, _dev(out, "out", None, gpu),
+                                  None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                  _stream(dev)), "mxfp4_matmul")
+    return out
+
+
+def mxfp4_grouped_matmul(a, a_scale, b, b_scale, offsets, rows=None, out_dtype=torch.bfloat16, out=None):
+    """Products of rows in the order of their experts, each with its expert's weights -> [M, N].
+
+    a, a_scale: [R, K/2] and [R, K/32]; b, b_scale: [E, N, K/2] and [E, N, K/32], uint8 as
+    mxfp4_quantize gives them; offsets: int32 [E + 1] and rows: int32 [M], as bucket_by_group
+    gives them: rows offsets[e] .. offsets[e+1] - 1 of the result are a[rows[m]] B[e]^T
+    (a[m] without ``rows``, M = R).  Rows outside all offsets are left as they were in
+    ``out`` (not written at all)."""
+    if a.dim() != 2 or b.dim() != 3 or a.shape[1] != b.shape[2]:
+        raise EsgError("a must be [R, K/2] and b [E, N, K/2]")
+    (R, KH), (experts, N), dev, gpu, u8 = a.shape, b.shape[:2], a.device, a.get_device(), torch.uint8
+    if a_scale.shape != (R, KH // 16) or b_scale.shape != (experts, N, KH // 16):
+        raise EsgError("a_scale must be [R, K/32] and b_scale [E, N, K/32]")
+    if offsets.shape != (experts + 1,) or (rows is not None and rows.dim() != 1):
+        raise EsgError("offsets must be int32 [E + 1] and rows int32 [M]")
+    M = R if rows is None else rows.shape[0]
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    elif out.shape != (M, N):
+        raise EsgError("out must be [M, N]")
+    i32 = torch.int32
+    _check(lib().esg_mxfp4_grouped_matmul(
+        _dev(a, "a", u8), _dev(a_scale, "a_scale", u8, gpu), R, _dev(rows, "rows", i32, gpu), _dev(b, "b", u8, gpu),
+        _dev(b_scale, "b_scale", u8, gpu), experts, _dev(offsets, "offsets", i32, gpu), _dtype_code(out), M, N, 2 * KH,
+        _dev(out, "out", None, gpu), _stream(dev)), "mxfp4_grouped_matmul")
+    return out
 
 
 def mfma_rate_probe(blocks: int, iters: int, out: torch.Tensor) -> None:

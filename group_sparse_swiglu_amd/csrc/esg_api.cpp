@@ -814,6 +814,62 @@ int esg_mxfp4_dequant(const void* q, const void* scale, int dtype, int64_t rows,
   return hip_status(launch_mx_dequant(dtype, q, scale, rows * (cols / 32), y, (hipStream_t)stream));
 }
 
+namespace {
+// Launches of fewer than 2^32 threads, row chunks in a grid's second dimension, 32-bit offsets inside what a workgroup reads.
+int mx_shape(int M, int N, int K, int experts) {
+  if (M < 0 || N < 0 || K <= 0 || experts < 1) return ESG_ERR_INVALID_ARG;
+  if (K % 32 != 0 || K > (1 << 22) || M > (1 << 30) || N > (1 << 25) || experts > kMaxGroups) return ESG_ERR_UNSUPPORTED;
+  const long long tiles = ((long long)M / 128 + 1 + experts) * ((N + 127) / 128);
+  const long long few = ((N + 15) / 16) * (2ll * experts + 1);  // workgroups of at most 512 threads
+  return tiles >= (1 << 23) || few >= (1 << 23) ? ESG_ERR_UNSUPPORTED : ESG_OK;
+}
+int mx_operands(const void* a, const void* a_scale, const void* b, const void* b_scale, int out_dtype, const void* y) {
+  if (a == nullptr || a_scale == nullptr || b == nullptr || b_scale == nullptr || y == nullptr) return ESG_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(y)) return ESG_ERR_INVALID_ARG;
+  if ((((uintptr_t)a_scale | (uintptr_t)b_scale) & 3u) != 0) return ESG_ERR_INVALID_ARG;
+  return float_dtype(out_dtype) ? ESG_OK : ESG_ERR_UNSUPPORTED;
+}
+}  // namespace
+
+int esg_mxfp4_matmul_workspace_size(int M, int N, int K, size_t* workspace_bytes) {
+  if (workspace_bytes == nullptr) return ESG_ERR_INVALID_ARG;
+  const int e = mx_shape(M, N, K, 1);
+  if (e != ESG_OK) return e;
+  *workspace_bytes = mx_matmul_workspace_bytes(M, N, K);
+  return ESG_OK;
+}
+
+int esg_mxfp4_matmul(const void* a, const void* a_scale, const void* b, const void* b_scale, int out_dtype, int M, int N,
+                     int K, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  int e = mx_shape(M, N, K, 1);
+  if (e != ESG_OK) return e;
+  if (M == 0 || N == 0) return float_dtype(out_dtype) ? ESG_OK : ESG_ERR_UNSUPPORTED;
+  e = mx_operands(a, a_scale, b, b_scale, out_dtype, y);
+  if (e != ESG_OK) return e;
+  const size_t need = mx_matmul_workspace_bytes(M, N, K);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return ESG_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_mx_matmul(MxMatmul{a, a_scale, b, b_scale, nullptr, nullptr, out_dtype, M, M, N, K, 1, y,
+                                              workspace},
+                                     (hipStream_t)stream));
+}
+
+int esg_mxfp4_grouped_matmul(const void* a, const void* a_scale, int a_rows, const int32_t* rows, const void* b,
+                             const void* b_scale, int experts, const int32_t* offsets, int out_dtype, int M, int N,
+                             int K, void* y, void* stream) {
+  int e = mx_shape(M, N, K, experts);
+  if (e != ESG_OK) return e;
+  if (a_rows < 0 || (rows == nullptr && a_rows < M)) return ESG_ERR_INVALID_ARG;
+  if (rows != nullptr && (long long)a_rows * (K / 2) >= (1ll << 31)) return ESG_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return float_dtype(out_dtype) ? ESG_OK : ESG_ERR_UNSUPPORTED;
+  e = mx_operands(a, a_scale, b, b_scale, out_dtype, y);
+  if (e != ESG_OK) return e;
+  if (offsets == nullptr || (((uintptr_t)offsets | (uintptr_t)rows) & 3u) != 0) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_mx_matmul(MxMatmul{a, a_scale, b, b_scale, offsets, rows, out_dtype, a_rows, M, N, K, experts,
+                                              y, nullptr},
+                                     (hipStream_t)stream));
+}
+
 int esg_moe_decode_supported(int tokens, int experts, int topk, int d_model, int d_ff, int w_dtype) {
   return tokens >= 0 && tokens <= kMoeMaxTokens && experts >= 1 && experts <= kMoeMaxExperts && topk >= 1 &&
          topk <= kRouteMaxK && topk <= experts && d_model >= 16 && d_model % 16 == 0 && d_model <= (1 << 17) &&

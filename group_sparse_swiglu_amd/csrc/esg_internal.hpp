@@ -219,6 +219,19 @@ hipError_t launch_mx_quant(int dtype, const void* x, int64_t blocks, void* q, vo
 hipError_t launch_mx_dequant(int dtype, const void* q, const void* scale, int64_t blocks, void* y,
                              hipStream_t stream);
 
+// ---- 4-bit products (esg_mx_gemm.hip) -----------------------------------------------
+struct MxMatmul {
+  const void *a, *sa, *b, *sb;
+  const int32_t* offsets;  // [E + 1], or NULL (E 1): one b for all rows
+  const int32_t* rows;     // [M], or NULL: row m is a[m]
+  int out_dtype;           // 0 float32, 1 bf16
+  int a_rows, M, N, K, E;
+  void* y;
+  void* workspace;         // mx_matmul_workspace_bytes of a product without offsets
+};
+size_t mx_matmul_workspace_bytes(int M, int N, int K);
+hipError_t launch_mx_matmul(const MxMatmul& c, hipStream_t stream);
+
 // ---- whole expert layer for a few tokens (esg_moe.hip) --------------------------
 constexpr int kMoeMaxTokens = 64;     // a 64-bit token set per expert
 constexpr int kMoeMaxExperts = 1024;

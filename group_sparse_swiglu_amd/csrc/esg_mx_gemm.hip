@@ -1,0 +1,624 @@
+// Matrix product of 4-bit floating point (e2m1) operands with a power of two per 32
+// K elements, of one pair or of rows grouped by expert:
+//   y[m, n] = sum over k of a[m, k] 2^(sa[m, k/32] - 127) * b[n, k] 2^(sb[n, k/32] - 127)
+// a: [M, K] (activations), b: [N, K] or [E, N, K] (weights), two codes a byte, K a
+// multiple of 32.  Grouped: rows offsets[e] .. offsets[e+1] - 1 of y take b[e]; row m of
+// the left operand is a[rows[m]] where rows is given.
+//
+// The matrix cores apply the powers of two themselves, one byte per lane and 32
+// elements.  Products of codes have 4 significant bits and, inside a block, a range
+// of 8, so a block's sum is exact; sums of blocks are float32 (measured: off by at most
+// 2^-22.5 of the sum of the |terms| of 128 elements and the accumulator), whatever the
+// result's type.  b is the products' row side: a lane then holds four consecutive n of
+// one m.
+//
+// Two kernels: mx_rows_kernel for few rows, bound by the read of b, and mx_tile_kernel
+// for many; plan() chooses between them.
+#include <algorithm>
+
+#include "esg_internal.hpp"
+#include "esg_mx.hpp"
+#include "esg_pipe.hpp"
+
+namespace esg {
+namespace {
+
+constexpr int kStepK = 256;  // K elements of a step: 128 bytes of a row, 8 exponents
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+struct MxArgs {
+  const uint8_t* a;
+  const uint8_t* b;
+  const uint8_t* sa;
+  const uint8_t* sb;
+  const int32_t* offsets;  // [E + 1], or NULL: one b for all rows
+  const int32_t* rows;     // [M], or NULL
+  void* y;
+  int a_rows, M, N, K, E;
+  int nm, nn;              // row chunks or tiles (grouped: at most so many), tiles along n
+};
+
+// Rows m0 .. m1 - 1 of y with b[e]; none for m1 <= m0.
+struct Span {
+  int e, m0, m1;
+};
+
+// The z-th chunk of up to `chunk` rows: of all rows, or counted expert after expert.  Every wave looks for itself: 64
+// experts at a time, their chunks counted by a prefix sum over the lanes.  Offsets are taken into 0 .. M.
+__device__ __forceinline__ Span find_span(const MxArgs& g, int z, int chunk, int lane) {
+  if (g.offsets == nullptr) return Span{0, z * chunk, min(g.M, (z + 1) * chunk)};
+  for (int e0 = 0; e0 < g.E; e0 += 64) {
+    const int e = e0 + lane;
+    int lo = 0, hi = 0;
+    if (e < g.E) {
+      lo = min(max(g.offsets[e], 0), g.M);
+      hi = min(max(g.offsets[e + 1], 0), g.M);
+    }
+    const int own = hi > lo ? (hi - lo + chunk - 1) / chunk : 0;
+    int upto = own;
+#pragma unroll
+    for (int off = 1; off < 64; off *= 2) {
+      const int v = __shfl_up(upto, off);
+      upto += lane >= off ? v : 0;
+    }
+    const uint64_t has = __ballot(upto > z);
+    if (has != 0) {
+      const int at = __builtin_ctzll(has);
+      const int first = __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(own, at);
+      const int m0 = __builtin_amdgcn_readlane(lo, at) + (z - first) * chunk;
+      return Span{e0 + at, m0, min(__builtin_amdgcn_readlane(hi, at), m0 + chunk)};
+    }
+    z -= __builtin_amdgcn_readlane(upto, 63);
+  }
+  return Span{0, 0, 0};
+}
+
+// Descriptor of the exponents of `rows` rows from byte `from` of p (4-byte aligned), in whole dwords; skew: what
+// `from` lies past the descriptor's base.  A dword at either end that holds a wanted byte may hold others beside it.
+__device__ __forceinline__ DmaSrc scale_src(const uint8_t* p, size_t from, uint32_t bytes, uint32_t& skew) {
+  skew = (uint32_t)(from & 3);
+  return make_dma_src(p + (from - skew), (skew + bytes + 3) & ~3u);
+}
+
+// 16 x 16 x 128 and 32 x 32 x 64 products with exponents from byte OP of each side's word
+template <int OP>
+__device__ __forceinline__ void mma_mx16(f32x4& acc, const uint4& a, const uint4& b, uint32_t sa, uint32_t sb) {
+  const i32x8_t x = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i32x8_t y = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 4, 4, OP, (int)sa, OP, (int)sb);
+}
+template <int OP>
+__device__ __forceinline__ void mma_mx32(f32x16_t& acc, const u32x4_t& a, const u32x4_t& b, uint32_t sa, uint32_t sb) {
+  const i32x8_t x = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i32x8_t y = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc, 4, 4, OP, (int)sa, OP, (int)sb);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: a workgroup takes 16 rows of b and up to 64 rows of a (MT tiles of 16);
+// its NW waves take the steps of K in turn and add their sums in LDS in wave order.
+// The read of b bounds it.  Everything goes through LDS in whole 128-byte rows, a wave
+// into P slots of its own, and it waits for its own loads only.  The exponents of a
+// step (8 bytes of a row that starts at any byte) come as the three dwords that hold
+// them, and the one needed is read back as a byte.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 64;
+
+template <int MT>
+struct Slot {
+  static constexpr int A_AT = 2048, SB_AT = A_AT + MT * 2048, SA_AT = SB_AT + 256, BYTES = SA_AT + MT * 256;
+  static constexpr int NI = 3 + 3 * MT;                 // load instructions of a step
+  static constexpr int P = MT == 1 ? 2 : 1;
+  static_assert((P - 1) * NI < 64, "vmcnt range");
+};
+template <int NW, int MTMAX>
+constexpr int rows_lds() {
+  int most = 0;
+  for (int mt = 1; mt <= MTMAX; ++mt) {
+    const int slot = (mt == 1 ? 2 : 1) * (2048 + 256) * (1 + mt), red = mt * 1024;
+    most = most > slot ? most : slot;
+    most = most > red ? most : red;
+  }
+  return NW * most;
+}
+
+template <int MT, int NW, int OUT>
+__device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* lds_) {
+  using S = Slot<MT>;
+  constexpr int P = S::P;
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int lr = lane & 15, lg = lane >> 4;
+  ESG_LDS char* const ring = (ESG_LDS char*)lds_ + w * P * S::BYTES;
+  const int n0 = blockIdx.x * 16, nrows = min(16, g.N - n0), mrows = s.m1 - s.m0;
+  const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + kStepK - 1) / kStepK;
+  const size_t b0 = (size_t)s.e * g.N + n0;
+  uint32_t b_skew, a_skew;
+  const DmaSrc rb = make_dma_src(g.b + b0 * KH, (uint32_t)(nrows * KH));
+  const DmaSrc rsb = scale_src(g.sb, b0 * KS, (uint32_t)(nrows * KS), b_skew);
+  const bool gather = g.rows != nullptr;
+  const DmaSrc ra = gather ? make_dma_src(g.a, (uint32_t)g.a_rows * (uint32_t)KH)
+                           : make_dma_src(g.a + (size_t)s.m0 * KH, (uint32_t)(mrows * KH));
+  const DmaSrc rsa = gather ? scale_src(g.sa, 0, (uint32_t)g.a_rows * (uint32_t)KS, a_skew)
+                            : scale_src(g.sa, (size_t)s.m0 * KS, (uint32_t)(mrows * KS), a_skew);
+  // row of a behind row i of the span; -1: none
+  auto a_row = [&](int i) __attribute__((always_inline)) {
+    if (i >= mrows) return -1;
+    if (!gather) return i;
+    const int r = g.rows[s.m0 + i];
+    return (unsigned)r < (unsigned)g.a_rows ? r : -1;
+  };
+  // rows of eight, 16-byte chunks in the K-row swizzle; offsets of step 0
+  const int koff = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t ob[2], oa[2 * MT], osa[MT], osb;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = i * 8 + (lane >> 3);
+    ob[i] = r < nrows ? (uint32_t)(r * KH + koff) : kOOB;
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i) {
+    const int r = a_row(i * 8 + (lane >> 3));
+    oa[i] = r >= 0 ? (uint32_t)r * (uint32_t)KH + koff : kOOB;
+  }
+  // exponents: lane = dword * 16 + row; of row lr the byte for chunk lg of the first and second 128 elements
+  int eb[2], ea[MT][2];
+  {
+    const uint32_t at = b_skew + (uint32_t)(lr * KS);
+    osb = lr < nrows && lg < 3 ? (at & ~3u) + lg * 4 : kOOB;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int p = (int)(at & 3) + j * 4 + lg;
+      eb[j] = S::SB_AT + (p >> 2) * 64 + lr * 4 + (p & 3);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int r = a_row(i * 16 + lr);
+    const uint32_t at = a_skew + (uint32_t)(r >= 0 ? r : 0) * (uint32_t)KS;
+    osa[i] = r >= 0 && lg < 3 ? (at & ~3u) + lg * 4 : kOOB;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int p = (int)(at & 3) + j * 4 + lg;
+      ea[i][j] = S::SA_AT + i * 256 + (p >> 2) * 64 + lr * 4 + (p & 3);
+    }
+  }
+  // step t into a slot; past the last step: zeros (so every step is the same number of loads).  kOOB plus an offset
+  // below 2^31 stays past every buffer.
+  auto request = [&](int t, ESG_LDS char* slot) __attribute__((always_inline)) {
+    const bool in = t < steps && t * 128 + koff < KH;
+    const uint32_t k = (uint32_t)t * 128u, ks = (uint32_t)t * 8u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) dma16(rb, slot + i * 1024, in ? ob[i] + k : kOOB);
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) dma16(ra, slot + S::A_AT + i * 1024, in ? oa[i] + k : kOOB);
+    dma4(rsb, slot + S::SB_AT, t < steps ? osb + ks : kOOB);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) dma4(rsa, slot + S::SA_AT + i * 256, t < steps ? osa[i] + ks : kOOB);
+  };
+  f32x4 acc[MT];
+  zero_acc(acc);
+#pragma unroll
+  for (int u = 0; u < P; ++u) request(w + u * NW, ring + u * S::BYTES);
+  int at = 0;
+  for (int t = w; t < steps; t += NW) {
+    ESG_LDS char* slot = ring + at * S::BYTES;
+    at = at + 1 == P ? 0 : at + 1;
+    wait_vmcnt<(P - 1) * S::NI>();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      // past K the codes are zeros, and the exponents those of other rows: any but 255 will do
+      const bool in = t * kStepK + (j * 4 + lg) * 32 < g.K;
+      const uint4 bv = frag_krow(slot, lr, j * 4 + lg);
+      const uint32_t bs = in ? *(const ESG_LDS uint8_t*)(slot + eb[j]) : 0u;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const uint4 av = frag_krow(slot + S::A_AT, i * 16 + lr, j * 4 + lg);
+        const uint32_t as = in ? *(const ESG_LDS uint8_t*)(slot + ea[i][j]) : 0u;
+        mma_mx16<0>(acc[i], bv, av, bs, as);
+      }
+    }
+    wait_lgkm0();  // the slot has been read
+    __builtin_amdgcn_sched_barrier(0);
+    request(t + P * NW, slot);
+  }
+  wait_vmcnt<0>();
+  __syncthreads();  // the slots become the sums of the waves
+  f32x4* red = (f32x4*)lds_;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) red[(w * MT + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  const float* rf = (const float*)red;
+  for (int o = threadIdx.x; o < mrows * 16; o += NW * 64) {
+    const int n = o & 15, m = o >> 4;
+    const int at_o = ((m >> 4) * 64 + (n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
+    float v = rf[at_o];
+#pragma unroll
+    for (int u = 1; u < NW; ++u) v += rf[u * MT * 256 + at_o];
+    if (n < nrows) {
+      const size_t out = (size_t)(s.m0 + m) * g.N + n0 + n;
+      if constexpr (OUT == 1)
+        store_elem<bf16_t>((bf16_t*)g.y + out, v);
+      else
+        ((float*)g.y)[out] = v;
+    }
+  }
+}
+
+template <int NW, int OUT>
+__global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs g) {
+  __shared__ __attribute__((aligned(1024))) char lds[rows_lds<NW, 4>()];
+  const Span s = find_span(g, blockIdx.y, kFewRows, threadIdx.x & 63);
+  const int mrows = s.m1 - s.m0;
+  if (mrows <= 0) return;
+  if (mrows > 48)
+    few_rows<4, NW, OUT>(g, s, lds);
+  else if (mrows > 32)
+    few_rows<3, NW, OUT>(g, s, lds);
+  else if (mrows > 16)
+    few_rows<2, NW, OUT>(g, s, lds);
+  else
+    few_rows<1, NW, OUT>(g, s, lds);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles.  BM x BN outputs per workgroup of four waves, each BM/2 x BN/2; K in steps of
+// 256 (128 bytes per row) through two direct-to-LDS stages of K-row tiles; in a step
+// four slices of 64, each FN x FM products of 32 x 32 x 64.
+//
+// A slice's operands are read under the products of the one before; the barrier sits
+// before the products of the last slice, whose operands are in registers: under them
+// the next step's first slice is read and the loads of the step after that are issued.
+// The exponents of a step go through registers to LDS, eight bytes per row and step, and
+// are read once per step and fragment.
+// ---------------------------------------------------------------------------
+template <int BM, int BN>
+struct Tile {
+  static constexpr int NTH = 256, NW = 4;
+  static constexpr int WM = BM / 2, WN = BN / 2;
+  static constexpr int FM = WM / 32, FN = WN / 32;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
+  static constexpr int SROWS = BM + BN, SPT = SROWS / NTH;  // rows of exponents, of a thread
+  static constexpr int SLOT = SROWS * 8;
+  static constexpr int LDS = 2 * STAGE + 2 * SLOT;
+  static_assert(SROWS % NTH == 0, "whole rows of exponents per thread");
+};
+
+// position of 16-byte chunk c of row r: 16 consecutive rows at one chunk lie in different banks
+__device__ __forceinline__ int mx_swz(int r) { return (r >> 1) & 7; }
+
+__device__ __forceinline__ void dma16_at(const DmaSrc& s, ESG_LDS char* wave_base, uint32_t voff, uint32_t soff) {
+  const int m = __builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)wave_base);
+  const int so = __builtin_amdgcn_readfirstlane((int)soff);
+  asm volatile("buffer_load_dwordx4 %0, %1, %3 offen lds" : : "v"(voff), "s"(s.d), "{m0}"(m), "s"(so) : "memory");
+}
+
+// Block id -> tile: each XCD (id % 8) takes a contiguous run of an order that walks eight m tiles, then the next n
+// tile, so the workgroups of an XCD share operand panels in its L2.
+__device__ __forceinline__ void tile_of(int id, int total, int nm, int nn, int& tm, int& tn) {
+  const int per = total >> 3, extra = total & 7, x = id & 7;
+  const int o = x * per + (x < extra ? x : extra) + (id >> 3);
+  const int band = 8 * nn;
+  const int bi = o / band, in = o - bi * band;
+  const int rows = min(8, nm - bi * 8);
+  tm = bi * 8 + in % rows;
+  tn = in / rows;
+}
+
+template <int BM, int BN, int OUT>
+__global__ __launch_bounds__(256, 1) void mx_tile_kernel(MxArgs g) {
+  using C = Tile<BM, BN>;
+  __shared__ __attribute__((aligned(1024))) char lds_[C::LDS];
+  ESG_LDS char* const lds = (ESG_LDS char*)lds_;
+  ESG_LDS char* const slots = lds + 2 * C::STAGE;
+  const int lane = threadIdx.x & 63, w = wave_id();
+  const int wm = w & 1, wn = w >> 1;
+  const int lr = lane & 31, lh = lane >> 5;
+  int tm, tn;
+  tile_of(blockIdx.x, g.nm * g.nn, g.nm, g.nn, tm, tn);
+  const Span s = find_span(g, tm, BM, lane);
+  const int mrows = s.m1 - s.m0;
+  if (mrows <= 0) return;
+  const int n0 = tn * BN, nrows = min(BN, g.N - n0);
+  const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + kStepK - 1) / kStepK;
+  const bool gather = g.rows != nullptr;
+  const size_t b0 = (size_t)s.e * g.N + n0;
+  const DmaSrc rb = make_dma_src(g.b + b0 * KH, (uint32_t)(nrows * KH));
+  const DmaSrc ra = gather ? make_dma_src(g.a, (uint32_t)g.a_rows * (uint32_t)KH)
+                           : make_dma_src(g.a + (size_t)s.m0 * KH, (uint32_t)(mrows * KH));
+  auto a_row = [&](int i) __attribute__((always_inline)) {
+    if (i >= mrows) return -1;
+    if (!gather) return i;
+    const int r = g.rows[s.m0 + i];
+    return (unsigned)r < (unsigned)g.a_rows ? r : -1;
+  };
+
+  // ---- loads: one instruction fills eight rows of 128 bytes ----
+  constexpr int NA = BM / 8 / 4, NB = BN / 8 / 4;  // instructions of a wave and step
+  uint32_t oa[NA], ob[NB];
+  auto chunk_at = [&](int i) __attribute__((always_inline)) {  // K bytes of this lane in the wave's i-th eight rows
+    return ((lane & 7) ^ mx_swz(i * 8 + (lane >> 3))) * 16;
+  };
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    const int r = a_row((w * NA + i) * 8 + (lane >> 3));
+    oa[i] = r >= 0 ? (uint32_t)r * (uint32_t)KH + chunk_at(w * NA + i) : kOOB;
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int r = (w * NB + i) * 8 + (lane >> 3);
+    ob[i] = r < nrows ? (uint32_t)(r * KH) + chunk_at(w * NB + i) : kOOB;
+  }
+  // loads of step t into a stage; past the last step: the last one's again (not used)
+  auto issue = [&](int t, ESG_LDS char* st) __attribute__((always_inline)) {
+    const uint32_t k = (uint32_t)min(t, steps - 1) * 128u;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) dma16_at(ra, st + (w * NA + i) * 1024, oa[i], k);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) dma16_at(rb, st + C::A_BYTES + (w * NB + i) * 1024, ob[i], k);
+  };
+  // before the step that K cuts short is issued: chunks at or past K read zeros from here on
+  auto cut = [&](int t) __attribute__((always_inline)) {
+    if (t == steps - 1 && g.K % kStepK != 0) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i) oa[i] = t * 128 + chunk_at(w * NA + i) < KH ? oa[i] : kOOB;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) ob[i] = t * 128 + chunk_at(w * NB + i) < KH ? ob[i] : kOOB;
+    }
+  };
+
+  // ---- exponents: this thread's rows, the three dwords that hold a step's eight bytes ----
+  uint32_t os[C::SPT], skew[C::SPT];
+  rsrc_t rs[C::SPT];
+#pragma unroll
+  for (int i = 0; i < C::SPT; ++i) {
+    const int r = i * 256 + (int)threadIdx.x;
+    if (i * 256 + w * 64 < BM) {  // a wave's rows lie on one side: BM is a multiple of 64
+      const size_t from = gather ? 0 : (size_t)s.m0 * KS;
+      const uint32_t bytes = (uint32_t)(gather ? g.a_rows : mrows) * (uint32_t)KS, sk = (uint32_t)(from & 3);
+      rs[i] = make_rsrc(g.sa + (from - sk), (sk + bytes + 3) & ~3u);
+      const int ar = a_row(r);
+      const uint32_t at = sk + (uint32_t)(ar >= 0 ? ar : 0) * (uint32_t)KS;
+      os[i] = ar >= 0 ? at & ~3u : kOOB;
+      skew[i] = at & 3;
+    } else {
+      const size_t from = b0 * KS;
+      const uint32_t sk = (uint32_t)(from & 3);
+      rs[i] = make_rsrc(g.sb + (from - sk), (sk + (uint32_t)(nrows * KS) + 3) & ~3u);
+      const uint32_t at = sk + (uint32_t)((r - BM) * KS);
+      os[i] = r - BM < nrows ? at & ~3u : kOOB;
+      skew[i] = at & 3;
+    }
+  }
+  uint32_t sreg[C::SPT][3];
+  auto load_scales = [&](int t) __attribute__((always_inline)) {
+    const uint32_t k = (uint32_t)min(t, steps - 1) * 8u;
+#pragma unroll
+    for (int i = 0; i < C::SPT; ++i)
+#pragma unroll
+      for (int d = 0; d < 3; ++d)
+        sreg[i][d] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs[i], (int)(os[i] + k + d * 4), 0, 0);
+  };
+  auto put_scales = [&](int t, ESG_LDS char* slot) __attribute__((always_inline)) {
+    const int left = KS - min(t, steps - 1) * 8;  // bytes of the row still in K; those past it are other rows'
+    const uint32_t m0 = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+    const uint32_t m1 = left >= 8 ? ~0u : left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u;
+#pragma unroll
+    for (int i = 0; i < C::SPT; ++i) {
+      const uint32_t lo = __builtin_amdgcn_alignbyte(sreg[i][1], sreg[i][0], skew[i]);
+      const uint32_t hi = __builtin_amdgcn_alignbyte(sreg[i][2], sreg[i][1], skew[i]);
+      lds_write8(slot + (i * 256 + (int)threadIdx.x) * 8, lo & m0, hi & m1);
+    }
+  };
+
+  f32x16_t acc[C::FN][C::FM];
+#pragma unroll
+  for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  // operands of a slice, and the exponents of a step as this lane's half needs them: bytes 0 and 2 of two words
+  u32x4_t av[2][C::FM], bv[2][C::FN];
+  uint32_t as[C::FM][2], bs[C::FN][2];
+  const int ra0 = wm * C::WM + lr, rb0 = wn * C::WN + lr;
+  // 32 rows further on are 32 * 128 bytes: the swizzle repeats every 16 rows
+  auto read_slice = [&](ESG_LDS char* st, int sl, int to) __attribute__((always_inline)) {
+    const ESG_LDS char* pa = st + ra0 * 128 + (((sl * 2 + lh) ^ mx_swz(ra0)) << 4);
+    const ESG_LDS char* pb = st + C::A_BYTES + rb0 * 128 + (((sl * 2 + lh) ^ mx_swz(rb0)) << 4);
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) av[to][j] = *(const ESG_LDS u32x4_t*)(pa + j * 4096);
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) bv[to][i] = *(const ESG_LDS u32x4_t*)(pb + i * 4096);
+  };
+  auto read_scales = [&](ESG_LDS char* slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) {
+      const u32x2_t v = *(const ESG_LDS u32x2_t*)(slot + (ra0 + j * 32) * 8);
+      as[j][0] = v.x >> (8 * lh);
+      as[j][1] = v.y >> (8 * lh);
+    }
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) {
+      const u32x2_t v = *(const ESG_LDS u32x2_t*)(slot + (BM + rb0 + i * 32) * 8);
+      bs[i][0] = v.x >> (8 * lh);
+      bs[i][1] = v.y >> (8 * lh);
+    }
+  };
+  auto products = [&](int sl, int from) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j) {
+        if (sl & 1)
+          mma_mx32<2>(acc[i][j], bv[from][i], av[from][j], bs[i][sl >> 1], as[j][sl >> 1]);
+        else
+          mma_mx32<0>(acc[i][j], bv[from][i], av[from][j], bs[i][sl >> 1], as[j][sl >> 1]);
+      }
+  };
+
+  load_scales(0);
+  cut(0);
+  issue(0, lds);
+  put_scales(0, slots);
+  load_scales(1);
+  cut(1);
+  issue(1, lds + C::STAGE);
+  put_scales(1, slots + C::SLOT);
+  wait_vmcnt<0>();
+  wait_lgkm0();
+  barrier();
+  read_scales(slots);
+  read_slice(lds, 0, 0);
+  for (int t = 0; t < steps; ++t) {
+    ESG_LDS char* const st = lds + (t & 1) * C::STAGE;
+    ESG_LDS char* const st2 = lds + ((t & 1) ^ 1) * C::STAGE;
+    ESG_LDS char* const slot = slots + (t & 1) * C::SLOT;
+    ESG_LDS char* const slot2 = slots + ((t & 1) ^ 1) * C::SLOT;
+    load_scales(t + 2);
+    read_slice(st, 1, 1);
+    products(0, 0);
+    read_slice(st, 2, 0);
+    products(1, 1);
+    read_slice(st, 3, 1);
+    products(2, 0);
+    // this step's operands are all in registers; the next step's have landed
+    __builtin_amdgcn_sched_barrier(0);
+    wait_lgkm0();
+    wait_vmcnt<0>();
+    barrier();
+    put_scales(t + 2, slot);
+    __builtin_amdgcn_sched_barrier(0);
+    cut(t + 2);
+    issue(t + 2, st);
+    read_slice(st2, 0, 0);
+    products(3, 1);
+    read_scales(slot2);
+  }
+  wait_lgkm0();
+  wait_vmcnt<0>();
+  barrier();  // the stages are free
+
+  // ---- results: a lane holds, of one m, four consecutive n out of every eight.  A wave takes 32 rows at a time
+  // through LDS of its own, in 16-byte chunks swizzled by row, and stores whole rows of its WN columns. ----
+  constexpr int ES = OUT == 1 ? 2 : 4;
+  constexpr int NCH = C::WN * ES / 16;  // chunks per row
+  char* y = (char*)g.y;
+  const int mw = wm * C::WM, nw = n0 + wn * C::WN;
+  if (g.N * ES % 16 == 0 && ((uintptr_t)y & 15) == 0) {
+    static_assert(32 * NCH * 16 * 4 <= 2 * C::STAGE, "the pieces lie in the stages");
+    ESG_LDS char* out = lds + w * (32 * NCH * 16);
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) {
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16_t& v = acc[i][j];
+          if constexpr (ES == 2)
+            lds_write8(out + (lr * NCH + ((i * 4 + q) ^ (lr & (NCH - 1)))) * 16 + lh * 8,
+                       pack_bf16x2(v[q * 4], v[q * 4 + 1]), pack_bf16x2(v[q * 4 + 2], v[q * 4 + 3]));
+          else
+            *(ESG_LDS f32x4*)(out + (lr * NCH + ((i * 8 + q * 2 + lh) ^ (lr & (NCH - 1)))) * 16) =
+                f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
+        }
+      wait_lgkm0();
+#pragma unroll
+      for (int h = 0; h < 32 * NCH / 64; ++h) {
+        const int r = (h * 64 + lane) / NCH, c = lane % NCH;
+        const u32x4_t v = *(const ESG_LDS u32x4_t*)(out + (r * NCH + (c ^ (r & (NCH - 1)))) * 16);
+        const int m = mw + j * 32 + r, n = nw + c * (16 / ES);
+        if (m < mrows && n < g.N) *(u32x4_t*)(y + ((size_t)(s.m0 + m) * g.N + n) * ES) = v;
+      }
+      wait_lgkm0();  // read before the next rows are written
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) {
+      const int m = mw + j * 32 + lr;
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int n = nw + i * 32 + (e >> 2) * 8 + lh * 4 + (e & 3);
+          if (m < mrows && n < g.N) {
+            const size_t at = (size_t)(s.m0 + m) * g.N + n;
+            if constexpr (OUT == 1)
+              store_elem<bf16_t>((bf16_t*)y + at, acc[i][j][e]);
+            else
+              ((float*)y)[at] = acc[i][j][e];
+          }
+        }
+    }
+  }
+}
+
+// Kernel and tile size by shape alone (so a shape rounds alike everywhere).
+struct Plan {
+  int tile = 0;   // 0: few rows
+  int nm = 0, nn = 0;
+};
+// chunks of `chunk` rows, at most: grouped rows leave up to one short chunk per expert
+long long chunks(const MxArgs& g, int chunk) {
+  return g.offsets == nullptr ? (g.M + chunk - 1) / chunk : (long long)g.M / chunk + std::min(g.E, g.M);
+}
+Plan plan(const MxArgs& g) {
+  Plan p;
+  const int per = g.offsets == nullptr ? g.M : (g.M + g.E - 1) / g.E;  // rows that share a b, on average
+  const long long wgs = (long long)((g.N + 15) / 16) * ((g.M + kFewRows - 1) / kFewRows);
+  if (per <= kFewRows || (g.offsets == nullptr && wgs <= kNominalCUs)) {
+    p.nm = (int)chunks(g, kFewRows);
+    p.nn = (g.N + 15) / 16;
+    return p;
+  }
+  const long long big = (long long)((g.M + 255) / 256) * ((g.N + 255) / 256);
+  p.tile = big >= kNominalCUs && per >= 256 ? 256 : 128;
+  p.nm = (int)chunks(g, p.tile);
+  p.nn = (g.N + p.tile - 1) / p.tile;
+  return p;
+}
+
+template <int OUT>
+hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
+  if (p.tile == 0) {
+    LaunchTimer timer("mx_rows", stream);
+    if ((long long)p.nn * p.nm > kNominalCUs)
+      hipLaunchKernelGGL((mx_rows_kernel<4, OUT>), dim3(p.nn, p.nm), dim3(256), 0, stream, g);
+    else
+      hipLaunchKernelGGL((mx_rows_kernel<8, OUT>), dim3(p.nn, p.nm), dim3(512), 0, stream, g);
+    return hipGetLastError();
+  }
+  LaunchTimer timer("mx_tile", stream);
+  if (p.tile == 256)
+    hipLaunchKernelGGL((mx_tile_kernel<256, 256, OUT>), dim3(p.nm * p.nn), dim3(256), 0, stream, g);
+  else
+    hipLaunchKernelGGL((mx_tile_kernel<128, 128, OUT>), dim3(p.nm * p.nn), dim3(256), 0, stream, g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t mx_matmul_workspace_bytes(int, int, int) { return 0; }
+
+hipError_t launch_mx_matmul(const MxMatmul& c, hipStream_t stream) {
+  MxArgs g{};
+  g.a = (const uint8_t*)c.a;
+  g.b = (const uint8_t*)c.b;
+  g.sa = (const uint8_t*)c.sa;
+  g.sb = (const uint8_t*)c.sb;
+  g.offsets = c.offsets;
+  g.rows = c.rows;
+  g.y = c.y;
+  g.a_rows = c.a_rows;
+  g.M = c.M;
+  g.N = c.N;
+  g.K = c.K;
+  g.E = c.E;
+  const Plan p = plan(g);
+  g.nm = p.nm;
+  g.nn = p.nn;
+  return c.out_dtype == 1 ? run<1>(g, p, stream) : run<0>(g, p, stream);
+}
+
+}  // namespace esg

@@ -584,6 +584,39 @@ int esg_mxfp4_quant(const void* x, int dtype, int64_t rows, int cols, void* q, v
 int esg_mxfp4_dequant(const void* q, const void* scale, int dtype, int64_t rows, int cols, void* y, void* stream);
 
 /*
+ * Product of such 4-bit operands:
+ *   y[m, n] = sum_k  a[m, k] 2^(a_scale[m, k/32] - 127) * b[n, k] 2^(b_scale[n, k/32] - 127)
+ * a: [M, K/2] bytes, a_scale: [M, K/32] bytes, b: [N, K/2], b_scale: [N, K/32], as
+ * esg_mxfp4_quant gives them; y: out_dtype (ESG_F32 or ESG_BF16) [M, N], overwritten.
+ * The sum of a block is exact, sums of blocks are float32; their order depends on the
+ * shape alone and no atomics are used (bitwise reproducible).  A block of the byte 255
+ * makes what it adds to NaN.
+ * workspace: esg_mxfp4_matmul_workspace_size() bytes, 16-byte aligned (shapes with few
+ * output tiles split K and add the parts there; it may be 0, then workspace may be NULL).
+ * M == 0 or N == 0 enqueues nothing.
+ *
+ * esg_mxfp4_grouped_matmul: the same for rows in the order of their experts, b: [experts,
+ * N, K/2], b_scale: [experts, N, K/32]; offsets: device int32 [experts + 1] (of
+ * esg_bucket_by_group): rows offsets[e] .. offsets[e+1] - 1 of y take b[e].  rows
+ * (device int32 [M], or NULL): row m is row rows[m] of a [a_rows, K/2] instead of row m
+ * (perm_token of esg_bucket_by_group: the tokens need no copy in the experts' order); an
+ * index outside 0 .. a_rows - 1 is a row of zeros.  Rows of y before offsets[0] and from
+ * offsets[experts] on are left as they were.  Offsets are taken into 0 .. M; where they
+ * descend, which b the rows between take is not specified.
+ * Errors: ESG_ERR_INVALID_ARG (null pointer, a, b, y or workspace not 16-byte aligned, a
+ * scale, offsets or rows not 4-byte aligned, negative size, K <= 0, experts < 1, a_rows < M
+ * without rows), ESG_ERR_UNSUPPORTED (out_dtype, K not a multiple of 32 or above 2^22, M
+ * above 2^30, N above 2^25, experts above 1024, 2^23 output tiles of 128 x 128 or more, or
+ * with rows a of 2^31 bytes or more), ESG_ERR_WORKSPACE.
+ */
+int esg_mxfp4_matmul_workspace_size(int M, int N, int K, size_t* workspace_bytes);
+int esg_mxfp4_matmul(const void* a, const void* a_scale, const void* b, const void* b_scale, int out_dtype, int M, int N,
+                     int K, void* y, void* workspace, size_t workspace_bytes, void* stream);
+int esg_mxfp4_grouped_matmul(const void* a, const void* a_scale, int a_rows, const int32_t* rows, const void* b,
+                             const void* b_scale, int experts, const int32_t* offsets, int out_dtype, int M, int N,
+                             int K, void* y, void* stream);
+
+/*
  * A whole mixture-of-experts feed-forward layer for a few tokens (decode):
  *   s[t,e] = sigmoid(x[t] . w_router[e])  (the fp32 sum's fp64 sigmoid, rounded once to fp32);
  *   indices, probs: the top-k rule of esg_sigmoid_topk_routing on s and expert_bias;

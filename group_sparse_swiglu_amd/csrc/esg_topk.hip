@@ -84,6 +84,22 @@ struct Or {
   __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a | b; }
 };
 
+// Sum over the lanes up to and with this one of its row.
+template <int LPR>
+__device__ __forceinline__ uint32_t row_scan(uint32_t v) {
+  v += dpp<0x111>(v);  // from 1, 2, 4, 8 lanes below, 0 past the lower end of 16
+  v += dpp<0x112>(v);
+  v += dpp<0x114>(v);
+  v += dpp<0x118>(v);
+  if constexpr (LPR == 64) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 15), b = (uint32_t)__builtin_amdgcn_readlane((int)v, 31),
+                   c = (uint32_t)__builtin_amdgcn_readlane((int)v, 47);
+    v += (lane >= 16 ? a : 0u) + (lane >= 32 ? b : 0u) + (lane >= 48 ? c : 0u);
+  }
+  return v;
+}
+
 // ---- scores ----
 // e^(x + rest) to about 2 units in the last place, |rest| at most half a unit of x: the
 // exponent's product with log2(e) in two parts.  x is taken into [-150, 88], whose
@@ -158,30 +174,30 @@ __device__ __forceinline__ void load_logits(const bf16_t* p, int n, int vec, flo
   for (int c = 0; c < C; ++c) z[c] = c < n ? load_elem<bf16_t>(p + c) : 0.f;
 }
 
-// ---- ordered keys with their slot in the low bits; 0 is no key ----
+// ---- ordered keys, exact ones above what is left of the row behind their slot; 0 is no key ----
 __device__ __forceinline__ float key_float(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u);
 }
-template <int SLOTS, bool EXACT>
+template <bool EXACT>
 struct Key;
-template <int SLOTS>
-struct Key<SLOTS, false> {
+template <>
+struct Key<false> {
   using type = uint32_t;
-  static constexpr uint32_t MASK = SLOTS - 1;
-  __device__ static __forceinline__ type make(float f, int slot) {
-    return (order_key(f) & ~MASK) | (MASK - (uint32_t)slot);
-  }
-  __device__ static __forceinline__ float value(type k) { return key_float(k & ~MASK); }
+  __device__ static __forceinline__ type make(float f, int) { return order_key(f); }
+  __device__ static __forceinline__ float value(type k) { return key_float(k); }
 };
-template <int SLOTS>
-struct Key<SLOTS, true> {
+template <>
+struct Key<true> {
   using type = uint64_t;
-  static constexpr uint32_t MASK = SLOTS - 1;
   __device__ static __forceinline__ type make(float f, int slot) {
-    return (uint64_t)order_key(f) << 32 | (MASK - (uint32_t)slot);
+    return (uint64_t)order_key(f) << 32 | (uint32_t)(kRouteMaxExperts - slot);
   }
   __device__ static __forceinline__ float value(type k) { return key_float((uint32_t)(k >> 32)); }
 };
+
+// by value: a condition between two elements of an array becomes an index into it
+template <typename V>
+__device__ __forceinline__ V choose(bool c, V a, V b) { return c ? a : b; }
 
 // descending, a bitonic network
 template <int C, typename V>
@@ -202,16 +218,20 @@ __device__ __forceinline__ void sort_desc(V (&v)[C]) {
       }
 }
 
-// The k-th largest key of the row's best groups from keys u (0: none); sure: whether the estimates decide it
-// (always, for exact keys).  abs_err: bound on the error of an estimate beside its last places.
+// A score's estimate is off by at most this of itself: two to three units in its last place from exponential and
+// reciprocal, and with softmax up to 20 additions of the row's sum.
+constexpr float kEstimate = 0x1p-19f;
+
+// The k-th largest key of the row's best groups from keys u (0: none) and, of estimates, the one after it; sure:
+// whether they decide which groups stay (always, for exact keys).  An estimate is off by at most kEstimate of itself
+// and abs_err.
 template <int LPR, int C, bool EXACT>
-__device__ __forceinline__ typename Key<LPR * C, EXACT>::type threshold(
-    const typename Key<LPR * C, EXACT>::type (&u)[C], const RouteArgs& g, int l, float abs_err, uint32_t& in_group,
-    bool& sure) {
-  using K = Key<LPR * C, EXACT>;
+__device__ __forceinline__ typename Key<EXACT>::type threshold(const typename Key<EXACT>::type (&u)[C],
+                                                               const RouteArgs& g, int l, float abs_err,
+                                                               uint32_t& in_group, bool& sure,
+                                                               typename Key<EXACT>::type& next) {
+  using K = Key<EXACT>;
   using V = typename K::type;
-  // an estimate cut to its upper bits is off by at most one unit of those, 2^-23 SLOTS of its value, and by abs_err
-  constexpr float kRel = (float)(LPR * C) / 4194304.f;  // 2^-22
   V s[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) s[c] = u[c];
@@ -244,7 +264,7 @@ __device__ __forceinline__ typename Key<LPR * C, EXACT>::type threshold(
       size += fabsf(second);
     }
     // rank of this lane's group: groups with a larger score, or an equal one and a lower number
-    const int lane = threadIdx.x & 63, row0 = lane - l;
+    const int row0 = (int)(threadIdx.x & 63) - l;
     int rank = 0;
     for (int o = g.lanes; o < LPR; o += g.lanes) {
       const int from = (l + o) & (LPR - 1);
@@ -256,25 +276,29 @@ __device__ __forceinline__ typename Key<LPR * C, EXACT>::type threshold(
       const float kept = row_reduce<LPR>(in_group ? score : INFINITY, Min{});
       const float gone = row_reduce<LPR>(in_group ? -INFINITY : score, Max{});
       const float most = row_reduce<LPR>(t.a == 0 ? 0.f : size, Max{});
-      sure = kept - gone > most * (2.f * kRel) + 4.f * abs_err;
+      sure = kept - gone > most * (2.f * kEstimate) + 4.f * abs_err;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) s[c] = in_group ? s[c] : V(0);
   }
   V thr = 0, m = 0;
+  const int lane = threadIdx.x & 63;
+  const uint64_t below = ((1ull << l) - 1ull) << (lane - l);  // the row's lanes below this one
   for (int j = 0; j < g.topk + (EXACT ? 0 : 1); ++j) {
     thr = m;
     m = row_reduce<LPR>(s[0], Max{});
-    const bool mine = s[0] == m;
+    bool mine = s[0] == m;
+    if constexpr (!EXACT) mine = mine && (__ballot(mine) & below) == 0;  // of equal heads the lowest lane's
 #pragma unroll
-    for (int c = 0; c < C; ++c) s[c] = mine ? (c + 1 < C ? s[c + 1 < C ? c + 1 : c] : V(0)) : s[c];
+    for (int c = 0; c < C; ++c) s[c] = choose(mine, c + 1 < C ? s[c + 1 < C ? c + 1 : c] : V(0), s[c]);
   }
-  if constexpr (EXACT) return m;
-  if (m != 0) {
-    const float a = K::value(thr), b = K::value(m);
-    sure = sure && a - b > (fabsf(a) + fabsf(b)) * kRel + 2.f * abs_err;
-  }
-  return thr;
+  next = m;
+  return EXACT ? m : thr;
+}
+
+// whether estimates a >= b are further apart than they may be off
+__device__ __forceinline__ bool apart(float a, float b, float abs_err) {
+  return a - b > (fabsf(a) + fabsf(b)) * kEstimate + 2.f * abs_err;
 }
 
 template <typename T, int LPR, int C>
@@ -303,7 +327,7 @@ __global__ __launch_bounds__(kThreads) void topk_routing_kernel(RouteArgs g, int
     bad |= nan;
     z[c] = nan ? -INFINITY : z[c];
   }
-  float s[C], top = 0.f;
+  float s[C], top = 0.f, most = 1.f;  // most: no score of the row is larger
   if (scoring == SIGMOID) {
 #pragma unroll
     for (int c = 0; c < C; ++c) s[c] = fast_sigmoid(z[c]);
@@ -321,13 +345,14 @@ __global__ __launch_bounds__(kThreads) void topk_routing_kernel(RouteArgs g, int
     }
     sum = row_reduce<LPR>(sum, Add{});
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    most = inv;
 #pragma unroll
     for (int c = 0; c < C; ++c) s[c] *= inv;
   }
-  // scores are off by at most 2^-20 of themselves, and those below the normal range by themselves
-  const float abs_err = (g.bias != nullptr ? 0x1p-20f : 0.f) + 0x1p-125f;
-  using Fast = Key<LPR * C, false>;
-  using Exact = Key<LPR * C, true>;
+  // beside a bias the error of the score counts whole; scores below the normal range are off by themselves
+  const float abs_err = (g.bias != nullptr ? most * kEstimate : 0.f) + 0x1p-125f;
+  using Fast = Key<false>;
+  using Exact = Key<true>;
   uint32_t flags = 0;  // bit c: chosen
   bool sure = true;
   uint32_t in_group;
@@ -335,9 +360,52 @@ __global__ __launch_bounds__(kThreads) void topk_routing_kernel(RouteArgs g, int
     uint32_t u[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) u[c] = c < n ? Fast::make(s[c] + b[c], l * C + c) : 0u;
-    const uint32_t thr = threshold<LPR, C, false>(u, g, l, abs_err, in_group, sure);
+    uint32_t next;
+    const uint32_t thr = threshold<LPR, C, false>(u, g, l, abs_err, in_group, sure, next);
+    uint32_t equal = 0;
 #pragma unroll
-    for (int c = 0; c < C; ++c) flags |= (uint32_t)(c < n && in_group && u[c] >= thr) << c;
+    for (int c = 0; c < C; ++c) {
+      u[c] = in_group ? u[c] : 0u;
+      flags |= (uint32_t)(u[c] >= thr) << c;
+      equal |= (uint32_t)(u[c] == thr) << c;
+    }
+    const bool tie = next == thr;
+    const float ft = Fast::value(thr);
+    if (!tie && next != 0) sure = sure && apart(ft, Fast::value(next), abs_err);
+    if (__ballot(live && tie) != 0) {
+      // equal estimates on both sides of the border (logits of 16 bits have many equals): the lower ones are taken, if
+      // all of them come from equal logits and biases and no other estimate is near
+      uint32_t over = 0xffffffffu, under = 0, zlo = 0xffffffffu, zhi = 0, blo = 0xffffffffu, bhi = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const bool eq = u[c] == thr;
+        const uint32_t kz = order_key(z[c]), kb = order_key(b[c]);
+        over = u[c] > thr ? Min{}(over, u[c]) : over;
+        under = u[c] < thr ? Max{}(under, u[c]) : under;
+        zlo = eq ? Min{}(zlo, kz) : zlo;
+        zhi = eq ? Max{}(zhi, kz) : zhi;
+        blo = eq ? Min{}(blo, kb) : blo;
+        bhi = eq ? Max{}(bhi, kb) : bhi;
+      }
+      over = row_reduce<LPR>(over, Min{});
+      under = row_reduce<LPR>(under, Max{});
+      const bool same = row_reduce<LPR>(zlo, Min{}) == row_reduce<LPR>(zhi, Max{}) &&
+                        row_reduce<LPR>(blo, Min{}) == row_reduce<LPR>(bhi, Max{});
+      const bool alone = (over == 0xffffffffu || apart(Fast::value(over), ft, abs_err)) &&
+                         (under == 0 || apart(ft, Fast::value(under), abs_err));
+      const uint32_t above = row_reduce<LPR>((uint32_t)__popc(flags & ~equal), Add{});
+      const int before = (int)(row_scan<LPR>((uint32_t)__popc(equal)) - __popc(equal));
+      int need = g.topk - (int)above - before;
+      uint32_t kept = flags & ~equal;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const bool take = (equal >> c & 1) && need > 0;
+        kept |= (uint32_t)take << c;
+        need -= take;
+      }
+      flags = tie ? kept : flags;
+      sure = tie ? sure && same && alone : sure;
+    }
   }
   if (__ballot(live && !sure) != 0) {
     // for the unsure rows alone: what a row gives does not depend on the others of its wave
@@ -358,7 +426,8 @@ __global__ __launch_bounds__(kThreads) void topk_routing_kernel(RouteArgs g, int
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) u[c] = c < n ? Exact::make(x[c] + b[c], l * C + c) : 0ull;
-    const uint64_t thr = threshold<LPR, C, true>(u, g, l, 0.f, in_group, sure);
+    uint64_t next;
+    const uint64_t thr = threshold<LPR, C, true>(u, g, l, 0.f, in_group, sure, next);
     uint32_t exact = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -368,14 +437,7 @@ __global__ __launch_bounds__(kThreads) void topk_routing_kernel(RouteArgs g, int
     flags = redo ? exact : flags;
   }
   // place of this lane's first chosen expert: chosen ones of the lanes below it
-  int place = __popc(flags);
-  const int own = place;
-#pragma unroll
-  for (int off = 1; off < LPR; off *= 2) {
-    const int v = __shfl_up(place, off, LPR);
-    place += l >= off ? v : 0;
-  }
-  place -= own;
+  int place = (int)(row_scan<LPR>((uint32_t)__popc(flags)) - __popc(flags));
   float sum = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) sum += (flags >> c & 1) ? s[c] : 0.f;

@@ -23,7 +23,6 @@
 namespace esg {
 namespace {
 
-constexpr int kStepK = 256;  // K elements of a step: 128 bytes of a row, 8 exponents
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 struct MxArgs {
@@ -103,6 +102,7 @@ __device__ __forceinline__ void mma_mx32(f32x16_t& acc, const u32x4_t& a, const 
 // them, and the one needed is read back as a byte.
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 64;
+constexpr int kFewK = 256;  // K elements of a step: 128 bytes of a row, 8 exponents
 
 template <int MT>
 struct Slot {
@@ -130,7 +130,7 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
   const int lr = lane & 15, lg = lane >> 4;
   ESG_LDS char* const ring = (ESG_LDS char*)lds_ + w * P * S::BYTES;
   const int n0 = blockIdx.x * 16, nrows = min(16, g.N - n0), mrows = s.m1 - s.m0;
-  const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + kStepK - 1) / kStepK;
+  const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + kFewK - 1) / kFewK;
   const size_t b0 = (size_t)s.e * g.N + n0;
   uint32_t b_skew, a_skew;
   const DmaSrc rb = make_dma_src(g.b + b0 * KH, (uint32_t)(nrows * KH));
@@ -208,7 +208,7 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       // past K the codes are zeros, and the exponents those of other rows: any but 255 will do
-      const bool in = t * kStepK + (j * 4 + lg) * 32 < g.K;
+      const bool in = t * kFewK + (j * 4 + lg) * 32 < g.K;
       const uint4 bv = frag_krow(slot, lr, j * 4 + lg);
       const uint32_t bs = in ? *(const ESG_LDS uint8_t*)(slot + eb[j]) : 0u;
 #pragma unroll
@@ -262,30 +262,33 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs g) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiles.  BM x BN outputs per workgroup of four waves, each BM/2 x BN/2; K in steps of
-// 256 (128 bytes per row) through two direct-to-LDS stages of K-row tiles; in a step
-// four slices of 64, each FN x FM products of 32 x 32 x 64.
+// Tiles.  BM x BN outputs per workgroup of waves of 64 x BN/2 each.  K in steps of 128
+// (64 bytes per row) through a ring of four direct-to-LDS stages; in a step two slices of
+// 64, each FN x FM products of 32 x 32 x 64.
 //
-// A slice's operands are read under the products of the one before; the barrier sits
-// before the products of the last slice, whose operands are in registers: under them
-// the next step's first slice is read and the loads of the step after that are issued.
-// The exponents of a step go through registers to LDS, eight bytes per row and step, and
-// are read once per step and fragment.
+// A slice's operands are read under the products of the one before.  The barrier of a step
+// sits before the products of its second slice, whose operands are in registers: behind
+// it the step's stage is free, and the loads of four steps on go there, spread over the
+// next two slices' products.  So three steps' loads are on their way at any time, and the
+// only wait is for the oldest.
+// The exponents of four steps (16 bytes of a row that starts at any byte) come by the same
+// way, as the five dwords that hold them, into two slots; a step's four bytes of a row are
+// put together by the lanes that use them.
 // ---------------------------------------------------------------------------
 template <int BM, int BN>
 struct Tile {
-  static constexpr int NTH = 256, NW = 4;
-  static constexpr int WM = BM / 2, WN = BN / 2;
+  static constexpr int NWM = BM / 64, NWN = 2, NW = NWM * NWN, NTH = NW * 64;
+  static constexpr int WM = 64, WN = BN / NWN;
   static constexpr int FM = WM / 32, FN = WN / 32;
-  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
-  static constexpr int SROWS = BM + BN, SPT = SROWS / NTH;  // rows of exponents, of a thread
-  static constexpr int SLOT = SROWS * 8;
-  static constexpr int LDS = 2 * STAGE + 2 * SLOT;
-  static_assert(SROWS % NTH == 0, "whole rows of exponents per thread");
+  static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64, STAGE = A_BYTES + B_BYTES;
+  static constexpr int SROWS = BM + BN;                 // rows of exponents: one per thread
+  static constexpr int SLOT = SROWS * 20;               // 16 bytes of each row, then 4 of each
+  static constexpr int LDS = 4 * STAGE + 2 * SLOT;
+  static_assert(SROWS == NTH, "a row of exponents per thread");
 };
 
 // position of 16-byte chunk c of row r: 16 consecutive rows at one chunk lie in different banks
-__device__ __forceinline__ int mx_swz(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int mx_swz(int r) { return (r >> 2) & 3; }
 
 __device__ __forceinline__ void dma16_at(const DmaSrc& s, ESG_LDS char* wave_base, uint32_t voff, uint32_t soff) {
   const int m = __builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)wave_base);
@@ -306,13 +309,13 @@ __device__ __forceinline__ void tile_of(int id, int total, int nm, int nn, int& 
 }
 
 template <int BM, int BN, int OUT>
-__global__ __launch_bounds__(256, 1) void mx_tile_kernel(MxArgs g) {
+__global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs g) {
   using C = Tile<BM, BN>;
   __shared__ __attribute__((aligned(1024))) char lds_[C::LDS];
   ESG_LDS char* const lds = (ESG_LDS char*)lds_;
-  ESG_LDS char* const slots = lds + 2 * C::STAGE;
+  ESG_LDS char* const slots = lds + 4 * C::STAGE;
   const int lane = threadIdx.x & 63, w = wave_id();
-  const int wm = w & 1, wn = w >> 1;
+  const int wm = w % C::NWM, wn = w / C::NWM;
   const int lr = lane & 31, lh = lane >> 5;
   int tm, tn;
   tile_of(blockIdx.x, g.nm * g.nn, g.nm, g.nn, tm, tn);
@@ -320,7 +323,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(MxArgs g) {
   const int mrows = s.m1 - s.m0;
   if (mrows <= 0) return;
   const int n0 = tn * BN, nrows = min(BN, g.N - n0);
-  const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + kStepK - 1) / kStepK;
+  const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + 127) / 128;
   const bool gather = g.rows != nullptr;
   const size_t b0 = (size_t)s.e * g.N + n0;
   const DmaSrc rb = make_dma_src(g.b + b0 * KH, (uint32_t)(nrows * KH));
@@ -333,82 +336,55 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(MxArgs g) {
     return (unsigned)r < (unsigned)g.a_rows ? r : -1;
   };
 
-  // ---- loads: one instruction fills eight rows of 128 bytes ----
-  constexpr int NA = BM / 8 / 4, NB = BN / 8 / 4;  // instructions of a wave and step
+  // ---- loads: one instruction fills sixteen rows of 64 bytes ----
+  constexpr int NA = BM / 16 / C::NW, NB = BN / 16 / C::NW, NL = NA + NB;  // instructions of a wave and step
   uint32_t oa[NA], ob[NB];
-  auto chunk_at = [&](int i) __attribute__((always_inline)) {  // K bytes of this lane in the wave's i-th eight rows
-    return ((lane & 7) ^ mx_swz(i * 8 + (lane >> 3))) * 16;
-  };
+  const int koff = ((lane & 3) ^ mx_swz(lane >> 2)) * 16;
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
-    const int r = a_row((w * NA + i) * 8 + (lane >> 3));
-    oa[i] = r >= 0 ? (uint32_t)r * (uint32_t)KH + chunk_at(w * NA + i) : kOOB;
+    const int r = a_row((w * NA + i) * 16 + (lane >> 2));
+    oa[i] = r >= 0 ? (uint32_t)r * (uint32_t)KH + koff : kOOB;
   }
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int r = (w * NB + i) * 8 + (lane >> 3);
-    ob[i] = r < nrows ? (uint32_t)(r * KH) + chunk_at(w * NB + i) : kOOB;
+    const int r = (w * NB + i) * 16 + (lane >> 2);
+    ob[i] = r < nrows ? (uint32_t)(r * KH) + koff : kOOB;
   }
-  // loads of step t into a stage; past the last step: the last one's again (not used)
-  auto issue = [&](int t, ESG_LDS char* st) __attribute__((always_inline)) {
-    const uint32_t k = (uint32_t)min(t, steps - 1) * 128u;
-#pragma unroll
-    for (int i = 0; i < NA; ++i) dma16_at(ra, st + (w * NA + i) * 1024, oa[i], k);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) dma16_at(rb, st + C::A_BYTES + (w * NB + i) * 1024, ob[i], k);
-  };
-  // before the step that K cuts short is issued: chunks at or past K read zeros from here on
-  auto cut = [&](int t) __attribute__((always_inline)) {
-    if (t == steps - 1 && g.K % kStepK != 0) {
-#pragma unroll
-      for (int i = 0; i < NA; ++i) oa[i] = t * 128 + chunk_at(w * NA + i) < KH ? oa[i] : kOOB;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) ob[i] = t * 128 + chunk_at(w * NB + i) < KH ? ob[i] : kOOB;
-    }
+  // The wave's i-th load of step t into its stage; past the last step: of the last one again (not used).  Chunks at or
+  // past K read zeros.  (No branch: one between two slices would draw the products before it behind it.)
+  auto issue = [&](int t, int S, int i) __attribute__((always_inline)) {
+    ESG_LDS char* const st = lds + S * C::STAGE;
+    const int k = min(t, steps - 1) * 64;
+    const uint32_t at = i < NA ? oa[i < NA ? i : 0] : ob[i < NA ? 0 : i - NA];
+    const uint32_t voff = koff < KH - k ? at : kOOB;
+    if (i < NA)
+      dma16_at(ra, st + (w * NA + i) * 1024, voff, (uint32_t)k);
+    else
+      dma16_at(rb, st + C::A_BYTES + (w * NB + i - NA) * 1024, voff, (uint32_t)k);
   };
 
-  // ---- exponents: this thread's rows, the three dwords that hold a step's eight bytes ----
-  uint32_t os[C::SPT], skew[C::SPT];
-  rsrc_t rs[C::SPT];
-#pragma unroll
-  for (int i = 0; i < C::SPT; ++i) {
-    const int r = i * 256 + (int)threadIdx.x;
-    if (i * 256 + w * 64 < BM) {  // a wave's rows lie on one side: BM is a multiple of 64
-      const size_t from = gather ? 0 : (size_t)s.m0 * KS;
-      const uint32_t bytes = (uint32_t)(gather ? g.a_rows : mrows) * (uint32_t)KS, sk = (uint32_t)(from & 3);
-      rs[i] = make_rsrc(g.sa + (from - sk), (sk + bytes + 3) & ~3u);
-      const int ar = a_row(r);
-      const uint32_t at = sk + (uint32_t)(ar >= 0 ? ar : 0) * (uint32_t)KS;
-      os[i] = ar >= 0 ? at & ~3u : kOOB;
-      skew[i] = at & 3;
-    } else {
-      const size_t from = b0 * KS;
-      const uint32_t sk = (uint32_t)(from & 3);
-      rs[i] = make_rsrc(g.sb + (from - sk), (sk + (uint32_t)(nrows * KS) + 3) & ~3u);
-      const uint32_t at = sk + (uint32_t)((r - BM) * KS);
-      os[i] = r - BM < nrows ? at & ~3u : kOOB;
-      skew[i] = at & 3;
-    }
+  // ---- exponents: this thread's row of the four steps of group u, from the dword that holds its first byte ----
+  DmaSrc rs;
+  uint32_t os;
+  const bool skewed = (KS & 3) != 0;  // some row starts inside a dword
+  uint32_t a_skew, b_skew;
+  const DmaSrc rsb = scale_src(g.sb, b0 * KS, (uint32_t)(nrows * KS), b_skew);
+  const DmaSrc rsa = gather ? scale_src(g.sa, 0, (uint32_t)g.a_rows * (uint32_t)KS, a_skew)
+                            : scale_src(g.sa, (size_t)s.m0 * KS, (uint32_t)(mrows * KS), a_skew);
+  if (w * 64 < BM) {  // a wave's rows lie on one side: BM is a multiple of 64
+    rs = rsa;
+    const int r = a_row((int)threadIdx.x);
+    os = r >= 0 ? (a_skew + (uint32_t)r * (uint32_t)KS) & ~3u : kOOB;
+  } else {
+    rs = rsb;
+    const int r = (int)threadIdx.x - BM;
+    os = r < nrows ? (b_skew + (uint32_t)(r * KS)) & ~3u : kOOB;
   }
-  uint32_t sreg[C::SPT][3];
-  auto load_scales = [&](int t) __attribute__((always_inline)) {
-    const uint32_t k = (uint32_t)min(t, steps - 1) * 8u;
-#pragma unroll
-    for (int i = 0; i < C::SPT; ++i)
-#pragma unroll
-      for (int d = 0; d < 3; ++d)
-        sreg[i][d] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs[i], (int)(os[i] + k + d * 4), 0, 0);
-  };
-  auto put_scales = [&](int t, ESG_LDS char* slot) __attribute__((always_inline)) {
-    const int left = KS - min(t, steps - 1) * 8;  // bytes of the row still in K; those past it are other rows'
-    const uint32_t m0 = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
-    const uint32_t m1 = left >= 8 ? ~0u : left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u;
-#pragma unroll
-    for (int i = 0; i < C::SPT; ++i) {
-      const uint32_t lo = __builtin_amdgcn_alignbyte(sreg[i][1], sreg[i][0], skew[i]);
-      const uint32_t hi = __builtin_amdgcn_alignbyte(sreg[i][2], sreg[i][1], skew[i]);
-      lds_write8(slot + (i * 256 + (int)threadIdx.x) * 8, lo & m0, hi & m1);
-    }
+  auto issue_scales = [&](int u, int slot) __attribute__((always_inline)) {
+    ESG_LDS char* const to = slots + slot * C::SLOT;
+    const uint32_t k = os + (uint32_t)min(u, (steps - 1) >> 2) * 16u;
+    dma16(rs, to + w * 1024, k);
+    dma4(rs, to + C::SROWS * 16 + w * 256, skewed ? k + 16u : kOOB);
   };
 
   f32x16_t acc[C::FN][C::FM];
@@ -419,82 +395,127 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(MxArgs g) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-  // operands of a slice, and the exponents of a step as this lane's half needs them: bytes 0 and 2 of two words
+  // operands of a slice, and the exponents of a step as this lane's half needs them: bytes 0 and 2 of a word
+  constexpr int PER = C::FM * C::FN, FR = C::FM + C::FN;
   u32x4_t av[2][C::FM], bv[2][C::FN];
-  uint32_t as[C::FM][2], bs[C::FN][2];
+  uint32_t es[FR], raw[FR][2], skew[FR];  // fragments in the order b0, a0 .., b1 ..
   const int ra0 = wm * C::WM + lr, rb0 = wn * C::WN + lr;
-  // 32 rows further on are 32 * 128 bytes: the swizzle repeats every 16 rows
-  auto read_slice = [&](ESG_LDS char* st, int sl, int to) __attribute__((always_inline)) {
-    const ESG_LDS char* pa = st + ra0 * 128 + (((sl * 2 + lh) ^ mx_swz(ra0)) << 4);
-    const ESG_LDS char* pb = st + C::A_BYTES + rb0 * 128 + (((sl * 2 + lh) ^ mx_swz(rb0)) << 4);
-#pragma unroll
-    for (int j = 0; j < C::FM; ++j) av[to][j] = *(const ESG_LDS u32x4_t*)(pa + j * 4096);
-#pragma unroll
-    for (int i = 0; i < C::FN; ++i) bv[to][i] = *(const ESG_LDS u32x4_t*)(pb + i * 4096);
+  auto is_a = [](int f) { return f >= 1 && f <= C::FM; };
+  auto frag_row = [&](int f) __attribute__((always_inline)) {  // of the tile's rows, A's then B's
+    return is_a(f) ? ra0 + (f - 1) * 32 : BM + rb0 + (f == 0 ? 0 : f - C::FM) * 32;
   };
-  auto read_scales = [&](ESG_LDS char* slot) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j) {
-      const u32x2_t v = *(const ESG_LDS u32x2_t*)(slot + (ra0 + j * 32) * 8);
-      as[j][0] = v.x >> (8 * lh);
-      as[j][1] = v.y >> (8 * lh);
+  for (int f = 0; f < FR; ++f) {
+    const int r = frag_row(f);
+    if (is_a(f)) {
+      const int ar = a_row(r);
+      skew[f] = (a_skew + (uint32_t)(ar >= 0 ? ar : 0) * (uint32_t)KS) & 3;
+    } else {
+      skew[f] = (b_skew + (uint32_t)((r - BM) * KS)) & 3;
     }
-#pragma unroll
-    for (int i = 0; i < C::FN; ++i) {
-      const u32x2_t v = *(const ESG_LDS u32x2_t*)(slot + (BM + rb0 + i * 32) * 8);
-      bs[i][0] = v.x >> (8 * lh);
-      bs[i][1] = v.y >> (8 * lh);
+  }
+  // 32 rows further on are 32 * 64 bytes: the swizzle repeats every 16 rows
+  auto read_frag = [&](int S, int sl, int to, int f) __attribute__((always_inline)) {
+    const ESG_LDS char* const st = lds + S * C::STAGE;
+    if (is_a(f)) {
+      const ESG_LDS char* p = st + ra0 * 64 + (((sl * 2 + lh) ^ mx_swz(ra0)) << 4);
+      av[to][f - 1] = *(const ESG_LDS u32x4_t*)(p + (f - 1) * 2048);
+    } else {
+      const ESG_LDS char* p = st + C::A_BYTES + rb0 * 64 + (((sl * 2 + lh) ^ mx_swz(rb0)) << 4);
+      bv[to][f == 0 ? 0 : f - C::FM] = *(const ESG_LDS u32x4_t*)(p + (f == 0 ? 0 : f - C::FM) * 2048);
     }
   };
-  auto products = [&](int sl, int from) __attribute__((always_inline)) {
+  // the two dwords that hold the step's bytes: the fifth dword of a row lies apart
+  auto read_raw = [&](int slot, int S, int f) __attribute__((always_inline)) {
+    const ESG_LDS char* const sc = slots + slot * C::SLOT;
+    raw[f][0] = *(const ESG_LDS uint32_t*)(sc + frag_row(f) * 16 + S * 4);
+    raw[f][1] = S < 3 ? *(const ESG_LDS uint32_t*)(sc + frag_row(f) * 16 + S * 4 + 4)
+                      : *(const ESG_LDS uint32_t*)(sc + C::SROWS * 16 + frag_row(f) * 4);
+  };
+  auto set_scales = [&](int t) __attribute__((always_inline)) {
+    const int left = KS - t * 4;  // bytes of the row still in K; those past it are other rows'
+    const uint32_t mask = left >= 4 ? ~0u : left > 0 ? (1u << (8 * left)) - 1u : 0u;
+#pragma unroll
+    for (int f = 0; f < FR; ++f) es[f] = (__builtin_amdgcn_alignbyte(raw[f][1], raw[f][0], skew[f]) & mask) >> (8 * lh);
+  };
+  // the products of a slice, with `beside(p)` in the issue order behind the p-th of them
+  auto products = [&](int sl, auto&& beside) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < C::FN; ++i)
 #pragma unroll
       for (int j = 0; j < C::FM; ++j) {
-        if (sl & 1)
-          mma_mx32<2>(acc[i][j], bv[from][i], av[from][j], bs[i][sl >> 1], as[j][sl >> 1]);
+        const uint32_t eb = es[i == 0 ? 0 : C::FM + i], ea = es[1 + j];
+        if (sl == 1)
+          mma_mx32<2>(acc[i][j], bv[sl][i], av[sl][j], eb, ea);
         else
-          mma_mx32<0>(acc[i][j], bv[from][i], av[from][j], bs[i][sl >> 1], as[j][sl >> 1]);
+          mma_mx32<0>(acc[i][j], bv[sl][i], av[sl][j], eb, ea);
+        beside(i * C::FM + j);
+        __builtin_amdgcn_sched_barrier(0);
       }
   };
+  // the parts of n pieces of work that go behind the p-th product
+  auto spread = [&](int n, int p, auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = p * n / PER; i < (p + 1) * n / PER; ++i) f(i);
+  };
+  constexpr int HALF = NL / 2;  // loads of a step issued behind its barrier's slice; the others in the next one
 
-  load_scales(0);
-  cut(0);
-  issue(0, lds);
-  put_scales(0, slots);
-  load_scales(1);
-  cut(1);
-  issue(1, lds + C::STAGE);
-  put_scales(1, slots + C::SLOT);
-  wait_vmcnt<0>();
-  wait_lgkm0();
+  issue_scales(0, 0);
+#pragma unroll
+  for (int i = 0; i < NL; ++i) issue(0, 0, i);
+  issue_scales(1, 1);
+#pragma unroll
+  for (int t = 1; t < 4; ++t) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (t < 3 || i < HALF) issue(t, t, i);
+  }
+  wait_vmcnt<2 + 2 * NL + HALF>();
   barrier();
-  read_scales(slots);
-  read_slice(lds, 0, 0);
-  for (int t = 0; t < steps; ++t) {
-    ESG_LDS char* const st = lds + (t & 1) * C::STAGE;
-    ESG_LDS char* const st2 = lds + ((t & 1) ^ 1) * C::STAGE;
-    ESG_LDS char* const slot = slots + (t & 1) * C::SLOT;
-    ESG_LDS char* const slot2 = slots + ((t & 1) ^ 1) * C::SLOT;
-    load_scales(t + 2);
-    read_slice(st, 1, 1);
-    products(0, 0);
-    read_slice(st, 2, 0);
-    products(1, 1);
-    read_slice(st, 3, 1);
-    products(2, 0);
-    // this step's operands are all in registers; the next step's have landed
-    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int f = 0; f < FR; ++f) {
+    read_raw(0, 0, f);
+    read_frag(0, 0, 0, f);
+  }
+  set_scales(0);
+  // Step t in stage S = t % 4, exponents in slot U = t / 4 % 2 (constants at each place).
+  auto step = [&](int t, int S, int U) __attribute__((always_inline)) {
+    products(0, [&](int p) __attribute__((always_inline)) {
+      spread(FR, p, [&](int f) __attribute__((always_inline)) { read_frag(S, 1, 1, f); });
+      spread(NL - HALF, p, [&](int i) __attribute__((always_inline)) { issue(t + 3, (S + 3) & 3, HALF + i); });
+    });
+    // the second slice's operands are in registers and the next step's have landed: two steps' loads are newer
     wait_lgkm0();
-    wait_vmcnt<0>();
+    wait_vmcnt<2 * NL>();
     barrier();
-    put_scales(t + 2, slot);
+    if (S == 3) issue_scales((t >> 2) + 2, U);  // the slot's last bytes were read before the barrier
     __builtin_amdgcn_sched_barrier(0);
-    cut(t + 2);
-    issue(t + 2, st);
-    read_slice(st2, 0, 0);
-    products(3, 1);
-    read_scales(slot2);
+    products(1, [&](int p) __attribute__((always_inline)) {
+      spread(FR, p, [&](int f) __attribute__((always_inline)) {
+        read_frag((S + 1) & 3, 0, 0, f);
+        read_raw(S == 3 ? U ^ 1 : U, (S + 1) & 3, f);
+      });
+      spread(HALF, p, [&](int i) __attribute__((always_inline)) { issue(t + 4, S, i); });
+    });
+    set_scales(t + 1);
+  };
+  for (int t = 0;; t += 8) {
+    step(t, 0, 0);
+    if (t + 1 >= steps) break;
+    step(t + 1, 1, 0);
+    if (t + 2 >= steps) break;
+    step(t + 2, 2, 0);
+    if (t + 3 >= steps) break;
+    step(t + 3, 3, 0);
+    if (t + 4 >= steps) break;
+    step(t + 4, 0, 1);
+    if (t + 5 >= steps) break;
+    step(t + 5, 1, 1);
+    if (t + 6 >= steps) break;
+    step(t + 6, 2, 1);
+    if (t + 7 >= steps) break;
+    step(t + 7, 3, 1);
+    if (t + 8 >= steps) break;
   }
   wait_lgkm0();
   wait_vmcnt<0>();
@@ -507,7 +528,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(MxArgs g) {
   char* y = (char*)g.y;
   const int mw = wm * C::WM, nw = n0 + wn * C::WN;
   if (g.N * ES % 16 == 0 && ((uintptr_t)y & 15) == 0) {
-    static_assert(32 * NCH * 16 * 4 <= 2 * C::STAGE, "the pieces lie in the stages");
+    static_assert(32 * NCH * 16 * C::NW <= 4 * C::STAGE, "the pieces lie in the stages");
     ESG_LDS char* out = lds + w * (32 * NCH * 16);
 #pragma unroll
     for (int j = 0; j < C::FM; ++j) {
@@ -591,9 +612,9 @@ hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
   }
   LaunchTimer timer("mx_tile", stream);
   if (p.tile == 256)
-    hipLaunchKernelGGL((mx_tile_kernel<256, 256, OUT>), dim3(p.nm * p.nn), dim3(256), 0, stream, g);
+    hipLaunchKernelGGL((mx_tile_kernel<256, 256, OUT>), dim3(p.nm * p.nn), dim3(Tile<256, 256>::NTH), 0, stream, g);
   else
-    hipLaunchKernelGGL((mx_tile_kernel<128, 128, OUT>), dim3(p.nm * p.nn), dim3(256), 0, stream, g);
+    hipLaunchKernelGGL((mx_tile_kernel<128, 128, OUT>), dim3(p.nm * p.nn), dim3(Tile<128, 128>::NTH), 0, stream, g);
   return hipGetLastError();
 }
 

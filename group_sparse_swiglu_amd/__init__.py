@@ -44,6 +44,7 @@ __all__ = [
     "rms_norm", "rms_norm_fwd", "rms_norm_bwd", "rms_norm_bwd_workspace_size", "rms_norm_quantize",
     "topk_routing", "topk_routing_fwd", "topk_routing_bwd", "topk_routing_supported",
     "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_matmul", "mxfp4_matmul_workspace_size", "mxfp4_grouped_matmul",
+    "mxfp4_grouped_matmul_workspace_size",
 ]
 
 ESG_F32 = 0
@@ -138,7 +139,8 @@ _SIGNATURES = {
     "esg_mxfp4_matmul": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_vp, _c_vp, _c_size,
                                   _c_vp]),
     "esg_mxfp4_grouped_matmul": (_c_int, [_c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_int,
-                                          _c_int, _c_int, _c_vp, _c_vp]),
+                                          _c_int, _c_int, _c_vp, _c_vp, _c_size, _c_vp]),
+    "esg_mxfp4_grouped_matmul_workspace_size": (_c_int, [_c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_c_size)]),
     "esg_mfma_rate_probe": (_c_int, [_c_int, _c_int, _c_vp, _c_vp]),
     "esg_timing_enable": (_c_int, [_c_int]),
     "esg_timing_reset": (_c_int, []),
@@ -1120,14 +1122,25 @@ def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, wor
     return out
 
 
-def mxfp4_grouped_matmul(a, a_scale, b, b_scale, offsets, rows=None, out_dtype=torch.bfloat16, out=None):
+@functools.lru_cache(maxsize=4096)
+def mxfp4_grouped_matmul_workspace_size(M: int, N: int, K: int, experts: int) -> int:
+    """Bytes of scratch esg_mxfp4_grouped_matmul needs for this shape (0 for most)."""
+    need = _c_size()
+    _check(lib().esg_mxfp4_grouped_matmul_workspace_size(M, N, K, experts, ctypes.byref(need)),
+           "mxfp4_grouped_matmul_workspace_size")
+    return need.value
+
+
+def mxfp4_grouped_matmul(a, a_scale, b, b_scale, offsets, rows=None, out_dtype=torch.bfloat16, out=None,
+                         workspace: Optional[dict] = None):
     """Products of rows in the order of their experts, each with its expert's weights -> [M, N].
 
     a, a_scale: [R, K/2] and [R, K/32]; b, b_scale: [E, N, K/2] and [E, N, K/32], uint8 as
     mxfp4_quantize gives them; offsets: int32 [E + 1] and rows: int32 [M], as bucket_by_group
     gives them: rows offsets[e] .. offsets[e+1] - 1 of the result are a[rows[m]] B[e]^T
     (a[m] without ``rows``, M = R).  Rows outside all offsets are left as they were in
-    ``out`` (not written at all)."""
+    ``out`` (not written at all).  ``workspace``: optional dict reused across calls to hold the
+    scratch buffer (one per stream)."""
     if a.dim() != 2 or b.dim() != 3 or a.shape[1] != b.shape[2]:
         raise EsgError("a must be [R, K/2] and b [E, N, K/2]")
     (R, KH), (experts, N), dev, gpu, u8 = a.shape, b.shape[:2], a.device, a.get_device(), torch.uint8
@@ -1141,10 +1154,13 @@ def mxfp4_grouped_matmul(a, a_scale, b, b_scale, offsets, rows=None, out_dtype=t
     elif out.shape != (M, N):
         raise EsgError("out must be [M, N]")
     i32 = torch.int32
+    need = mxfp4_grouped_matmul_workspace_size(M, N, 2 * KH, experts)
+    ws = _ws(need, dev, workspace, "mxfp4_grouped_matmul") if need else None
     _check(lib().esg_mxfp4_grouped_matmul(
         _dev(a, "a", u8), _dev(a_scale, "a_scale", u8, gpu), R, _dev(rows, "rows", i32, gpu), _dev(b, "b", u8, gpu),
         _dev(b_scale, "b_scale", u8, gpu), experts, _dev(offsets, "offsets", i32, gpu), _dtype_code(out), M, N, 2 * KH,
-        _dev(out, "out", None, gpu), _stream(dev)), "mxfp4_grouped_matmul")
+        _dev(out, "out", None, gpu), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _stream(dev)),
+        "mxfp4_grouped_matmul")
     return out
 
 

@@ -831,11 +831,29 @@ int mx_operands(const void* a, const void* a_scale, const void* b, const void* b
 }
 }  // namespace
 
+namespace {
+MxMatmul mx_sizes(int grouped, int M, int N, int K, int experts) {
+  MxMatmul c{};
+  c.grouped = grouped;
+  c.a_rows = c.M = M;
+  c.N = N;
+  c.K = K;
+  c.E = experts;
+  return c;
+}
+int mx_launch(const MxMatmul& c, size_t workspace_bytes, void* stream) {
+  const size_t need = mx_matmul_workspace_bytes(c);
+  if (need > 0 && (c.workspace == nullptr || workspace_bytes < need)) return ESG_ERR_WORKSPACE;
+  if (!aligned16(c.workspace)) return ESG_ERR_INVALID_ARG;
+  return hip_status(launch_mx_matmul(c, (hipStream_t)stream));
+}
+}  // namespace
+
 int esg_mxfp4_matmul_workspace_size(int M, int N, int K, size_t* workspace_bytes) {
   if (workspace_bytes == nullptr) return ESG_ERR_INVALID_ARG;
   const int e = mx_shape(M, N, K, 1);
   if (e != ESG_OK) return e;
-  *workspace_bytes = mx_matmul_workspace_bytes(M, N, K);
+  *workspace_bytes = mx_matmul_workspace_bytes(mx_sizes(0, M, N, K, 1));
   return ESG_OK;
 }
 
@@ -846,17 +864,21 @@ int esg_mxfp4_matmul(const void* a, const void* a_scale, const void* b, const vo
   if (M == 0 || N == 0) return float_dtype(out_dtype) ? ESG_OK : ESG_ERR_UNSUPPORTED;
   e = mx_operands(a, a_scale, b, b_scale, out_dtype, y);
   if (e != ESG_OK) return e;
-  const size_t need = mx_matmul_workspace_bytes(M, N, K);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return ESG_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return ESG_ERR_INVALID_ARG;
-  return hip_status(launch_mx_matmul(MxMatmul{a, a_scale, b, b_scale, nullptr, nullptr, out_dtype, M, M, N, K, 1, y,
-                                              workspace},
-                                     (hipStream_t)stream));
+  return mx_launch(MxMatmul{a, a_scale, b, b_scale, 0, nullptr, nullptr, out_dtype, M, M, N, K, 1, y, workspace},
+                   workspace_bytes, stream);
+}
+
+int esg_mxfp4_grouped_matmul_workspace_size(int M, int N, int K, int experts, size_t* workspace_bytes) {
+  if (workspace_bytes == nullptr) return ESG_ERR_INVALID_ARG;
+  const int e = mx_shape(M, N, K, experts);
+  if (e != ESG_OK) return e;
+  *workspace_bytes = mx_matmul_workspace_bytes(mx_sizes(1, M, N, K, experts));
+  return ESG_OK;
 }
 
 int esg_mxfp4_grouped_matmul(const void* a, const void* a_scale, int a_rows, const int32_t* rows, const void* b,
                              const void* b_scale, int experts, const int32_t* offsets, int out_dtype, int M, int N,
-                             int K, void* y, void* stream) {
+                             int K, void* y, void* workspace, size_t workspace_bytes, void* stream) {
   int e = mx_shape(M, N, K, experts);
   if (e != ESG_OK) return e;
   if (a_rows < 0 || (rows == nullptr && a_rows < M)) return ESG_ERR_INVALID_ARG;
@@ -865,9 +887,8 @@ int esg_mxfp4_grouped_matmul(const void* a, const void* a_scale, int a_rows, con
   e = mx_operands(a, a_scale, b, b_scale, out_dtype, y);
   if (e != ESG_OK) return e;
   if (offsets == nullptr || (((uintptr_t)offsets | (uintptr_t)rows) & 3u) != 0) return ESG_ERR_INVALID_ARG;
-  return hip_status(launch_mx_matmul(MxMatmul{a, a_scale, b, b_scale, offsets, rows, out_dtype, a_rows, M, N, K, experts,
-                                              y, nullptr},
-                                     (hipStream_t)stream));
+  return mx_launch(MxMatmul{a, a_scale, b, b_scale, 1, offsets, rows, out_dtype, a_rows, M, N, K, experts, y, workspace},
+                   workspace_bytes, stream);
 }
 
 int esg_moe_decode_supported(int tokens, int experts, int topk, int d_model, int d_ff, int w_dtype) {

@@ -222,14 +222,15 @@ hipError_t launch_mx_dequant(int dtype, const void* q, const void* scale, int64_
 // ---- 4-bit products (esg_mx_gemm.hip) -----------------------------------------------
 struct MxMatmul {
   const void *a, *sa, *b, *sb;
-  const int32_t* offsets;  // [E + 1], or NULL (E 1): one b for all rows
+  int grouped;             // rows by expert, through offsets; else one b (E 1)
+  const int32_t* offsets;  // [E + 1]
   const int32_t* rows;     // [M], or NULL: row m is a[m]
   int out_dtype;           // 0 float32, 1 bf16
   int a_rows, M, N, K, E;
   void* y;
-  void* workspace;         // mx_matmul_workspace_bytes of a product without offsets
+  void* workspace;         // mx_matmul_workspace_bytes
 };
-size_t mx_matmul_workspace_bytes(int M, int N, int K);
+size_t mx_matmul_workspace_bytes(const MxMatmul& c);  // of c's grouped and sizes
 hipError_t launch_mx_matmul(const MxMatmul& c, hipStream_t stream);
 
 // ---- whole expert layer for a few tokens (esg_moe.hip) --------------------------

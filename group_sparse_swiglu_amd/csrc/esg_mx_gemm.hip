@@ -33,7 +33,9 @@ struct MxArgs {
   const int32_t* offsets;  // [E + 1], or NULL: one b for all rows
   const int32_t* rows;     // [M], or NULL
   void* y;
-  int a_rows, M, N, K, E;
+  const uint32_t* ta;      // exponents as the large tiles take them: [ceil(K/128)][M] and [ceil(K/128)][E N] words
+  const uint32_t* tb;
+  int a_rows, M, N, K, E, grouped;
   int nm, nn;              // row chunks or tiles (grouped: at most so many), tiles along n
 };
 
@@ -72,6 +74,23 @@ __device__ __forceinline__ Span find_span(const MxArgs& g, int z, int chunk, int
   return Span{0, 0, 0};
 }
 
+// Direct-to-LDS loads (see dma16) of 16 bytes per lane at voff + soff, soff scalar and not past the buffer (the range
+// check compares voff with the buffer's size less soff), and of 4.  The compiler does not see which scalar registers an
+// asm block reads, and one that a vector instruction wrote (a readlane, of a spilled descriptor for one) may be read
+// by a load five states later at the earliest: hence the s_nop.
+__device__ __forceinline__ void load16(const DmaSrc& s, ESG_LDS char* wave_base, uint32_t voff, uint32_t soff = 0) {
+  const int m = __builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)wave_base);
+  const int so = __builtin_amdgcn_readfirstlane((int)soff);
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+               :
+               : "v"(voff), "s"(s.d), "{m0}"(m), "s"(so)
+               : "memory");
+}
+__device__ __forceinline__ void load4(const DmaSrc& s, ESG_LDS char* wave_base, uint32_t voff) {
+  const int m = __builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)wave_base);
+  asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(voff), "s"(s.d), "{m0}"(m) : "memory");
+}
+
 // Descriptor of the exponents of `rows` rows from byte `from` of p (4-byte aligned), in whole dwords; skew: what
 // `from` lies past the descriptor's base.  A dword at either end that holds a wanted byte may hold others beside it.
 __device__ __forceinline__ DmaSrc scale_src(const uint8_t* p, size_t from, uint32_t bytes, uint32_t& skew) {
@@ -101,6 +120,7 @@ __device__ __forceinline__ void mma_mx32(f32x16_t& acc, const u32x4_t& a, const 
 // step (8 bytes of a row that starts at any byte) come as the three dwords that hold
 // them, and the one needed is read back as a byte.
 // ---------------------------------------------------------------------------
+constexpr int kStream = 2;   // store policy: past the caches
 constexpr int kFewRows = 64;
 constexpr int kFewK = 256;  // K elements of a step: 128 bytes of a row, 8 exponents
 
@@ -188,12 +208,12 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
     const bool in = t < steps && t * 128 + koff < KH;
     const uint32_t k = (uint32_t)t * 128u, ks = (uint32_t)t * 8u;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) dma16(rb, slot + i * 1024, in ? ob[i] + k : kOOB);
+    for (int i = 0; i < 2; ++i) load16(rb, slot + i * 1024, in ? ob[i] + k : kOOB);
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) dma16(ra, slot + S::A_AT + i * 1024, in ? oa[i] + k : kOOB);
-    dma4(rsb, slot + S::SB_AT, t < steps ? osb + ks : kOOB);
+    for (int i = 0; i < 2 * MT; ++i) load16(ra, slot + S::A_AT + i * 1024, in ? oa[i] + k : kOOB);
+    load4(rsb, slot + S::SB_AT, t < steps ? osb + ks : kOOB);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) dma4(rsa, slot + S::SA_AT + i * 256, t < steps ? osa[i] + ks : kOOB);
+    for (int i = 0; i < MT; ++i) load4(rsa, slot + S::SA_AT + i * 256, t < steps ? osa[i] + ks : kOOB);
   };
   f32x4 acc[MT];
   zero_acc(acc);
@@ -271,9 +291,13 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs g) {
 // it the step's stage is free, and the loads of four steps on go there, spread over the
 // next two slices' products.  So three steps' loads are on their way at any time, and the
 // only wait is for the oldest.
-// The exponents of four steps (16 bytes of a row that starts at any byte) come by the same
-// way, as the five dwords that hold them, into two slots; a step's four bytes of a row are
-// put together by the lanes that use them.
+// The exponents of a step are a word per row and step.  Large tiles take them from arrays in
+// which a step's words of neighbouring rows are neighbours (mx_words_kernel lays them out
+// first): one load of whole lines per wave and step.  Read where they are, 16 bytes of each
+// of 64 rows at a time, they took a quarter of the loop (30000 cycles against 22000 for 16
+// steps).  The small tile, whose products are too short for a launch before them, does read
+// them there: the five dwords that hold the bytes of four steps (a row starts at any byte)
+// go into two slots, and the lanes that use a step's four bytes put them together.
 // ---------------------------------------------------------------------------
 template <int BM, int BN>
 struct Tile {
@@ -282,19 +306,14 @@ struct Tile {
   static constexpr int FM = WM / 32, FN = WN / 32;
   static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64, STAGE = A_BYTES + B_BYTES;
   static constexpr int SROWS = BM + BN;                 // rows of exponents: one per thread
-  static constexpr int SLOT = SROWS * 20;               // 16 bytes of each row, then 4 of each
-  static constexpr int LDS = 4 * STAGE + 2 * SLOT;
+  static constexpr bool WORDS = BM * BN > 128 * 128;    // exponents laid out in words before
+  static constexpr int SLOT = SROWS * (WORDS ? 4 : 20); // of a step; or 16 bytes of each row, then 4 of each
+  static constexpr int LDS = 4 * STAGE + (WORDS ? 4 : 2) * SLOT;
   static_assert(SROWS == NTH, "a row of exponents per thread");
 };
 
 // position of 16-byte chunk c of row r: 16 consecutive rows at one chunk lie in different banks
 __device__ __forceinline__ int mx_swz(int r) { return (r >> 2) & 3; }
-
-__device__ __forceinline__ void dma16_at(const DmaSrc& s, ESG_LDS char* wave_base, uint32_t voff, uint32_t soff) {
-  const int m = __builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)wave_base);
-  const int so = __builtin_amdgcn_readfirstlane((int)soff);
-  asm volatile("buffer_load_dwordx4 %0, %1, %3 offen lds" : : "v"(voff), "s"(s.d), "{m0}"(m), "s"(so) : "memory");
-}
 
 // Block id -> tile: each XCD (id % 8) takes a contiguous run of an order that walks eight m tiles, then the next n
 // tile, so the workgroups of an XCD share operand panels in its L2.
@@ -314,106 +333,140 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   __shared__ __attribute__((aligned(1024))) char lds_[C::LDS];
   ESG_LDS char* const lds = (ESG_LDS char*)lds_;
   ESG_LDS char* const slots = lds + 4 * C::STAGE;
-  const int lane = threadIdx.x & 63, w = wave_id();
+  const int w = wave_id();
   const int wm = w % C::NWM, wn = w / C::NWM;
-  const int lr = lane & 31, lh = lane >> 5;
-  int tm, tn;
-  tile_of(blockIdx.x, g.nm * g.nn, g.nm, g.nn, tm, tn);
-  const Span s = find_span(g, tm, BM, lane);
-  const int mrows = s.m1 - s.m0;
-  if (mrows <= 0) return;
-  const int n0 = tn * BN, nrows = min(BN, g.N - n0);
+  int lane, lr, lh;
   const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + 127) / 128;
-  const bool gather = g.rows != nullptr;
-  const size_t b0 = (size_t)s.e * g.N + n0;
-  const DmaSrc rb = make_dma_src(g.b + b0 * KH, (uint32_t)(nrows * KH));
-  const DmaSrc ra = gather ? make_dma_src(g.a, (uint32_t)g.a_rows * (uint32_t)KH)
-                           : make_dma_src(g.a + (size_t)s.m0 * KH, (uint32_t)(mrows * KH));
-  auto a_row = [&](int i) __attribute__((always_inline)) {
-    if (i >= mrows) return -1;
-    if (!gather) return i;
-    const int r = g.rows[s.m0 + i];
-    return (unsigned)r < (unsigned)g.a_rows ? r : -1;
-  };
+  const bool gather = g.rows != nullptr, skewed = (KS & 3) != 0;  // skewed: some row of exponents starts inside a dword
 
-  // ---- loads: one instruction fills sixteen rows of 64 bytes ----
-  constexpr int NA = BM / 16 / C::NW, NB = BN / 16 / C::NW, NL = NA + NB;  // instructions of a wave and step
-  uint32_t oa[NA], ob[NB];
-  const int koff = ((lane & 3) ^ mx_swz(lane >> 2)) * 16;
-#pragma unroll
-  for (int i = 0; i < NA; ++i) {
-    const int r = a_row((w * NA + i) * 16 + (lane >> 2));
-    oa[i] = r >= 0 ? (uint32_t)r * (uint32_t)KH + koff : kOOB;
-  }
-#pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const int r = (w * NB + i) * 16 + (lane >> 2);
-    ob[i] = r < nrows ? (uint32_t)(r * KH) + koff : kOOB;
-  }
-  // The wave's i-th load of step t into its stage; past the last step: of the last one again (not used).  Chunks at or
-  // past K read zeros.  (No branch: one between two slices would draw the products before it behind it.)
-  auto issue = [&](int t, int S, int i) __attribute__((always_inline)) {
-    ESG_LDS char* const st = lds + S * C::STAGE;
-    const int k = min(t, steps - 1) * 64;
-    const uint32_t at = i < NA ? oa[i < NA ? i : 0] : ob[i < NA ? 0 : i - NA];
-    const uint32_t voff = koff < KH - k ? at : kOOB;
-    if (i < NA)
-      dma16_at(ra, st + (w * NA + i) * 1024, voff, (uint32_t)k);
-    else
-      dma16_at(rb, st + C::A_BYTES + (w * NB + i - NA) * 1024, voff, (uint32_t)k);
-  };
-
-  // ---- exponents: this thread's row of the four steps of group u, from the dword that holds its first byte ----
-  DmaSrc rs;
-  uint32_t os;
-  const bool skewed = (KS & 3) != 0;  // some row starts inside a dword
-  uint32_t a_skew, b_skew;
-  const DmaSrc rsb = scale_src(g.sb, b0 * KS, (uint32_t)(nrows * KS), b_skew);
-  const DmaSrc rsa = gather ? scale_src(g.sa, 0, (uint32_t)g.a_rows * (uint32_t)KS, a_skew)
-                            : scale_src(g.sa, (size_t)s.m0 * KS, (uint32_t)(mrows * KS), a_skew);
-  if (w * 64 < BM) {  // a wave's rows lie on one side: BM is a multiple of 64
-    rs = rsa;
-    const int r = a_row((int)threadIdx.x);
-    os = r >= 0 ? (a_skew + (uint32_t)r * (uint32_t)KS) & ~3u : kOOB;
-  } else {
-    rs = rsb;
-    const int r = (int)threadIdx.x - BM;
-    os = r < nrows ? (b_skew + (uint32_t)(r * KS)) & ~3u : kOOB;
-  }
-  auto issue_scales = [&](int u, int slot) __attribute__((always_inline)) {
-    ESG_LDS char* const to = slots + slot * C::SLOT;
-    const uint32_t k = os + (uint32_t)min(u, (steps - 1) >> 2) * 16u;
-    dma16(rs, to + w * 1024, k);
-    dma4(rs, to + C::SROWS * 16 + w * 256, skewed ? k + 16u : kOOB);
-  };
-
-  f32x16_t acc[C::FN][C::FM];
-#pragma unroll
-  for (int i = 0; i < C::FN; ++i)
-#pragma unroll
-    for (int j = 0; j < C::FM; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-
-  // operands of a slice, and the exponents of a step as this lane's half needs them: bytes 0 and 2 of a word
+  // ---- the tile: its rows and columns, where its loads start ----
+  constexpr int NA = BM / 16 / C::NW, NB = BN / 16 / C::NW, NL = NA + NB + C::WORDS;  // loads of a wave and step
   constexpr int PER = C::FM * C::FN, FR = C::FM + C::FN;
-  u32x4_t av[2][C::FM], bv[2][C::FN];
-  uint32_t es[FR], raw[FR][2], skew[FR];  // fragments in the order b0, a0 .., b1 ..
-  const int ra0 = wm * C::WM + lr, rb0 = wn * C::WN + lr;
-  auto is_a = [](int f) { return f >= 1 && f <= C::FM; };
+  int koff, ra0, rb0;
+  // what follows from the lane, each time anew: kept over the tiles, its many addresses would drive out the sums
+  auto set_lane = [&]() __attribute__((always_inline)) {
+    lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    lr = lane & 31;
+    lh = lane >> 5;
+    koff = ((lane & 3) ^ mx_swz(lane >> 2)) * 16;  // a load fills sixteen rows of 64 bytes
+    ra0 = wm * C::WM + lr;
+    rb0 = wn * C::WN + lr;
+  };
+  auto is_a = [](int f) { return f >= 1 && f <= C::FM; };  // fragments in the order b0, a0 .., b1 ..
   auto frag_row = [&](int f) __attribute__((always_inline)) {  // of the tile's rows, A's then B's
     return is_a(f) ? ra0 + (f - 1) * 32 : BM + rb0 + (f == 0 ? 0 : f - C::FM) * 32;
   };
+  Span s;
+  int n0;
+  DmaSrc ra, rb, rs;
+  uint32_t oa[NA], ob[NB], os, skew[FR];
+  // the id-th tile; false: there is none (grouped rows may fill fewer tiles than are counted)
+  auto set_tile = [&](int id) __attribute__((always_inline)) {
+    int tm, tn;
+    tile_of(id, g.nm * g.nn, g.nm, g.nn, tm, tn);
+    s = find_span(g, tm, BM, lane);
+    const int mrows = s.m1 - s.m0;
+    if (mrows <= 0) return false;
+    n0 = tn * BN;
+    const int nrows = min(BN, g.N - n0);
+    const size_t b0 = (size_t)s.e * g.N + n0;
+    rb = make_dma_src(g.b + b0 * KH, (uint32_t)(nrows * KH));
+    ra = gather ? make_dma_src(g.a, (uint32_t)g.a_rows * (uint32_t)KH)
+                : make_dma_src(g.a + (size_t)s.m0 * KH, (uint32_t)(mrows * KH));
+    auto a_row = [&](int i) __attribute__((always_inline)) {
+      if (i >= mrows) return -1;
+      if (!gather) return i;
+      const int r = g.rows[s.m0 + i];
+      return (unsigned)r < (unsigned)g.a_rows ? r : -1;
+    };
 #pragma unroll
-  for (int f = 0; f < FR; ++f) {
-    const int r = frag_row(f);
-    if (is_a(f)) {
-      const int ar = a_row(r);
-      skew[f] = (a_skew + (uint32_t)(ar >= 0 ? ar : 0) * (uint32_t)KS) & 3;
-    } else {
-      skew[f] = (b_skew + (uint32_t)((r - BM) * KS)) & 3;
+    for (int i = 0; i < NA; ++i) {
+      const int r = a_row((w * NA + i) * 16 + (lane >> 2));
+      oa[i] = r >= 0 ? (uint32_t)r * (uint32_t)KH + koff : kOOB;
     }
-  }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int r = (w * NB + i) * 16 + (lane >> 2);
+      ob[i] = r < nrows ? (uint32_t)(r * KH) + koff : kOOB;
+    }
+    if constexpr (C::WORDS) {
+      // a wave's rows lie on one side (BM is a multiple of 64); the step's distance is soff, so no range check: the words
+      // of rows past the tile are those of others, or zeros, and meet zeros or results that are not stored
+      rs = w * 64 < BM ? make_dma_src(g.ta, (uint32_t)g.M * (uint32_t)steps * 4u)
+                       : make_dma_src(g.tb, (uint32_t)(g.E * g.N) * (uint32_t)steps * 4u);
+      os = (uint32_t)(w * 64 < BM ? s.m0 + (int)threadIdx.x : (int)b0 + (int)threadIdx.x - BM) * 4u;
+    } else {
+      // this thread's row of the tile, from the dword that holds its first byte
+      uint32_t a_skew, b_skew;
+      const DmaSrc rsb = scale_src(g.sb, b0 * KS, (uint32_t)(nrows * KS), b_skew);
+      const DmaSrc rsa = gather ? scale_src(g.sa, 0, (uint32_t)g.a_rows * (uint32_t)KS, a_skew)
+                                : scale_src(g.sa, (size_t)s.m0 * KS, (uint32_t)(mrows * KS), a_skew);
+      if (w * 64 < BM) {
+        rs = rsa;
+        const int r = a_row((int)threadIdx.x);
+        os = r >= 0 ? (a_skew + (uint32_t)r * (uint32_t)KS) & ~3u : kOOB;
+      } else {
+        rs = rsb;
+        const int r = (int)threadIdx.x - BM;
+        os = r < nrows ? (b_skew + (uint32_t)(r * KS)) & ~3u : kOOB;
+      }
+#pragma unroll
+      for (int f = 0; f < FR; ++f) {
+        const int r = frag_row(f);
+        skew[f] = 0;
+        if (skewed) {
+          const int ar = is_a(f) ? a_row(r) : 0;
+          skew[f] = (is_a(f) ? a_skew + (uint32_t)(ar >= 0 ? ar : 0) * (uint32_t)KS
+                             : b_skew + (uint32_t)((r - BM) * KS)) & 3;
+        }
+      }
+    }
+    return true;
+  };
+
+  // ---- loads ----
+  // The wave's i-th load of step t into its stage (the last: its exponents).  Chunks at or past K, and steps past the last, read zeros.  (No
+  // branch: one between two slices would draw the products before it behind it.)
+  auto issue = [&](int t, int S, int i) __attribute__((always_inline)) {
+    ESG_LDS char* const st = lds + S * C::STAGE;
+    if (C::WORDS && i == NA + NB) {  // (a step past the last: its last's, not used)
+      const uint32_t row = w * 64 < BM ? (uint32_t)g.M : (uint32_t)(g.E * g.N);
+      load4(rs, slots + S * C::SLOT + w * 256, os + (uint32_t)min(t, steps - 1) * row * 4u);
+      return;
+    }
+    const int k = t * 64;
+    const uint32_t at = i < NA ? oa[i < NA ? i : 0] : ob[i < NA ? 0 : i - NA];
+    const uint32_t voff = koff < KH - k ? at : kOOB;
+    const uint32_t soff = (uint32_t)min(k, KH);
+    if (i < NA)
+      load16(ra, st + (w * NA + i) * 1024, voff, soff);
+    else
+      load16(rb, st + C::A_BYTES + (w * NB + i - NA) * 1024, voff, soff);
+  };
+  // exponents of the four steps of group u, where they are read as they are
+  auto issue_scales = [&](int u, int slot) __attribute__((always_inline)) {
+    if constexpr (C::WORDS) return;
+    ESG_LDS char* const to = slots + slot * C::SLOT;
+    const uint32_t k = u * 4 < steps ? os + (uint32_t)u * 16u : kOOB;
+    load16(rs, to + w * 1024, k);
+    load4(rs, to + C::SROWS * 16 + w * 256, skewed ? k + 16u : kOOB);
+  };
+  // a tile's first loads: steps 0 to 2, the exponents of steps 0 to 7
+  auto first_loads = [&]() __attribute__((always_inline)) {
+    issue_scales(0, 0);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) issue(t, t, i);
+      if (t == 0) issue_scales(1, 1);
+    }
+  };
+  constexpr int BEHIND_FIRST = (C::WORDS ? 0 : 2) + 2 * NL;  // of them those behind step 0's
+
+  // ---- operands of a slice, and the exponents of a step as this lane's half needs them: bytes 0 and 2 of a word ----
+  u32x4_t av[2][C::FM], bv[2][C::FN];
+  uint32_t es[2][FR], raw[FR][2];  // of even and odd steps
   // 32 rows further on are 32 * 64 bytes: the swizzle repeats every 16 rows
   auto read_frag = [&](int S, int sl, int to, int f) __attribute__((always_inline)) {
     const ESG_LDS char* const st = lds + S * C::STAGE;
@@ -427,24 +480,34 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   };
   // the two dwords that hold the step's bytes: the fifth dword of a row lies apart
   auto read_raw = [&](int slot, int S, int f) __attribute__((always_inline)) {
+    if constexpr (C::WORDS) {
+      raw[f][0] = *(const ESG_LDS uint32_t*)(slots + S * C::SLOT + frag_row(f) * 4);
+      return;
+    }
     const ESG_LDS char* const sc = slots + slot * C::SLOT;
     raw[f][0] = *(const ESG_LDS uint32_t*)(sc + frag_row(f) * 16 + S * 4);
     raw[f][1] = S < 3 ? *(const ESG_LDS uint32_t*)(sc + frag_row(f) * 16 + S * 4 + 4)
                       : *(const ESG_LDS uint32_t*)(sc + C::SROWS * 16 + frag_row(f) * 4);
   };
-  auto set_scales = [&](int t) __attribute__((always_inline)) {
+  auto set_scales = [&](int t, int to) __attribute__((always_inline)) {
+    if constexpr (C::WORDS) {
+#pragma unroll
+      for (int f = 0; f < FR; ++f) es[to][f] = raw[f][0] >> (8 * lh);
+      return;
+    }
     const int left = KS - t * 4;  // bytes of the row still in K; those past it are other rows'
     const uint32_t mask = left >= 4 ? ~0u : left > 0 ? (1u << (8 * left)) - 1u : 0u;
 #pragma unroll
-    for (int f = 0; f < FR; ++f) es[f] = (__builtin_amdgcn_alignbyte(raw[f][1], raw[f][0], skew[f]) & mask) >> (8 * lh);
+    for (int f = 0; f < FR; ++f) es[to][f] = (__builtin_amdgcn_alignbyte(raw[f][1], raw[f][0], skew[f]) & mask) >> (8 * lh);
   };
+  f32x16_t acc[C::FN][C::FM];
   // the products of a slice, with `beside(p)` in the issue order behind the p-th of them
-  auto products = [&](int sl, auto&& beside) __attribute__((always_inline)) {
+  auto products = [&](int sl, int of, auto&& beside) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < C::FN; ++i)
 #pragma unroll
       for (int j = 0; j < C::FM; ++j) {
-        const uint32_t eb = es[i == 0 ? 0 : C::FM + i], ea = es[1 + j];
+        const uint32_t eb = es[of][i == 0 ? 0 : C::FM + i], ea = es[of][1 + j];
         if (sl == 1)
           mma_mx32<2>(acc[i][j], bv[sl][i], av[sl][j], eb, ea);
         else
@@ -453,125 +516,193 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
         __builtin_amdgcn_sched_barrier(0);
       }
   };
-  // the parts of n pieces of work that go behind the p-th product
-  auto spread = [&](int n, int p, auto&& f) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = p * n / PER; i < (p + 1) * n / PER; ++i) f(i);
-  };
-  constexpr int HALF = NL / 2;  // loads of a step issued behind its barrier's slice; the others in the next one
-
-  issue_scales(0, 0);
-#pragma unroll
-  for (int i = 0; i < NL; ++i) issue(0, 0, i);
-  issue_scales(1, 1);
-#pragma unroll
-  for (int t = 1; t < 4; ++t) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i)
-      if (t < 3 || i < HALF) issue(t, t, i);
-  }
-  wait_vmcnt<2 + 2 * NL + HALF>();
-  barrier();
-#pragma unroll
-  for (int f = 0; f < FR; ++f) {
-    read_raw(0, 0, f);
-    read_frag(0, 0, 0, f);
-  }
-  set_scales(0);
-  // Step t in stage S = t % 4, exponents in slot U = t / 4 % 2 (constants at each place).
+  constexpr int HALF = NL / 2;  // loads of a step issued behind its barrier; the others in the next slice
+  // Step t in stage S = t % 4, exponents in slot U = t / 4 % 2 (constants at each place).  What the next slice needs is
+  // read behind a slice's first products, two reads at a time, so that it is there when they end: both waves of a SIMD
+  // are at the same place, and what one of them waits for nothing covers.  The barrier lies before the last quarter of
+  // the first slice's products, which cover some of it.
   auto step = [&](int t, int S, int U) __attribute__((always_inline)) {
-    products(0, [&](int p) __attribute__((always_inline)) {
-      spread(FR, p, [&](int f) __attribute__((always_inline)) { read_frag(S, 1, 1, f); });
-      spread(NL - HALF, p, [&](int i) __attribute__((always_inline)) { issue(t + 3, (S + 3) & 3, HALF + i); });
-    });
-    // the second slice's operands are in registers and the next step's have landed: two steps' loads are newer
-    wait_lgkm0();
-    wait_vmcnt<2 * NL>();
-    barrier();
-    if (S == 3) issue_scales((t >> 2) + 2, U);  // the slot's last bytes were read before the barrier
-    __builtin_amdgcn_sched_barrier(0);
-    products(1, [&](int p) __attribute__((always_inline)) {
-      spread(FR, p, [&](int f) __attribute__((always_inline)) {
-        read_frag((S + 1) & 3, 0, 0, f);
-        read_raw(S == 3 ? U ^ 1 : U, (S + 1) & 3, f);
-      });
-      spread(HALF, p, [&](int i) __attribute__((always_inline)) { issue(t + 4, S, i); });
-    });
-    set_scales(t + 1);
-  };
-  for (int t = 0;; t += 8) {
-    step(t, 0, 0);
-    if (t + 1 >= steps) break;
-    step(t + 1, 1, 0);
-    if (t + 2 >= steps) break;
-    step(t + 2, 2, 0);
-    if (t + 3 >= steps) break;
-    step(t + 3, 3, 0);
-    if (t + 4 >= steps) break;
-    step(t + 4, 0, 1);
-    if (t + 5 >= steps) break;
-    step(t + 5, 1, 1);
-    if (t + 6 >= steps) break;
-    step(t + 6, 2, 1);
-    if (t + 7 >= steps) break;
-    step(t + 7, 3, 1);
-    if (t + 8 >= steps) break;
-  }
-  wait_lgkm0();
-  wait_vmcnt<0>();
-  barrier();  // the stages are free
-
-  // ---- results: a lane holds, of one m, four consecutive n out of every eight.  A wave takes 32 rows at a time
-  // through LDS of its own, in 16-byte chunks swizzled by row, and stores whole rows of its WN columns. ----
-  constexpr int ES = OUT == 1 ? 2 : 4;
-  constexpr int NCH = C::WN * ES / 16;  // chunks per row
-  char* y = (char*)g.y;
-  const int mw = wm * C::WM, nw = n0 + wn * C::WN;
-  if (g.N * ES % 16 == 0 && ((uintptr_t)y & 15) == 0) {
-    static_assert(32 * NCH * 16 * C::NW <= 4 * C::STAGE, "the pieces lie in the stages");
-    ESG_LDS char* out = lds + w * (32 * NCH * 16);
-#pragma unroll
-    for (int j = 0; j < C::FM; ++j) {
-#pragma unroll
-      for (int i = 0; i < C::FN; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16_t& v = acc[i][j];
-          if constexpr (ES == 2)
-            lds_write8(out + (lr * NCH + ((i * 4 + q) ^ (lr & (NCH - 1)))) * 16 + lh * 8,
-                       pack_bf16x2(v[q * 4], v[q * 4 + 1]), pack_bf16x2(v[q * 4 + 2], v[q * 4 + 3]));
-          else
-            *(ESG_LDS f32x4*)(out + (lr * NCH + ((i * 8 + q * 2 + lh) ^ (lr & (NCH - 1)))) * 16) =
-                f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
-        }
-      wait_lgkm0();
-#pragma unroll
-      for (int h = 0; h < 32 * NCH / 64; ++h) {
-        const int r = (h * 64 + lane) / NCH, c = lane % NCH;
-        const u32x4_t v = *(const ESG_LDS u32x4_t*)(out + (r * NCH + (c ^ (r & (NCH - 1)))) * 16);
-        const int m = mw + j * 32 + r, n = nw + c * (16 / ES);
-        if (m < mrows && n < g.N) *(u32x4_t*)(y + ((size_t)(s.m0 + m) * g.N + n) * ES) = v;
+    constexpr int WAIT = PER * 3 / 4 - 1;
+    products(0, S & 1, [&](int p) __attribute__((always_inline)) {
+      if (p < FR / 2) {
+        read_frag(S, 1, 1, 2 * p);
+        read_frag(S, 1, 1, 2 * p + 1);
       }
-      wait_lgkm0();  // read before the next rows are written
+      if (p >= PER / 4 - 1 && p < PER / 4 - 1 + NL - HALF) issue(t + 3, (S + 3) & 3, HALF + p - PER / 4 + 1);
+      if (p == WAIT) {
+        // the second slice's operands are in registers and the next step's have landed: two steps' loads are newer
+        wait_lgkm0();
+        wait_vmcnt<2 * NL>();
+        barrier();
+        if (S == 3) issue_scales((t >> 2) + 2, U);  // the slot's last bytes were read before the barrier
+      }
+    });
+    products(1, S & 1, [&](int p) __attribute__((always_inline)) {
+      if (p < FR / 2) {
+        read_frag((S + 1) & 3, 0, 0, 2 * p);
+        read_frag((S + 1) & 3, 0, 0, 2 * p + 1);
+      }
+      if (p == (FR + 1) / 2 - 1) {
+#pragma unroll
+        for (int f = 0; f < FR; ++f) read_raw(S == 3 ? U ^ 1 : U, (S + 1) & 3, f);
+      }
+      if (p >= PER / 4 && p < PER / 4 + HALF) issue(t + 4, S, p - PER / 4);
+      if (p == PER - 2) set_scales(t + 1, (S & 1) ^ 1);
+    });
+  };
+  static_assert(FR % 2 == 0 && FR / 2 <= PER * 3 / 4 && PER / 4 - 1 + NL - HALF <= PER * 3 / 4, "reads and loads before the barrier");
+
+  constexpr int ES = OUT == 1 ? 2 : 4;
+  constexpr int NCH = C::WN * ES / 16;                     // 16-byte chunks of a wave's row
+  constexpr int PIECE = C::STAGE / C::NW / (NCH * 16);     // rows of a wave that its share of a stage holds
+  static_assert(PIECE <= 32 && 32 % PIECE == 0 && PIECE * NCH % 64 == 0, "whole pieces");
+  const bool whole = g.N * ES % 16 == 0;
+
+  const int total = g.nm * g.nn;
+  int id = blockIdx.x;
+  set_lane();
+  while (id < total && !set_tile(id)) id += gridDim.x;
+  if (id >= total) return;
+  first_loads();
+  for (;;) {
+    set_lane();
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    // Loads come back in the order of their issue, but stores not in order with them: with so many of both under way,
+    // step 0's loads, which have as many loads behind them, are done.
+    wait_vmcnt<BEHIND_FIRST>();
+    barrier();  // step 0 has landed, and the last stage is free of the results
+#pragma unroll
+    for (int i = 0; i < HALF; ++i) issue(3, 3, i);
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+      read_raw(0, 0, f);
+      read_frag(0, 0, 0, f);
     }
-  } else {
+    set_scales(0, 0);
+    for (int t = 0;; t += 8) {
+      step(t, 0, 0);
+      if (t + 1 >= steps) break;
+      step(t + 1, 1, 0);
+      if (t + 2 >= steps) break;
+      step(t + 2, 2, 0);
+      if (t + 3 >= steps) break;
+      step(t + 3, 3, 0);
+      if (t + 4 >= steps) break;
+      step(t + 4, 0, 1);
+      if (t + 5 >= steps) break;
+      step(t + 5, 1, 1);
+      if (t + 6 >= steps) break;
+      step(t + 6, 2, 1);
+      if (t + 7 >= steps) break;
+      step(t + 7, 3, 1);
+      if (t + 8 >= steps) break;
+    }
+    const int m0 = s.m0 + wm * C::WM, mend = s.m1, nw = n0 + wn * C::WN;
+    wait_lgkm0();
+    wait_vmcnt<0>();
+    barrier();  // the stages are free
+    // the next tile's first loads go out before this one's results
+    set_lane();
+    id += gridDim.x;
+    while (id < total && !set_tile(id)) id += gridDim.x;
+    if (id < total) first_loads();
+
+    // ---- results: a lane holds, of one m, four consecutive n out of every eight.  A wave takes PIECE rows at a time
+    // through its share of the last stage, in 16-byte chunks swizzled by row, and stores whole rows of its WN columns,
+    // past the caches: what a product leaves is larger than they are, or read elsewhere. ----
+    char* y = (char*)g.y;
+    if (whole) {
+      ESG_LDS char* out = lds + 3 * C::STAGE + w * (PIECE * NCH * 16);
+      const int row = lr % PIECE;
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j) {
-      const int m = mw + j * 32 + lr;
+      for (int j = 0; j < C::FM; ++j)
 #pragma unroll
-      for (int i = 0; i < C::FN; ++i)
+        for (int h = 0; h < 32 / PIECE; ++h) {
+          const int m = m0 + j * 32 + h * PIECE, live = min(max(mend - m, 0), PIECE);
+          const rsrc_t to = make_rsrc(y + (size_t)m * g.N * ES, (uint32_t)(live * g.N) * ES);
+          if (lr / PIECE == h) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int n = nw + i * 32 + (e >> 2) * 8 + lh * 4 + (e & 3);
-          if (m < mrows && n < g.N) {
-            const size_t at = (size_t)(s.m0 + m) * g.N + n;
-            if constexpr (OUT == 1)
-              store_elem<bf16_t>((bf16_t*)y + at, acc[i][j][e]);
-            else
-              ((float*)y)[at] = acc[i][j][e];
+            for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const f32x16_t v = acc[i][j];
+                if constexpr (ES == 2)
+                  lds_write8(out + (row * NCH + ((i * 4 + q) ^ (row & (NCH - 1)))) * 16 + lh * 8,
+                             pack_bf16x2(v[q * 4], v[q * 4 + 1]), pack_bf16x2(v[q * 4 + 2], v[q * 4 + 3]));
+                else
+                  *(ESG_LDS f32x4*)(out + (row * NCH + ((i * 8 + q * 2 + lh) ^ (row & (NCH - 1)))) * 16) =
+                      f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
+              }
           }
+          wait_lgkm0();
+#pragma unroll
+          for (int c0 = 0; c0 < PIECE * NCH / 64; ++c0) {
+            const int r = (c0 * 64 + lane) / NCH, c = lane % NCH;
+            const u32x4_t v = *(const ESG_LDS u32x4_t*)(out + (r * NCH + (c ^ (r & (NCH - 1)))) * 16);
+            const int n = nw + c * (16 / ES);
+            __builtin_amdgcn_raw_buffer_store_b128(v, to, n < g.N ? (r * g.N + n) * ES : (int)kOOB, 0, kStream);
+          }
+          wait_lgkm0();  // read before the next rows are written
         }
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j) {
+        const int m = m0 + j * 32 + lr;
+#pragma unroll
+        for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int n = nw + i * 32 + (e >> 2) * 8 + lh * 4 + (e & 3);
+            if (m < mend && n < g.N) {
+              const size_t at = (size_t)m * g.N + n;
+              if constexpr (OUT == 1)
+                store_elem<bf16_t>((bf16_t*)y + at, acc[i][j][e]);
+              else
+                ((float*)y)[at] = acc[i][j][e];
+            }
+          }
+      }
     }
+    if (id >= total) return;
+  }
+}
+
+// The exponents of a and b as words, [ceil(K/128)][rows]: word (t, r) holds those of elements 128 t .. 128 t + 127 of row
+// r, zeros past K.  A thread takes four words of a row; a's rows in the order of y's (zeros for rows[] outside a).
+struct WordsSide {
+  const uint8_t* scale;
+  const int32_t* index;  // or NULL
+  uint32_t* out;
+  int rows, src_rows;
+};
+__global__ __launch_bounds__(256) void mx_words_kernel(WordsSide a, WordsSide b, unsigned a_blocks, int KS) {
+  const bool second = blockIdx.x >= a_blocks;
+  const WordsSide& g = second ? b : a;
+  const unsigned block = second ? blockIdx.x - a_blocks : blockIdx.x;
+  const int words = (KS + 3) / 4, quads = (words + 3) / 4;
+  const unsigned chunk = block / quads;
+  const int t0 = (int)(block - chunk * quads) * 4;
+  const int r = (int)chunk * 256 + (int)threadIdx.x;
+  if (r >= g.rows) return;
+  const int src = g.index != nullptr ? g.index[r] : r;
+  const bool in = (unsigned)src < (unsigned)g.src_rows;
+  const uint8_t* p = g.scale + (size_t)(in ? src : 0) * KS + t0 * 4;
+  const int left = KS - t0 * 4;  // bytes of the row from t0 on
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (t0 + j >= words) break;
+    uint32_t v = 0;
+    if (in && (KS & 3) == 0) {
+      v = *(const uint32_t*)(p + j * 4);
+    } else if (in) {
+      for (int e = 0; e < 4; ++e) v |= j * 4 + e < left ? (uint32_t)p[j * 4 + e] << (8 * e) : 0u;
+    }
+    g.out[(size_t)(t0 + j) * g.rows + r] = v;
   }
 }
 
@@ -582,23 +713,27 @@ struct Plan {
 };
 // chunks of `chunk` rows, at most: grouped rows leave up to one short chunk per expert
 long long chunks(const MxArgs& g, int chunk) {
-  return g.offsets == nullptr ? (g.M + chunk - 1) / chunk : (long long)g.M / chunk + std::min(g.E, g.M);
+  return !g.grouped ? (g.M + chunk - 1) / chunk : (long long)g.M / chunk + std::min(g.E, g.M);
 }
 Plan plan(const MxArgs& g) {
   Plan p;
-  const int per = g.offsets == nullptr ? g.M : (g.M + g.E - 1) / g.E;  // rows that share a b, on average
+  const int per = g.grouped ? (g.M + g.E - 1) / g.E : g.M;  // rows that share a b, on average
   const long long wgs = (long long)((g.N + 15) / 16) * ((g.M + kFewRows - 1) / kFewRows);
-  if (per <= kFewRows || (g.offsets == nullptr && wgs <= kNominalCUs)) {
+  if (per <= kFewRows || (!g.grouped && wgs <= kNominalCUs)) {
     p.nm = (int)chunks(g, kFewRows);
     p.nn = (g.N + 15) / 16;
     return p;
   }
   const long long big = (long long)((g.M + 255) / 256) * ((g.N + 255) / 256);
-  p.tile = big >= kNominalCUs && per >= 256 ? 256 : 128;
+  // words of exponents within 32-bit offsets
+  const bool near = std::max<long long>(g.M, (long long)g.E * g.N) * ((g.K + 127) / 128) < (1 << 29);
+  p.tile = big >= kNominalCUs && per >= 256 && near ? 256 : 128;
   p.nm = (int)chunks(g, p.tile);
   p.nn = (g.N + p.tile - 1) / p.tile;
   return p;
 }
+
+size_t words_bytes(const MxArgs& g) { return ((size_t)g.M + (size_t)g.E * g.N) * ((g.K + 127) / 128) * 4; }
 
 template <int OUT>
 hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
@@ -610,19 +745,29 @@ hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
       hipLaunchKernelGGL((mx_rows_kernel<8, OUT>), dim3(p.nn, p.nm), dim3(512), 0, stream, g);
     return hipGetLastError();
   }
+  if (p.tile == 256) {
+    const int KS = g.K / 32, quads = ((g.K + 127) / 128 + 3) / 4;
+    const WordsSide a{g.sa, g.rows, (uint32_t*)g.ta, g.M, g.a_rows}, b{g.sb, nullptr, (uint32_t*)g.tb, g.E * g.N, g.E * g.N};
+    const unsigned na = (unsigned)((a.rows + 255) / 256) * quads, nb = (unsigned)((b.rows + 255) / 256) * quads;
+    LaunchTimer timer("mx_words", stream);
+    hipLaunchKernelGGL(mx_words_kernel, dim3(na + nb), dim3(256), 0, stream, a, b, na, KS);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   LaunchTimer timer("mx_tile", stream);
+  // as many workgroups as the LDS of the CUs holds at once: one, or two of the smaller tile
   if (p.tile == 256)
-    hipLaunchKernelGGL((mx_tile_kernel<256, 256, OUT>), dim3(p.nm * p.nn), dim3(Tile<256, 256>::NTH), 0, stream, g);
+    hipLaunchKernelGGL((mx_tile_kernel<256, 256, OUT>), dim3(std::min(p.nm * p.nn, compute_units())),
+                       dim3(Tile<256, 256>::NTH), 0, stream, g);
   else
-    hipLaunchKernelGGL((mx_tile_kernel<128, 128, OUT>), dim3(p.nm * p.nn), dim3(Tile<128, 128>::NTH), 0, stream, g);
+    hipLaunchKernelGGL((mx_tile_kernel<128, 128, OUT>), dim3(std::min(p.nm * p.nn, 2 * compute_units())),
+                       dim3(Tile<128, 128>::NTH), 0, stream, g);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t mx_matmul_workspace_bytes(int, int, int) { return 0; }
-
-hipError_t launch_mx_matmul(const MxMatmul& c, hipStream_t stream) {
+static MxArgs args_of(const MxMatmul& c) {
   MxArgs g{};
   g.a = (const uint8_t*)c.a;
   g.b = (const uint8_t*)c.b;
@@ -636,9 +781,22 @@ hipError_t launch_mx_matmul(const MxMatmul& c, hipStream_t stream) {
   g.N = c.N;
   g.K = c.K;
   g.E = c.E;
+  g.grouped = c.grouped;
+  return g;
+}
+
+size_t mx_matmul_workspace_bytes(const MxMatmul& c) {
+  const MxArgs g = args_of(c);
+  return c.M > 0 && c.N > 0 && plan(g).tile == 256 ? words_bytes(g) : 0;
+}
+
+hipError_t launch_mx_matmul(const MxMatmul& c, hipStream_t stream) {
+  MxArgs g = args_of(c);
   const Plan p = plan(g);
   g.nm = p.nm;
   g.nn = p.nn;
+  g.ta = (const uint32_t*)c.workspace;
+  g.tb = g.ta + (size_t)g.M * ((g.K + 127) / 128);
   return c.out_dtype == 1 ? run<1>(g, p, stream) : run<0>(g, p, stream);
 }
 

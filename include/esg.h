@@ -591,8 +591,9 @@ int esg_mxfp4_dequant(const void* q, const void* scale, int dtype, int64_t rows,
  * The sum of a block is exact, sums of blocks are float32; their order depends on the
  * shape alone and no atomics are used (bitwise reproducible).  A block of the byte 255
  * makes what it adds to NaN.
- * workspace: esg_mxfp4_matmul_workspace_size() bytes, 16-byte aligned (shapes with few
- * output tiles split K and add the parts there; it may be 0, then workspace may be NULL).
+ * workspace: esg_mxfp4_matmul_workspace_size() bytes (esg_mxfp4_grouped_matmul_workspace_size
+ * for the other), 16-byte aligned (large products lay the scales out anew there; it may be
+ * 0, then workspace may be NULL).
  * M == 0 or N == 0 enqueues nothing.
  *
  * esg_mxfp4_grouped_matmul: the same for rows in the order of their experts, b: [experts,
@@ -612,9 +613,10 @@ int esg_mxfp4_dequant(const void* q, const void* scale, int dtype, int64_t rows,
 int esg_mxfp4_matmul_workspace_size(int M, int N, int K, size_t* workspace_bytes);
 int esg_mxfp4_matmul(const void* a, const void* a_scale, const void* b, const void* b_scale, int out_dtype, int M, int N,
                      int K, void* y, void* workspace, size_t workspace_bytes, void* stream);
+int esg_mxfp4_grouped_matmul_workspace_size(int M, int N, int K, int experts, size_t* workspace_bytes);
 int esg_mxfp4_grouped_matmul(const void* a, const void* a_scale, int a_rows, const int32_t* rows, const void* b,
                              const void* b_scale, int experts, const int32_t* offsets, int out_dtype, int M, int N,
-                             int K, void* y, void* stream);
+                             int K, void* y, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * A whole mixture-of-experts feed-forward layer for a few tokens (decode):

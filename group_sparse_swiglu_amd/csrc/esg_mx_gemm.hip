@@ -357,17 +357,25 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   auto frag_row = [&](int f) __attribute__((always_inline)) {  // of the tile's rows, A's then B's
     return is_a(f) ? ra0 + (f - 1) * 32 : BM + rb0 + (f == 0 ? 0 : f - C::FM) * 32;
   };
-  Span s;
-  int n0;
+  Span s, snext;
+  int n0, id = blockIdx.x;
   DmaSrc ra, rb, rs;
   uint32_t oa[NA], ob[NB], os, skew[FR];
-  // the id-th tile; false: there is none (grouped rows may fill fewer tiles than are counted)
-  auto set_tile = [&](int id) __attribute__((always_inline)) {
+  const int total = g.nm * g.nn;
+  // this workgroup's next tile from id on, its rows in snext (grouped rows may fill fewer tiles than are counted)
+  auto find_tile = [&]() __attribute__((always_inline)) {
+    for (; id < total; id += gridDim.x) {
+      int tm, tn;
+      tile_of(id, total, g.nm, g.nn, tm, tn);
+      snext = find_span(g, tm, BM, lane);
+      if (snext.m1 > snext.m0) return;
+    }
+  };
+  auto set_tile = [&]() __attribute__((always_inline)) {  // the tile that find_tile found
     int tm, tn;
-    tile_of(id, g.nm * g.nn, g.nm, g.nn, tm, tn);
-    s = find_span(g, tm, BM, lane);
+    tile_of(id, total, g.nm, g.nn, tm, tn);
+    s = snext;
     const int mrows = s.m1 - s.m0;
-    if (mrows <= 0) return false;
     n0 = tn * BN;
     const int nrows = min(BN, g.N - n0);
     const size_t b0 = (size_t)s.e * g.N + n0;
@@ -422,7 +430,6 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
         }
       }
     }
-    return true;
   };
 
   // ---- loads ----
@@ -558,11 +565,10 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   static_assert(PIECE <= 32 && 32 % PIECE == 0 && PIECE * NCH % 64 == 0, "whole pieces");
   const bool whole = g.N * ES % 16 == 0;
 
-  const int total = g.nm * g.nn;
-  int id = blockIdx.x;
   set_lane();
-  while (id < total && !set_tile(id)) id += gridDim.x;
+  find_tile();
   if (id >= total) return;
+  set_tile();
   first_loads();
   for (;;) {
     set_lane();
@@ -584,6 +590,8 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
       read_frag(0, 0, 0, f);
     }
     set_scales(0, 0);
+    id += gridDim.x;
+    find_tile();  // its reads' latency passes here rather than between the tiles
     for (int t = 0;; t += 8) {
       step(t, 0, 0);
       if (t + 1 >= steps) break;
@@ -608,9 +616,10 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
     barrier();  // the stages are free
     // the next tile's first loads go out before this one's results
     set_lane();
-    id += gridDim.x;
-    while (id < total && !set_tile(id)) id += gridDim.x;
-    if (id < total) first_loads();
+    if (id < total) {
+      set_tile();
+      first_loads();
+    }
 
     // ---- results: a lane holds, of one m, four consecutive n out of every eight.  A wave takes PIECE rows at a time
     // through its share of the last stage, in 16-byte chunks swizzled by row, and stores whole rows of its WN columns,

@@ -44,9 +44,10 @@ struct Span {
   int e, m0, m1;
 };
 
-// The z-th chunk of up to `chunk` rows: of all rows, or counted expert after expert.  Every wave looks for itself: 64
-// experts at a time, their chunks counted by a prefix sum over the lanes.  Offsets are taken into 0 .. M.
-__device__ __forceinline__ Span find_span(const MxArgs& g, int z, int chunk, int lane) {
+// The z-th chunk of up to `chunk` rows: of all rows, or counted expert after expert, without the first `skip` of each.
+// Every wave looks for itself: 64 experts at a time, their chunks counted by a prefix sum over the lanes.  Offsets are
+// taken into 0 .. M.
+__device__ __forceinline__ Span find_span(const MxArgs& g, int z, int chunk, int lane, int skip = 0) {
   if (g.offsets == nullptr) return Span{0, z * chunk, min(g.M, (z + 1) * chunk)};
   for (int e0 = 0; e0 < g.E; e0 += 64) {
     const int e = e0 + lane;
@@ -55,7 +56,7 @@ __device__ __forceinline__ Span find_span(const MxArgs& g, int z, int chunk, int
       lo = min(max(g.offsets[e], 0), g.M);
       hi = min(max(g.offsets[e + 1], 0), g.M);
     }
-    const int own = hi > lo ? (hi - lo + chunk - 1) / chunk : 0;
+    const int own = hi > lo ? max((hi - lo + chunk - 1) / chunk - skip, 0) : 0;
     int upto = own;
 #pragma unroll
     for (int off = 1; off < 64; off *= 2) {
@@ -66,7 +67,7 @@ __device__ __forceinline__ Span find_span(const MxArgs& g, int z, int chunk, int
     if (has != 0) {
       const int at = __builtin_ctzll(has);
       const int first = __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(own, at);
-      const int m0 = __builtin_amdgcn_readlane(lo, at) + (z - first) * chunk;
+      const int m0 = __builtin_amdgcn_readlane(lo, at) + (z - first + skip) * chunk;
       return Span{e0 + at, m0, min(__builtin_amdgcn_readlane(hi, at), m0 + chunk)};
     }
     z -= __builtin_amdgcn_readlane(upto, 63);
@@ -89,6 +90,18 @@ __device__ __forceinline__ void load16(const DmaSrc& s, ESG_LDS char* wave_base,
 __device__ __forceinline__ void load4(const DmaSrc& s, ESG_LDS char* wave_base, uint32_t voff) {
   const int m = __builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)wave_base);
   asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(voff), "s"(s.d), "{m0}"(m) : "memory");
+}
+
+// The same for the few-row kernel, which asks for as many spans as there are experts and full chunks: the e-th is the
+// first chunk of expert e, two loads away and not a search, and those from E on are the other chunks, which only an
+// expert of more rows than a chunk has.
+__device__ __forceinline__ Span find_few(const MxArgs& g, int z, int chunk, int lane) {
+  if (g.offsets == nullptr) return Span{0, z * chunk, min(g.M, (z + 1) * chunk)};
+  if (z < g.E) {
+    const int lo = min(max(g.offsets[z], 0), g.M), hi = min(max(g.offsets[z + 1], 0), g.M);
+    return Span{z, lo, min(hi, lo + chunk)};
+  }
+  return find_span(g, z - g.E, chunk, lane, 1);
 }
 
 // Descriptor of the exponents of `rows` rows from byte `from` of p (4-byte aligned), in whole dwords; skew: what
@@ -116,9 +129,12 @@ __device__ __forceinline__ void mma_mx32(f32x16_t& acc, const u32x4_t& a, const 
 // Few rows: a workgroup takes 16 rows of b and up to 64 rows of a (MT tiles of 16);
 // its NW waves take the steps of K in turn and add their sums in LDS in wave order.
 // The read of b bounds it.  Everything goes through LDS in whole 128-byte rows, a wave
-// into P slots of its own, and it waits for its own loads only.  The exponents of a
-// step (8 bytes of a row that starts at any byte) come as the three dwords that hold
-// them, and the one needed is read back as a byte.
+// into a slot of its own, and it waits for its own loads only: what keeps memory busy is
+// many workgroups side by side, each short (64 tokens, 6 of 64 experts, N = 2816, K =
+// 2048: 33 us with two waves and one slot each, 36 with four, 51 with four waves of two
+// slots, which leave room for half as many workgroups).  The exponents of a step (8 bytes
+// of a row that starts at any byte) come as the three dwords that hold them, and the one
+// needed is read back as a byte.
 // ---------------------------------------------------------------------------
 constexpr int kStream = 2;   // store policy: past the caches
 constexpr int kFewRows = 64;
@@ -127,15 +143,12 @@ constexpr int kFewK = 256;  // K elements of a step: 128 bytes of a row, 8 expon
 template <int MT>
 struct Slot {
   static constexpr int A_AT = 2048, SB_AT = A_AT + MT * 2048, SA_AT = SB_AT + 256, BYTES = SA_AT + MT * 256;
-  static constexpr int NI = 3 + 3 * MT;                 // load instructions of a step
-  static constexpr int P = MT == 1 ? 2 : 1;
-  static_assert((P - 1) * NI < 64, "vmcnt range");
 };
 template <int NW, int MTMAX>
 constexpr int rows_lds() {
   int most = 0;
   for (int mt = 1; mt <= MTMAX; ++mt) {
-    const int slot = (mt == 1 ? 2 : 1) * (2048 + 256) * (1 + mt), red = mt * 1024;
+    const int slot = (2048 + 256) * (1 + mt), red = mt * 1024;
     most = most > slot ? most : slot;
     most = most > red ? most : red;
   }
@@ -145,10 +158,9 @@ constexpr int rows_lds() {
 template <int MT, int NW, int OUT>
 __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* lds_) {
   using S = Slot<MT>;
-  constexpr int P = S::P;
   const int lane = threadIdx.x & 63, w = wave_id();
   const int lr = lane & 15, lg = lane >> 4;
-  ESG_LDS char* const ring = (ESG_LDS char*)lds_ + w * P * S::BYTES;
+  ESG_LDS char* const slot = (ESG_LDS char*)lds_ + w * S::BYTES;
   const int n0 = blockIdx.x * 16, nrows = min(16, g.N - n0), mrows = s.m1 - s.m0;
   const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + kFewK - 1) / kFewK;
   const size_t b0 = (size_t)s.e * g.N + n0;
@@ -160,28 +172,16 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
                            : make_dma_src(g.a + (size_t)s.m0 * KH, (uint32_t)(mrows * KH));
   const DmaSrc rsa = gather ? scale_src(g.sa, 0, (uint32_t)g.a_rows * (uint32_t)KS, a_skew)
                             : scale_src(g.sa, (size_t)s.m0 * KS, (uint32_t)(mrows * KS), a_skew);
-  // row of a behind row i of the span; -1: none
-  auto a_row = [&](int i) __attribute__((always_inline)) {
-    if (i >= mrows) return -1;
-    if (!gather) return i;
-    const int r = g.rows[s.m0 + i];
-    return (unsigned)r < (unsigned)g.a_rows ? r : -1;
-  };
   // rows of eight, 16-byte chunks in the K-row swizzle; offsets of step 0
   const int koff = ((lane & 7) ^ (lane >> 3)) * 16;
   uint32_t ob[2], oa[2 * MT], osa[MT], osb;
+  // exponents: lane = dword * 16 + row; of row lr the byte for chunk lg of the first and second 128 elements
+  int eb[2], ea[MT][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = i * 8 + (lane >> 3);
     ob[i] = r < nrows ? (uint32_t)(r * KH + koff) : kOOB;
   }
-#pragma unroll
-  for (int i = 0; i < 2 * MT; ++i) {
-    const int r = a_row(i * 8 + (lane >> 3));
-    oa[i] = r >= 0 ? (uint32_t)r * (uint32_t)KH + koff : kOOB;
-  }
-  // exponents: lane = dword * 16 + row; of row lr the byte for chunk lg of the first and second 128 elements
-  int eb[2], ea[MT][2];
   {
     const uint32_t at = b_skew + (uint32_t)(lr * KS);
     osb = lr < nrows && lg < 3 ? (at & ~3u) + lg * 4 : kOOB;
@@ -190,6 +190,34 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
       const int p = (int)(at & 3) + j * 4 + lg;
       eb[j] = S::SB_AT + (p >> 2) * 64 + lr * 4 + (p & 3);
     }
+  }
+  // b's and a's part of step t into the slot, chunks at or past K as zeros (kOOB plus an offset below 2^31 stays past
+  // every buffer)
+  auto request_b = [&](int t) __attribute__((always_inline)) {
+    const bool in = t * 128 + koff < KH;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load16(rb, slot + i * 1024, in ? ob[i] + (uint32_t)t * 128u : kOOB);
+    load4(rsb, slot + S::SB_AT, osb + (uint32_t)t * 8u);
+  };
+  auto request_a = [&](int t) __attribute__((always_inline)) {
+    const bool in = t * 128 + koff < KH;
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) load16(ra, slot + S::A_AT + i * 1024, in ? oa[i] + (uint32_t)t * 128u : kOOB);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) load4(rsa, slot + S::SA_AT + i * 256, osa[i] + (uint32_t)t * 8u);
+  };
+  if (w < steps) request_b(w);  // b is on its way before the rows of a are looked up
+  // row of a behind row i of the span; -1: none
+  auto a_row = [&](int i) __attribute__((always_inline)) {
+    if (i >= mrows) return -1;
+    if (!gather) return i;
+    const int r = g.rows[s.m0 + i];
+    return (unsigned)r < (unsigned)g.a_rows ? r : -1;
+  };
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i) {
+    const int r = a_row(i * 8 + (lane >> 3));
+    oa[i] = r >= 0 ? (uint32_t)r * (uint32_t)KH + koff : kOOB;
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -202,28 +230,11 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
       ea[i][j] = S::SA_AT + i * 256 + (p >> 2) * 64 + lr * 4 + (p & 3);
     }
   }
-  // step t into a slot; past the last step: zeros (so every step is the same number of loads).  kOOB plus an offset
-  // below 2^31 stays past every buffer.
-  auto request = [&](int t, ESG_LDS char* slot) __attribute__((always_inline)) {
-    const bool in = t < steps && t * 128 + koff < KH;
-    const uint32_t k = (uint32_t)t * 128u, ks = (uint32_t)t * 8u;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) load16(rb, slot + i * 1024, in ? ob[i] + k : kOOB);
-#pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) load16(ra, slot + S::A_AT + i * 1024, in ? oa[i] + k : kOOB);
-    load4(rsb, slot + S::SB_AT, t < steps ? osb + ks : kOOB);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) load4(rsa, slot + S::SA_AT + i * 256, t < steps ? osa[i] + ks : kOOB);
-  };
+  if (w < steps) request_a(w);
   f32x4 acc[MT];
   zero_acc(acc);
-#pragma unroll
-  for (int u = 0; u < P; ++u) request(w + u * NW, ring + u * S::BYTES);
-  int at = 0;
   for (int t = w; t < steps; t += NW) {
-    ESG_LDS char* slot = ring + at * S::BYTES;
-    at = at + 1 == P ? 0 : at + 1;
-    wait_vmcnt<(P - 1) * S::NI>();
+    wait_vmcnt<0>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -240,7 +251,10 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
     }
     wait_lgkm0();  // the slot has been read
     __builtin_amdgcn_sched_barrier(0);
-    request(t + P * NW, slot);
+    if (t + NW < steps) {
+      request_b(t + NW);
+      request_a(t + NW);
+    }
   }
   wait_vmcnt<0>();
   __syncthreads();  // the slots become the sums of the waves
@@ -265,20 +279,19 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
   }
 }
 
-template <int NW, int OUT>
+// MTMAX * 16 rows of a at most: 64, or, for LDS that lets more workgroups stand side by side, 16
+template <int NW, int MTMAX, int OUT>
 __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs g) {
-  __shared__ __attribute__((aligned(1024))) char lds[rows_lds<NW, 4>()];
-  const Span s = find_span(g, blockIdx.y, kFewRows, threadIdx.x & 63);
+  __shared__ __attribute__((aligned(1024))) char lds[rows_lds<NW, MTMAX>()];
+  const Span s = find_few(g, blockIdx.y, MTMAX * 16, threadIdx.x & 63);
   const int mrows = s.m1 - s.m0;
   if (mrows <= 0) return;
-  if (mrows > 48)
-    few_rows<4, NW, OUT>(g, s, lds);
-  else if (mrows > 32)
-    few_rows<3, NW, OUT>(g, s, lds);
-  else if (mrows > 16)
-    few_rows<2, NW, OUT>(g, s, lds);
-  else
-    few_rows<1, NW, OUT>(g, s, lds);
+  if constexpr (MTMAX > 1) {
+    if (mrows > 48) return few_rows<4, NW, OUT>(g, s, lds);
+    if (mrows > 32) return few_rows<3, NW, OUT>(g, s, lds);
+    if (mrows > 16) return few_rows<2, NW, OUT>(g, s, lds);
+  }
+  few_rows<1, NW, OUT>(g, s, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -717,7 +730,8 @@ __global__ __launch_bounds__(256) void mx_words_kernel(WordsSide a, WordsSide b,
 
 // Kernel and tile size by shape alone (so a shape rounds alike everywhere).
 struct Plan {
-  int tile = 0;   // 0: few rows
+  int tile = 0;   // 0: few rows,
+  int few = 0;    // so many at a time
   int nm = 0, nn = 0;
 };
 // chunks of `chunk` rows, at most: grouped rows leave up to one short chunk per expert
@@ -728,8 +742,12 @@ Plan plan(const MxArgs& g) {
   Plan p;
   const int per = g.grouped ? (g.M + g.E - 1) / g.E : g.M;  // rows that share a b, on average
   const long long wgs = (long long)((g.N + 15) / 16) * ((g.M + kFewRows - 1) / kFewRows);
-  if (per <= kFewRows || (!g.grouped && wgs <= kNominalCUs)) {
-    p.nm = (int)chunks(g, kFewRows);
+  // By expert up to 16 rows of each on average (us, few rows / tiles, N = 2816, K = 2048, 64 experts: 9 rows 34 / 42, 15
+  // rows 45 / 47, 18 rows 72 / 47), whose chunks are 16 rows; else up to 64, or while there is a workgroup for no more
+  // than each CU.
+  if (g.grouped ? per <= 16 : per <= kFewRows || wgs <= kNominalCUs) {
+    p.few = per <= 16 ? 16 : kFewRows;
+    p.nm = (int)(g.grouped ? g.E + g.M / p.few : (g.M + p.few - 1) / p.few);
     p.nn = (g.N + 15) / 16;
     return p;
   }
@@ -748,10 +766,22 @@ template <int OUT>
 hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
   if (p.tile == 0) {
     LaunchTimer timer("mx_rows", stream);
-    if ((long long)p.nn * p.nm > kNominalCUs)
-      hipLaunchKernelGGL((mx_rows_kernel<4, OUT>), dim3(p.nn, p.nm), dim3(256), 0, stream, g);
-    else
-      hipLaunchKernelGGL((mx_rows_kernel<8, OUT>), dim3(p.nn, p.nm), dim3(512), 0, stream, g);
+    // Waves of a workgroup: the fewer the more workgroups there are (us, two / four / eight: 704 x 64 above 33 / 36 / 48;
+    // one row of N = 11008, K = 2048 6.2 / 6.2 / 6.9, of N = K = 8192 12.6 / 8.5 / 7.0)
+    const long long wgs = (long long)p.nn * p.nm;
+    const dim3 grid(p.nn, p.nm);
+    if (p.few == 16) {
+      if (wgs >= 16 * kNominalCUs)
+        hipLaunchKernelGGL((mx_rows_kernel<2, 1, OUT>), grid, dim3(128), 0, stream, g);
+      else if (wgs > 2 * kNominalCUs)
+        hipLaunchKernelGGL((mx_rows_kernel<4, 1, OUT>), grid, dim3(256), 0, stream, g);
+      else
+        hipLaunchKernelGGL((mx_rows_kernel<8, 1, OUT>), grid, dim3(512), 0, stream, g);
+    } else if (wgs > kNominalCUs) {
+      hipLaunchKernelGGL((mx_rows_kernel<4, 4, OUT>), grid, dim3(256), 0, stream, g);
+    } else {
+      hipLaunchKernelGGL((mx_rows_kernel<8, 4, OUT>), grid, dim3(512), 0, stream, g);
+    }
     return hipGetLastError();
   }
   if (p.tile == 256) {

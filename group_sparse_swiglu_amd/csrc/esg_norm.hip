@@ -1,6 +1,6 @@
 // Root-mean-square norm after the residual's addition, forward and backward.
 //   h = x + residual (rounded to their type: the new residual), r = (mean h^2 + eps)^-1/2, y = h r w
-//   backward, g = dy w:  dx = dresidual = dh + r (g - h r^2 mean(g h)),  dw = sum over the rows of dy h r
+//   backward, g = dy w:  dx = dresidual = dh + r (g - h r mean(g h r)),  dw = sum over the rows of dy h r
 // y leaves in the type of x, or in 8 bits (e4m3, a float32 scale per 1 x 128
 // block) or 4 bits (e2m1, a power of two per 32) from its float32 value.  Sums
 // and r are float32, every output is rounded once.
@@ -225,11 +225,12 @@ __global__ __launch_bounds__(256) void rms_norm_bwd_kernel(NormBwdArgs g) {
       yo[i].get(dy);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sum = fmaf(dy[j] * w[i][j], h[j], sum);
-        acc[i][j] = fmaf(dy[j], h[j] * r, acc[i][j]);
+        const float hr = h[j] * r;  // not h alone: its products with g may leave the range
+        sum = fmaf(dy[j] * w[i][j], hr, sum);
+        acc[i][j] = fmaf(dy[j], hr, acc[i][j]);
       }
     }
-    const float c2 = row_sum<TPR>(sum, lds[turn]) / (float)g.d * r * r;
+    const float mean = row_sum<TPR>(sum, lds[turn]) / (float)g.d;
     turn ^= 1;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -239,7 +240,7 @@ __global__ __launch_bounds__(256) void rms_norm_bwd_kernel(NormBwdArgs g) {
       yo[i].get(dy);
       no[i].get(o);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] += r * (dy[j] * w[i][j] - h[j] * c2);
+      for (int j = 0; j < 8; ++j) o[j] += r * (dy[j] * w[i][j] - h[j] * r * mean);
       if (c < g.d) store8<T>((T*)g.dx + at + c, o);
     }
   }

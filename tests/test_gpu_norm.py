@@ -202,3 +202,17 @@ def test_zero_and_large_rows():
     assert torch.allclose(y[3], torch.ones(512), rtol=1e-5)
     q, s = E.rms_norm_quantize(x.to(DEV), torch.ones(512, device=DEV), eps=EPS, format="mxfp4")
     assert (s[2] == 255).all() and (s[0] == 0).all() and not q[0].any()
+
+
+def test_gradient_of_large_values():
+    """h of 2^100: its products with the gradient leave float32's range unless r comes first."""
+    require_gpu()
+    note("norm gradient of large values")
+    for d in (512, 2048):
+        x = _rand(4, d, F32, 1).double() * 2.0 ** 100
+        w, dy = _rand(1, d, F32, 2)[0], _rand(4, d, F32, 3, 2.0 ** 40)
+        xd, wd = x.float().to(DEV).requires_grad_(), w.to(DEV).requires_grad_()
+        gx, gw = torch.autograd.grad(E.rms_norm(xd, wd, eps=EPS), (xd, wd), dy.to(DEV))
+        dx, dw, mx, mw = O.rms_norm_backward(f64(dy), x.numpy(), f64(w), EPS)
+        assert (np.abs(f64(gx) - dx) <= 226 * U * mx).all()
+        assert (np.abs(f64(gw) - dw) <= 53 * U * mw).all()

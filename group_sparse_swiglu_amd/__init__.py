@@ -533,6 +533,7 @@ def sigmoid_topk_routing(logits, expert_bias, topk: int, scaling_factor: Optiona
     if logits.dim() != 2:
         raise EsgError("logits must be [tokens, num_experts]")
     T, E = logits.shape
+    _rows32(T, E)
     if expert_bias.dim() != 1 or expert_bias.shape[0] != E or expert_bias.dtype != torch.float32:
         raise EsgError("expert_bias must be float32 [num_experts]")
     if not expert_bias.is_cuda or expert_bias.device != logits.device:
@@ -825,6 +826,12 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
     return y, probs, indices
 
 
+def _rows32(*sizes):
+    """The library counts rows in 32 bits; ctypes would drop the bits above."""
+    if max(sizes) >= 1 << 31:
+        raise EsgError(f"{max(sizes)} rows: at most 2^31 - 1 in a call")
+
+
 def _norm_args(x, weight, residual):
     """(tokens, d, device, GPU) of a norm's inputs, checked."""
     if x.dim() < 1 or weight.dim() != 1 or x.shape[-1] != weight.shape[0]:
@@ -832,7 +839,9 @@ def _norm_args(x, weight, residual):
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
         raise EsgError("residual must have the shape and dtype of x")
     d = x.shape[-1]
-    return x.numel() // d if d else 0, d, x.device, x.get_device()
+    T = x.numel() // d if d else 0
+    _rows32(T)
+    return T, d, x.device, x.get_device()
 
 
 def _like(out, x, name):
@@ -948,7 +957,7 @@ def rms_norm_quantize(x, weight, residual=None, eps: float = 1e-6, format: str =
     lead = x.shape[:-1]
     if format == "fp8":
         code = ESG_E4M3
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        q = torch.empty(*x.shape, dtype=torch.float8_e4m3fn, device=dev)
         scale = torch.empty(*lead, _ceil128(d), dtype=torch.float32, device=dev)
     elif format == "mxfp4":
         code = ESG_E2M1
@@ -989,6 +998,7 @@ def topk_routing_fwd(logits, topk: int, scoring: str = "softmax", expert_bias=No
     if logits.dim() != 2:
         raise EsgError("logits must be [tokens, num_experts]")
     T, E = logits.shape
+    _rows32(T, E)
     dev, gpu = logits.device, logits.get_device()
     stride = 1
     if expert_bias is not None:
@@ -1021,6 +1031,7 @@ def topk_routing_bwd(dprobs, logits, indices, scoring: str = "softmax", normaliz
     if logits.dim() != 2 or indices.dim() != 2 or indices.shape[0] != logits.shape[0] or dprobs.shape != indices.shape:
         raise EsgError("logits must be [tokens, num_experts], dprobs and indices [tokens, topk]")
     T, E = logits.shape
+    _rows32(T, E)
     dev, gpu = logits.device, logits.get_device()
     dz = torch.empty_like(logits, memory_format=torch.contiguous_format)
     _check(lib().esg_topk_routing_bwd(
@@ -1108,6 +1119,7 @@ def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, wor
     (M, KH), N, dev, gpu, u8 = a.shape, b.shape[0], a.device, a.get_device(), torch.uint8
     if a_scale.shape != (M, KH // 16) or b_scale.shape != (N, KH // 16):
         raise EsgError("a_scale must be [M, K/32] and b_scale [N, K/32]")
+    _rows32(M, N)
     if out is None:
         out = torch.empty(M, N, dtype=out_dtype, device=dev)
     elif out.shape != (M, N):
@@ -1149,6 +1161,7 @@ def mxfp4_grouped_matmul(a, a_scale, b, b_scale, offsets, rows=None, out_dtype=t
     if offsets.shape != (experts + 1,) or (rows is not None and rows.dim() != 1):
         raise EsgError("offsets must be int32 [E + 1] and rows int32 [M]")
     M = R if rows is None else rows.shape[0]
+    _rows32(M, N, R)
     if out is None:
         out = torch.empty(M, N, dtype=out_dtype, device=dev)
     elif out.shape != (M, N):

@@ -826,7 +826,6 @@ int mx_shape(int M, int N, int K, int experts) {
 int mx_operands(const void* a, const void* a_scale, const void* b, const void* b_scale, int out_dtype, const void* y) {
   if (a == nullptr || a_scale == nullptr || b == nullptr || b_scale == nullptr || y == nullptr) return ESG_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(b) || !aligned16(y)) return ESG_ERR_INVALID_ARG;
-  if ((((uintptr_t)a_scale | (uintptr_t)b_scale) & 3u) != 0) return ESG_ERR_INVALID_ARG;
   return float_dtype(out_dtype) ? ESG_OK : ESG_ERR_UNSUPPORTED;
 }
 }  // namespace

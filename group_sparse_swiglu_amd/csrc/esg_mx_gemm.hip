@@ -104,11 +104,11 @@ __device__ __forceinline__ Span find_few(const MxArgs& g, int z, int chunk, int 
   return find_span(g, z - g.E, chunk, lane, 1);
 }
 
-// Descriptor of the exponents of `rows` rows from byte `from` of p (4-byte aligned), in whole dwords; skew: what
-// `from` lies past the descriptor's base.  A dword at either end that holds a wanted byte may hold others beside it.
+// Descriptor of `bytes` exponents from byte `from` of p (at any address), in whole dwords; skew: what they start past
+// the descriptor's base.  A dword at either end that holds a wanted byte may hold others beside it.
 __device__ __forceinline__ DmaSrc scale_src(const uint8_t* p, size_t from, uint32_t bytes, uint32_t& skew) {
-  skew = (uint32_t)(from & 3);
-  return make_dma_src(p + (from - skew), (skew + bytes + 3) & ~3u);
+  skew = (uint32_t)((uintptr_t)(p + from) & 3);
+  return make_dma_src(p + from - skew, (skew + bytes + 3) & ~3u);
 }
 
 // 16 x 16 x 128 and 32 x 32 x 64 products with exponents from byte OP of each side's word
@@ -350,7 +350,8 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   const int wm = w % C::NWM, wn = w / C::NWM;
   int lane, lr, lh;
   const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + 127) / 128;
-  const bool gather = g.rows != nullptr, skewed = (KS & 3) != 0;  // skewed: some row of exponents starts inside a dword
+  const bool gather = g.rows != nullptr;
+  const bool skewed = (((uintptr_t)g.sa | (uintptr_t)g.sb | KS) & 3) != 0;  // some row of exponents starts inside a dword
 
   // ---- the tile: its rows and columns, where its loads start ----
   constexpr int NA = BM / 16 / C::NW, NB = BN / 16 / C::NW, NL = NA + NB + C::WORDS;  // loads of a wave and step
@@ -719,7 +720,7 @@ __global__ __launch_bounds__(256) void mx_words_kernel(WordsSide a, WordsSide b,
   for (int j = 0; j < 4; ++j) {
     if (t0 + j >= words) break;
     uint32_t v = 0;
-    if (in && (KS & 3) == 0) {
+    if (in && (((uintptr_t)g.scale | KS) & 3) == 0) {
       v = *(const uint32_t*)(p + j * 4);
     } else if (in) {
       for (int e = 0; e < 4; ++e) v |= j * 4 + e < left ? (uint32_t)p[j * 4 + e] << (8 * e) : 0u;

@@ -604,11 +604,11 @@ int esg_mxfp4_dequant(const void* q, const void* scale, int dtype, int64_t rows,
  * index outside 0 .. a_rows - 1 is a row of zeros.  Rows of y before offsets[0] and from
  * offsets[experts] on are left as they were.  Offsets are taken into 0 .. M; where they
  * descend, which b the rows between take is not specified.
- * Errors: ESG_ERR_INVALID_ARG (null pointer, a, b, y or workspace not 16-byte aligned, a
- * scale, offsets or rows not 4-byte aligned, negative size, K <= 0, experts < 1, a_rows < M
- * without rows), ESG_ERR_UNSUPPORTED (out_dtype, K not a multiple of 32 or above 2^22, M
- * above 2^30, N above 2^25, experts above 1024, 2^23 output tiles of 128 x 128 or more, or
- * with rows a of 2^31 bytes or more), ESG_ERR_WORKSPACE.
+ * Errors: ESG_ERR_INVALID_ARG (null pointer, a, b, y or workspace not 16-byte aligned,
+ * offsets or rows not 4-byte aligned, negative size, K <= 0, experts < 1, a_rows < M without
+ * rows), ESG_ERR_UNSUPPORTED (out_dtype, K not a multiple of 32 or above 2^22, M above 2^30,
+ * N above 2^25, experts above 1024, 2^23 output tiles of 128 x 128 or more, or with rows a of
+ * 2^31 bytes or more), ESG_ERR_WORKSPACE.
  */
 int esg_mxfp4_matmul_workspace_size(int M, int N, int K, size_t* workspace_bytes);
 int esg_mxfp4_matmul(const void* a, const void* a_scale, const void* b, const void* b_scale, int out_dtype, int M, int N,

@@ -117,3 +117,101 @@ def test_binding_refusals():
         E.mxfp4_dequantize(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.uint8))
     with pytest.raises(E.EsgError, match="GPU tensor"):
         E.mxfp4_quantize(x)
+
+
+def test_four_bit_product_refusals():
+    names = ("a", "sa", "b", "sb", "dt", "M", "N", "K", "y", "ws", "bytes", "stream")
+    call = _caller(E.lib().esg_mxfp4_matmul, names, (P, P, P, P, 1, 4, 16, 64, P, NULL, 0, NULL))
+    assert call(M=0) == 0 and call(N=0) == 0 and call(M=0, a=NULL, y=NULL) == 0 and call(M=0, dt=2) == 2
+    assert call(M=-1) == 1 and call(N=-1) == 1 and call(K=0) == 1 and call(K=-32) == 1
+    assert call(K=48) == 2 and call(K=(1 << 22) + 32) == 2 and call(dt=2) == 2 and call(dt=-1) == 2
+    assert call(M=(1 << 30) + 1) == 2 and call(N=(1 << 25) + 1) == 2 and call(M=1 << 30, N=1 << 10) == 2
+    for n in ("a", "b", "y"):
+        assert call(**{n: NULL}) == 1 and call(**{n: P + 8}) == 1
+    assert call(sa=NULL) == 1 and call(sb=NULL) == 1
+    assert call(M=4096, N=4096, K=256) == 3 and call(M=4096, N=4096, K=256, ws=P, bytes=16) == 3
+    assert call(M=4096, N=4096, K=256, ws=P + 8, bytes=1 << 40) == 1
+
+
+def test_four_bit_product_by_expert_refusals():
+    names = ("a", "sa", "R", "rows", "b", "sb", "E", "off", "dt", "M", "N", "K", "y", "ws", "bytes", "stream")
+    call = _caller(E.lib().esg_mxfp4_grouped_matmul, names, (P, P, 9, P, P, P, 3, P, 1, 4, 16, 64, P, NULL, 0, NULL))
+    assert call(M=0) == 0 and call(N=0) == 0 and call(M=0, dt=3) == 2
+    assert call(M=-1) == 1 and call(K=0) == 1 and call(E=0) == 1 and call(R=-1) == 1
+    assert call(rows=NULL, R=3) == 1                       # every row of y has one of a
+    assert call(K=80) == 2 and call(E=1025) == 2 and call(dt=2) == 2
+    assert call(K=64, R=(1 << 26)) == 2 and call(M=1 << 29, N=1 << 10) == 2    # rows are gathered at 32-bit offsets
+    for n in ("a", "b", "y"):
+        assert call(**{n: NULL}) == 1 and call(**{n: P + 8}) == 1
+    for n in ("sa", "sb", "off"):
+        assert call(**{n: NULL}) == 1
+    assert call(rows=P + 2) == 1 and call(off=P + 2) == 1
+    assert call(M=8192, N=2048) == 3 and call(M=8192, N=2048, ws=P, bytes=100) == 3
+
+
+def test_four_bit_product_workspaces():
+    for f, args in ((E.lib().esg_mxfp4_matmul_workspace_size, (64, 64, 64)),
+                    (E.lib().esg_mxfp4_grouped_matmul_workspace_size, (64, 64, 64, 4))):
+        need = ctypes.c_size_t(7)
+        assert f(*args, NULL) == 1 and f(*args, ctypes.byref(need)) == 0 and need.value == 0
+        assert f(-1, *args[1:], ctypes.byref(need)) == 1 and f(64, 64, 40, *args[3:], ctypes.byref(need)) == 2
+    assert E.mxfp4_matmul_workspace_size(0, 64, 64) == 0 and E.mxfp4_matmul_workspace_size(1, 1 << 20, 64) == 0
+    # one word for every 128 elements of a row of either side
+    assert E.mxfp4_matmul_workspace_size(8192, 4096, 160) == (8192 + 4096) * 2 * 4
+    assert E.mxfp4_grouped_matmul_workspace_size(8192, 2048, 160, 8) == (8192 + 8 * 2048) * 2 * 4
+    with pytest.raises(E.EsgError):
+        E.mxfp4_matmul_workspace_size(4, 4, 33)
+    with pytest.raises(E.EsgError):
+        E.mxfp4_grouped_matmul_workspace_size(4, 4, 32, 0)
+
+
+def test_four_bit_product_binding_refusals():
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    a, sa, b, sb = u8(4, 32), u8(4, 2), u8(8, 32), u8(8, 2)
+    for bad in ((u8(4, 16), sa, b, sb), (a[0], sa, b, sb), (a, sa, b[None], sb)):
+        with pytest.raises(E.EsgError, match="K/2"):
+            E.mxfp4_matmul(*bad)
+    for bad in ((a, u8(4, 1), b, sb), (a, sa, b, u8(7, 2))):
+        with pytest.raises(E.EsgError, match="K/32"):
+            E.mxfp4_matmul(*bad)
+    with pytest.raises(E.EsgError, match="out must be"):
+        E.mxfp4_matmul(a, sa, b, sb, out=torch.zeros(4, 7))
+    with pytest.raises(E.EsgError, match="dtype"):
+        E.mxfp4_matmul(a, sa, b, sb, out_dtype=torch.float16)
+    with pytest.raises(E.EsgError, match="GPU tensor"):
+        E.mxfp4_matmul(a, sa, b, sb)
+    b, sb, off = u8(3, 8, 32), u8(3, 8, 2), torch.zeros(4, dtype=torch.int32)
+    for bad in ((a, sa, b[0], sb, off), (u8(4, 64), u8(4, 4), b, sb, off)):
+        with pytest.raises(E.EsgError, match="K/2"):
+            E.mxfp4_grouped_matmul(*bad)
+    with pytest.raises(E.EsgError, match="K/32"):
+        E.mxfp4_grouped_matmul(a, sa, b, u8(3, 8, 1), off)
+    for kw in (dict(offsets=off[:3]), dict(offsets=off, rows=torch.zeros(2, 2, dtype=torch.int32))):
+        with pytest.raises(E.EsgError, match="offsets"):
+            E.mxfp4_grouped_matmul(a, sa, b, sb, **kw)
+    with pytest.raises(E.EsgError, match="out must be"):
+        E.mxfp4_grouped_matmul(a, sa, b, sb, off, rows=torch.zeros(9, dtype=torch.int32), out=torch.zeros(4, 8))
+    with pytest.raises(E.EsgError, match="GPU tensor"):
+        E.mxfp4_grouped_matmul(a, sa, b, sb, off)
+
+
+def test_more_rows_than_the_library_counts():
+    """2^32 + 1 rows are not one."""
+    meta = dict(device="meta")
+    n = (1 << 32) + 1
+    with pytest.raises(E.EsgError, match="rows"):
+        E.rms_norm(torch.empty(n, 16, **meta), torch.empty(16, **meta))
+    with pytest.raises(E.EsgError, match="rows"):
+        E.rms_norm_quantize(torch.empty(n, 16, **meta), torch.empty(16, **meta))
+    with pytest.raises(E.EsgError, match="rows"):
+        E.topk_routing(torch.empty(n, 4, **meta), 2)
+    with pytest.raises(E.EsgError, match="rows"):
+        E.topk_routing_bwd(torch.empty(n, 1, **meta), torch.empty(n, 4, **meta), torch.empty(n, 1, **meta))
+    u8 = dict(dtype=torch.uint8, **meta)
+    a, sa = torch.empty(n, 16, **u8), torch.empty(n, 1, **u8)
+    b, sb = torch.empty(4, 16, **u8), torch.empty(4, 1, **u8)
+    for args in ((a, sa, b, sb), (b, sb, a, sa)):
+        with pytest.raises(E.EsgError, match="rows"):
+            E.mxfp4_matmul(*args)
+    with pytest.raises(E.EsgError, match="rows"):
+        E.mxfp4_grouped_matmul(a, sa, b[None], sb[None], torch.empty(2, dtype=torch.int32, **meta))

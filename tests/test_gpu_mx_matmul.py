@@ -165,3 +165,75 @@ def test_empty():
                                torch.zeros(2, 8, 2, **u8), torch.zeros(3, dtype=torch.int32, device=DEV),
                                rows=torch.empty(0, dtype=torch.int32, device=DEV))
     assert y.shape == (0, 8)
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("counts,N,K", [([1024] * 8, 2048, 160), ([4000, 0, 300, 1, 255, 2049], 3000, 96),
+                                        ([2100, 256, 4200, 3, 700], 2061, 544), ([5000, 3300], 2056, 1184)])
+def test_large_tiles_by_expert(counts, N, K, gather):
+    """Tiles of 256, several for a workgroup, exponents that start at any byte, rows outside a and behind the last expert's."""
+    require_gpu()
+    note(f"mx grouped large tiles {counts} {N} {K} gather={gather}")
+    n_e, used = len(counts), sum(counts)
+    M = used + 60
+    assert E.mxfp4_grouped_matmul_workspace_size(M, N, K, n_e) > 0
+    offsets = torch.tensor([0] + counts).cumsum(0).int()
+    R = 777 if gather else M
+    a, b = _operand(R, K, 3), _operand(n_e * N, K, 4)
+    rows = torch.randint(0, R, (M,), generator=torch.Generator().manual_seed(N)).int() if gather else None
+    if gather:
+        rows[5], rows[used - 1] = -1, R
+    d = [t.to(DEV) for t in (*a, b[0].view(n_e, N, -1), b[1].view(n_e, N, -1), offsets)]
+    av, bv = _vals(*a), _vals(*b).view(n_e, N, K)
+    x = av if rows is None else av[rows.long().clamp(0, R - 1)]
+    if gather:
+        x[5] = x[used - 1] = 0
+    ws = {}
+    for dtype in (BF, F32):
+        out = torch.full((M, N), 5.0, dtype=dtype, device=DEV)
+        E.mxfp4_grouped_matmul(*d, rows=None if rows is None else rows.to(DEV), out=out, workspace=ws)
+        assert (out[used:] == 5).all()
+        for e in range(n_e):
+            lo, hi = int(offsets[e]), int(offsets[e + 1])
+            _close(out[lo:hi], x[lo:hi] @ bv[e].t(), x[lo:hi].abs() @ bv[e].abs().t(), K, dtype)
+
+
+@pytest.mark.parametrize("M,N,K,counts", [(60, 100, 288, [0, 50, 0, 10]), (64, 64, 96, [0, 0, 0, 64]), (160, 48, 544, [3] * 4 + [145] + [0] * 5 + [1] * 3),
+                                          (1000, 4112, 64, [0] * 60 + [17, 900, 16, 33] + [0] * 10)])
+def test_few_rows_with_a_crowded_expert(M, N, K, counts):
+    """At most 16 rows for each expert on average, and more for some."""
+    require_gpu()
+    note(f"mx crowded expert {M} {N} {K}")
+    n_e, used = len(counts), sum(counts)
+    offsets = torch.tensor([0] + counts).cumsum(0).int()
+    a, b = _operand(M, K, 3), _operand(n_e * N, K, 4)
+    d = [t.to(DEV) for t in (*a, b[0].view(n_e, N, -1), b[1].view(n_e, N, -1), offsets)]
+    av, bv = _vals(*a), _vals(*b).view(n_e, N, K)
+    out = torch.full((M, N), 5.0, dtype=F32, device=DEV)
+    E.mxfp4_grouped_matmul(*d, out=out)
+    assert (out[used:] == 5).all()
+    for e in range(n_e):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        _close(out[lo:hi], av[lo:hi] @ bv[e].t(), av[lo:hi].abs() @ bv[e].abs().t(), K, F32)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 96), (130, 700, 160), (130, 700, 256), (4100, 4100, 128), (4100, 4100, 160)])
+def test_slices_of_rows(M, N, K):
+    """Rows from the middle of larger operands: their exponents start at any byte."""
+    require_gpu()
+    note(f"mx matmul of slices {M}x{N}x{K}")
+    (a, sa), (b, sb) = ([t.to(DEV) for t in _operand(n + 7, K, n)] for n in (M, N))
+    buf = torch.empty(sa.numel() + 3, dtype=torch.uint8, device=DEV)
+    for at in (0, 1, 3):
+        sa_ = buf[at:at + sa.numel()].view(sa.shape).copy_(sa)
+        got = E.mxfp4_matmul(a[3:3 + M], sa_[3:3 + M], b[1:1 + N], sb[1:1 + N], out_dtype=F32)
+        want = E.mxfp4_matmul(*(t.clone() for t in (a[3:3 + M], sa[3:3 + M], b[1:1 + N], sb[1:1 + N])), out_dtype=F32)
+        assert torch.equal(got, want)
+        off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+        got = E.mxfp4_grouped_matmul(a[3:3 + M], sa_[3:3 + M], b[1:1 + N][None], sb[1:1 + N][None], off, out_dtype=F32)
+        again = E.mxfp4_grouped_matmul(*(t.clone() for t in (a[3:3 + M], sa[3:3 + M], b[1:1 + N][None], sb[1:1 + N][None])), off,
+                                       out_dtype=F32)
+        assert torch.equal(got, again)
+    av, bv = _vals(a[3:3 + M].cpu(), sa[3:3 + M].cpu()), _vals(b[1:1 + N].cpu(), sb[1:1 + N].cpu())
+    _close(want, av @ bv.t(), av.abs() @ bv.abs().t(), K, F32)
+    _close(got, av @ bv.t(), av.abs() @ bv.abs().t(), K, F32)

@@ -340,6 +340,26 @@ __device__ __forceinline__ void tile_of(int id, int total, int nm, int nn, int& 
   tn = in / rows;
 }
 
+// The first `left` elements of v (all if there are more) to y, aligned to an element: rows whose length is no multiple of
+// 16 bytes (32768 x 5501 x 2048: 272 us; element by element 598).
+template <int OUT>
+__device__ __forceinline__ void store_chunk(char* y, const u32x4_t& v, int left) {
+  typedef u32x4_t chunk_t __attribute__((aligned(2)));
+  constexpr int PER = OUT == 1 ? 8 : 4;
+  if (left >= PER) {
+    *(chunk_t*)y = v;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < PER - 1; ++e)
+    if (e < left) {
+      if constexpr (OUT == 1)
+        *(uint16_t*)(y + e * 2) = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+      else
+        *(uint32_t*)(y + e * 4) = v[e];
+    }
+}
+
 template <int BM, int BN, int OUT>
 __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs g) {
   using C = Tile<BM, BN>;
@@ -637,60 +657,43 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
 
     // ---- results: a lane holds, of one m, four consecutive n out of every eight.  A wave takes PIECE rows at a time
     // through its share of the last stage, in 16-byte chunks swizzled by row, and stores whole rows of its WN columns,
-    // past the caches: what a product leaves is larger than they are, or read elsewhere. ----
-    char* y = (char*)g.y;
-    if (whole) {
-      ESG_LDS char* out = lds + 3 * C::STAGE + w * (PIECE * NCH * 16);
-      const int row = lr % PIECE;
+    // past the caches where chunks are aligned: what a product leaves is larger than they are, or read elsewhere. ----
+    ESG_LDS char* const out = lds + 3 * C::STAGE + w * (PIECE * NCH * 16);
+    const int row = lr % PIECE;
 #pragma unroll
-      for (int j = 0; j < C::FM; ++j)
+    for (int j = 0; j < C::FM; ++j)
 #pragma unroll
-        for (int h = 0; h < 32 / PIECE; ++h) {
-          const int m = m0 + j * 32 + h * PIECE, live = min(max(mend - m, 0), PIECE);
-          const rsrc_t to = make_rsrc(y + (size_t)m * g.N * ES, (uint32_t)(live * g.N) * ES);
-          if (lr / PIECE == h) {
+      for (int h = 0; h < 32 / PIECE; ++h) {
+        const int m = m0 + j * 32 + h * PIECE, live = min(max(mend - m, 0), PIECE);
+        const rsrc_t to = make_rsrc((char*)g.y + (size_t)m * g.N * ES, (uint32_t)(live * g.N) * ES);
+        if (lr / PIECE == h) {
 #pragma unroll
-            for (int i = 0; i < C::FN; ++i)
+          for (int i = 0; i < C::FN; ++i)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const f32x16_t v = acc[i][j];
-                if constexpr (ES == 2)
-                  lds_write8(out + (row * NCH + ((i * 4 + q) ^ (row & (NCH - 1)))) * 16 + lh * 8,
-                             pack_bf16x2(v[q * 4], v[q * 4 + 1]), pack_bf16x2(v[q * 4 + 2], v[q * 4 + 3]));
-                else
-                  *(ESG_LDS f32x4*)(out + (row * NCH + ((i * 8 + q * 2 + lh) ^ (row & (NCH - 1)))) * 16) =
-                      f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
-              }
-          }
-          wait_lgkm0();
-#pragma unroll
-          for (int c0 = 0; c0 < PIECE * NCH / 64; ++c0) {
-            const int r = (c0 * 64 + lane) / NCH, c = lane % NCH;
-            const u32x4_t v = *(const ESG_LDS u32x4_t*)(out + (r * NCH + (c ^ (r & (NCH - 1)))) * 16);
-            const int n = nw + c * (16 / ES);
-            __builtin_amdgcn_raw_buffer_store_b128(v, to, n < g.N ? (r * g.N + n) * ES : (int)kOOB, 0, kStream);
-          }
-          wait_lgkm0();  // read before the next rows are written
-        }
-    } else {
-#pragma unroll
-      for (int j = 0; j < C::FM; ++j) {
-        const int m = m0 + j * 32 + lr;
-#pragma unroll
-        for (int i = 0; i < C::FN; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int n = nw + i * 32 + (e >> 2) * 8 + lh * 4 + (e & 3);
-            if (m < mend && n < g.N) {
-              const size_t at = (size_t)m * g.N + n;
-              if constexpr (OUT == 1)
-                store_elem<bf16_t>((bf16_t*)y + at, acc[i][j][e]);
+            for (int q = 0; q < 4; ++q) {
+              const f32x16_t v = acc[i][j];
+              if constexpr (ES == 2)
+                lds_write8(out + (row * NCH + ((i * 4 + q) ^ (row & (NCH - 1)))) * 16 + lh * 8,
+                           pack_bf16x2(v[q * 4], v[q * 4 + 1]), pack_bf16x2(v[q * 4 + 2], v[q * 4 + 3]));
               else
-                ((float*)y)[at] = acc[i][j][e];
+                *(ESG_LDS f32x4*)(out + (row * NCH + ((i * 8 + q * 2 + lh) ^ (row & (NCH - 1)))) * 16) =
+                    f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
             }
+        }
+        wait_lgkm0();
+#pragma unroll
+        for (int c0 = 0; c0 < PIECE * NCH / 64; ++c0) {
+          const int r = (c0 * 64 + lane) / NCH, c = lane % NCH;
+          const u32x4_t v = *(const ESG_LDS u32x4_t*)(out + (r * NCH + (c ^ (r & (NCH - 1)))) * 16);
+          const int n = nw + c * (16 / ES);
+          if (whole) {
+            __builtin_amdgcn_raw_buffer_store_b128(v, to, n < g.N ? (r * g.N + n) * ES : (int)kOOB, 0, kStream);
+          } else if (r < live) {
+            store_chunk<OUT>((char*)g.y + ((size_t)(m + r) * g.N + n) * ES, v, g.N - n);
           }
+        }
+        wait_lgkm0();  // read before the next rows are written
       }
-    }
     if (id >= total) return;
   }
 }
@@ -752,10 +755,18 @@ Plan plan(const MxArgs& g) {
     p.nn = (g.N + 15) / 16;
     return p;
   }
-  const long long big = (long long)((g.M + 255) / 256) * ((g.N + 255) / 256);
+  // Tiles in rounds of one for each CU: a round of 256 x 256 takes as long as three of 128 x 128, two of which run side by
+  // side (us, 256 / 128, K = 2048: 4096 x 4096, 1 and 4 rounds, 28 / 40; 3000 x 5504, 2 and 5, 42 / 36; 4096 x 5504, 2
+  // and 6, 41 / 44; 32768 x 5504, 11 and 43, 272 / 335).  By expert half a tile of rows is expected to stay empty, and a
+  // tie goes to the small ones (64 experts, N = 2816: 3000 tokens, 6 of 64, 5 and 15, 130 / 130; 8192, 10 and 36, 234 /
+  // 352; 32 experts, N = 2048, 2500 tokens, 4 of 32, 2 and 6, 62 / 52).
+  auto rounds = [&](int tile) {
+    const long long m = (g.M + tile - 1) / tile + (g.grouped ? std::min(g.E, g.M) / 2 : 0);
+    return (m * ((g.N + tile - 1) / tile) + kNominalCUs - 1) / kNominalCUs;
+  };
   // words of exponents within 32-bit offsets
   const bool near = std::max<long long>(g.M, (long long)g.E * g.N) * ((g.K + 127) / 128) < (1 << 29);
-  p.tile = big >= kNominalCUs && per >= 256 && near ? 256 : 128;
+  p.tile = near && 3 * rounds(256) < rounds(128) + !g.grouped ? 256 : 128;
   p.nm = (int)chunks(g, p.tile);
   p.nn = (g.N + p.tile - 1) / p.tile;
   return p;

@@ -129,6 +129,7 @@ def test_four_bit_product_refusals():
     for n in ("a", "b", "y"):
         assert call(**{n: NULL}) == 1 and call(**{n: P + 8}) == 1
     assert call(sa=NULL) == 1 and call(sb=NULL) == 1
+    assert E.mxfp4_matmul_workspace_size(4096, 4096, 256) > 16
     assert call(M=4096, N=4096, K=256) == 3 and call(M=4096, N=4096, K=256, ws=P, bytes=16) == 3
     assert call(M=4096, N=4096, K=256, ws=P + 8, bytes=1 << 40) == 1
 
@@ -146,7 +147,8 @@ def test_four_bit_product_by_expert_refusals():
     for n in ("sa", "sb", "off"):
         assert call(**{n: NULL}) == 1
     assert call(rows=P + 2) == 1 and call(off=P + 2) == 1
-    assert call(M=8192, N=2048) == 3 and call(M=8192, N=2048, ws=P, bytes=100) == 3
+    assert E.mxfp4_grouped_matmul_workspace_size(12288, 4096, 64, 3) > 100
+    assert call(M=12288, N=4096) == 3 and call(M=12288, N=4096, ws=P, bytes=100) == 3
 
 
 def test_four_bit_product_workspaces():
@@ -158,7 +160,7 @@ def test_four_bit_product_workspaces():
     assert E.mxfp4_matmul_workspace_size(0, 64, 64) == 0 and E.mxfp4_matmul_workspace_size(1, 1 << 20, 64) == 0
     # one word for every 128 elements of a row of either side
     assert E.mxfp4_matmul_workspace_size(8192, 4096, 160) == (8192 + 4096) * 2 * 4
-    assert E.mxfp4_grouped_matmul_workspace_size(8192, 2048, 160, 8) == (8192 + 8 * 2048) * 2 * 4
+    assert E.mxfp4_grouped_matmul_workspace_size(12288, 4096, 160, 8) == (12288 + 8 * 4096) * 2 * 4
     with pytest.raises(E.EsgError):
         E.mxfp4_matmul_workspace_size(4, 4, 33)
     with pytest.raises(E.EsgError):

@@ -208,14 +208,14 @@ def test_streams_share_a_dict():
         x, dy = _input(T, n, i)
         w = torch.ones(n, device=DEV)
         _, h, r = E.rms_norm_fwd(x, w)
-        a, b = E.mxfp4_quantize(_input(4096 + 8 * i, 320 + 32 * i, i)[0]), E.mxfp4_quantize(_input(4100, 320 + 32 * i, i + 5)[0])
-        be = [t.view(2, 2050, -1) for t in b]
-        off = torch.tensor([0, 2000 + i, 4096], dtype=torch.int32, device=DEV)
-        assert E.mxfp4_matmul_workspace_size(a[0].shape[0], 4100, 320 + 32 * i) > 0
+        a, b = E.mxfp4_quantize(_input(5000 + 8 * i, 320 + 32 * i, i)[0]), E.mxfp4_quantize(_input(5400, 320 + 32 * i, i + 5)[0])
+        be = [t.view(2, 2700, -1) for t in b]
+        off = torch.tensor([0, 2000 + i, 4996], dtype=torch.int32, device=DEV)
+        assert E.mxfp4_matmul_workspace_size(5000 + 8 * i, 5400, 320) > 0 < E.mxfp4_grouped_matmul_workspace_size(5000 + 8 * i, 2700, 320, 2)
         cases.append((lambda dy=dy, h=h, w=w, r=r: E.rms_norm_bwd(dy, h, w, r, workspace=cache),
                       lambda a=a, b=b: (E.mxfp4_matmul(*a, *b, workspace=cache),),
                       lambda a=a, be=be, off=off: (E.mxfp4_grouped_matmul(*a, *be, off, workspace=cache,
-                                                                          out=torch.zeros(a[0].shape[0], 2050, device=DEV)),)))
+                                                                          out=torch.zeros(a[0].shape[0], 2700, device=DEV)),)))
     want = [[f() for f in c] for c in cases]
     streams = [torch.cuda.Stream() for _ in cases]
     for s in streams:

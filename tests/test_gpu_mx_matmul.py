@@ -37,7 +37,8 @@ def _close(y, want, mag, K, dtype):
 
 SHAPES = [(1, 16, 32), (1, 11008, 2048), (3, 40, 96), (16, 16, 128), (17, 100, 160), (33, 72, 512), (37, 2048, 5504),
           (49, 17, 1056), (64, 64, 4096), (65, 256, 544), (100, 33, 64), (200, 300, 1376), (129, 4096, 288),
-          (300, 4097, 320), (513, 2049, 256), (640, 2056, 800), (1000, 4608, 2080), (2050, 8200, 256), (4096, 4100, 608)]
+          (300, 4097, 320), (513, 2049, 256), (640, 2056, 800), (1000, 4608, 2080), (2050, 8200, 256), (4096, 4100, 608),
+          (2500, 5504, 608), (2500, 5501, 160), (2430, 5500, 32), (6000, 8200, 96)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -72,7 +73,7 @@ def test_quantised_operands_and_out():
 
 def test_wide_exponents_and_nan_blocks():
     require_gpu()
-    for M, N in ((20, 48), (500, 3000)):
+    for M, N in ((20, 48), (500, 3000), (2500, 5504)):
         note(f"mx matmul wide exponents {M}x{N}")
         K = 416
         a, b = _operand(M, K, 1, 40), _operand(N, K, 2, 40)
@@ -93,7 +94,7 @@ def test_nan_of_the_next_row_stays_there():
     """Exponent rows start at any byte and are read in dwords: none of a neighbour's reaches a row."""
     require_gpu()
     note("mx matmul neighbours")
-    for M, N, K in ((40, 64, 32), (40, 64, 96), (700, 1600, 160)):
+    for M, N, K in ((40, 64, 32), (40, 64, 96), (700, 1600, 160), (2500, 5504, 160)):
         a, b = _operand(M, K, 1), _operand(N, K, 2)
         y = E.mxfp4_matmul(*(t.to(DEV) for t in (*a, *b)), out_dtype=F32).cpu()
         a[1][1::2] = 255
@@ -168,8 +169,8 @@ def test_empty():
 
 
 @pytest.mark.parametrize("gather", [True, False])
-@pytest.mark.parametrize("counts,N,K", [([1024] * 8, 2048, 160), ([4000, 0, 300, 1, 255, 2049], 3000, 96),
-                                        ([2100, 256, 4200, 3, 700], 2061, 544), ([5000, 3300], 2056, 1184)])
+@pytest.mark.parametrize("counts,N,K", [([1024] * 8, 3000, 160), ([4000, 0, 300, 1, 255, 2049], 4100, 96),
+                                        ([2100, 256, 4200, 3, 700], 4001, 544), ([5000, 3300], 3080, 1184)])
 def test_large_tiles_by_expert(counts, N, K, gather):
     """Tiles of 256, several for a workgroup, exponents that start at any byte, rows outside a and behind the last expert's."""
     require_gpu()
@@ -217,7 +218,7 @@ def test_few_rows_with_a_crowded_expert(M, N, K, counts):
         _close(out[lo:hi], av[lo:hi] @ bv[e].t(), av[lo:hi].abs() @ bv[e].abs().t(), K, F32)
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 40, 96), (130, 700, 160), (130, 700, 256), (4100, 4100, 128), (4100, 4100, 160)])
+@pytest.mark.parametrize("M,N,K", [(5, 40, 96), (130, 700, 160), (130, 700, 256), (2500, 5504, 128), (2500, 5504, 160)])
 def test_slices_of_rows(M, N, K):
     """Rows from the middle of larger operands: their exponents start at any byte."""
     require_gpu()
@@ -237,3 +238,10 @@ def test_slices_of_rows(M, N, K):
     av, bv = _vals(a[3:3 + M].cpu(), sa[3:3 + M].cpu()), _vals(b[1:1 + N].cpu(), sb[1:1 + N].cpu())
     _close(want, av @ bv.t(), av.abs() @ bv.abs().t(), K, F32)
     _close(got, av @ bv.t(), av.abs() @ bv.abs().t(), K, F32)
+
+
+def test_shapes_reach_every_kernel():
+    size = E.mxfp4_matmul_workspace_size
+    large = [s for s in SHAPES if size(*s) > 0]
+    assert {N % 8 == 0 for _, N, _ in large} == {True, False} and {K % 128 == 0 for _, _, K in SHAPES} == {True, False}
+    assert size(2500, 5504, 160) > 0 and size(700, 1600, 160) == 0

@@ -151,3 +151,22 @@ def test_unaligned_rows():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
         d = torch.randn(64, 8, device=DEV)
         assert torch.equal(E.topk_routing_bwd(d, z, a[1]), E.topk_routing_bwd(d, z.clone(), a[1]))
+
+
+@pytest.mark.parametrize("gap", [10.0, 22.0, 40.0, 45.0, 60.0])
+def test_chosen_scores_far_below_one(gap):
+    """The expert that holds the softmax is kept out by its bias: the chosen ones' sum is e^-gap, down to 1e-20 and below."""
+    require_gpu()
+    for E_, k in ((12, 3), (256, 8), (600, 5)):
+        note(f"route chosen scores of e^-{gap}, {E_} experts")
+        z = torch.randn(40, E_, generator=torch.Generator().manual_seed(E_))
+        z[:, 3] = gap + 3.0
+        bias = torch.zeros(E_)
+        bias[3] = -5.0
+        zn = f64(z)
+        idx = torch.stack([torch.randperm(E_ - 4, generator=torch.Generator().manual_seed(t))[:k].sort().values + 4 for t in range(40)]).int()
+        assert 3 not in E.topk_routing(z.to(DEV), k, "softmax", bias.to(DEV))[1]
+        dp = torch.randn(40, k, generator=torch.Generator().manual_seed(9))
+        dz = E.topk_routing_bwd(dp.to(DEV), z.to(DEV), idx.to(DEV), "softmax", True, 2.5)
+        wz, mag = O.weights_backward(f64(dp), zn, idx.numpy(), "softmax", True, 2.5)
+        assert (np.abs(f64(dz) - wz) <= 2.0 ** -24 * np.abs(wz) + 2.0 ** -17 * (mag + np.abs(wz)) + 2.0 ** -53).all()

@@ -37,7 +37,11 @@ struct MxArgs {
   const uint32_t* tb;
   int a_rows, M, N, K, E, grouped;
   int nm, nn;              // row chunks or tiles (grouped: at most so many), tiles along n
+  int parts, per_part;     // K in parts of so many steps (of kFewK or 128 elements); one: y is written, not float32 parts
 };
+
+// Type of the result: float32, bfloat16, or float32 sums of parts of K, [parts][M][N].
+enum { OUT_F32 = 0, OUT_BF16 = 1, OUT_PARTS = 2 };
 
 // Rows m0 .. m1 - 1 of y with b[e]; none for m1 <= m0.
 struct Span {
@@ -206,7 +210,9 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
 #pragma unroll
     for (int i = 0; i < MT; ++i) load4(rsa, slot + S::SA_AT + i * 256, osa[i] + (uint32_t)t * 8u);
   };
-  if (w < steps) request_b(w);  // b is on its way before the rows of a are looked up
+  const int t0 = OUT == OUT_PARTS ? blockIdx.z * g.per_part : 0;
+  const int t1 = OUT == OUT_PARTS ? min(t0 + g.per_part, steps) : steps;
+  if (t0 + w < t1) request_b(t0 + w);  // b is on its way before the rows of a are looked up
   // row of a behind row i of the span; -1: none
   auto a_row = [&](int i) __attribute__((always_inline)) {
     if (i >= mrows) return -1;
@@ -230,10 +236,10 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
       ea[i][j] = S::SA_AT + i * 256 + (p >> 2) * 64 + lr * 4 + (p & 3);
     }
   }
-  if (w < steps) request_a(w);
+  if (t0 + w < t1) request_a(t0 + w);
   f32x4 acc[MT];
   zero_acc(acc);
-  for (int t = w; t < steps; t += NW) {
+  for (int t = t0 + w; t < t1; t += NW) {
     wait_vmcnt<0>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -251,7 +257,7 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
     }
     wait_lgkm0();  // the slot has been read
     __builtin_amdgcn_sched_barrier(0);
-    if (t + NW < steps) {
+    if (t + NW < t1) {
       request_b(t + NW);
       request_a(t + NW);
     }
@@ -263,6 +269,7 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
   for (int i = 0; i < MT; ++i) red[(w * MT + i) * 64 + lane] = acc[i];
   __syncthreads();
   const float* rf = (const float*)red;
+  float* const part = (float*)g.y + (OUT == OUT_PARTS ? (size_t)blockIdx.z * g.M * g.N : 0);
   for (int o = threadIdx.x; o < mrows * 16; o += NW * 64) {
     const int n = o & 15, m = o >> 4;
     const int at_o = ((m >> 4) * 64 + (n >> 2) * 16 + (m & 15)) * 4 + (n & 3);
@@ -271,10 +278,10 @@ __device__ __forceinline__ void few_rows(const MxArgs& g, const Span& s, char* l
     for (int u = 1; u < NW; ++u) v += rf[u * MT * 256 + at_o];
     if (n < nrows) {
       const size_t out = (size_t)(s.m0 + m) * g.N + n0 + n;
-      if constexpr (OUT == 1)
+      if constexpr (OUT == OUT_BF16)
         store_elem<bf16_t>((bf16_t*)g.y + out, v);
       else
-        ((float*)g.y)[out] = v;
+        part[out] = v;
     }
   }
 }
@@ -345,7 +352,7 @@ __device__ __forceinline__ void tile_of(int id, int total, int nm, int nn, int& 
 template <int OUT>
 __device__ __forceinline__ void store_chunk(char* y, const u32x4_t& v, int left) {
   typedef u32x4_t chunk_t __attribute__((aligned(2)));
-  constexpr int PER = OUT == 1 ? 8 : 4;
+  constexpr int PER = OUT == OUT_BF16 ? 8 : 4;
   if (left >= PER) {
     *(chunk_t*)y = v;
     return;
@@ -353,7 +360,7 @@ __device__ __forceinline__ void store_chunk(char* y, const u32x4_t& v, int left)
 #pragma unroll
   for (int e = 0; e < PER - 1; ++e)
     if (e < left) {
-      if constexpr (OUT == 1)
+      if constexpr (OUT == OUT_BF16)
         *(uint16_t*)(y + e * 2) = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
       else
         *(uint32_t*)(y + e * 4) = v[e];
@@ -369,7 +376,8 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   const int w = wave_id();
   const int wm = w % C::NWM, wn = w / C::NWM;
   int lane, lr, lh;
-  const int KH = g.K >> 1, KS = g.K >> 5, steps = (g.K + 127) / 128;
+  const int KH = g.K >> 1, KS = g.K >> 5;
+  int steps = (g.K + 127) / 128;
   const bool gather = g.rows != nullptr;
   const bool skewed = (((uintptr_t)g.sa | (uintptr_t)g.sb | KS) & 3) != 0;  // some row of exponents starts inside a dword
 
@@ -395,19 +403,28 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   int n0, id = blockIdx.x;
   DmaSrc ra, rb, rs;
   uint32_t oa[NA], ob[NB], os, skew[FR];
-  const int total = g.nm * g.nn;
+  constexpr bool PARTS = OUT == OUT_PARTS;
+  static_assert(!PARTS || !C::WORDS, "parts of K: small tiles");
+  const int tiles = g.nm * g.nn, total = PARTS ? tiles * g.parts : tiles;
+  int t0 = 0, kend = KH, part = 0;  // the part's first step, where its bytes of a row end
   // this workgroup's next tile from id on, its rows in snext (grouped rows may fill fewer tiles than are counted)
   auto find_tile = [&]() __attribute__((always_inline)) {
     for (; id < total; id += gridDim.x) {
       int tm, tn;
-      tile_of(id, total, g.nm, g.nn, tm, tn);
+      tile_of(PARTS ? id % tiles : id, tiles, g.nm, g.nn, tm, tn);
       snext = find_span(g, tm, BM, lane);
       if (snext.m1 > snext.m0) return;
     }
   };
   auto set_tile = [&]() __attribute__((always_inline)) {  // the tile that find_tile found
     int tm, tn;
-    tile_of(id, total, g.nm, g.nn, tm, tn);
+    tile_of(PARTS ? id % tiles : id, tiles, g.nm, g.nn, tm, tn);
+    if constexpr (PARTS) {
+      part = id / tiles;
+      t0 = part * g.per_part;  // a multiple of four
+      steps = min(g.per_part, (g.K + 127) / 128 - t0);
+      kend = min(KH, (t0 + steps) * 64);
+    }
     s = snext;
     const int mrows = s.m1 - s.m0;
     n0 = tn * BN;
@@ -476,9 +493,9 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
       load4(rs, slots + S * C::SLOT + w * 256, os + (uint32_t)min(t, steps - 1) * row * 4u);
       return;
     }
-    const int k = t * 64;
+    const int k = (t0 + t) * 64;
     const uint32_t at = i < NA ? oa[i < NA ? i : 0] : ob[i < NA ? 0 : i - NA];
-    const uint32_t voff = koff < KH - k ? at : kOOB;
+    const uint32_t voff = koff < kend - k ? at : kOOB;
     const uint32_t soff = (uint32_t)min(k, KH);
     if (i < NA)
       load16(ra, st + (w * NA + i) * 1024, voff, soff);
@@ -489,7 +506,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   auto issue_scales = [&](int u, int slot) __attribute__((always_inline)) {
     if constexpr (C::WORDS) return;
     ESG_LDS char* const to = slots + slot * C::SLOT;
-    const uint32_t k = u * 4 < steps ? os + (uint32_t)u * 16u : kOOB;
+    const uint32_t k = u * 4 < steps ? os + (uint32_t)(t0 + u * 4) * 4u : kOOB;
     load16(rs, to + w * 1024, k);
     load4(rs, to + C::SROWS * 16 + w * 256, skewed ? k + 16u : kOOB);
   };
@@ -536,7 +553,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
       for (int f = 0; f < FR; ++f) es[to][f] = raw[f][0] >> (8 * lh);
       return;
     }
-    const int left = KS - t * 4;  // bytes of the row still in K; those past it are other rows'
+    const int left = KS - (t0 + t) * 4;  // bytes of the row still in K; those past it are other rows'
     const uint32_t mask = left >= 4 ? ~0u : left > 0 ? (1u << (8 * left)) - 1u : 0u;
 #pragma unroll
     for (int f = 0; f < FR; ++f) es[to][f] = (__builtin_amdgcn_alignbyte(raw[f][1], raw[f][0], skew[f]) & mask) >> (8 * lh);
@@ -593,7 +610,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   };
   static_assert(FR % 2 == 0 && FR / 2 <= PER * 3 / 4 && PER / 4 - 1 + NL - HALF <= PER * 3 / 4, "reads and loads before the barrier");
 
-  constexpr int ES = OUT == 1 ? 2 : 4;
+  constexpr int ES = OUT == OUT_BF16 ? 2 : 4;
   constexpr int NCH = C::WN * ES / 16;                     // 16-byte chunks of a wave's row
   constexpr int PIECE = C::STAGE / C::NW / (NCH * 16);     // rows of a wave that its share of a stage holds
   static_assert(PIECE <= 32 && 32 % PIECE == 0 && PIECE * NCH % 64 == 0, "whole pieces");
@@ -645,6 +662,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
       if (t + 8 >= steps) break;
     }
     const int m0 = s.m0 + wm * C::WM, mend = s.m1, nw = n0 + wn * C::WN;
+    char* const y = (char*)g.y + (PARTS ? (size_t)part * g.M * g.N * ES : 0);
     wait_lgkm0();
     wait_vmcnt<0>();
     barrier();  // the stages are free
@@ -665,7 +683,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
 #pragma unroll
       for (int h = 0; h < 32 / PIECE; ++h) {
         const int m = m0 + j * 32 + h * PIECE, live = min(max(mend - m, 0), PIECE);
-        const rsrc_t to = make_rsrc((char*)g.y + (size_t)m * g.N * ES, (uint32_t)(live * g.N) * ES);
+        const rsrc_t to = make_rsrc(y + (size_t)m * g.N * ES, (uint32_t)(live * g.N) * ES);
         if (lr / PIECE == h) {
 #pragma unroll
           for (int i = 0; i < C::FN; ++i)
@@ -689,7 +707,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
           if (whole) {
             __builtin_amdgcn_raw_buffer_store_b128(v, to, n < g.N ? (r * g.N + n) * ES : (int)kOOB, 0, kStream);
           } else if (r < live) {
-            store_chunk<OUT>((char*)g.y + ((size_t)(m + r) * g.N + n) * ES, v, g.N - n);
+            store_chunk<OUT>(y + ((size_t)(m + r) * g.N + n) * ES, v, g.N - n);
           }
         }
         wait_lgkm0();  // read before the next rows are written
@@ -732,11 +750,46 @@ __global__ __launch_bounds__(256) void mx_words_kernel(WordsSide a, WordsSide b,
   }
 }
 
+// y = sum of the parts, in their order.  V elements of a thread.
+template <int V, int OUT>
+__global__ __launch_bounds__(256) void mx_parts_kernel(const float* __restrict__ part, int parts, size_t n,
+                                                       void* __restrict__ y) {
+  const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * V;
+  if (at >= n) return;
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    if constexpr (V == 4) {
+      const float4 q = *(const float4*)(part + p * n + at);
+      v[0] += q.x;
+      v[1] += q.y;
+      v[2] += q.z;
+      v[3] += q.w;
+    } else {
+      v[0] += part[p * n + at];
+    }
+  }
+  if constexpr (OUT == OUT_BF16) {
+    if constexpr (V == 4)
+      *(uint2*)((bf16_t*)y + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else
+      store_elem<bf16_t>((bf16_t*)y + at, v[0]);
+  } else {
+    if constexpr (V == 4)
+      *(float4*)((float*)y + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      ((float*)y)[at] = v[0];
+  }
+}
+
 // Kernel and tile size by shape alone (so a shape rounds alike everywhere).
 struct Plan {
   int tile = 0;   // 0: few rows,
   int few = 0;    // so many at a time
   int nm = 0, nn = 0;
+  int parts = 1, per_part = 0;
 };
 // chunks of `chunk` rows, at most: grouped rows leave up to one short chunk per expert
 long long chunks(const MxArgs& g, int chunk) {
@@ -744,15 +797,32 @@ long long chunks(const MxArgs& g, int chunk) {
 }
 Plan plan(const MxArgs& g) {
   Plan p;
+  // K in parts of a multiple of `unit` steps where that leaves no more workgroups than CUs and takes `spare` steps or
+  // more off each one's chain: a second kernel adds the parts, whose launch and reads cost 5 to 9 us.
+  auto split = [&](int steps, int unit, int spare) {
+    const long long wgs = (long long)p.nm * p.nn;
+    if (g.grouped || wgs * 2 > kNominalCUs) return;
+    const int units = (steps + unit - 1) / unit, most = (int)std::min<long long>(units, kNominalCUs / wgs);
+    const int per = (units + most - 1) / most * unit;
+    if (steps - per < spare) return;
+    p.parts = (steps + per - 1) / per;
+    p.per_part = per;
+  };
   const int per = g.grouped ? (g.M + g.E - 1) / g.E : g.M;  // rows that share a b, on average
   const long long wgs = (long long)((g.N + 15) / 16) * ((g.M + kFewRows - 1) / kFewRows);
   // By expert up to 16 rows of each on average (us, few rows / tiles, N = 2816, K = 2048, 64 experts: 9 rows 34 / 42, 15
-  // rows 45 / 47, 18 rows 72 / 47), whose chunks are 16 rows; else up to 64, or while there is a workgroup for no more
-  // than each CU.
-  if (g.grouped ? per <= 16 : per <= kFewRows || wgs <= kNominalCUs) {
+  // rows 45 / 47, 18 rows 72 / 47), whose chunks are 16 rows; else up to 64, or while the workgroups are no more than
+  // three for each CU (few rows / tiles: 256 x 2048 x 5504, 512 of them, 9.8 / 16.9; 100 x 5504 x 2048, 688, 7.4 / 9.7;
+  // 128 x 8192 x 2048, 1024, 10.7 / 9.4) or, where K is long enough for tiles in parts, one (200 x 2048 x 8192, 512,
+  // 15.8 / 15.2; 200 x 3000 x 8192, 752, 22 / 17).
+  constexpr int kLongK = 56 * 128;
+  if (g.grouped ? per <= 16 : per <= kFewRows || wgs <= kNominalCUs * (g.K < kLongK ? 3 : 1)) {
     p.few = per <= 16 ? 16 : kFewRows;
     p.nm = (int)(g.grouped ? g.E + g.M / p.few : (g.M + p.few - 1) / p.few);
     p.nn = (g.N + 15) / 16;
+    // a round of the eight waves takes 0.5 us for one row and 1.5 for 64 (us, whole / parts: 64 x 512 x 16384 14.3 / 10.2;
+    // 1 x 512 x 16384 6.7 / 10.2, 40 x 256 x 8192 7.3 / 10.5)
+    split((g.K + kFewK - 1) / kFewK, 8, 2560 / (16 + std::min(g.M, kFewRows)));
     return p;
   }
   // Tiles in rounds of one for each CU: a round of 256 x 256 takes as long as three of 128 x 128, two of which run side by
@@ -769,6 +839,9 @@ Plan plan(const MxArgs& g) {
   p.tile = near && 3 * rounds(256) < rounds(128) + !g.grouped ? 256 : 128;
   p.nm = (int)chunks(g, p.tile);
   p.nn = (g.N + p.tile - 1) / p.tile;
+  // a step takes 0.28 us (us, whole / parts: 300 x 1024 x 16384 40.7 / 17.2, 1000 x 512 x 8192 23.2 / 17.5; 1024 x 1024 x
+  // 4096 14.8 / 18.1)
+  if (p.tile == 128) split((g.K + 127) / 128, 16, 40);
   return p;
 }
 
@@ -776,13 +849,33 @@ size_t words_bytes(const MxArgs& g) { return ((size_t)g.M + (size_t)g.E * g.N) *
 
 template <int OUT>
 hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
+  if (OUT != OUT_PARTS && p.parts > 1) {
+    MxArgs to = g;
+    to.y = (void*)g.ta;
+    const hipError_t e = run<OUT_PARTS>(to, p, stream);
+    if (e != hipSuccess) return e;
+    LaunchTimer timer("mx_parts", stream);
+    const size_t n = (size_t)g.M * g.N;
+    if (n % 4 == 0)
+      hipLaunchKernelGGL((mx_parts_kernel<4, OUT>), dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, stream,
+                         (const float*)to.y, p.parts, n, g.y);
+    else
+      hipLaunchKernelGGL((mx_parts_kernel<1, OUT>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
+                         (const float*)to.y, p.parts, n, g.y);
+    return hipGetLastError();
+  }
   if (p.tile == 0) {
     LaunchTimer timer("mx_rows", stream);
     // Waves of a workgroup: the fewer the more workgroups there are (us, two / four / eight: 704 x 64 above 33 / 36 / 48;
     // one row of N = 11008, K = 2048 6.2 / 6.2 / 6.9, of N = K = 8192 12.6 / 8.5 / 7.0)
     const long long wgs = (long long)p.nn * p.nm;
-    const dim3 grid(p.nn, p.nm);
-    if (p.few == 16) {
+    const dim3 grid(p.nn, p.nm, p.parts);
+    if constexpr (OUT == OUT_PARTS) {  // fewer than CUs
+      if (p.few == 16)
+        hipLaunchKernelGGL((mx_rows_kernel<8, 1, OUT>), grid, dim3(512), 0, stream, g);
+      else
+        hipLaunchKernelGGL((mx_rows_kernel<8, 4, OUT>), grid, dim3(512), 0, stream, g);
+    } else if (p.few == 16) {
       if (wgs >= 16 * kNominalCUs)
         hipLaunchKernelGGL((mx_rows_kernel<2, 1, OUT>), grid, dim3(128), 0, stream, g);
       else if (wgs > 2 * kNominalCUs)
@@ -796,7 +889,7 @@ hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
     }
     return hipGetLastError();
   }
-  if (p.tile == 256) {
+  if constexpr (OUT != OUT_PARTS) if (p.tile == 256) {
     const int KS = g.K / 32, quads = ((g.K + 127) / 128 + 3) / 4;
     const WordsSide a{g.sa, g.rows, (uint32_t*)g.ta, g.M, g.a_rows}, b{g.sb, nullptr, (uint32_t*)g.tb, g.E * g.N, g.E * g.N};
     const unsigned na = (unsigned)((a.rows + 255) / 256) * quads, nb = (unsigned)((b.rows + 255) / 256) * quads;
@@ -807,12 +900,15 @@ hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
   }
   LaunchTimer timer("mx_tile", stream);
   // as many workgroups as the LDS of the CUs holds at once: one, or two of the smaller tile
-  if (p.tile == 256)
-    hipLaunchKernelGGL((mx_tile_kernel<256, 256, OUT>), dim3(std::min(p.nm * p.nn, compute_units())),
-                       dim3(Tile<256, 256>::NTH), 0, stream, g);
-  else
-    hipLaunchKernelGGL((mx_tile_kernel<128, 128, OUT>), dim3(std::min(p.nm * p.nn, 2 * compute_units())),
-                       dim3(Tile<128, 128>::NTH), 0, stream, g);
+  if constexpr (OUT != OUT_PARTS) {
+    if (p.tile == 256) {
+      hipLaunchKernelGGL((mx_tile_kernel<256, 256, OUT>), dim3(std::min(p.nm * p.nn, compute_units())),
+                         dim3(Tile<256, 256>::NTH), 0, stream, g);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((mx_tile_kernel<128, 128, OUT>), dim3(std::min(p.nm * p.nn * p.parts, 2 * compute_units())),
+                     dim3(Tile<128, 128>::NTH), 0, stream, g);
   return hipGetLastError();
 }
 
@@ -838,7 +934,9 @@ static MxArgs args_of(const MxMatmul& c) {
 
 size_t mx_matmul_workspace_bytes(const MxMatmul& c) {
   const MxArgs g = args_of(c);
-  return c.M > 0 && c.N > 0 && plan(g).tile == 256 ? words_bytes(g) : 0;
+  if (c.M <= 0 || c.N <= 0) return 0;
+  const Plan p = plan(g);
+  return p.tile == 256 ? words_bytes(g) : p.parts > 1 ? (size_t)p.parts * c.M * c.N * 4 : 0;
 }
 
 hipError_t launch_mx_matmul(const MxMatmul& c, hipStream_t stream) {
@@ -846,9 +944,11 @@ hipError_t launch_mx_matmul(const MxMatmul& c, hipStream_t stream) {
   const Plan p = plan(g);
   g.nm = p.nm;
   g.nn = p.nn;
+  g.parts = p.parts;
+  g.per_part = p.per_part;
   g.ta = (const uint32_t*)c.workspace;
   g.tb = g.ta + (size_t)g.M * ((g.K + 127) / 128);
-  return c.out_dtype == 1 ? run<1>(g, p, stream) : run<0>(g, p, stream);
+  return c.out_dtype == 1 ? run<OUT_BF16>(g, p, stream) : run<OUT_F32>(g, p, stream);
 }
 
 }  // namespace esg

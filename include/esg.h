@@ -592,8 +592,8 @@ int esg_mxfp4_dequant(const void* q, const void* scale, int dtype, int64_t rows,
  * shape alone and no atomics are used (bitwise reproducible).  A block of the byte 255
  * makes what it adds to NaN.
  * workspace: esg_mxfp4_matmul_workspace_size() bytes (esg_mxfp4_grouped_matmul_workspace_size
- * for the other), 16-byte aligned (large products lay the scales out anew there; it may be
- * 0, then workspace may be NULL).
+ * for the other), 16-byte aligned (large products lay the scales out anew there, those of few
+ * outputs and long K keep the sums of parts of K; it may be 0, then workspace may be NULL).
  * M == 0 or N == 0 enqueues nothing.
  *
  * esg_mxfp4_grouped_matmul: the same for rows in the order of their experts, b: [experts,

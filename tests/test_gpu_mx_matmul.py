@@ -38,7 +38,8 @@ def _close(y, want, mag, K, dtype):
 SHAPES = [(1, 16, 32), (1, 11008, 2048), (3, 40, 96), (16, 16, 128), (17, 100, 160), (33, 72, 512), (37, 2048, 5504),
           (49, 17, 1056), (64, 64, 4096), (65, 256, 544), (100, 33, 64), (200, 300, 1376), (129, 4096, 288),
           (300, 4097, 320), (513, 2049, 256), (640, 2056, 800), (1000, 4608, 2080), (2050, 8200, 256), (4096, 4100, 608),
-          (2500, 5504, 608), (2500, 5501, 160), (2430, 5500, 32), (6000, 8200, 96)]
+          (2500, 5504, 608), (2500, 5501, 160), (2430, 5500, 32), (6000, 8200, 96),
+          (130, 1500, 4128), (2, 48, 65536), (64, 512, 16384), (33, 77, 40032), (300, 1024, 8192), (513, 701, 7200), (700, 1001, 9696)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -245,3 +246,6 @@ def test_shapes_reach_every_kernel():
     large = [s for s in SHAPES if size(*s) > 0]
     assert {N % 8 == 0 for _, N, _ in large} == {True, False} and {K % 128 == 0 for _, _, K in SHAPES} == {True, False}
     assert size(2500, 5504, 160) > 0 and size(700, 1600, 160) == 0
+    # K in parts: few rows and tiles
+    assert size(64, 512, 16384) == 8 * 64 * 512 * 4 and size(300, 1024, 8192) % (300 * 1024 * 4) == 0 < size(300, 1024, 8192)
+    assert all(size(*s) > 0 for s in SHAPES[-6:])

@@ -809,14 +809,16 @@ Plan plan(const MxArgs& g) {
     p.per_part = per;
   };
   const int per = g.grouped ? (g.M + g.E - 1) / g.E : g.M;  // rows that share a b, on average
-  const long long wgs = (long long)((g.N + 15) / 16) * ((g.M + kFewRows - 1) / kFewRows);
-  // By expert up to 16 rows of each on average (us, few rows / tiles, N = 2816, K = 2048, 64 experts: 9 rows 34 / 42, 15
-  // rows 45 / 47, 18 rows 72 / 47), whose chunks are 16 rows; else up to 64, or while the workgroups are no more than
-  // three for each CU (few rows / tiles: 256 x 2048 x 5504, 512 of them, 9.8 / 16.9; 100 x 5504 x 2048, 688, 7.4 / 9.7;
-  // 128 x 8192 x 2048, 1024, 10.7 / 9.4) or, where K is long enough for tiles in parts, one (200 x 2048 x 8192, 512,
-  // 15.8 / 15.2; 200 x 3000 x 8192, 752, 22 / 17).
+  const long long wgs =
+      (long long)((g.N + 15) / 16) * (g.grouped ? g.M / kFewRows + std::min(g.E, g.M) : (g.M + kFewRows - 1) / kFewRows);
+  // Few rows: by expert up to 16 of each on average (us, few rows / tiles, N = 2816, K = 2048, 64 experts: 9 rows 34 /
+  // 42, 15 rows 45 / 47, 18 rows 72 / 47), in chunks of 16, else up to 64; or while the workgroups are no more than three
+  // for each CU (256 x 2048 x 5504, 512 of them, 9.8 / 16.9; 100 x 5504 x 2048, 688, 7.4 / 9.7; 128 x 8192 x 2048, 1024,
+  // 10.7 / 9.4; 87 tokens, 2 of 5 experts, 232 x 1952, 105, 7.7 / 10.6; 1000, 2 of 8, 512 x 1024, 1248, 11 / 8.5) or,
+  // where K is long enough for tiles in parts, one (200 x 2048 x 8192, 512, 15.8 / 15.2; 200 x 3000 x 8192, 752, 22 / 17).
   constexpr int kLongK = 56 * 128;
-  if (g.grouped ? per <= 16 : per <= kFewRows || wgs <= kNominalCUs * (g.K < kLongK ? 3 : 1)) {
+  const int most = g.grouped || g.K < kLongK ? 3 : 1;
+  if (per <= (g.grouped ? 16 : kFewRows) || wgs <= kNominalCUs * most) {
     p.few = per <= 16 ? 16 : kFewRows;
     p.nm = (int)(g.grouped ? g.E + g.M / p.few : (g.M + p.few - 1) / p.few);
     p.nn = (g.N + 15) / 16;

@@ -107,7 +107,8 @@ def test_nan_of_the_next_row_stays_there():
 
 GROUPED = [(1, 16, 32, [1]), (5, 40, 96, [0, 5, 0]), (7, 48, 160, [3, 0, 4]), (64, 128, 512, [1] * 64),
            (384, 272, 1024, None), (300, 100, 288, [70, 0, 17, 1, 49, 33, 64, 65]), (1000, 520, 352, [129, 600, 0, 1, 127, 128]),
-           (2000, 1032, 544, [300, 256, 1400]), (2100, 136, 256, [2, 2000, 3]), (700, 77, 96, [0, 0, 690, 0])]
+           (2000, 1032, 544, [300, 256, 1400]), (2100, 136, 256, [2, 2000, 3]), (700, 77, 96, [0, 0, 690, 0]),
+           (1000, 2056, 352, [129, 600, 0, 1, 127, 128]), (700, 1501, 96, [0, 0, 690, 0]), (2100, 1500, 416, [2, 2000, 3])]
 
 
 @pytest.mark.parametrize("gather", [True, False])
@@ -138,22 +139,21 @@ def test_grouped(M, N, K, counts, gather):
 def test_grouped_bad_rows_and_offsets():
     require_gpu()
     note("mx grouped bad rows, offsets past the ends")
-    a, b = _operand(10, 64, 1), _operand(3 * 32, 64, 2)
-    for M in (20, 400):                                    # few rows, tiles
+    for M, N in ((20, 32), (400, 32), (400, 2000)):        # few rows in chunks of 16 and 64, tiles
+        a, b = _operand(10, 64, 1), _operand(3 * N, 64, 2)
         rows = torch.arange(M).int() % 10
         rows[3], rows[4], rows[5] = -1, 10, 2 ** 31 - 1
         offsets = torch.tensor([-4, 6, M + 100, M + 100]).int()
-        out = torch.full((M, 32), 5.0, device=DEV)
-        E.mxfp4_grouped_matmul(*(t.to(DEV) for t in (*a, b[0].view(3, 32, 32), b[1].view(3, 32, 2), offsets)), rows=rows.to(DEV),
-                               out=out)
+        out = torch.full((M, N), 5.0, device=DEV)
+        d = [t.to(DEV) for t in (*a, b[0].view(3, N, 32), b[1].view(3, N, 2))]
+        E.mxfp4_grouped_matmul(*d, offsets.to(DEV), rows=rows.to(DEV), out=out)
         x = _vals(*a)[rows.long().clamp(0, 9)]
         x[3:6] = 0
-        bv = _vals(*b).view(3, 32, 64)
+        bv = _vals(*b).view(3, N, 64)
         want = torch.cat((x[:6] @ bv[0].t(), x[6:] @ bv[1].t()))
         assert torch.allclose(out.double().cpu(), want, rtol=1e-5, atol=1e-5)
         out.fill_(5.0)                                     # no rows at all
-        E.mxfp4_grouped_matmul(*(t.to(DEV) for t in (*a, b[0].view(3, 32, 32), b[1].view(3, 32, 2), torch.zeros(4).int())),
-                               rows=rows.to(DEV), out=out)
+        E.mxfp4_grouped_matmul(*d, torch.zeros(4).int().to(DEV), rows=rows.to(DEV), out=out)
         assert (out == 5).all()
 
 

@@ -13,7 +13,8 @@
 // one m.
 //
 // Two kernels: mx_rows_kernel for few rows, bound by the read of b, and mx_tile_kernel
-// for many; plan() chooses between them.
+// for many; plan() chooses between them, and cuts a long K into parts where outputs are
+// few.
 #include <algorithm>
 
 #include "esg_internal.hpp"
@@ -318,6 +319,11 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs g) {
 // steps).  The small tile, whose products are too short for a launch before them, does read
 // them there: the five dwords that hold the bytes of four steps (a row starts at any byte)
 // go into two slots, and the lanes that use a step's four bytes put them together.
+//
+// 32768 x 5504 x 2048 to bf16: 211 to 272 us (2.7 to 3.5 PFLOP/s), 8192 cubed 260 to 290 (3.8 to 4.2).  Bound by the
+// power that the products draw (registers alone: 10 PFLOP/s on zeros, 5.7 to 6.6 on random codes, at a clock of 1.4 to
+// 1.9 GHz) and, with few steps a tile, by the stores, which come from all CUs at once: the matrix cores are busy for 48 %
+// of the cycles of the first, 69 % of the second's.
 // ---------------------------------------------------------------------------
 template <int BM, int BN>
 struct Tile {

@@ -876,7 +876,7 @@ def rms_norm_fwd(x, weight, residual=None, eps: float = 1e-6, need_rstd: bool = 
 
 @functools.lru_cache(maxsize=4096)
 def rms_norm_bwd_workspace_size(tokens: int, d_model: int) -> int:
-    """Bytes of scratch the weight gradient of rms_norm needs."""
+    """Bytes of scratch the weight gradient of rms_norm needs (0 for few tokens)."""
     need = _c_size()
     _check(lib().esg_rms_norm_bwd_workspace_size(tokens, d_model, ctypes.byref(need)), "rms_norm_bwd_workspace_size")
     return need.value
@@ -899,7 +899,8 @@ def rms_norm_bwd(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspace: 
     dw = ws = None
     if need_dw:
         dw = torch.empty_like(weight)
-        ws = _ws(rms_norm_bwd_workspace_size(T, d), dev, workspace, "rms_norm_bwd")
+        need = rms_norm_bwd_workspace_size(T, d)
+        ws = _ws(need, dev, workspace, "rms_norm_bwd") if need else None
     _check(lib().esg_rms_norm_bwd(
         _dev(dy, "dy", None, gpu), _dev(dh, "dh", None, gpu), _dev(h, "h"), _dev(weight, "weight", None, gpu),
         _dev(rstd, "rstd", torch.float32, gpu), _dtype_code(h), _dtype_code(weight), T, d, dx.data_ptr(),
@@ -939,7 +940,6 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6):
     h = x + residual (rounded to their dtype), y = h (mean h^2 + eps)^-1/2 weight -> y,
     or (y, h) with a residual: h is the new one.  x, residual: [..., d], float32 or
     bfloat16, d a multiple of 16, at most 16384; weight: [d], float32 or bfloat16."""
-    _norm_args(x, weight, residual)
     if not torch.is_grad_enabled():
         y, h, _ = rms_norm_fwd(_whole(x), _whole(weight), None if residual is None else _whole(residual), eps, False)
         return y if residual is None else (y, h)

@@ -739,8 +739,9 @@ int esg_rms_norm_bwd(const void* dy, const void* dh, const void* h, const void* 
     for (const void* p : {dy, dh, h, w, (const void*)dx})
       if (!aligned16(p)) return ESG_ERR_INVALID_ARG;
     if (((uintptr_t)rstd & 3u) != 0) return ESG_ERR_INVALID_ARG;
-    if (dw != nullptr && (workspace == nullptr || workspace_bytes < rms_norm_bwd_bytes(tokens, d_model)))
-      return ESG_ERR_WORKSPACE;
+    if (dw != nullptr && dx == dy) return ESG_ERR_INVALID_ARG;  // dw's workgroups read dy beside those that write dx
+    const size_t need = dw != nullptr ? rms_norm_bwd_bytes(tokens, d_model) : 0;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return ESG_ERR_WORKSPACE;
   }
   if (!aligned16(dw) || !aligned16(workspace)) return ESG_ERR_INVALID_ARG;
   return hip_status(launch_rms_norm_bwd(dtype, w_dtype, dy, dh, h, w, rstd, tokens, d_model, dx, dw, workspace,

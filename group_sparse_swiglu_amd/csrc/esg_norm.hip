@@ -166,12 +166,50 @@ struct NormBwdArgs {
   const float* rstd;
   int rows, d;
   void* dx;
-  float* part;     // [gridDim.x][d], or NULL: no weight gradient
+  float* part;     // [row_wgs][d], or NULL: no weight gradient, or by the workgroups from row_wgs on
+  void* dw;        // theirs
+  int row_wgs;
 };
 
-// The weight gradient's sum stays in registers over the rows of a workgroup and leaves once as a float32 row.
+// The weight gradient of 32 columns, straight from dy and h: eight threads take them, 32 row groups.
+template <typename T>
+__device__ __forceinline__ void dw_columns(const NormBwdArgs& g, int wg) {
+  __shared__ float4 lds[4][8];
+  const int cl = threadIdx.x & 7, rg = threadIdx.x >> 3, c = wg * 32 + cl * 4;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < g.d) {
+#pragma unroll 8
+    for (int row = rg; row < g.rows; row += 32) {
+      float dy[4], h[4];
+      Quad<T>::load((const T*)g.dy + (int64_t)row * g.d + c, dy);
+      Quad<T>::load((const T*)g.h + (int64_t)row * g.d + c, h);
+      const float r = g.rstd[row];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] = fmaf(dy[j], h[j] * r, s[j]);
+    }
+  }
+#pragma unroll
+  for (int off = 8; off < 64; off *= 2)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] += __shfl_xor(s[j], off);
+  if ((threadIdx.x & 63) < 8) lds[threadIdx.x >> 6][cl] = make_float4(s[0], s[1], s[2], s[3]);
+  __syncthreads();
+  if (threadIdx.x < 8 && c < g.d) {
+    const float4 a = lds[0][cl], b = lds[1][cl], e = lds[2][cl], f = lds[3][cl];
+    const float o[4] = {(a.x + b.x) + (e.x + f.x), (a.y + b.y) + (e.y + f.y), (a.z + b.z) + (e.z + f.z),
+                        (a.w + b.w) + (e.w + f.w)};
+    if (g.w_f32)
+      Quad<float>::store((float*)g.dw + c, o);
+    else
+      Quad<bf16_t>::store((bf16_t*)g.dw + c, o);
+  }
+}
+
+// The weight gradient's sum stays in registers over the rows of a workgroup and leaves once as a float32 row (or, of few
+// rows, is the business of other workgroups).
 template <typename T, int TPR, int NV>
 __global__ __launch_bounds__(256) void rms_norm_bwd_kernel(NormBwdArgs g) {
+  if ((int)blockIdx.x >= g.row_wgs) return dw_columns<T>(g, blockIdx.x - g.row_wgs);
   constexpr int RPW = 256 / TPR;
   __shared__ float lds[2][4];
   __shared__ float dw_lds[RPW > 1 ? RPW : 1][RPW > 1 ? TPR * NV * 8 : 1];
@@ -183,7 +221,7 @@ __global__ __launch_bounds__(256) void rms_norm_bwd_kernel(NormBwdArgs g) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
   int turn = 0;
-  const int64_t stride = (int64_t)gridDim.x * RPW;
+  const int64_t stride = (int64_t)g.row_wgs * RPW;
   int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
   Oct<T> hn[NV], yn[NV], nn[NV];  // the next row's values
   float rn = 0.f;
@@ -327,10 +365,10 @@ hipError_t fwd_t(const NormArgs& g, hipStream_t stream) {
 }
 
 template <typename T>
-hipError_t bwd_t(const NormBwdArgs& g, int parts, hipStream_t stream) {
+hipError_t bwd_t(const NormBwdArgs& g, int wgs, hipStream_t stream) {
   return by_width(g.d, [&](auto tpr, auto nv) {
     LaunchTimer timer("rms_norm_bwd", stream);
-    hipLaunchKernelGGL((rms_norm_bwd_kernel<T, tpr.value, nv.value>), dim3(parts), dim3(256), 0, stream, g);
+    hipLaunchKernelGGL((rms_norm_bwd_kernel<T, tpr.value, nv.value>), dim3(wgs), dim3(256), 0, stream, g);
     return hipGetLastError();
   });
 }
@@ -352,18 +390,26 @@ static int bwd_parts(int rows, int d) {
   return std::min((int)(((int64_t)rows + rows_per_wg(d) - 1) / rows_per_wg(d)), kNominalCUs * (d > 8192 ? 1 : 2));
 }
 
-size_t rms_norm_bwd_bytes(int rows, int d) { return (size_t)bwd_parts(rows, d) * d * 4; }
+// Few rows: the weight gradient needs no second kernel, workgroups beside those of the rows read dy and h again, out of
+// the caches (us, bf16, one / two kernels: 64 x 2048 2.8 / 6.1, 333 x 768 3.4 / 7.0, 1024 x 2048
+// 5.7 / 10.1, 512 x 8192 12.5 / 17.6; 1024 x 8192 22.5 / 17.8, 2048 x 2048 13.5 / 11.9).
+static bool direct_dw(int rows, int d) { return rows <= 1024 && (int64_t)rows * d <= 1024 * 4096; }
+
+size_t rms_norm_bwd_bytes(int rows, int d) { return direct_dw(rows, d) ? 0 : (size_t)bwd_parts(rows, d) * d * 4; }
 
 hipError_t launch_rms_norm_bwd(int dtype, int w_dtype, const void* dy, const void* dh, const void* h, const void* w,
                                const float* rstd, int rows, int d, void* dx, void* dw, void* workspace,
                                hipStream_t stream) {
   const int parts = bwd_parts(rows, d);
-  if (rows > 0) {
-    const NormBwdArgs g{dy, dh, h, w, w_dtype == 0, rstd, rows, d, dx, dw != nullptr ? (float*)workspace : nullptr};
-    const hipError_t e = dtype == 0 ? bwd_t<float>(g, parts, stream) : bwd_t<bf16_t>(g, parts, stream);
+  const bool direct = direct_dw(rows, d);
+  const NormBwdArgs g{dy, dh, h, w, w_dtype == 0, rstd, rows, d, dx, dw != nullptr && !direct ? (float*)workspace : nullptr,
+                      dw, parts};
+  const int wgs = parts + (dw != nullptr && direct ? (d + 31) / 32 : 0);
+  if (wgs > 0) {  // (without rows the weight gradient is zeros)
+    const hipError_t e = dtype == 0 ? bwd_t<float>(g, wgs, stream) : bwd_t<bf16_t>(g, wgs, stream);
     if (e != hipSuccess) return e;
   }
-  if (dw == nullptr) return hipSuccess;
+  if (dw == nullptr || direct) return hipSuccess;
   LaunchTimer timer("rms_norm_dw", stream);
   if (w_dtype == 0)
     hipLaunchKernelGGL(rms_norm_dw_kernel<float>, dim3((d + 63) / 64), dim3(256), 0, stream, (const float*)workspace,

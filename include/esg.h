@@ -500,14 +500,14 @@ int esg_fp8_linear_bwd(const void* dy, int x_dtype, int w_dtype, int tokens, int
  *
  * esg_rms_norm_bwd: with dy = dL/dy and dh = dL/dh (dtype; dh NULL: zero), h (x
  * where there was no residual) and rstd of the forward, g = dy w:
- *   dx = dh + r (g - h r^2 mean(g h))   (the gradient of x and of residual alike);
- *   dw = sum over tokens of dy h r      (w_dtype [d_model]; NULL: not computed).
- * dx may be dy or dh.  Both are overwritten (tokens == 0: dw is zero).  The sum of g h
- * over a row has to stay in float32's range.  dw's sum is
- * float32 in a fixed order (bitwise reproducible).  workspace (16-byte aligned):
- * esg_rms_norm_bwd_workspace_size() bytes, needed for dw only.
+ *   dx = dh + r (g - h r mean(g h r))   (the gradient of x and of residual alike);
+ *   dw = sum over tokens of dy h r       (w_dtype [d_model]; NULL: not computed).
+ * dx may be dh, and dy if dw is NULL.  Both are overwritten (tokens == 0: dw is zero).
+ * Sums are float32, dw's in a fixed order (bitwise reproducible).  workspace (16-byte
+ * aligned): esg_rms_norm_bwd_workspace_size() bytes (0 for few tokens: it may be NULL),
+ * needed for dw only.
  * Errors: ESG_ERR_INVALID_ARG (null or misaligned pointer, h without residual or
- * the reverse, negative tokens, d_model <= 0), ESG_ERR_UNSUPPORTED (a dtype, d_model
+ * the reverse, dx == dy with dw, negative tokens, d_model <= 0), ESG_ERR_UNSUPPORTED (a dtype, d_model
  * not a multiple of 16 or above 16384), ESG_ERR_WORKSPACE.
  */
 int esg_rms_norm_fwd(const void* x, const void* residual, const void* w, int dtype, int w_dtype, int tokens, int d_model,

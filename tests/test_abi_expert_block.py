@@ -38,15 +38,17 @@ def test_norm_quant_refusals():
 
 def test_norm_backward_refusals_and_workspace():
     names = ("dy", "dh", "h", "w", "rstd", "dt", "wdt", "T", "d", "dx", "dw", "ws", "bytes", "stream")
-    call = _caller(E.lib().esg_rms_norm_bwd, names, (P, NULL, P, P, P, 1, 1, 4, 64, P, P, P, 1 << 40, NULL))
+    call = _caller(E.lib().esg_rms_norm_bwd, names, (P, NULL, P, P, P, 1, 1, 4, 64, 2 * P, P, P, 1 << 40, NULL))
+    assert call(dx=P) == 1                                  # dy itself, which dw still needs
     assert call(T=0, dw=NULL) == 0 and call(T=0, dw=NULL, dy=NULL, h=NULL) == 0
     for n in ("dy", "h", "w", "rstd", "dx"):
         assert call(**{n: NULL}) == 1
     for n in ("dy", "dh", "h", "w", "dx", "dw", "ws"):
         assert call(**{n: P + 8}) == 1
-    assert call(ws=NULL) == 3 and call(bytes=0) == 3 and call(d=40) == 2 and call(T=-2) == 1
+    assert E.rms_norm_bwd_workspace_size(5000, 64) > 0
+    assert call(T=5000, ws=NULL) == 3 and call(T=5000, bytes=0) == 3 and call(d=40) == 2 and call(T=-2) == 1
     assert E.rms_norm_bwd_workspace_size(0, 64) == 0
-    assert E.rms_norm_bwd_workspace_size(5, 2048) >= 2048 * 4
+    assert E.rms_norm_bwd_workspace_size(5, 2048) == 0 and E.rms_norm_bwd_workspace_size(5000, 2048) >= 2048 * 4
     assert E.rms_norm_bwd_workspace_size(1 << 30, 16384) <= 1 << 27
     need = ctypes.c_size_t()
     assert E.lib().esg_rms_norm_bwd_workspace_size(4, 50, ctypes.byref(need)) == 2

@@ -216,3 +216,21 @@ def test_gradient_of_large_values():
         dx, dw, mx, mw = O.rms_norm_backward(f64(dy), x.numpy(), f64(w), EPS)
         assert (np.abs(f64(gx) - dx) <= 226 * U * mx).all()
         assert (np.abs(f64(gw) - dw) <= 53 * U * mw).all()
+
+
+@pytest.mark.parametrize("T", [15, 31, 33, 257, 1023, 1024, 1025])
+def test_weight_gradient_around_the_change_of_kernels(T):
+    require_gpu()
+    for d, dtype, wdtype in ((16, F32, BF), (80, BF, F32), (1040, BF, BF), (2064, F32, F32)):
+        note(f"norm weight gradient {T}x{d} {dtype} {wdtype}")
+        x, _, w, _ = _case(T, d, dtype, wdtype, False, T)
+        dy = _rand(T, d, dtype, 5)
+        xd = x.to(DEV)
+        _, h, r = E.rms_norm_fwd(xd, w.to(DEV), eps=EPS)
+        gx, gw = E.rms_norm_bwd(dy.to(DEV), h, w.to(DEV), r)
+        dx, dw, mx, mw = O.rms_norm_backward(f64(dy), f64(x), f64(w), EPS)
+        assert (np.abs(f64(gx) - dx) <= _out(dtype) * np.abs(dx) + 225 * U * mx).all()
+        assert (np.abs(f64(gw) - dw) <= _out(wdtype) * np.abs(dw) + (T + 48) * U * mw).all()
+        again = E.rms_norm_bwd(dy.to(DEV), h, w.to(DEV), r)
+        assert torch.equal(gx, again[0]) and torch.equal(gw, again[1])
+        assert torch.equal(gx, E.rms_norm_bwd(dy.to(DEV), h, w.to(DEV), r, need_dw=False)[0])

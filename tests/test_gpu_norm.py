@@ -234,3 +234,22 @@ def test_weight_gradient_around_the_change_of_kernels(T):
         again = E.rms_norm_bwd(dy.to(DEV), h, w.to(DEV), r)
         assert torch.equal(gx, again[0]) and torch.equal(gw, again[1])
         assert torch.equal(gx, E.rms_norm_bwd(dy.to(DEV), h, w.to(DEV), r, need_dw=False)[0])
+
+
+def test_expanded_gradients_and_no_second_derivative():
+    require_gpu()
+    note("norm expanded gradients, second derivatives refused")
+    x, res, w, h = _case(6, 528, F32, BF, True, 3)
+    xd, rd, wd = (t.to(DEV).requires_grad_() for t in (x, res, w))
+    y, hd = E.rms_norm(xd, wd, rd, EPS)
+    gx, gw = torch.autograd.grad(y.sum() + 2 * hd.sum(), (xd, wd))     # gradients of stride 0
+    dx, dw, mx, mw = O.rms_norm_backward(np.ones(h.shape), f64(h), f64(w), EPS, 2 * np.ones(h.shape))
+    assert (np.abs(f64(gx) - dx) <= 226 * U * mx).all() and (np.abs(f64(gw) - dw) <= 2.0 ** -8 * np.abs(dw) + 55 * U * mw).all()
+    y, _ = E.rms_norm(xd, wd, rd, EPS)
+    g, = torch.autograd.grad(y, xd, torch.ones_like(y).requires_grad_(), create_graph=True)
+    assert torch.equal(g, torch.autograd.grad(E.rms_norm(xd, wd, rd, EPS)[0].sum(), xd)[0])
+    with pytest.raises(RuntimeError, match="once_differentiable|differentiat"):
+        torch.autograd.grad(g.sum(), xd)
+    with torch.autograd.set_multithreading_enabled(False):             # the backward on this thread
+        y, _ = E.rms_norm(xd, wd, rd, EPS)
+        assert torch.equal(torch.autograd.grad(y.sum() + 0 * y.sum(), xd)[0], g)

@@ -170,3 +170,16 @@ def test_chosen_scores_far_below_one(gap):
         dz = E.topk_routing_bwd(dp.to(DEV), z.to(DEV), idx.to(DEV), "softmax", True, 2.5)
         wz, mag = O.weights_backward(f64(dp), zn, idx.numpy(), "softmax", True, 2.5)
         assert (np.abs(f64(dz) - wz) <= 2.0 ** -24 * np.abs(wz) + 2.0 ** -17 * (mag + np.abs(wz)) + 2.0 ** -53).all()
+
+
+def test_expanded_gradients_and_no_second_derivative():
+    require_gpu()
+    note("route expanded gradients, second derivatives refused")
+    z = _logits(9, 60, F32, "normal", 1)
+    zd = z.to(DEV).requires_grad_()
+    p, idx = E.topk_routing(zd, 6, "sigmoid", normalize=False)
+    g, = torch.autograd.grad(p, zd, torch.ones(1, 1, device=DEV).expand(p.shape).requires_grad_(), create_graph=True)  # stride 0
+    wz, mag = O.weights_backward(np.ones(p.shape), f64(z), idx.cpu().numpy(), "sigmoid", False, 1.0)
+    assert (np.abs(f64(g) - wz) <= 2.0 ** -17 * mag).all()
+    with pytest.raises(RuntimeError, match="once_differentiable|differentiat"):
+        torch.autograd.grad(g.sum(), zd)

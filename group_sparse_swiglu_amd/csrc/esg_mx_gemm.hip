@@ -311,7 +311,10 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs g) {
 // sits before the products of its second slice, whose operands are in registers: behind
 // it the step's stage is free, and the loads of four steps on go there, spread over the
 // next two slices' products.  So three steps' loads are on their way at any time, and the
-// only wait is for the oldest.
+// only wait is for the oldest.  In large tiles a step's loads all go to the stage that the
+// step before has left, and those of a tile's last three steps are the next tile's first:
+// the ring runs on from tile to tile (8191 tokens, 6 of 64 experts, 2048 x 1408, eleven
+// steps: 136 -> 126 us; 32768 x 5504 x 2048, sixteen: equal, see below).
 // The exponents of a step are a word per row and step.  Large tiles take them from arrays in
 // which a step's words of neighbouring rows are neighbours (mx_words_kernel lays them out
 // first): one load of whole lines per wave and step.  Read where they are, 16 bytes of each
@@ -516,13 +519,14 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
     load16(rs, to + w * 1024, k);
     load4(rs, to + C::SROWS * 16 + w * 256, skewed ? k + 16u : kOOB);
   };
+  int ring = 0;  // stage of the tile's step 0 (large tiles: they follow each other around the ring)
   // a tile's first loads: steps 0 to 2, the exponents of steps 0 to 7
   auto first_loads = [&]() __attribute__((always_inline)) {
     issue_scales(0, 0);
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
 #pragma unroll
-      for (int i = 0; i < NL; ++i) issue(t, t, i);
+      for (int i = 0; i < NL; ++i) issue(t, C::WORDS ? (ring + t) & 3 : t, i);
       if (t == 0) issue_scales(1, 1);
     }
   };
@@ -614,6 +618,36 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
       if (p == PER - 2) set_scales(t + 1, (S & 1) ^ 1);
     });
   };
+  // The same for large tiles: stage and step's parity apart, and the loads are those of three steps on, all of them, so
+  // that they pass from one tile to the next between two steps.  `from`: the load's step 0 in steps of this tile.
+  auto large_step = [&](int t, int P, int from) __attribute__((always_inline)) {
+    constexpr int WAIT = PER * 3 / 4 - 1, FIRST = NL - HALF;
+    const int S = (ring + t) & 3, S1 = (ring + t + 1) & 3, S3 = (ring + t + 3) & 3;
+    products(0, P, [&](int p) __attribute__((always_inline)) {
+      if (p < FR / 2) {
+        read_frag(S, 1, 1, 2 * p);
+        read_frag(S, 1, 1, 2 * p + 1);
+      }
+      if (p >= PER / 4 - 1 && p < PER / 4 - 1 + FIRST) issue(t + 3 - from, S3, p - PER / 4 + 1);
+      if (p == WAIT) {
+        wait_lgkm0();
+        wait_vmcnt<NL + FIRST>();  // the next step has landed: newer are one step's loads and a part of another's
+        barrier();
+      }
+    });
+    products(1, P, [&](int p) __attribute__((always_inline)) {
+      if (p < FR / 2) {
+        read_frag(S1, 0, 0, 2 * p);
+        read_frag(S1, 0, 0, 2 * p + 1);
+      }
+      if (p == (FR + 1) / 2 - 1) {
+#pragma unroll
+        for (int f = 0; f < FR; ++f) read_raw(0, S1, f);
+      }
+      if (p >= PER / 4 && p < PER / 4 + HALF) issue(t + 3 - from, S3, FIRST + p - PER / 4);
+      if (p == PER - 2) set_scales(t + 1, P ^ 1);
+    });
+  };
   static_assert(FR % 2 == 0 && FR / 2 <= PER * 3 / 4 && PER / 4 - 1 + NL - HALF <= PER * 3 / 4, "reads and loads before the barrier");
 
   constexpr int ES = OUT == OUT_BF16 ? 2 : 4;
@@ -627,6 +661,7 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
   if (id >= total) return;
   set_tile();
   first_loads();
+  bool loaded = false;  // the tile's first loads went out, and its step 0 landed, in the steps of the tile before
   for (;;) {
     set_lane();
 #pragma unroll
@@ -637,52 +672,77 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
     // Loads come back in the order of their issue, but stores not in order with them: with so many of both under way,
     // step 0's loads, which have as many loads behind them, are done.
-    wait_vmcnt<BEHIND_FIRST>();
+    if (!C::WORDS || !loaded) wait_vmcnt<BEHIND_FIRST>();
     barrier();  // step 0 has landed, and the last stage is free of the results
+    if constexpr (!C::WORDS) {
 #pragma unroll
-    for (int i = 0; i < HALF; ++i) issue(3, 3, i);
+      for (int i = 0; i < HALF; ++i) issue(3, 3, i);
+    }
 #pragma unroll
     for (int f = 0; f < FR; ++f) {
-      read_raw(0, 0, f);
-      read_frag(0, 0, 0, f);
+      read_raw(0, C::WORDS ? ring : 0, f);
+      read_frag(C::WORDS ? ring : 0, 0, 0, f);
     }
     set_scales(0, 0);
-    id += gridDim.x;
-    find_tile();  // its reads' latency passes here rather than between the tiles
-    for (int t = 0;; t += 8) {
-      step(t, 0, 0);
-      if (t + 1 >= steps) break;
-      step(t + 1, 1, 0);
-      if (t + 2 >= steps) break;
-      step(t + 2, 2, 0);
-      if (t + 3 >= steps) break;
-      step(t + 3, 3, 0);
-      if (t + 4 >= steps) break;
-      step(t + 4, 0, 1);
-      if (t + 5 >= steps) break;
-      step(t + 5, 1, 1);
-      if (t + 6 >= steps) break;
-      step(t + 6, 2, 1);
-      if (t + 7 >= steps) break;
-      step(t + 7, 3, 1);
-      if (t + 8 >= steps) break;
-    }
     const int m0 = s.m0 + wm * C::WM, mend = s.m1, nw = n0 + wn * C::WN;
     char* const y = (char*)g.y + (PARTS ? (size_t)part * g.M * g.N * ES : 0);
-    wait_lgkm0();
-    wait_vmcnt<0>();
-    barrier();  // the stages are free
-    // the next tile's first loads go out before this one's results
-    set_lane();
-    if (id < total) {
-      set_tile();
-      first_loads();
+    id += gridDim.x;
+    find_tile();  // its reads' latency passes here rather than between the tiles
+    if constexpr (C::WORDS) {
+      // the last three steps load the next tile's first three
+      loaded = steps >= 3;
+      const int last = steps, own = loaded && id < total ? steps - 3 : steps;
+      int from = 0;
+      for (int t = 0;; t += 2) {
+        if (t == own) {
+          set_tile();
+          from = last;
+        }
+        large_step(t, 0, from);
+        if (t + 1 >= last) break;
+        if (t + 1 == own) {
+          set_tile();
+          from = last;
+        }
+        large_step(t + 1, 1, from);
+        if (t + 2 >= last) break;
+      }
+    } else {
+      for (int t = 0;; t += 8) {
+        step(t, 0, 0);
+        if (t + 1 >= steps) break;
+        step(t + 1, 1, 0);
+        if (t + 2 >= steps) break;
+        step(t + 2, 2, 0);
+        if (t + 3 >= steps) break;
+        step(t + 3, 3, 0);
+        if (t + 4 >= steps) break;
+        step(t + 4, 0, 1);
+        if (t + 5 >= steps) break;
+        step(t + 5, 1, 1);
+        if (t + 6 >= steps) break;
+        step(t + 6, 2, 1);
+        if (t + 7 >= steps) break;
+        step(t + 7, 3, 1);
+        if (t + 8 >= steps) break;
+      }
     }
-
+    ring = (ring + steps) & 3;
+    wait_lgkm0();
+    if (!C::WORDS || !loaded) {
+      wait_vmcnt<0>();
+      barrier();  // the stages are free
+      // the next tile's first loads go out before this one's results
+      set_lane();
+      if (id < total) {
+        set_tile();
+        first_loads();
+      }
+    }
     // ---- results: a lane holds, of one m, four consecutive n out of every eight.  A wave takes PIECE rows at a time
     // through its share of the last stage, in 16-byte chunks swizzled by row, and stores whole rows of its WN columns,
     // past the caches where chunks are aligned: what a product leaves is larger than they are, or read elsewhere. ----
-    ESG_LDS char* const out = lds + 3 * C::STAGE + w * (PIECE * NCH * 16);
+    ESG_LDS char* const out = lds + (C::WORDS ? (ring + 3) & 3 : 3) * C::STAGE + w * (PIECE * NCH * 16);
     const int row = lr % PIECE;
 #pragma unroll
     for (int j = 0; j < C::FM; ++j)
@@ -718,7 +778,10 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
         }
         wait_lgkm0();  // read before the next rows are written
       }
-    if (id >= total) return;
+    if (id >= total) {
+      wait_vmcnt<0>();  // loads past the last tile, of zeros, have reached this workgroup's LDS
+      return;
+    }
   }
 }
 

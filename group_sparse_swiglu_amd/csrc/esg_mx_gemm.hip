@@ -786,37 +786,51 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
 }
 
 // The exponents of a and b as words, [ceil(K/128)][rows]: word (t, r) holds those of elements 128 t .. 128 t + 127 of row
-// r, zeros past K.  A thread takes four words of a row; a's rows in the order of y's (zeros for rows[] outside a).
+// r, zeros past K.  A thread takes 64 bytes of a row, from any address on; a's rows in the order of y's (zeros for rows[] outside a).
 struct WordsSide {
   const uint8_t* scale;
   const int32_t* index;  // or NULL
   uint32_t* out;
   int rows, src_rows;
 };
+constexpr int kWordLoads = 4;  // 16 bytes each
 __global__ __launch_bounds__(256) void mx_words_kernel(WordsSide a, WordsSide b, unsigned a_blocks, int KS) {
   const bool second = blockIdx.x >= a_blocks;
   const WordsSide& g = second ? b : a;
   const unsigned block = second ? blockIdx.x - a_blocks : blockIdx.x;
-  const int words = (KS + 3) / 4, quads = (words + 3) / 4;
-  const unsigned chunk = block / quads;
-  const int t0 = (int)(block - chunk * quads) * 4;
+  const int words = (KS + 3) / 4, pieces = (words + 4 * kWordLoads - 1) / (4 * kWordLoads);
+  const unsigned chunk = block / pieces;
+  const int t0 = (int)(block - chunk * pieces) * 4 * kWordLoads;
   const int r = (int)chunk * 256 + (int)threadIdx.x;
   if (r >= g.rows) return;
   const int src = g.index != nullptr ? g.index[r] : r;
   const bool in = (unsigned)src < (unsigned)g.src_rows;
   const uint8_t* p = g.scale + (size_t)(in ? src : 0) * KS + t0 * 4;
-  const int left = KS - t0 * 4;  // bytes of the row from t0 on
+  const int left = in ? KS - t0 * 4 : 0;  // bytes of the row from t0 on
+  typedef u32x4_t piece_t __attribute__((aligned(1)));
+  typedef uint32_t word_t __attribute__((aligned(1)));
+  u32x4_t v[kWordLoads];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (t0 + j >= words) break;
-    uint32_t v = 0;
-    if (in && (((uintptr_t)g.scale | KS) & 3) == 0) {
-      v = *(const uint32_t*)(p + j * 4);
-    } else if (in) {
-      for (int e = 0; e < 4; ++e) v |= j * 4 + e < left ? (uint32_t)p[j * 4 + e] << (8 * e) : 0u;
+  for (int i = 0; i < kWordLoads; ++i) {
+    v[i] = u32x4_t{0, 0, 0, 0};
+    if (left >= 16 * (i + 1)) {
+      v[i] = *(const piece_t*)(p + 16 * i);
+    } else if (left > 16 * i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = 16 * i + 4 * j;
+        if (at + 4 <= left) {
+          v[i][j] = *(const word_t*)(p + at);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 3; ++e) v[i][j] |= at + e < left ? (uint32_t)p[at + e] << (8 * e) : 0u;
+        }
+      }
     }
-    g.out[(size_t)(t0 + j) * g.rows + r] = v;
   }
+#pragma unroll
+  for (int j = 0; j < 4 * kWordLoads; ++j)
+    if (t0 + j < words) g.out[(size_t)(t0 + j) * g.rows + r] = v[j / 4][j % 4];
 }
 
 // y = sum of the parts, in their order.  V elements of a thread.
@@ -961,9 +975,9 @@ hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
     return hipGetLastError();
   }
   if constexpr (OUT != OUT_PARTS) if (p.tile == 256) {
-    const int KS = g.K / 32, quads = ((g.K + 127) / 128 + 3) / 4;
+    const int KS = g.K / 32, pieces = ((g.K + 127) / 128 + 4 * kWordLoads - 1) / (4 * kWordLoads);
     const WordsSide a{g.sa, g.rows, (uint32_t*)g.ta, g.M, g.a_rows}, b{g.sb, nullptr, (uint32_t*)g.tb, g.E * g.N, g.E * g.N};
-    const unsigned na = (unsigned)((a.rows + 255) / 256) * quads, nb = (unsigned)((b.rows + 255) / 256) * quads;
+    const unsigned na = (unsigned)((a.rows + 255) / 256) * pieces, nb = (unsigned)((b.rows + 255) / 256) * pieces;
     LaunchTimer timer("mx_words", stream);
     hipLaunchKernelGGL(mx_words_kernel, dim3(na + nb), dim3(256), 0, stream, a, b, na, KS);
     const hipError_t e = hipGetLastError();

@@ -911,10 +911,10 @@ Plan plan(const MxArgs& g) {
     return p;
   }
   // Tiles in rounds of one for each CU: a round of 256 x 256 takes as long as three of 128 x 128, two of which run side by
-  // side (us, 256 / 128, K = 2048: 4096 x 4096, 1 and 4 rounds, 28 / 40; 3000 x 5504, 2 and 5, 42 / 36; 4096 x 5504, 2
-  // and 6, 41 / 44; 32768 x 5504, 11 and 43, 272 / 335).  By expert half a tile of rows is expected to stay empty, and a
-  // tie goes to the small ones (64 experts, N = 2816: 3000 tokens, 6 of 64, 5 and 15, 130 / 130; 8192, 10 and 36, 234 /
-  // 352; 32 experts, N = 2048, 2500 tokens, 4 of 32, 2 and 6, 62 / 52).
+  // side (us, 256 / 128, K = 2048: 4096 x 4096, 1 and 4 rounds, 30 / 36; 3000 x 5504, 2 and 5, 40 / 35; 4096 x 5504, 2
+  // and 6, 42 / 43; 32768 x 5504, 11 and 43, 272 / 335).  By expert half a tile of rows is expected to stay empty, and a
+  // tie goes to the small ones (N = 2048, 2500 tokens, 4 of 32, 2 and 6, 59 / 51; N = 2816, 2700 tokens, 6 of 64, 5 and
+  // 14, 113 / 120; 3000, 5 and 15, 114 / 125; 8192, 10 and 36, 222 / 350).
   auto rounds = [&](int tile) {
     const long long m = (g.M + tile - 1) / tile + (g.grouped ? std::min(g.E, g.M) / 2 : 0);
     return (m * ((g.N + tile - 1) / tile) + kNominalCUs - 1) / kNominalCUs;

@@ -249,3 +249,22 @@ def test_shapes_reach_every_kernel():
     # K in parts: few rows and tiles
     assert size(64, 512, 16384) == 8 * 64 * 512 * 4 and size(300, 1024, 8192) % (300 * 1024 * 4) == 0 < size(300, 1024, 8192)
     assert all(size(*s) > 0 for s in SHAPES[-6:])
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 96), (900, 1700, 160), (2500, 5504, 160)])
+def test_exponents_at_the_ends(M, N, K):
+    """2^-127 on one side, 2^127 on the other; the largest sums leave float32's range and are infinite."""
+    require_gpu()
+    note(f"mx matmul end exponents {M}x{N}x{K}")
+    a, b = _operand(M, K, 1, 2), _operand(N, K, 2, 2)
+    g = torch.Generator().manual_seed(3)
+    a[1].copy_(torch.randint(0, 3, a[1].shape, generator=g))
+    b[1].copy_(torch.randint(252, 255, b[1].shape, generator=g))
+    av, bv = _vals(*a), _vals(*b)
+    d = [t.to(DEV) for t in (*a, *b)]
+    _close(E.mxfp4_matmul(*d, out_dtype=F32), av @ bv.t(), av.abs() @ bv.abs().t(), K, F32)
+    a[1][0] = 250
+    y = E.mxfp4_matmul(*(t.to(DEV) for t in (*a, *b)), out_dtype=F32).cpu()
+    want = _vals(*a)[:1] @ bv.t()
+    over = want.abs() > 2.0 ** 130
+    assert over.any() and not torch.isfinite(y[:1][over]).any() and torch.isfinite(y[1:]).all()

@@ -910,23 +910,26 @@ Plan plan(const MxArgs& g) {
     split((g.K + kFewK - 1) / kFewK, 8, 2560 / (16 + std::min(g.M, kFewRows)));
     return p;
   }
-  // Tiles in rounds of one for each CU: a round of 256 x 256 takes as long as three of 128 x 128, two of which run side by
-  // side (us, 256 / 128, K = 2048: 4096 x 4096, 1 and 4 rounds, 30 / 36; 3000 x 5504, 2 and 5, 40 / 35; 4096 x 5504, 2
-  // and 6, 42 / 43; 32768 x 5504, 11 and 43, 272 / 335).  By expert half a tile of rows is expected to stay empty, and a
-  // tie goes to the small ones (N = 2048, 2500 tokens, 4 of 32, 2 and 6, 59 / 51; N = 2816, 2700 tokens, 6 of 64, 5 and
-  // 14, 113 / 120; 3000, 5 and 15, 114 / 125; 8192, 10 and 36, 222 / 350).
+  // Tiles, by the microseconds of each size: rounds of a tile for each CU, a round by its steps and the way between tiles
+  // (of the small ones, two of which run side by side, half of it; a quarter more where rows of exponents start inside
+  // dwords), and the words' launch before the large.  By expert half a tile of rows is expected to stay empty.  Measured,
+  // 256 / 128: 4096 x 4096 x 2048, 1 and 4 rounds, 30 / 36; x 512 16.4 / 15; 3000 x 5504 x 2048, 2 and 5, 40 / 35; 4096 x
+  // 5504 x 2048, 2 and 6, 42 / 43; 32768 x 5504 x 2048, 11 and 43, 272 / 335; by expert 2500 tokens, 4 of 32, 2048 x 2048,
+  // 2 and 6, 59 / 51; 3000, 6 of 64, 2816 x 2048, 5 and 15, 114 / 125; 3006, 5 of 27, 1116 x 3808, 2 and 5, 76 / 98.
+  const int steps = (g.K + 127) / 128;
   auto rounds = [&](int tile) {
     const long long m = (g.M + tile - 1) / tile + (g.grouped ? std::min(g.E, g.M) / 2 : 0);
-    return (m * ((g.N + tile - 1) / tile) + kNominalCUs - 1) / kNominalCUs;
+    return (double)((m * ((g.N + tile - 1) / tile) + kNominalCUs - 1) / kNominalCUs);
   };
+  const double large = rounds(256) * (3. + steps) + 5., small = rounds(128) * (1.5 + steps * (g.K % 128 != 0 ? 0.45 : 0.36));
   // words of exponents within 32-bit offsets
   const bool near = std::max<long long>(g.M, (long long)g.E * g.N) * ((g.K + 127) / 128) < (1 << 29);
-  p.tile = near && 3 * rounds(256) < rounds(128) + !g.grouped ? 256 : 128;
+  p.tile = near && large < small ? 256 : 128;
   p.nm = (int)chunks(g, p.tile);
   p.nn = (g.N + p.tile - 1) / p.tile;
   // a step takes 0.28 us (us, whole / parts: 300 x 1024 x 16384 40.7 / 17.2, 1000 x 512 x 8192 23.2 / 17.5; 1024 x 1024 x
   // 4096 14.8 / 18.1)
-  if (p.tile == 128) split((g.K + 127) / 128, 16, 40);
+  if (p.tile == 128) split(steps, 16, 40);
   return p;
 }
 

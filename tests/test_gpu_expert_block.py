@@ -232,7 +232,8 @@ def test_streams_share_a_dict():
 def test_a_graph_keeps_its_scratch_while_the_dict_grows():
     require_gpu()
     note("4-bit product: graph beside a growing dict")
-    ops = [(E.mxfp4_quantize(_input(M, K, M)[0]), E.mxfp4_quantize(_input(4096, K, K)[0])) for M, K in ((4096, 256), (6000, 1056))]
+    ops = [(E.mxfp4_quantize(_input(M, K, M)[0]), E.mxfp4_quantize(_input(4096, K, K)[0])) for M, K in ((4096, 1056), (6000, 2080))]
+    assert all(E.mxfp4_matmul_workspace_size(M, 4096, K) > 0 for M, K in ((4096, 1056), (6000, 2080)))
     want = [E.mxfp4_matmul(*a, *b) for a, b in ops]
     cache = {}
     small = lambda: E.mxfp4_matmul(*ops[0][0], *ops[0][1], workspace=cache)  # noqa: E731

@@ -166,7 +166,7 @@ def prepare(case, seed):
     rows = (order.indices // k).int()                       # token of each sorted row
     offsets = torch.searchsorted(order.values, torch.arange(E + 1, device=DEV)).int()
     cap = int((offsets[1:] - offsets[:-1]).max())
-    return dict(case=case, a=a, sa=sa, b=b, sb=sb, rows=rows, offsets=offsets, cap=cap)
+    return dict(case=case, a=a, sa=sa, b=b, sb=sb, rows=rows, offsets=offsets, cap=cap, workspace={})
 
 
 # -------------------------------------------------------------- plain forms
@@ -309,7 +309,7 @@ def run(s):
     if op == "matmul":
         return E.mxfp4_matmul(s["a"], s["sa"], s["b"], s["sb"], out_dtype=TYPES[c["out"]], workspace=s["workspace"])
     return E.mxfp4_grouped_matmul(s["a"], s["sa"], s["b"], s["sb"], s["offsets"], rows=s["rows"],
-                                  out_dtype=TYPES[c["out"]])
+                                  out_dtype=TYPES[c["out"]], workspace=s["workspace"])
 
 
 def work(case):

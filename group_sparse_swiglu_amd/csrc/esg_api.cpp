@@ -824,8 +824,10 @@ int mx_shape(int M, int N, int K, int experts) {
   const long long few = ((N + 15) / 16) * (2ll * experts + 1);  // workgroups of at most 512 threads
   return tiles >= (1 << 23) || few >= (1 << 23) ? ESG_ERR_UNSUPPORTED : ESG_OK;
 }
-int mx_operands(const void* a, const void* a_scale, const void* b, const void* b_scale, int out_dtype, const void* y) {
-  if (a == nullptr || a_scale == nullptr || b == nullptr || b_scale == nullptr || y == nullptr) return ESG_ERR_INVALID_ARG;
+int mx_operands(const void* a, const void* a_scale, int a_rows, const void* b, const void* b_scale, int out_dtype,
+                const void* y) {
+  if (a_rows > 0 && (a == nullptr || a_scale == nullptr)) return ESG_ERR_INVALID_ARG;  // no rows: neither is read
+  if (b == nullptr || b_scale == nullptr || y == nullptr) return ESG_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(b) || !aligned16(y)) return ESG_ERR_INVALID_ARG;
   return float_dtype(out_dtype) ? ESG_OK : ESG_ERR_UNSUPPORTED;
 }
@@ -862,7 +864,7 @@ int esg_mxfp4_matmul(const void* a, const void* a_scale, const void* b, const vo
   int e = mx_shape(M, N, K, 1);
   if (e != ESG_OK) return e;
   if (M == 0 || N == 0) return float_dtype(out_dtype) ? ESG_OK : ESG_ERR_UNSUPPORTED;
-  e = mx_operands(a, a_scale, b, b_scale, out_dtype, y);
+  e = mx_operands(a, a_scale, M, b, b_scale, out_dtype, y);
   if (e != ESG_OK) return e;
   return mx_launch(MxMatmul{a, a_scale, b, b_scale, 0, nullptr, nullptr, out_dtype, M, M, N, K, 1, y, workspace},
                    workspace_bytes, stream);
@@ -884,7 +886,7 @@ int esg_mxfp4_grouped_matmul(const void* a, const void* a_scale, int a_rows, con
   if (a_rows < 0 || (rows == nullptr && a_rows < M)) return ESG_ERR_INVALID_ARG;
   if (rows != nullptr && (long long)a_rows * (K / 2) >= (1ll << 31)) return ESG_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return float_dtype(out_dtype) ? ESG_OK : ESG_ERR_UNSUPPORTED;
-  e = mx_operands(a, a_scale, b, b_scale, out_dtype, y);
+  e = mx_operands(a, a_scale, a_rows, b, b_scale, out_dtype, y);
   if (e != ESG_OK) return e;
   if (offsets == nullptr || (((uintptr_t)offsets | (uintptr_t)rows) & 3u) != 0) return ESG_ERR_INVALID_ARG;
   return mx_launch(MxMatmul{a, a_scale, b, b_scale, 1, offsets, rows, out_dtype, a_rows, M, N, K, experts, y, workspace},

@@ -440,7 +440,8 @@ __global__ __launch_bounds__((Tile<BM, BN>::NTH), 2) void mx_tile_kernel(MxArgs 
     const int nrows = min(BN, g.N - n0);
     const size_t b0 = (size_t)s.e * g.N + n0;
     rb = make_dma_src(g.b + b0 * KH, (uint32_t)(nrows * KH));
-    ra = gather ? make_dma_src(g.a, (uint32_t)g.a_rows * (uint32_t)KH)
+    // (a without rows: the bytes of one, for soff; none is read)
+    ra = gather ? make_dma_src(g.a, (uint32_t)max(g.a_rows, 1) * (uint32_t)KH)
                 : make_dma_src(g.a + (size_t)s.m0 * KH, (uint32_t)(mrows * KH));
     auto a_row = [&](int i) __attribute__((always_inline)) {
       if (i >= mrows) return -1;

@@ -601,7 +601,8 @@ int esg_mxfp4_dequant(const void* q, const void* scale, int dtype, int64_t rows,
  * esg_bucket_by_group): rows offsets[e] .. offsets[e+1] - 1 of y take b[e].  rows
  * (device int32 [M], or NULL): row m is row rows[m] of a [a_rows, K/2] instead of row m
  * (perm_token of esg_bucket_by_group: the tokens need no copy in the experts' order); an
- * index outside 0 .. a_rows - 1 is a row of zeros.  Rows of y before offsets[0] and from
+ * index outside 0 .. a_rows - 1 is a row of zeros (a_rows == 0: all of them, and a and
+ * a_scale may be NULL).  Rows of y before offsets[0] and from
  * offsets[experts] on are left as they were.  Offsets are taken into 0 .. M; where they
  * descend, which b the rows between take is not specified.
  * Errors: ESG_ERR_INVALID_ARG (null pointer, a, b, y or workspace not 16-byte aligned,

@@ -902,9 +902,7 @@ def rms_norm_bwd(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspace: 
 
 
 def _rms_norm_bwd(dy, h, weight, rstd, dh, need_dw, T, d, code, w_code, need, dev, workspace=None):
-    # The backward's thread sleeps between calls and wakes wherever there is room, far from what the forward left in its
-    # caches: what is known to hold is not looked at again there (333 x 768 f32, both directions: 95 -> 75 us).
-    dx = torch.empty_like(h)
+    dx = torch.empty_like(h, memory_format=torch.contiguous_format)
     dw = ws = None
     if need_dw:
         dw = torch.empty_like(weight)
@@ -925,6 +923,14 @@ def _whole(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+def _kept(t, dtype, gpu, numel, name):
+    """t, which the backward is given: hooks on saved tensors and on nodes may have put another in its place."""
+    if t.dtype != dtype or t.get_device() != gpu or t.numel() != numel:
+        raise EsgError(f"{name} of the backward must be {dtype} as in the forward, with {numel} elements on the same device; "
+                       f"it is {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(fctx, x, weight, residual, eps):
@@ -934,6 +940,7 @@ class _RmsNorm(torch.autograd.Function):
         fctx.set_materialize_grads(False)
         T, d = rstd.shape[0], weight.shape[0]
         fctx.esg = (T, d, _dtype_code(h), _dtype_code(weight), rms_norm_bwd_workspace_size(T, d), h.device)
+        fctx.kinds = (h.dtype, weight.dtype, h.get_device())
         return y if residual is None else (y, h)
 
     def backward(fctx, dy, dh=None):
@@ -943,9 +950,13 @@ class _RmsNorm(torch.autograd.Function):
         need_x, need_w, need_r, _ = fctx.needs_input_grad
         if dy is None:  # only the new residual was used
             return dh if need_x else None, None, dh if need_r else None, None
+        dtype, w_dtype, gpu = fctx.kinds
+        T, d = fctx.esg[:2]
         if dh is not None:
-            dh = _whole(dh)
-        dx, dw = _rms_norm_bwd(_whole(dy), h, weight, rstd, dh, need_w, *fctx.esg)
+            dh = _kept(dh, dtype, gpu, T * d, "dh")
+        dx, dw = _rms_norm_bwd(_kept(dy, dtype, gpu, T * d, "dy"), _kept(h, dtype, gpu, T * d, "h"),
+                               _kept(weight, w_dtype, gpu, d, "weight"), _kept(rstd, torch.float32, gpu, T, "rstd"), dh,
+                               need_w, *fctx.esg)
         return dx if need_x else None, dw, dx if need_r else None, None
 
     once = staticmethod(torch.autograd.function.once_differentiable(backward))
@@ -1057,7 +1068,7 @@ def topk_routing_bwd(dprobs, logits, indices, scoring: str = "softmax", normaliz
 
 
 def _topk_routing_bwd(dprobs, logits, indices, dev, code, T, E, topk, scoring, normalize, scaling):
-    dz = torch.empty_like(logits)
+    dz = torch.empty_like(logits, memory_format=torch.contiguous_format)
     status = lib().esg_topk_routing_bwd(dprobs.data_ptr(), logits.data_ptr(), code, indices.data_ptr(), T, E, topk, scoring,
                                         normalize, scaling, dz.data_ptr(), _stream(dev))
     if status:
@@ -1074,6 +1085,7 @@ class _TopkRouting(torch.autograd.Function):
         fctx.save_for_backward(logits, indices)
         fctx.esg = (logits.device, _dtype_code(logits), *logits.shape, topk, _scoring_code(scoring), int(normalize),
                     1.0 if scaling_factor is None else float(scaling_factor))
+        fctx.kinds = (logits.dtype, logits.get_device())
         fctx.mark_non_differentiable(indices)
         return probs, indices
 
@@ -1081,7 +1093,12 @@ class _TopkRouting(torch.autograd.Function):
         if torch.is_grad_enabled():
             return _TopkRouting.once(fctx, dprobs, _)
         logits, indices = fctx.saved_tensors
-        return _topk_routing_bwd(dprobs.contiguous(), logits, indices, *fctx.esg), None, None, None, None, None, None, None
+        dtype, gpu = fctx.kinds
+        T, experts, topk = fctx.esg[2:5]
+        dz = _topk_routing_bwd(_kept(dprobs, torch.float32, gpu, T * topk, "dprobs"),
+                               _kept(logits, dtype, gpu, T * experts, "logits"),
+                               _kept(indices, torch.int32, gpu, T * topk, "indices"), *fctx.esg)
+        return dz, None, None, None, None, None, None, None
 
     once = staticmethod(torch.autograd.function.once_differentiable(backward))
     backward = staticmethod(backward)

@@ -22,3 +22,79 @@ def test_products_by_expert_of_no_rows():
     assert call(R=0, a=NULL, sa=NULL) == 3 and call(R=0) == 3
     assert call(a=NULL) == 1 and call(sa=NULL) == 1
     assert call(R=0, rows=NULL) == 1 and call(R=0, a=P + 8) == 1
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """The autograd paths on CPU tensors, the launches stood in for: name -> arguments, and what lay at the inputs' addresses."""
+    seen, real, dev = [], E.lib(), E._dev
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith(("_size", "_string")):
+                return getattr(real, name)
+
+            def launch(*args):
+                if name == "esg_rms_norm_bwd":
+                    dy, dh, h, w, rstd, code, w_code, T, d = args[:9]
+                    read = {k: ctypes.string_at(p, n * (4 if c == 0 else 2)) for k, p, n, c in
+                            (("dy", dy, T * d, code), ("h", h, T * d, code), ("weight", w, d, w_code))}
+                    seen.append({**read, "code": code, "rstd": ctypes.string_at(rstd, 4 * T)})
+                if name == "esg_topk_routing_bwd":
+                    dp, z, code, idx, T, n, k = args[:7]
+                    seen.append(dict(dprobs=ctypes.string_at(dp, 4 * T * k), indices=ctypes.string_at(idx, 4 * T * k),
+                                     logits=ctypes.string_at(z, T * n * (4 if code == 0 else 2)), code=code))
+                return 0
+
+            return launch
+
+    monkeypatch.setattr(E, "lib", Lib)
+    monkeypatch.setattr(E, "_stream", lambda dev: 0)
+    monkeypatch.setattr(E, "_dev", lambda t, name, dtype=None, on=None: None if t is None else dev(
+        t, name, dtype, t.get_device() if on is None else on))
+    return seen
+
+
+def _bytes(t):
+    return t.detach().contiguous().view(torch.uint8).numpy().tobytes()
+
+
+def _strided(t):
+    """t's values, every other element of a larger buffer."""
+    return torch.stack((t, t), -1)[..., 0] if t.dim() else t
+
+
+def _through(hook):
+    return torch.autograd.graph.saved_tensors_hooks(lambda t: t.detach().clone(), hook)
+
+
+def test_saved_tensors_may_come_back_strided(launches):
+    x, w = torch.randn(5, 64).bfloat16().requires_grad_(), torch.randn(64, requires_grad=True)
+    with _through(_strided):
+        y = E.rms_norm(x, w)
+    torch.autograd.grad(y, (x, w), torch.ones_like(y))
+    assert launches[-1]["h"] == _bytes(x) and launches[-1]["weight"] == _bytes(w)
+    z = torch.randn(5, 16).bfloat16().requires_grad_()
+    with _through(_strided):
+        p, idx = E.topk_routing(z, 2)
+        kept = idx.clone()
+    torch.autograd.grad(p, z, torch.ones_like(p))
+    assert launches[-1]["logits"] == _bytes(z) and launches[-1]["indices"] == _bytes(kept)
+
+
+def test_saved_tensors_of_another_kind_are_refused(launches):
+    for widen in (lambda t: t.float() if t.dtype == torch.bfloat16 else t, lambda t: t[:, :-16] if t.dim() == 2 else t):
+        x, w = torch.randn(5, 64).bfloat16().requires_grad_(), torch.randn(64, requires_grad=True)
+        with _through(widen):
+            y = E.rms_norm(x, w)
+        with pytest.raises(E.EsgError, match="h of the backward"):
+            torch.autograd.grad(y, (x, w), torch.ones_like(y))
+        z = torch.randn(5, 32).bfloat16().requires_grad_()
+        with _through(lambda t: widen(t) if t.dtype == torch.bfloat16 else t):
+            p, _ = E.topk_routing(z, 2)
+        with pytest.raises(E.EsgError, match="logits of the backward"):
+            torch.autograd.grad(p, z, torch.ones_like(p))
+    assert not launches
+    for bad in (dict(dtype=torch.float32), dict(gpu=1), dict(numel=7)):
+        with pytest.raises(E.EsgError, match="here of the backward"):
+            E._kept(torch.zeros(8).bfloat16(), **{**dict(dtype=torch.bfloat16, gpu=-1, numel=8, name="here"), **bad})

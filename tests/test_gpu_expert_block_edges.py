@@ -24,3 +24,28 @@ def test_products_by_expert_of_no_rows(M, N, K):
     a, sa = torch.empty(0, K // 2, dtype=U8, device=DEV), torch.empty(0, K // 32, dtype=U8, device=DEV)
     E.mxfp4_grouped_matmul(a, sa, b, sb, offsets, rows=rows, out=out)
     assert not out[:M - 2].any() and (out[M - 2:] == 5).all()
+
+
+def test_gradients_through_saved_tensor_hooks():
+    """Tensors saved on the host, or given back strided: the same gradients; of another type or device: refused."""
+    require_gpu()
+    note("norm and routing through saved-tensor hooks")
+    hooks = torch.autograd.graph.saved_tensors_hooks
+    x, r, w, z = (torch.randn(*s, device=DEV).to(t).requires_grad_() for s, t in (((37, 528), BF), ((37, 528), BF), ((528,), F32), ((37, 43), BF)))
+
+    def gradients():
+        y, h = E.rms_norm(x, w, r)
+        p, _ = E.topk_routing(z, 5)
+        gy, gp = (torch.arange(t.numel(), device=DEV).remainder(7).to(t.dtype).view(t.shape) - 3 for t in (y, p))
+        return lambda: (*torch.autograd.grad((y, h), (x, r, w), (gy, gy)), *torch.autograd.grad(p, z, gp))
+
+    want = gradients()()
+    for pack, unpack in ((lambda t: t.cpu(), lambda t: t.to(DEV)), (lambda t: t.clone(), lambda t: torch.stack((t, t), -1)[..., 0])):
+        with hooks(pack, unpack):
+            again = gradients()
+        assert all(torch.equal(a, b) for a, b in zip(again(), want))
+    for unpack in (lambda t: t, lambda t: t.to(DEV).double()):
+        with hooks(lambda t: t.cpu(), unpack):
+            again = gradients()
+        with pytest.raises(E.EsgError, match="of the backward"):
+            again()

@@ -29,6 +29,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 __all__ = [
     "ESG_F32", "ESG_BF16", "EsgError", "lib", "library_path", "make_subsample_index", "grouped_topk_select",
@@ -712,6 +713,11 @@ def _rows(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+def _dual() -> bool:
+    """Whether forward-mode gradients are in use: the way past an autograd function would drop a tangent, which the function refuses."""
+    return forward_ad._current_level >= 0
+
+
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     def forward(fctx, x, w):
@@ -741,7 +747,7 @@ def fp8_linear(x, w):
         raise EsgError("x must be [..., K] and w [N, K]")
     if w.shape[0] % 16 or w.shape[1] % 16:
         raise EsgError("both dimensions of w must be multiples of 16")
-    if not torch.is_grad_enabled():  # the function's needs_input_grad reports requires_grad here too
+    if not torch.is_grad_enabled() and not _dual():  # the function's needs_input_grad reports requires_grad here too
         y, _ = fp8_linear_fwd(_rows(x), _rows(w), False, False)
         return y.view(*x.shape[:-1], w.shape[0])
     return _Fp8Linear.apply(x, w)
@@ -969,7 +975,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6):
     h = x + residual (rounded to their dtype), y = h (mean h^2 + eps)^-1/2 weight -> y,
     or (y, h) with a residual: h is the new one.  x, residual: [..., d], float32 or
     bfloat16, d a multiple of 16, at most 16384; weight: [d], float32 or bfloat16."""
-    if not torch.is_grad_enabled():
+    if not torch.is_grad_enabled() and not _dual():
         y, h, _ = rms_norm_fwd(_whole(x), _whole(weight), None if residual is None else _whole(residual), eps, False)
         return y if residual is None else (y, h)
     return _RmsNorm.apply(x, weight, residual, eps)
@@ -1114,7 +1120,7 @@ def topk_routing(logits, topk: int, scoring: str = "softmax", expert_bias=None, 
     (``scoring`` "softmax" or "sigmoid"), divided by their sum with ``normalize`` and times
     ``scaling_factor``.  expert_bias: float32 [E] (a strided view is accepted), for the
     choice only.  The gradient goes through the weights to the logits."""
-    if not torch.is_grad_enabled() or not logits.requires_grad:
+    if not (torch.is_grad_enabled() and logits.requires_grad or _dual()):
         return topk_routing_fwd(logits.contiguous(), topk, scoring, expert_bias, groups, topk_groups, normalize,
                                 scaling_factor)
     return _TopkRouting.apply(logits, topk, scoring, expert_bias, groups, topk_groups, normalize, scaling_factor)

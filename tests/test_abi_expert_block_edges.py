@@ -98,3 +98,17 @@ def test_saved_tensors_of_another_kind_are_refused(launches):
     for bad in (dict(dtype=torch.float32), dict(gpu=1), dict(numel=7)):
         with pytest.raises(E.EsgError, match="here of the backward"):
             E._kept(torch.zeros(8).bfloat16(), **{**dict(dtype=torch.bfloat16, gpu=-1, numel=8, name="here"), **bad})
+
+
+def test_tangents_are_not_dropped(launches):
+    """The operators have no forward-mode gradient: a dual tensor is refused, whatever asks for reverse ones."""
+    x, w, z = torch.randn(5, 64), torch.randn(64), torch.randn(5, 16)
+    calls = {"x": lambda t: E.rms_norm(t, w), "w": lambda t: E.rms_norm(x, t), "r": lambda t: E.rms_norm(x, w, t),
+             "z": lambda t: E.topk_routing(t, 2), "l": lambda t: E.fp8_linear(t, torch.randn(32, 64))}
+    arg = {"x": x, "w": w, "r": x, "z": z, "l": x}
+    for grad in (False, True):
+        with torch.set_grad_enabled(grad), torch.autograd.forward_ad.dual_level():
+            for name, call in calls.items():
+                with pytest.raises(NotImplementedError, match="jvp"):
+                    call(torch.autograd.forward_ad.make_dual(arg[name], torch.ones_like(arg[name])))
+                call(arg[name])                            # without a tangent as ever

@@ -495,10 +495,13 @@ __global__ __launch_bounds__(kThreads) void topk_routing_bwd_kernel(RouteBwdArgs
   const T* const lrow = (const T*)g.logits + (live ? row : 0) * g.experts;
   const int n = live ? min(max(g.experts - l * C, 0), C) : 0;
   float base[C], top = 0.f, inv = 0.f;
+  // both kinds of scores read the whole row: a logit that made its weights NaN makes its gradient NaN
+  load_logits<C>(lrow + (n > 0 ? l * C : 0), n, g.vec && n == C, base);
+  uint32_t bad = 0;
 #pragma unroll
-  for (int c = 0; c < C; ++c) base[c] = 0.f;
+  for (int c = 0; c < C; ++c) bad |= base[c] != base[c] || (scoring == SOFTMAX && base[c] == INFINITY);
+  bad = row_reduce<LPR>(bad, Or{});
   if (scoring == SOFTMAX) {
-    load_logits<C>(lrow + (n > 0 ? l * C : 0), n, g.vec && n == C, base);
     top = -INFINITY;
 #pragma unroll
     for (int c = 0; c < C; ++c) top = c < n ? fmaxf(top, base[c]) : top;
@@ -533,12 +536,12 @@ __global__ __launch_bounds__(kThreads) void topk_routing_bwd_kernel(RouteBwdArgs
   gs = row_reduce<LPR>(gs, Add{});
   const float total = sum + 1e-20f;
   // gradient of a chosen score: a (dp - m); dot = sum of s ds
-  const float a = g.normalize ? g.scaling / total : g.scaling;
+  const float a = bad ? NAN : g.normalize ? g.scaling / total : g.scaling;
   const float m = g.normalize ? gs / total : 0.f;
   float dot = 0.f;  // with the weights normalised, total - sum being 1e-20, what that leaves of it
   if (scoring == SOFTMAX) dot = g.normalize ? a * m * 1e-20f : a * gs;
 #pragma unroll
-  for (int c = 0; c < C; ++c) base[c] = scoring == SOFTMAX ? -(base[c] * inv) * dot : 0.f;
+  for (int c = 0; c < C; ++c) base[c] = bad ? NAN : scoring == SOFTMAX ? -(base[c] * inv) * dot : 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) buf[l * C + c] = base[c];
   wave_lds_sync();

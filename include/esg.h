@@ -544,6 +544,7 @@ int esg_rms_norm_bwd(const void* dy, const void* dh, const void* h, const void* 
  * dL/dprobs (float, like probs) and the forward's indices.  The choice has no gradient,
  * the bias none either.  With ds_j the gradient of a chosen score: sigmoid dz_j = ds_j
  * s_j (1 - s_j), 0 for the others; softmax dz_e = s_e (ds_e - sum over j of s_j ds_j).
+ * A row whose probs are NaN for a logit of it has NaN for all of its dlogits.
  * An index outside 0..num_experts-1 is skipped; the indices of a row have to differ.
  *
  * esg_topk_routing_supported returns 1 when 1 <= topk <= 32, topk_groups is in

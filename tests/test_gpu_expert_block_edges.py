@@ -49,3 +49,30 @@ def test_gradients_through_saved_tensor_hooks():
             again = gradients()
         with pytest.raises(E.EsgError, match="of the backward"):
             again()
+
+
+@pytest.mark.parametrize("Ex,k", [(40, 4), (256, 8), (43, 20), (1000, 5)])
+def test_routing_gradient_of_non_finite_rows(Ex, k):
+    """A logit that makes its row's weights NaN makes all of the row's gradient NaN, whatever dprobs are; no other row's."""
+    require_gpu()
+    for dtype in (F32, BF):
+        for scoring in ("softmax", "sigmoid"):
+            for normalize in (True, False):
+                note(f"route backward non-finite {Ex} {k} {dtype} {scoring} {normalize}")
+                z = torch.randn(7, Ex, generator=torch.Generator().manual_seed(Ex)).to(dtype)
+                clean = z.clone()
+                z[1, 3] = float("nan")
+                z[2, Ex - 1] = float("inf")
+                z[3] = float("nan")
+                z[4, k:] = float("-inf")
+                z[6, 0] = float("nan")
+                bad = [1, 3, 6] + ([2] if scoring == "softmax" else [])
+                fine = [t for t in range(7) if t not in bad]
+                zd = z.to(DEV).requires_grad_()
+                p, idx = E.topk_routing(zd, k, scoring, normalize=normalize)
+                assert torch.isnan(p[bad]).all() and torch.isfinite(p[fine]).all()
+                dp = torch.randn(7, k, generator=torch.Generator().manual_seed(1)).to(DEV)
+                dz, = torch.autograd.grad(p, zd, dp)
+                assert torch.isnan(dz[bad]).all() and torch.isfinite(dz[fine]).all()
+                want = E.topk_routing_bwd(dp, clean.to(DEV), idx, scoring, normalize)
+                assert torch.equal(dz[[0, 5]], want[[0, 5]])

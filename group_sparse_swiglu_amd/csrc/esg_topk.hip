@@ -266,6 +266,7 @@ __device__ __forceinline__ typename Key<EXACT>::type threshold(const typename Ke
     if (t.b != 0) {
       const float second = K::value(t.b);
       score = score + second;
+      score = score == score ? score : INFINITY;  // +infinity (of the first) and -infinity: an expert that has to be there
       size += fabsf(second);
     }
     // rank of this lane's group: groups with a larger score, or an equal one and a lower number

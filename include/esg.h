@@ -526,8 +526,8 @@ int esg_rms_norm_bwd(const void* dy, const void* dh, const void* h, const void* 
  *   key_e = s_e + expert_bias[e * bias_stride], one fp32 addition (expert_bias NULL: s_e);
  *   the num_experts / groups experts of a group follow each other; a group's rank
  *   is by the sum of its two largest keys (one fp32 addition; its only key if it has
- *   one), and the topk_groups best ones stay, equal ones by lower group (all of them
- *   for topk_groups == groups);
+ *   one; +infinity where they are +infinity and -infinity), and the topk_groups best
+ *   ones stay, equal ones by lower group (all of them for topk_groups == groups);
  *   indices = the topk experts of these with the largest keys, equal ones by lower
  *   expert, in ascending order;
  *   probs_j = s_j / (sum of the chosen s + 1e-20) * scaling_factor with normalize, else

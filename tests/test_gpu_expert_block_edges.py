@@ -76,3 +76,31 @@ def test_routing_gradient_of_non_finite_rows(Ex, k):
                 assert torch.isnan(dz[bad]).all() and torch.isfinite(dz[fine]).all()
                 want = E.topk_routing_bwd(dp, clean.to(DEV), idx, scoring, normalize)
                 assert torch.equal(dz[[0, 5]], want[[0, 5]])
+
+
+@pytest.mark.parametrize("Ex,groups,keep,k", [(32, 4, 2, 4), (256, 8, 3, 8), (60, 6, 2, 3), (384, 6, 1, 2), (512, 32, 4, 6)])
+def test_groups_of_a_forced_and_masked_experts(Ex, groups, keep, k):
+    """A group whose largest keys are +infinity and -infinity (a NaN bias is one) counts as +infinity: it stays, before
+    finite groups and after equal ones of lower number, and no more than topk_groups stay."""
+    require_gpu()
+    per = Ex // groups
+    for scoring in ("softmax", "sigmoid"):
+        for dtype in (F32, BF):
+            for masked in (float("-inf"), float("nan")):
+                note(f"route forced and masked {Ex} {groups}/{keep} {k} {scoring} {dtype} {masked}")
+                z = torch.randn(9, Ex, generator=torch.Generator().manual_seed(Ex)).to(dtype)
+                bias = 0.1 * torch.randn(Ex, generator=torch.Generator().manual_seed(1))
+                for g in range(1, groups, 2):              # every other group, more than may stay for the larger shapes
+                    bias[g * per:(g + 1) * per] = masked
+                    bias[g * per + g % per] = float("inf")
+                _, idx = E.topk_routing(z.to(DEV), k, scoring, bias.to(DEV), groups, keep)
+                key = O.scores(f64(z), scoring).astype(np.float32) + bias.nan_to_num(nan=-np.inf, posinf=np.inf, neginf=-np.inf).numpy()
+                two = np.sort(key.reshape(9, groups, per), axis=2)[:, :, ::-1][:, :, :2]
+                with np.errstate(invalid="ignore"):
+                    rank = two[:, :, 0] + two[:, :, 1]
+                rank[np.isnan(rank)] = np.inf
+                best = np.argsort(-rank, axis=1, kind="stable")[:, :keep]
+                for t in range(9):
+                    allowed = np.concatenate([np.arange(g * per, (g + 1) * per) for g in sorted(best[t])])
+                    want = np.sort(allowed[np.argsort(-key[t, allowed], kind="stable")[:k]])
+                    assert np.array_equal(idx[t].cpu().numpy(), want)

@@ -122,15 +122,27 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs g) {
     sum = row_sum<TPR>(sum, lds[turn]);
     turn ^= 1;
     float r = 1.0f / sqrtf(sum / (float)g.d + g.eps);
+    float rstd = r;
     if (!(sum <= FLT_MAX)) {  // the squares leave the range: again from 2^-80 h (the whole row branches alike)
       sum = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j] * 0x1p-80f, v[i][j] * 0x1p-80f, sum);
-      r = 0x1p-80f / sqrtf(row_sum<TPR>(sum, lds[2]) / (float)g.d);
+      rstd = r = 0x1p-80f / sqrtf(row_sum<TPR>(sum, lds[2]) / (float)g.d + g.eps * 0x1p-80f * 0x1p-80f);
+    } else if (sum < 0x1p-100f && fabsf(g.eps) < 0x1p-100f) {  // at its other end, and eps does not cover what they lose
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] *= 0x1p100f;
+          sum = fmaf(v[i][j], v[i][j], sum);
+        }
+      r = 1.0f / sqrtf(row_sum<TPR>(sum, lds[2]) / (float)g.d + g.eps * 0x1p100f * 0x1p100f);
+      rstd = r * 0x1p100f;
     }
-    if (g.rstd != nullptr && l == 0) g.rstd[row] = r;
+    if (g.rstd != nullptr && l == 0) g.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + l) * 8;

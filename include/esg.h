@@ -489,8 +489,10 @@ int esg_fp8_linear_bwd(const void* dy, int x_dtype, int w_dtype, int tokens, int
  * NULL.  rstd (or NULL): float [tokens], r for the backward.  y may be x, and h
  * may be residual or x (buffers that overlap otherwise are not allowed).
  * The sum of squares, r and y's products are float32 (where the squares leave its
- * range, those of 2^-80 h); each output is rounded once.  A row's result does not
- * depend on the others (bitwise).
+ * range, those of 2^-80 h, or of 2^100 h where eps is below 2^-100 too); each output
+ * is rounded once.  rstd is infinite where r is past float32 (rows of less than 2^-128,
+ * with such an eps), which have no finite gradient.  A row's result does not depend on
+ * the others (bitwise).
  *
  * esg_rms_norm_quant gives the same float32 y in q_dtype instead, as the products
  * take it: ESG_E4M3, q e4m3 [tokens, d_model] with scale float [tokens,

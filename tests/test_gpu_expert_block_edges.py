@@ -104,3 +104,43 @@ def test_groups_of_a_forced_and_masked_experts(Ex, groups, keep, k):
                     allowed = np.concatenate([np.arange(g * per, (g + 1) * per) for g in sorted(best[t])])
                     want = np.sort(allowed[np.argsort(-key[t, allowed], kind="stable")[:k]])
                     assert np.array_equal(idx[t].cpu().numpy(), want)
+
+
+U = 2.0 ** -24  # one float32 rounding
+
+
+@pytest.mark.parametrize("d", [16, 144, 528, 1024, 2048, 5504, 16384])
+def test_norm_of_tiny_rows(d):
+    """Squares below float32's range and an eps that does not cover them: the bounds of the norm's other tests (45 roundings
+    of y, 225 of the sum of dx's terms), whatever the size of h; dw is not looked at where r is past float32."""
+    require_gpu()
+    g = torch.Generator().manual_seed(d)
+    size = torch.tensor([1e-16, 1e-19, 1e-22, 1e-25, 1e-30, 1e-36, 1e-42, 1.0], dtype=torch.float64)[:, None]
+    w = 1 + 0.3 * torch.randn(d, generator=g)
+    for dtype in (F32, BF):
+        x = (torch.randn(8, d, generator=g).double() * size).to(dtype)
+        half = 2.0 ** -8 if dtype == BF else U
+        for eps in (0.0, 1e-44, 1e-40, 1e-35, 1e-30, 1e-12):
+            note(f"norm of tiny rows {d} {dtype} eps={eps}")
+            e = float(torch.tensor(eps, dtype=F32))
+            with np.errstate(divide="ignore", invalid="ignore"):
+                want, r = O.rms_norm(f64(x), f64(w), e)
+            y, _, rstd = E.rms_norm_fwd(x.to(DEV), w.to(DEV), eps=eps)
+            zero = ~f64(x).any(1) & (e == 0)               # 1e-42 is zero in bf16, and 0 / 0 is NaN
+            assert np.isnan(f64(y)[zero]).all()
+            assert (np.abs(f64(y) - want) <= (half + 45 * U) * np.abs(want) + 2.0 ** -149)[~zero].all()
+            past = r[:, 0] > 2.0 ** 127.999
+            assert (np.abs(f64(rstd)[~past] - r[~past, 0]) <= 41 * U * r[~past, 0]).all() and np.isinf(f64(rstd)[past]).all()
+            q, s = E.rms_norm_quantize(x.to(DEV), w.to(DEV), eps=eps)
+            top = np.stack([np.abs(want[:, i:i + 128]).max(1) for i in range(0, d, 128)], 1)
+            big = top > 2.0 ** -90                         # below, the scale of an empty block
+            assert (np.abs(f64(s) - top / 448)[big] <= 48 * U * f64(s)[big]).all()
+            v, unit = f64(q) * np.repeat(f64(s), 128, 1)[:, :d], np.repeat(f64(s), 128, 1)[:, :d]
+            near = np.abs(v - want) <= np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10 * unit) + 100 * U * np.abs(want)
+            assert near[np.repeat(big, 128, 1)[:, :d]].all()
+            keep = r[:, 0] < 1e30
+            dy = torch.randn(8, d, generator=g).to(dtype)
+            dx, _ = E.rms_norm_bwd(dy.to(DEV), x.to(DEV), w.to(DEV), rstd)
+            with np.errstate(divide="ignore", invalid="ignore"):
+                wx, _, mx, _ = O.rms_norm_backward(f64(dy), f64(x), f64(w), e)
+            assert (np.abs(f64(dx) - wx)[keep] <= (half * np.abs(wx) + 225 * U * mx)[keep]).all()

@@ -864,7 +864,7 @@ def rms_norm_fwd(x, weight, residual=None, eps: float = 1e-6, need_rstd: bool = 
     x, residual: [..., d] and weight: [d], float32 or bfloat16.  h = x + residual is
     the new residual (x itself without one); rstd: float32 [tokens] for
     rms_norm_bwd (None without ``need_rstd``).  ``out`` may be x, and ``residual_out``
-    residual or x."""
+    residual, or x where ``out`` is not."""
     T, d, dev, gpu = _norm_args(x, weight, residual)
     y = _like(out, x, "out")
     h = None

@@ -686,9 +686,10 @@ int norm_shape(int dtype, int w_dtype, int tokens, int d) {
   if (!float_dtype(dtype) || !float_dtype(w_dtype)) return ESG_ERR_UNSUPPORTED;
   return d % 16 != 0 || d > kNormMaxWidth ? ESG_ERR_UNSUPPORTED : ESG_OK;
 }
-// x, w and y present, residual and h together, everything aligned
+// x, w and y present, residual and h together, y and h apart, everything aligned
 int norm_args(const void* x, const void* residual, const void* w, const void* y, const void* h) {
   if (x == nullptr || w == nullptr || y == nullptr || (residual == nullptr) != (h == nullptr)) return ESG_ERR_INVALID_ARG;
+  if (y == h) return ESG_ERR_INVALID_ARG;  // x may be either, but not both
   for (const void* p : {x, residual, w, y, h})
     if (!aligned16(p)) return ESG_ERR_INVALID_ARG;
   return ESG_OK;

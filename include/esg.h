@@ -487,7 +487,7 @@ int esg_fp8_linear_bwd(const void* dy, int x_dtype, int w_dtype, int tokens, int
  * x, residual, y, h: dtype [tokens, d_model]; w: w_dtype [d_model] (ESG_F32 or
  * ESG_BF16 each, and not the same one necessarily).  residual NULL: h has to be
  * NULL.  rstd (or NULL): float [tokens], r for the backward.  y may be x, and h
- * may be residual or x (buffers that overlap otherwise are not allowed).
+ * may be residual or x, but y not h (buffers that overlap otherwise are not allowed).
  * The sum of squares, r and y's products are float32 (where the squares leave its
  * range, those of 2^-80 h, or of 2^100 h where eps is below 2^-100 too); each output
  * is rounded once.  rstd is infinite where r is past float32 (rows of less than 2^-128,
@@ -509,7 +509,7 @@ int esg_fp8_linear_bwd(const void* dy, int x_dtype, int w_dtype, int tokens, int
  * aligned): esg_rms_norm_bwd_workspace_size() bytes (0 for few tokens: it may be NULL),
  * needed for dw only.
  * Errors: ESG_ERR_INVALID_ARG (null or misaligned pointer, h without residual or
- * the reverse, dx == dy with dw, negative tokens, d_model <= 0), ESG_ERR_UNSUPPORTED (a dtype, d_model
+ * the reverse, y == h, dx == dy with dw, negative tokens, d_model <= 0), ESG_ERR_UNSUPPORTED (a dtype, d_model
  * not a multiple of 16 or above 16384), ESG_ERR_WORKSPACE.
  */
 int esg_rms_norm_fwd(const void* x, const void* residual, const void* w, int dtype, int w_dtype, int tokens, int d_model,

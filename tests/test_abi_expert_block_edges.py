@@ -112,3 +112,13 @@ def test_tangents_are_not_dropped(launches):
                 with pytest.raises(NotImplementedError, match="jvp"):
                     call(torch.autograd.forward_ad.make_dual(arg[name], torch.ones_like(arg[name])))
                 call(arg[name])                            # without a tangent as ever
+
+
+def test_norm_leaves_both_results():
+    """y in the place of x and the new residual too would leave one of them."""
+    names = ("x", "res", "w", "dt", "wdt", "T", "d", "eps", "y", "h", "rstd", "stream")
+    call = _caller(E.lib().esg_rms_norm_fwd, names, (P, 2 * P, P, 1, 0, 4, 64, 1e-6, P, P, P, NULL))
+    assert call() == 1 and call(y=3 * P, h=3 * P) == 1 and call(T=0) == 0
+    names = ("x", "res", "w", "dt", "wdt", "T", "d", "eps", "qt", "q", "scale", "h", "stream")
+    call = _caller(E.lib().esg_rms_norm_quant, names, (P, 2 * P, P, 1, 1, 4, 64, 1e-6, 2, 3 * P, P, 3 * P, NULL))
+    assert call() == 1

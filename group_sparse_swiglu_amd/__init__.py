@@ -833,9 +833,9 @@ def moe_decode(x, w_router, expert_bias, w_gate, w_up, w_down, topk: int, scalin
 
 
 def _rows32(*sizes):
-    """The library counts rows in 32 bits; ctypes would drop the bits above."""
-    if max(sizes) >= 1 << 31:
-        raise EsgError(f"{max(sizes)} rows: at most 2^31 - 1 in a call")
+    """The library counts rows and what else has a size in 32 bits; ctypes would drop the bits above."""
+    if max(sizes) >= 1 << 31 or min(sizes) < -1 << 31:
+        raise EsgError(f"a size of {max(sizes, key=abs)}: rows, widths and counts are at most 2^31 - 1")
 
 
 def _norm_args(x, weight, residual):
@@ -846,7 +846,7 @@ def _norm_args(x, weight, residual):
         raise EsgError("residual must have the shape and dtype of x")
     d = x.shape[-1]
     T = x.numel() // d if d else 0
-    _rows32(T)
+    _rows32(T, d)
     return T, d, x.device, x.get_device()
 
 
@@ -883,6 +883,7 @@ def rms_norm_fwd(x, weight, residual=None, eps: float = 1e-6, need_rstd: bool = 
 @functools.lru_cache(maxsize=4096)
 def rms_norm_bwd_workspace_size(tokens: int, d_model: int) -> int:
     """Bytes of scratch the weight gradient of rms_norm needs (0 for few tokens)."""
+    _rows32(tokens, d_model)
     need = _c_size()
     _check(lib().esg_rms_norm_bwd_workspace_size(tokens, d_model, ctypes.byref(need)), "rms_norm_bwd_workspace_size")
     return need.value
@@ -1017,7 +1018,10 @@ _SCORES = {"sigmoid": 0, "softmax": 1}
 
 def topk_routing_supported(num_experts: int, topk: int, groups: int = 1, topk_groups: Optional[int] = None) -> bool:
     """Whether topk_routing takes this shape (topk <= 32, at most 1024 experts and 64 groups; see include/esg.h)."""
-    return bool(lib().esg_topk_routing_supported(num_experts, topk, groups, groups if topk_groups is None else topk_groups))
+    topk_groups = groups if topk_groups is None else topk_groups
+    if max(num_experts, topk, groups, topk_groups) >= 1 << 31 or min(num_experts, topk, groups, topk_groups) < 1:
+        return False
+    return bool(lib().esg_topk_routing_supported(num_experts, topk, groups, topk_groups))
 
 
 def _scoring_code(scoring: str) -> int:
@@ -1033,7 +1037,7 @@ def topk_routing_fwd(logits, topk: int, scoring: str = "softmax", expert_bias=No
     if logits.dim() != 2:
         raise EsgError("logits must be [tokens, num_experts]")
     T, E = logits.shape
-    _rows32(T, E)
+    topk_groups = groups if topk_groups is None else topk_groups
     dev, gpu = logits.device, logits.get_device()
     stride = 1
     if expert_bias is not None:
@@ -1044,6 +1048,7 @@ def topk_routing_fwd(logits, topk: int, scoring: str = "softmax", expert_bias=No
         stride = expert_bias.stride(0) if E > 1 else 1
         if stride < 1:
             raise EsgError("expert_bias must have a positive stride")
+    _rows32(T, E, topk, groups, topk_groups, stride)
     code = _scoring_code(scoring)
     if out is None:
         probs = torch.empty(T, topk, dtype=torch.float32, device=dev)
@@ -1054,7 +1059,7 @@ def topk_routing_fwd(logits, topk: int, scoring: str = "softmax", expert_bias=No
             raise EsgError("out must be two [tokens, topk] tensors")
     _check(lib().esg_topk_routing_fwd(
         _dev(logits, "logits"), _dtype_code(logits), None if expert_bias is None else expert_bias.data_ptr(), stride, T, E,
-        topk, code, groups, groups if topk_groups is None else topk_groups, int(normalize),
+        topk, code, groups, topk_groups, int(normalize),
         1.0 if scaling_factor is None else float(scaling_factor), _dev(probs, "probs", torch.float32, gpu),
         _dev(indices, "indices", torch.int32, gpu), _stream(dev)), "topk_routing")
     return probs, indices
@@ -1066,7 +1071,7 @@ def topk_routing_bwd(dprobs, logits, indices, scoring: str = "softmax", normaliz
     if logits.dim() != 2 or indices.dim() != 2 or indices.shape[0] != logits.shape[0] or dprobs.shape != indices.shape:
         raise EsgError("logits must be [tokens, num_experts], dprobs and indices [tokens, topk]")
     T, E = logits.shape
-    _rows32(T, E)
+    _rows32(T, E, indices.shape[1])
     gpu = logits.get_device()
     _dev(dprobs, "dprobs", torch.float32, gpu), _dev(logits, "logits"), _dev(indices, "indices", torch.int32, gpu)
     return _topk_routing_bwd(dprobs, logits, indices, logits.device, _dtype_code(logits), T, E, indices.shape[1],
@@ -1133,6 +1138,7 @@ def mxfp4_quantize(x):
     if x.dim() < 1 or x.shape[-1] < 1:
         raise EsgError("x must be [..., K]")
     K, dev = x.shape[-1], x.device
+    _rows32(K)
     q = torch.empty(*x.shape[:-1], K // 2, dtype=torch.uint8, device=dev)
     scale = torch.empty(*x.shape[:-1], K // 32, dtype=torch.uint8, device=dev)
     _check(lib().esg_mxfp4_quant(_dev(x, "x"), _dtype_code(x), x.numel() // K, K, q.data_ptr(), scale.data_ptr(),
@@ -1145,6 +1151,7 @@ def mxfp4_dequantize(q, scale, dtype=torch.bfloat16):
     if q.dim() < 1 or q.dim() != scale.dim() or q.shape[:-1] != scale.shape[:-1] or q.shape[-1] != 16 * scale.shape[-1]:
         raise EsgError("q must be [..., K/2] and scale [..., K/32]")
     K, dev, u8 = 2 * q.shape[-1], q.device, torch.uint8
+    _rows32(K)
     y = torch.empty(*q.shape[:-1], K, dtype=dtype, device=dev)
     _check(lib().esg_mxfp4_dequant(_dev(q, "q", u8), _dev(scale, "scale", u8, q.get_device()), _dtype_code(y),
                                    q.numel() * 2 // K if K else 0, K, y.data_ptr(), _stream(dev)), "mxfp4_dequantize")
@@ -1154,6 +1161,7 @@ def mxfp4_dequantize(q, scale, dtype=torch.bfloat16):
 @functools.lru_cache(maxsize=4096)
 def mxfp4_matmul_workspace_size(M: int, N: int, K: int) -> int:
     """Bytes of scratch esg_mxfp4_matmul needs for this shape (0 for most)."""
+    _rows32(M, N, K)
     need = _c_size()
     _check(lib().esg_mxfp4_matmul_workspace_size(M, N, K, ctypes.byref(need)), "mxfp4_matmul_workspace_size")
     return need.value
@@ -1170,7 +1178,7 @@ def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, wor
     (M, KH), N, dev, gpu, u8 = a.shape, b.shape[0], a.device, a.get_device(), torch.uint8
     if a_scale.shape != (M, KH // 16) or b_scale.shape != (N, KH // 16):
         raise EsgError("a_scale must be [M, K/32] and b_scale [N, K/32]")
-    _rows32(M, N)
+    _rows32(M, N, 2 * KH)
     if out is None:
         out = torch.empty(M, N, dtype=out_dtype, device=dev)
     elif out.shape != (M, N):
@@ -1188,6 +1196,7 @@ def mxfp4_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, wor
 @functools.lru_cache(maxsize=4096)
 def mxfp4_grouped_matmul_workspace_size(M: int, N: int, K: int, experts: int) -> int:
     """Bytes of scratch esg_mxfp4_grouped_matmul needs for this shape (0 for most)."""
+    _rows32(M, N, K, experts)
     need = _c_size()
     _check(lib().esg_mxfp4_grouped_matmul_workspace_size(M, N, K, experts, ctypes.byref(need)),
            "mxfp4_grouped_matmul_workspace_size")
@@ -1212,7 +1221,7 @@ def mxfp4_grouped_matmul(a, a_scale, b, b_scale, offsets, rows=None, out_dtype=t
     if offsets.shape != (experts + 1,) or (rows is not None and rows.dim() != 1):
         raise EsgError("offsets must be int32 [E + 1] and rows int32 [M]")
     M = R if rows is None else rows.shape[0]
-    _rows32(M, N, R)
+    _rows32(M, N, R, 2 * KH, experts)
     if out is None:
         out = torch.empty(M, N, dtype=out_dtype, device=dev)
     elif out.shape != (M, N):

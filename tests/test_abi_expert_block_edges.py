@@ -122,3 +122,40 @@ def test_norm_leaves_both_results():
     names = ("x", "res", "w", "dt", "wdt", "T", "d", "eps", "qt", "q", "scale", "h", "stream")
     call = _caller(E.lib().esg_rms_norm_quant, names, (P, 2 * P, P, 1, 1, 4, 64, 1e-6, 2, 3 * P, P, 3 * P, NULL))
     assert call() == 1
+
+
+def test_widths_and_counts_past_32_bits():
+    """2^32 + 64 is not 64, whichever size it is.  (The message is that of too many rows; no tensor holds memory.)"""
+    meta, n = dict(device="meta"), (1 << 32) + 64
+    u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, **meta)  # noqa: E731
+    i32 = lambda *s: torch.empty(*s, dtype=torch.int32, **meta)  # noqa: E731
+    x = torch.empty(2, n, **meta)
+    z, p = torch.empty(0, 8, **meta), torch.empty(0, 2, **meta)
+    calls = [lambda: E.rms_norm(x, x[0]), lambda: E.rms_norm_quantize(x, x[0]), lambda: E.mxfp4_quantize(x),
+             lambda: E.mxfp4_dequantize(u8(2, n // 2), u8(2, n // 32)),
+             lambda: E.mxfp4_matmul(u8(2, n // 2), u8(2, n // 32), u8(3, n // 2), u8(3, n // 32)),
+             lambda: E.mxfp4_grouped_matmul(u8(2, n // 2), u8(2, n // 32), u8(1, 3, n // 2), u8(1, 3, n // 32), i32(2)),
+             lambda: E.mxfp4_grouped_matmul(u8(2, 16), u8(2, 1), u8(n, 0, 16), u8(n, 0, 1), i32(n + 1)),
+             lambda: E.topk_routing(z, n), lambda: E.topk_routing(z, 2, groups=n), lambda: E.topk_routing(z, 2, groups=4, topk_groups=n),
+             lambda: E.topk_routing_bwd(p.expand(0, 2), torch.empty(0, n, **meta), i32(0, 2)),
+             lambda: E.topk_routing_bwd(torch.empty(0, n, **meta), z, i32(0, n)),
+             lambda: E.rms_norm_bwd_workspace_size(4, n), lambda: E.mxfp4_matmul_workspace_size(4, n, 64),
+             lambda: E.mxfp4_matmul_workspace_size(4, 64, n), lambda: E.mxfp4_grouped_matmul_workspace_size(4, 4, 64, n),
+             lambda: E.rms_norm_bwd_workspace_size(-n, 64)]
+    for i, call in enumerate(calls):
+        with pytest.raises(E.EsgError, match="rows, widths and counts"):
+            print("call", i)
+            call()
+    ok = E.topk_routing_supported
+    assert ok(64, 8) and not ok(n, 8) and not ok(64, (1 << 32) + 8) and not ok(64, 8, (1 << 32) + 1, 1) and not ok(64 - (1 << 32), 8)
+
+
+def test_bias_strides_past_32_bits(launches):
+    """The library takes the bias's stride in 32 bits."""
+    bias = torch.zeros(1).as_strided((1,), (1,)).expand(8)
+    far = type("Far", (), dict(dim=lambda s: 1, shape=torch.Size([8]), dtype=torch.float32, is_cuda=True, get_device=lambda s: -1,
+                               stride=lambda s, i: (1 << 32) + 1))()
+    with pytest.raises(E.EsgError, match="rows, widths and counts"):
+        E.topk_routing_fwd(torch.zeros(4, 8), 2, expert_bias=far)
+    with pytest.raises(E.EsgError, match="GPU"):
+        E.topk_routing_fwd(torch.zeros(4, 8), 2, expert_bias=bias)

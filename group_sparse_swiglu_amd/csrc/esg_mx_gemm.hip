@@ -954,29 +954,24 @@ hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
     return hipGetLastError();
   }
   if (p.tile == 0) {
-    LaunchTimer timer("mx_rows", stream);
     // Waves of a workgroup: the fewer the more workgroups there are (us, two / four / eight: 704 x 64 above 33 / 36 / 48;
     // one row of N = 11008, K = 2048 6.2 / 6.2 / 6.9, of N = K = 8192 12.6 / 8.5 / 7.0)
     const long long wgs = (long long)p.nn * p.nm;
-    const dim3 grid(p.nn, p.nm, p.parts);
-    if constexpr (OUT == OUT_PARTS) {  // fewer than CUs
-      if (p.few == 16)
-        hipLaunchKernelGGL((mx_rows_kernel<8, 1, OUT>), grid, dim3(512), 0, stream, g);
-      else
-        hipLaunchKernelGGL((mx_rows_kernel<8, 4, OUT>), grid, dim3(512), 0, stream, g);
-    } else if (p.few == 16) {
-      if (wgs >= 16 * kNominalCUs)
-        hipLaunchKernelGGL((mx_rows_kernel<2, 1, OUT>), grid, dim3(128), 0, stream, g);
-      else if (wgs > 2 * kNominalCUs)
-        hipLaunchKernelGGL((mx_rows_kernel<4, 1, OUT>), grid, dim3(256), 0, stream, g);
-      else
-        hipLaunchKernelGGL((mx_rows_kernel<8, 1, OUT>), grid, dim3(512), 0, stream, g);
-    } else if (wgs > kNominalCUs) {
-      hipLaunchKernelGGL((mx_rows_kernel<4, 4, OUT>), grid, dim3(256), 0, stream, g);
-    } else {
-      hipLaunchKernelGGL((mx_rows_kernel<8, 4, OUT>), grid, dim3(512), 0, stream, g);
+    auto launch = [&](const char* name, auto* kernel, int waves) {
+      LaunchTimer timer(name, stream);
+      hipLaunchKernelGGL(kernel, dim3(p.nn, p.nm, p.parts), dim3(waves * 64), 0, stream, g);
+      return hipGetLastError();
+    };
+    if constexpr (OUT != OUT_PARTS) {  // (in parts they are fewer than CUs)
+      if (p.few == 16) {
+        if (wgs >= 16 * kNominalCUs) return launch("mx_rows_2_16", mx_rows_kernel<2, 1, OUT>, 2);
+        if (wgs > 2 * kNominalCUs) return launch("mx_rows_4_16", mx_rows_kernel<4, 1, OUT>, 4);
+      } else if (wgs > kNominalCUs) {
+        return launch("mx_rows_4_64", mx_rows_kernel<4, 4, OUT>, 4);
+      }
     }
-    return hipGetLastError();
+    if (p.few == 16) return launch("mx_rows_8_16", mx_rows_kernel<8, 1, OUT>, 8);
+    return launch("mx_rows_8_64", mx_rows_kernel<8, 4, OUT>, 8);
   }
   if constexpr (OUT != OUT_PARTS) if (p.tile == 256) {
     const int KS = g.K / 32, pieces = ((g.K + 127) / 128 + 4 * kWordLoads - 1) / (4 * kWordLoads);
@@ -987,7 +982,7 @@ hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  LaunchTimer timer("mx_tile", stream);
+  LaunchTimer timer(p.tile == 256 ? "mx_tile_256" : "mx_tile_128", stream);
   // as many workgroups as the LDS of the CUs holds at once: one, or two of the smaller tile
   if constexpr (OUT != OUT_PARTS) {
     if (p.tile == 256) {

@@ -135,9 +135,9 @@ __device__ __forceinline__ void mma_mx32(f32x16_t& acc, const u32x4_t& a, const 
 // its NW waves take the steps of K in turn and add their sums in LDS in wave order.
 // The read of b bounds it.  Everything goes through LDS in whole 128-byte rows, a wave
 // into a slot of its own, and it waits for its own loads only: what keeps memory busy is
-// many workgroups side by side, each short (64 tokens, 6 of 64 experts, N = 2816, K =
-// 2048: 33 us with two waves and one slot each, 36 with four, 51 with four waves of two
-// slots, which leave room for half as many workgroups).  The exponents of a step (8 bytes
+// many workgroups side by side (64 tokens, 6 of 64 experts, N = 2816, K = 2048: 40 us
+// with two or four waves and one slot each, 48 with eight; four waves of two slots, which
+// leave room for half as many workgroups, took 51 where one slot each took 36).  The exponents of a step (8 bytes
 // of a row that starts at any byte) come as the three dwords that hold them, and the one
 // needed is read back as a byte.
 // ---------------------------------------------------------------------------
@@ -954,8 +954,9 @@ hipError_t run(MxArgs& g, const Plan& p, hipStream_t stream) {
     return hipGetLastError();
   }
   if (p.tile == 0) {
-    // Waves of a workgroup: the fewer the more workgroups there are (us, two / four / eight: 704 x 64 above 33 / 36 / 48;
-    // one row of N = 11008, K = 2048 6.2 / 6.2 / 6.9, of N = K = 8192 12.6 / 8.5 / 7.0)
+    // Waves of a workgroup: the fewer the more workgroups there are (us, two / four / eight, in turn on one card: 64
+    // tokens, 6 of 64 experts, 2816 x 2048, 15488 of them, 39.9 / 39.7 / 48.5, 2048 x 1408 24.3 / 24.7 / 30.5; one row of
+    // N = 11008, K = 2048 6.2 / 6.2 / 6.9, of N = K = 8192 12.6 / 8.5 / 7.0)
     const long long wgs = (long long)p.nn * p.nm;
     auto launch = [&](const char* name, auto* kernel, int waves) {
       LaunchTimer timer(name, stream);

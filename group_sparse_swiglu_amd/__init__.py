@@ -988,7 +988,8 @@ def rms_norm_quantize(x, weight, residual=None, eps: float = 1e-6, format: str =
     ``format`` "fp8": q float8_e4m3fn [..., d], scale float32 [..., ceil(d/128)] as of
     fp8_quantize; "mxfp4": q uint8 [..., d/2], scale uint8 [..., d/32] as of
     mxfp4_quantize (d a multiple of 32).  No gradient.  ``residual_out`` may be
-    residual or x."""
+    residual or x.  As in all calls without a gradient, inputs have to be contiguous, here at
+    16-byte aligned addresses; rms_norm copies others."""
     T, d, dev, gpu = _norm_args(x, weight, residual)
     lead = x.shape[:-1]
     if format == "fp8":
@@ -1124,7 +1125,9 @@ def topk_routing(logits, topk: int, scoring: str = "softmax", expert_bias=None, 
     have the largest sum (all groups by default), ties to the lower number; their scores
     (``scoring`` "softmax" or "sigmoid"), divided by their sum with ``normalize`` and times
     ``scaling_factor``.  expert_bias: float32 [E] (a strided view is accepted), for the
-    choice only.  The gradient goes through the weights to the logits."""
+    choice only.  The gradient goes through the weights to the logits.  The choice is that of
+    exactly rounded scores, the weights are right to about 2^-20 of their value
+    (sigmoid_topk_routing, without groups or a gradient, rounds its scores once)."""
     if not (torch.is_grad_enabled() and logits.requires_grad or _dual()):
         return topk_routing_fwd(logits.contiguous(), topk, scoring, expert_bias, groups, topk_groups, normalize,
                                 scaling_factor)
@@ -1134,7 +1137,8 @@ def topk_routing(logits, topk: int, scoring: str = "softmax", expert_bias=None, 
 def mxfp4_quantize(x):
     """x (float32 or bfloat16 [..., K], K a multiple of 32) to 4-bit floating point with a power
     of two per 32 elements -> (q uint8 [..., K/2], two codes a byte, the first in the low half;
-    scale uint8 [..., K/32], a biased exponent each)."""
+    scale uint8 [..., K/32], a biased exponent each).  x has to be contiguous at a 16-byte
+    aligned address, as in all calls without a gradient."""
     if x.dim() < 1 or x.shape[-1] < 1:
         raise EsgError("x must be [..., K]")
     K, dev = x.shape[-1], x.device

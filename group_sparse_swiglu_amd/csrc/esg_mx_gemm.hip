@@ -323,10 +323,11 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs g) {
 // them there: the five dwords that hold the bytes of four steps (a row starts at any byte)
 // go into two slots, and the lanes that use a step's four bytes put them together.
 //
-// 32768 x 5504 x 2048 to bf16: 211 to 272 us (2.7 to 3.5 PFLOP/s), 8192 cubed 260 to 290 (3.8 to 4.2).  Bound by the
-// power that the products draw (registers alone: 10 PFLOP/s on zeros, 5.7 to 6.6 on random codes, at a clock of 1.4 to
-// 1.9 GHz) and, with few steps a tile, by the stores, which come from all CUs at once: the matrix cores are busy for 48 %
-// of the cycles of the first, 69 % of the second's.
+// 32768 x 5504 x 2048 to bf16: 211 to 272 us (2.7 to 3.5 PFLOP/s), 8192 cubed 260 to 290 (3.8 to 4.2).  Long loops are
+// bound by the power that the products draw (registers alone: 8.1 to 9.1 PFLOP/s on zeros, 5.9 to 6.4 on random codes,
+// at a clock of 1.4 to 1.5 GHz): the matrix cores are busy for 69 % of the second's cycles.  Of the first's they are for
+// 49 %: a step's reads and loads fill LDS for about as long as its products take, and the way between two tiles comes on
+// top (without the results' way 206 for 227, without their stores alone 214 to 223).
 // ---------------------------------------------------------------------------
 template <int BM, int BN>
 struct Tile {
